@@ -3,7 +3,7 @@
     python -m kda_chunked_prefill_02_gb300.build [--force]
 
 Compiles csrc/*.cu (one nvcc per translation unit, in parallel) and links
-  libkda.so          the product library (C ABI of include/kda.h)
+  libkda.so          the product library (C ABI of include/kda.h and include/kda_ops.h)
   libkda_selftest.so test-only checks of the tcgen05 / TMA building blocks
 next to this file.  Objects go to _build/ (git-ignored).
 """
@@ -22,9 +22,9 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "-I" + os.path.join(ROOT, "include"), "-diag-suppress", "1160"]
 
 LIB_SOURCES = ["kda_api.cu", "kda_prep.cu", "kda_state.cu", "kda_state_head.cu", "kda_verify.cu",
-               "kda_verify_wy.cu", "kda_noalloc.cu", "kda_host.cu"]
+               "kda_verify_wy.cu", "kda_noalloc.cu", "kda_host.cu", "kda_ops_api.cu", "kda_conv.cu", "kda_rope.cu", "kda_tree.cu"]
 SELFTEST_SOURCES = ["selftest.cu"]
-HEADERS = ["sm103.cuh", "kda_internal.h", "tmap.h"]
+HEADERS = ["sm103.cuh", "kda_internal.h", "ops_internal.h", "tmap.h"]
 
 LIB = os.path.join(HERE, "libkda.so")
 SELFTEST_LIB = os.path.join(HERE, "libkda_selftest.so")
@@ -39,7 +39,8 @@ def _nvcc():
 
 def _newest_input(srcs):
     files = [os.path.join(CSRC, s) for s in srcs + HEADERS] + [
-        os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)]
+        os.path.join(ROOT, "include", "kda.h"), os.path.join(ROOT, "include", "kda_ops.h"),
+        os.path.abspath(__file__)]
     return max(os.path.getmtime(f) for f in files)
 
 

@@ -1,0 +1,136 @@
+// ops_internal.h -- parameters passed from the host checks (kda_ops_api.cu) to
+// the kernels of include/kda_ops.h, their launchers, and the element-type
+// helpers those kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+struct ConvParams {
+    const void* x;
+    void* out;                // nullptr: states only
+    const void* w;
+    const float* bias;
+    void* pool;               // [P, W - 1, C] or nullptr
+    const int32_t* slot;
+    const int32_t* has_state;
+    const int32_t* accepted;
+    const int32_t* cu;        // nullptr: padded
+    int32_t* status;
+    int64_t xs[2], os[2];
+    int N, T;                 // sequences; tokens a sequence (padded) or in all (packed)
+    int64_t total;            // tokens in all
+    int C, norm_c, P;
+    int silu;
+    int tile;                 // tokens a tile (set by the launcher)
+    float eps;
+};
+cudaError_t launch_short_conv(const ConvParams& p, int width, bool f16, bool w_f32, int num_sms, cudaStream_t s);
+
+struct RopeParams {
+    const void *q, *k, *v;
+    void *q_out, *k_out, *k_cache, *v_cache;
+    const int64_t* slots;
+    const int32_t* positions;
+    const float* inv_freq;
+    const void *q_w, *k_w;
+    int32_t* status;
+    int64_t qs[3], ks[3], vs[3], qos[3], kos[3], kcs[3], vcs[3];
+    int64_t tokens;           // batch * T
+    int T, Hq, Hk, D, rot;
+    int64_t cache_rows;       // num_pages * page_size
+    int page;
+    int norm, interleaved, w_f32;
+    int chunks, chunk_passes; // a token's heads are cut into `chunks` runs (set by the launcher)
+    float eps, scale;
+};
+cudaError_t launch_qk_norm_rope(const RopeParams& p, bool f16, int num_sms, cudaStream_t s);
+
+struct TreeParams {
+    const void *q, *kc, *vc;
+    void* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* ctx;
+    const int32_t* nodes;
+    const uint64_t* mask;
+    int32_t* status;
+    float* part_o;            // [R, Hk, splits, rows, D]
+    float* part_lse;          // [R, Hk, splits, rows], base 2
+    int64_t qs[3], os[3], ks[3], vs[3], table_stride;
+    int R, N, Hq, Hk, G, rows, words;   // rows = N * G, words of a mask row
+    int P, page;
+    int64_t max_len;          // longest context and nodes of a request (at most what its page row holds)
+    uint32_t page_magic;      // floor(2^32 / page) (2^32 - 1 for page 1)
+    int chunk, splits;        // tokens a split; splits of the longest request
+    int row_blocks;           // set by the launcher
+    float scale_log2;         // scale * log2(e)
+};
+// How a call is cut: tokens a split and splits of the longest request.
+struct TreePlan {
+    int chunk, splits;
+};
+TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, int num_sms);
+cudaError_t launch_tree_attention(const TreeParams& p, int D, bool f16, cudaStream_t s);
+
+// ---------------------------------------------------------------- element types
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static constexpr uint32_t kExpMask = 0x7f80u;
+};
+template <> struct Elem<__half> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ float one(__half x) { return __half2float(x); }
+    static constexpr uint32_t kExpMask = 0x7c00u;
+};
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = Elem<T>::unpack(w[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]), Elem<T>::pack(f[4], f[5]),
+                      Elem<T>::pack(f[6], f[7]));
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+}  // namespace kda
