@@ -85,7 +85,8 @@ kda_status kda_short_conv(const kda_short_conv_args* a, void* stream) {
     if (!a->weight || (total > 0 && !a->x) || (!a->out && !a->conv_state) ||
         (a->conv_state && a->pool_size < 1) || (total > 0 && a->out == a->x))
         return KDA_ERR_INVALID_ARG;
-    if (!aligned16(a->x) || !aligned16(a->out) || !aligned16(a->conv_state) || !strides8(a->x_stride) ||
+    if (!aligned16(a->x) || !aligned16(a->out) || !aligned16(a->conv_state) ||
+        !aligned16(a->weight) || !aligned16(a->bias) || !strides8(a->x_stride) ||
         (a->out && !strides8(a->out_stride)))
         return KDA_ERR_UNSUPPORTED;
     const int sms = device_sm_count();
@@ -122,7 +123,8 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, void* stream) {
         (a->v_cache && (!cached || !a->v)) || (cached && (a->page_size < 1 || a->num_pages < 1)))
         return KDA_ERR_INVALID_ARG;
     if (cached && (a->page_size > INT32_MAX || a->num_pages > INT32_MAX)) return KDA_ERR_UNSUPPORTED;
-    const void* ptrs[] = {a->q, a->k, a->v, a->q_out, a->k_out, a->k_cache, a->v_cache};
+    const void* ptrs[] = {a->q, a->k, a->v, a->q_out, a->k_out, a->k_cache, a->v_cache,
+                          a->q_weight, a->k_weight};
     for (const void* ptr : ptrs)
         if (!aligned16(ptr)) return KDA_ERR_UNSUPPORTED;
     if ((a->num_q_heads > 0 && (!strides8(a->q_stride) || !strides8(a->q_out_stride))) ||

@@ -13,9 +13,13 @@
 // element; each element is read once and written once, and the kernel is bound
 // by HBM bandwidth (4 bytes an element).  A head's channels are kLanes adjacent
 // lanes (8, 16 or 32 for head sizes up to 64, 128 and 256); the sum of squares
-// is a shuffle reduction over them and the partner of a half-split pair one
-// shuffle of the packed input, since rot_dim / 2 is a multiple of a lane's 8
-// channels.
+// is a shuffle reduction over them, and the partner of a half-split pair lies in
+// another lane's piece, since rot_dim / 2 is a multiple of a lane's 8 channels.
+//
+// All of a warp's pieces are asked for at once by 16-byte asynchronous copies
+// into shared memory (up to kMaxPasses of 512 bytes), and A and B are formed
+// while they fly; with the loads in registers, four at a time, the same sums
+// took 171 us for 32768 tokens of 32 + 8 heads of 128.
 //
 // The angle.  t = position * f reaches 1e5 and more in a long context, where a
 // rounded fp32 product is off by 1e-2.  The product is kept in two fp32 parts
@@ -30,7 +34,7 @@ namespace kda {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;
+constexpr int kMaxPasses = 23;   // 512 bytes each, and as many zeros: 48 KB for a CTA's four warps
 
 // position * f modulo 2 pi, in about [-5, 5], within 1e-6.
 __device__ __forceinline__ float reduced_angle(int pos, float f) {
@@ -60,7 +64,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
     const int cc = act ? c0 : 0;
 
     const int qp = (p.Hq + kGroup - 1) / kGroup, kp = (p.Hk + kGroup - 1) / kGroup;
-    const int first = chunk * p.chunk_passes, end = first + p.chunk_passes;   // passes: q heads, k heads, v heads
+    const int first = chunk * p.chunk_passes;   // passes: q heads, k heads, v heads
+    const int end = min(first + p.chunk_passes, qp + kp + (p.v_cache ? kp : 0));
 
     // where the token's cache row is
     int64_t kc_off = -1, vc_off = -1;
@@ -75,11 +80,41 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
         }
     }
 
+    // every piece of this run of heads, on its way to shared memory
+    extern __shared__ __align__(16) uint4 pieces[];
+    uint4* const mine = pieces + (threadIdx.x >> 5) * (p.chunk_passes + 1) * 32;   // [pass][lane], then 32 zeros
+    const bool values = vc_off >= 0 && p.v_cache;
+    auto fetch = [&](int i0, int i1, int base, const T* src, int64_t hs, int heads) {
+        uint4* dst = mine + (i0 - first) * 32 + lane;
+        int h = (i0 - base) * kGroup + sub;
+        src += h * hs + cc;
+        for (int i = i0; i < i1; ++i) {
+            if (act && h < heads) cp_async16(dst, src);
+            else *dst = make_uint4(0, 0, 0, 0);
+            dst += 32;
+            h += kGroup;
+            src += kGroup * hs;
+        }
+    };
+    if (first < qp)
+        fetch(first, min(end, qp), 0, static_cast<const T*>(p.q) + b * p.qs[0] + t * p.qs[1], p.qs[2], p.Hq);
+    if (end > qp && first < qp + kp)
+        fetch(max(first, qp), min(end, qp + kp), qp, static_cast<const T*>(p.k) + b * p.ks[0] + t * p.ks[1], p.ks[2],
+              p.Hk);
+    if (end > qp + kp && values)
+        fetch(max(first, qp + kp), end, qp + kp, static_cast<const T*>(p.v) + b * p.vs[0] + t * p.vs[1], p.vs[2], p.Hk);
+    cp_async_commit();
+    mine[p.chunk_passes * 32 + lane] = make_uint4(0, 0, 0, 0);
+
     const bool rotates = c0 < p.rot;
     const int half = p.rot >> 1;
     const bool low = c0 < half;
-    // lane that holds the partner channels (itself unless a half-split pair)
-    const int mate = (!p.interleaved && rotates) ? lane + (low ? half / 8 : -half / 8) : lane;
+    // first of the partner channels (half-split; interleaved pairs lie within the piece)
+    const int pc0 = (p.interleaved || !rotates) ? cc : low ? cc + half : cc - half;
+    // Where a pass's partner piece is: for channels that do not rotate the zeros,
+    // so that they take no part of another channel, not even 0 * inf.
+    const int mate = rotates ? lane + (pc0 - cc) / 8 : p.chunk_passes * 32 + lane;
+    const int mate_step = rotates ? 32 : 0;
     float cs[8], sn[8];
     if (first < qp + kp) {
         const int pos = rotates ? p.positions[token] : 0;
@@ -87,94 +122,124 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
         for (int i = 0; i < 8; ++i) {
             cs[i] = 1.f;
             sn[i] = 0.f;
-            if (rotates) {
+            if (rotates && !(p.interleaved && (i & 1))) {
                 const int pair = p.interleaved ? (c0 + i) >> 1 : (low ? c0 + i : c0 + i - half);
-                const float a = reduced_angle(pos, p.inv_freq[pair]);
+                const float a = reduced_angle(pos, __ldg(p.inv_freq + pair));
                 cs[i] = p.scale * __cosf(a);
                 sn[i] = p.scale * __sinf(a);
             }
         }
+        if (rotates && p.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                cs[i + 1] = cs[i];
+                sn[i + 1] = sn[i];
+            }
+        }
     }
-    auto weight = [&](const void* w, int c) -> float {
-        if (!w) return 1.f;
-        return p.w_f32 ? static_cast<const float*>(w)[c] : Elem<T>::one(static_cast<const T*>(w)[c]);
+    auto weights = [&](const void* w, int c, float (&f)[8]) {
+        if (!w) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = 1.f;
+        } else if (p.w_f32) {
+            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+            const float4 a = __ldg(src), e = __ldg(src + 1);
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = e.x; f[5] = e.y; f[6] = e.z; f[7] = e.w;
+        } else {
+            F2 x[4];
+            unpack8<T>(ldg16(static_cast<const T*>(w) + c), x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = f2_parts(x[i]);
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        }
     };
+    bool landed = false;
+    const float inv_d = 1.f / (float)p.D;
 
-    // heads [h0, h1) of one tensor, normed and rotated
-    auto rotate = [&](const T* src, int64_t hs, const void* w, T* dst, int64_t dhs, T* dst2, int64_t dhs2, int h0,
-                      int h1) {
-        float A[8], B[8];
+    // passes [i0, i1), whose first is head 0 of a tensor at pass `base`, normed and rotated
+    auto rotate = [&](int i0, int i1, int base, int heads, const void* w, T* dst, int64_t dhs, T* dst2, int64_t dhs2) {
+        F2 A[4], B[4];
+        {
+            float own[8], other[8];
+            weights(w, cc, own);
+            weights(w, pc0, other);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int pc = !rotates ? cc + i : p.interleaved ? (cc + i) ^ 1 : low ? cc + i + half : cc + i - half;
-            const bool minus = p.interleaved ? (i & 1) == 0 : low;
-            A[i] = act ? weight(w, cc + i) * cs[i] : 0.f;
-            B[i] = act ? weight(w, pc) * (minus ? -sn[i] : sn[i]) : 0.f;
+            for (int k = 0; k < 4; ++k) {
+                A[k] = f2(own[2 * k] * cs[2 * k], own[2 * k + 1] * cs[2 * k + 1]);
+                B[k] = p.interleaved
+                           ? f2(-other[2 * k + 1] * sn[2 * k], other[2 * k] * sn[2 * k + 1])
+                           : f2(other[2 * k] * (low ? -sn[2 * k] : sn[2 * k]),
+                                other[2 * k + 1] * (low ? -sn[2 * k + 1] : sn[2 * k + 1]));
+            }
         }
-        for (int h = h0; h < h1; h += kGroup * kRopeUnroll) {
-            uint4 raw[kRopeUnroll];
+        if (!landed) {
+            cp_async_wait<0>();
+            __syncwarp();   // partners are read from other lanes' pieces
+            landed = true;
+        }
+        const uint4* src = mine + (i0 - first) * 32 + lane;
+        const uint4* msrc = mine + (i0 - first) * mate_step + mate;
+        int h = (i0 - base) * kGroup + sub;
+        if (dst) dst += h * dhs + cc;
+        if (dst2) dst2 += h * dhs2 + cc;
+#pragma unroll 2
+        for (int i = i0; i < i1; ++i) {
+            F2 x[4], y[4];
+            unpack8<T>(*src, x);
+            uint4 m = *msrc;
+            src += 32;
+            msrc += mate_step;
+            float r = 1.f;
+            if (p.norm) {
+                F2 s2 = f2_mul(x[0], x[0]);
 #pragma unroll
-            for (int u = 0; u < kRopeUnroll; ++u) {
-                const int hh = h + u * kGroup + sub;
-                raw[u] = (act && hh < h1) ? *reinterpret_cast<const uint4*>(src + hh * hs + cc) : make_uint4(0, 0, 0, 0);
+                for (int k = 1; k < 4; ++k) s2 = f2_fma(x[k], x[k], s2);
+                const float2 s = f2_parts(s2);
+                float ss = s.x + s.y;
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                r = rsqrt_approx(fmaf(ss, inv_d, p.eps));
             }
+            if (p.interleaved) {   // the partner is the other half of a 32-bit word
+                m.x = __byte_perm(m.x, 0, 0x1032);
+                m.y = __byte_perm(m.y, 0, 0x1032);
+                m.z = __byte_perm(m.z, 0, 0x1032);
+                m.w = __byte_perm(m.w, 0, 0x1032);
+            }
+            unpack8<T>(m, y);
 #pragma unroll
-            for (int u = 0; u < kRopeUnroll; ++u) {
-                const int hh = h + u * kGroup + sub;
-                if (h + u * kGroup >= h1) break;
-                float x[8], y[8];
-                unpack8<T>(raw[u], x);
-                float r = 1.f;
-                if (p.norm) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    r = rsqrt_approx(ss / (float)p.D + p.eps);
-                }
-                if (p.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-                } else {
-                    uint4 m;
-                    m.x = __shfl_sync(0xffffffffu, raw[u].x, mate);
-                    m.y = __shfl_sync(0xffffffffu, raw[u].y, mate);
-                    m.z = __shfl_sync(0xffffffffu, raw[u].z, mate);
-                    m.w = __shfl_sync(0xffffffffu, raw[u].w, mate);
-                    unpack8<T>(m, y);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // channels that do not rotate take no part of another, not even 0 * inf
-                    const float rest = rotates ? B[i] * y[i] : 0.f;
-                    y[i] = r * fmaf(A[i], x[i], rest);
-                }
+            for (int k = 0; k < 4; ++k) y[k] = f2_mul(f2(r, r), f2_fma(A[k], x[k], f2_mul(B[k], y[k])));
+            if (act && h < heads) {
                 const uint4 o = pack8<T>(y);
-                if (act && hh < h1) {
-                    if (dst) *reinterpret_cast<uint4*>(dst + hh * dhs + cc) = o;
-                    if (dst2) *reinterpret_cast<uint4*>(dst2 + hh * dhs2 + cc) = o;
-                }
+                if (dst) *reinterpret_cast<uint4*>(dst) = o;
+                if (dst2) *reinterpret_cast<uint4*>(dst2) = o;
             }
+            h += kGroup;
+            dst += kGroup * dhs;
+            dst2 += kGroup * dhs2;
         }
     };
-    if (first < qp) {
-        rotate(static_cast<const T*>(p.q) + b * p.qs[0] + t * p.qs[1], p.qs[2], p.q_w,
-               static_cast<T*>(p.q_out) + b * p.qos[0] + t * p.qos[1], p.qos[2], nullptr, 0, first * kGroup,
-               min(end * kGroup, p.Hq));
-    }
+    if (first < qp)
+        rotate(first, min(end, qp), 0, p.Hq, p.q_w, static_cast<T*>(p.q_out) + b * p.qos[0] + t * p.qos[1], p.qos[2],
+               nullptr, 0);
     if (end > qp && first < qp + kp) {
         T* out = p.k_out ? static_cast<T*>(p.k_out) + b * p.kos[0] + t * p.kos[1] : nullptr;
         T* cache = kc_off >= 0 ? static_cast<T*>(p.k_cache) + kc_off : nullptr;
-        rotate(static_cast<const T*>(p.k) + b * p.ks[0] + t * p.ks[1], p.ks[2], p.k_w, out, p.kos[2], cache, p.kcs[2],
-               max(first - qp, 0) * kGroup, min((end - qp) * kGroup, p.Hk));
+        rotate(max(first, qp), min(end, qp + kp), qp, p.Hk, p.k_w, out, out ? p.kos[2] : 0, cache,
+               cache ? p.kcs[2] : 0);
     }
-    if (end > qp + kp && vc_off >= 0 && p.v_cache) {
-        const T* src = static_cast<const T*>(p.v) + b * p.vs[0] + t * p.vs[1];
-        T* dst = static_cast<T*>(p.v_cache) + vc_off;
-        const int h1 = min((end - qp - kp) * kGroup, p.Hk);
-        for (int h = max(first - qp - kp, 0) * kGroup + sub; h < h1; h += kGroup)
-            if (act) *reinterpret_cast<uint4*>(dst + h * p.vcs[2] + cc) = ldg16(src + h * p.vs[2] + cc);
+    cp_async_wait<0>();
+    if (end > qp + kp && values) {
+        int i = max(first, qp + kp), h = (i - qp - kp) * kGroup + sub;
+        T* dst = static_cast<T*>(p.v_cache) + vc_off + h * p.vcs[2] + cc;
+        for (; i < end; ++i) {
+            if (act && h < p.Hk) *reinterpret_cast<uint4*>(dst) = mine[(i - first) * 32 + lane];
+            h += kGroup;
+            dst += kGroup * p.vcs[2];
+        }
     }
 }
 
@@ -183,19 +248,20 @@ cudaError_t launch_rope_t(RopeParams& p, int num_sms, cudaStream_t s) {
     const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32, group = 32 / lanes;
     const int qp = (p.Hq + group - 1) / group, kp = (p.Hk + group - 1) / group;
     const int passes = qp + kp + (p.v_cache ? kp : 0);
-    // A warp takes all of a token's heads (A and B are formed once) unless that
-    // leaves fewer than 16 warps an SM: then the heads are cut further, down to
-    // one unrolled run.
-    int chunks = 1;
-    while (p.tokens * chunks < 16LL * num_sms && chunks * kRopeUnroll < passes) chunks <<= 1;
+    // A warp takes all of a token's heads (A and B are formed once), as far as
+    // its shared memory goes, unless that leaves fewer than 16 warps an SM: then
+    // the heads are cut further, down to two passes.
+    int chunks = (passes + kMaxPasses - 1) / kMaxPasses;
+    while (p.tokens * chunks < 16LL * num_sms && chunks * 2 < passes) chunks <<= 1;
     p.chunk_passes = (passes + chunks - 1) / chunks;
     p.chunks = (passes + p.chunk_passes - 1) / p.chunk_passes;
+    const size_t smem = (size_t)(kRopeThreads / 32) * (p.chunk_passes + 1) * 512;
     const int64_t items = p.tokens * p.chunks, per = kRopeThreads / 32;
     const int64_t grid = (items + per - 1) / per;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    if (lanes == 8) qk_norm_rope_kernel<T, 8><<<(unsigned)grid, kRopeThreads, 0, s>>>(p);
-    else if (lanes == 16) qk_norm_rope_kernel<T, 16><<<(unsigned)grid, kRopeThreads, 0, s>>>(p);
-    else qk_norm_rope_kernel<T, 32><<<(unsigned)grid, kRopeThreads, 0, s>>>(p);
+    if (lanes == 8) qk_norm_rope_kernel<T, 8><<<(unsigned)grid, kRopeThreads, smem, s>>>(p);
+    else if (lanes == 16) qk_norm_rope_kernel<T, 16><<<(unsigned)grid, kRopeThreads, smem, s>>>(p);
+    else qk_norm_rope_kernel<T, 32><<<(unsigned)grid, kRopeThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -101,20 +101,70 @@ template <> struct Elem<__half> {
     static __device__ __forceinline__ float one(__half x) { return __half2float(x); }
     static constexpr uint32_t kExpMask = 0x7c00u;
 };
+// Two fp32 values in one 64-bit register pair, for the packed operations.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_parts(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+// 8 elements of 16 bits <-> 4 pairs.
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& r, F2 (&f)[4]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 v = Elem<T>::unpack(w[i]);
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
+        f[i] = f2(v.x, v.y);
     }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = f2_parts(f[i]);
+        w[i] = Elem<T>::pack(v.x, v.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]), Elem<T>::pack(f[4], f[5]),
                       Elem<T>::pack(f[6], f[7]));
+}
+// 16-byte asynchronous copies global -> shared.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
