@@ -22,7 +22,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "-I" + os.path.join(ROOT, "include"), "-diag-suppress", "1160"]
 
 LIB_SOURCES = ["kda_api.cu", "kda_prep.cu", "kda_state.cu", "kda_state_head.cu", "kda_verify.cu",
-               "kda_verify_wy.cu", "kda_noalloc.cu", "kda_host.cu", "kda_ops_api.cu", "kda_conv.cu", "kda_rope.cu", "kda_tree.cu"]
+               "kda_verify_wy.cu", "kda_noalloc.cu", "kda_host.cu", "kda_ops_api.cu", "kda_conv.cu",
+               "kda_rope.cu", "kda_tree.cu", "kda_tree_mma.cu"]
 SELFTEST_SOURCES = ["selftest.cu"]
 HEADERS = ["sm103.cuh", "kda_internal.h", "ops_internal.h", "tmap.h"]
 

@@ -57,7 +57,7 @@ int sm_count_or_default() {
 TreePlan plan_of(const kda_tree_attention_args* a, int64_t max_len) {
     return tree_plan((int)a->num_requests, (int)a->num_k_heads,
                      (int)(a->max_nodes * (a->num_q_heads / a->num_k_heads)), (int)a->head_dim, max_len,
-                     (int)a->page_size, sm_count_or_default());
+                     (int)a->page_size, a->scale, sm_count_or_default());
 }
 
 size_t tree_workspace(const kda_tree_attention_args* a, const TreePlan& plan) {
@@ -188,7 +188,7 @@ kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
     p.part_o = static_cast<float*>(a->workspace);
     p.part_lse = p.part_o + (need ? (size_t)p.R * p.Hk * p.splits * p.rows * a->head_dim : 0);
     p.scale_log2 = a->scale * 1.4426950408889634f;
-    return status_of(launch_tree_attention(p, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
+    return status_of(launch_tree_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
                                            static_cast<cudaStream_t>(stream)));
 }
 

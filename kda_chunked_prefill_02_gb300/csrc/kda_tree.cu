@@ -76,23 +76,6 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// n / page for n < 2^32: the magic product is short by at most one.
-__device__ __forceinline__ uint32_t page_div(uint32_t n, uint32_t page, uint32_t magic) {
-    uint32_t q = __umulhi(n, magic);
-    if (n - q * page >= page) ++q;
-    return q;
-}
-
-// Context and drafted tokens of a request; false (and no tokens) if they do
-// not fit the call.
-__device__ __forceinline__ bool tree_lengths(const TreeParams& p, int r, int& ctx, int& n) {
-    ctx = p.ctx[r];
-    n = p.nodes ? p.nodes[r] : p.N;
-    const bool ok = ctx >= 0 && n >= 0 && n <= p.N && (int64_t)ctx + n <= p.max_len;
-    if (!ok) ctx = n = 0;
-    return ok;
-}
-
 // Byte offset of 16-byte piece c of row r in a tile of rows of D elements.
 template <int D>
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {
@@ -440,41 +423,58 @@ cudaError_t launch_rows_t(const TreeParams& q, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(p.splits * p.row_blocks), (unsigned)p.Hk, (unsigned)p.R);
     tree_rows_kernel<T, D, MT><<<grid, kTreeThreads, smem, s>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
-    const dim3 jgrid((unsigned)((p.rows + 3) / 4), (unsigned)p.Hk, (unsigned)p.R);
-    return launch_maybe_pdl(tree_join_kernel<T, D>, jgrid, dim3(128), 0, s, true, p);
+    return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_tree_t(const TreeParams& p, int D, cudaStream_t s) {
+cudaError_t launch_rows(const TreeParams& p, int D, cudaStream_t s) {
     const bool one = rows_per_block(p.rows, D) == 16;
     if (D == 64) return one ? launch_rows_t<T, 64, 1>(p, s) : launch_rows_t<T, 64, 2>(p, s);
     if (D == 128) return one ? launch_rows_t<T, 128, 1>(p, s) : launch_rows_t<T, 128, 2>(p, s);
     return launch_rows_t<T, 256, 1>(p, s);
 }
 
+template <typename T>
+cudaError_t launch_join(const TreeParams& p, int D, cudaStream_t s) {
+    const dim3 grid((unsigned)((p.rows + 3) / 4), (unsigned)p.Hk, (unsigned)p.R);
+    const auto kernel = D == 64 ? tree_join_kernel<T, 64> : D == 128 ? tree_join_kernel<T, 128> : tree_join_kernel<T, 256>;
+    return launch_maybe_pdl(kernel, grid, dim3(128), 0, s, true, p);
+}
+
 }  // namespace
 
-TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, int num_sms) {
-    const int rb = rows_per_block(rows, D);
-    const int64_t items = (int64_t)R * Hk * ((rows + rb - 1) / rb);
-    const int64_t target = 8LL * num_sms;   // CTAs of the longest contexts: four waves of two an SM
-    int64_t splits = items >= target ? 1 : (target + items - 1) / items;
-    // at least 256 tokens a split, and at most 1024 pages
-    const int64_t most = (max_len + 255) / 256;
+TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms) {
+    TreePlan t;
+    // More rows than the warp-level kernel takes at a time: the 128-row products,
+    // where pages are whole 8-row groups of a tile.
+    t.mma = rows > 32 && D <= 128 && page >= 8 && (page & (page - 1)) == 0 && scale > 0.f;
+    const int block = t.mma ? 256 : rows_per_block(rows, D);
+    const int unit = t.mma ? 128 : kTile;
+    const int64_t items = (int64_t)R * Hk * ((rows + block - 1) / block);
+    // CTAs of the longest contexts: four waves of two an SM (rows kernel); one
+    // wave of one an SM for one request, whose splits are all alike, else four.
+    const int64_t target = t.mma ? (R == 1 ? 1LL : 4LL) * num_sms : 8LL * num_sms;
+    int64_t splits = target / items;
+    // at least 256 (1024) tokens a split, and at most 1024 pages
+    const int64_t least = t.mma ? 1024 : 256, most = (max_len + least - 1) / least;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
     int64_t chunk = (max_len + splits - 1) / splits;
     if (chunk > 1024LL * page) chunk = 1024LL * page;
-    chunk = (chunk + kTile - 1) / kTile * kTile;
-    if (chunk < kTile) chunk = kTile;
+    chunk = (chunk + unit - 1) / unit * unit;
+    if (chunk < unit) chunk = unit;
     splits = (max_len + chunk - 1) / chunk;
-    return {(int)chunk, (int)(splits > 0 ? splits : 1)};
+    t.chunk = (int)chunk;
+    t.splits = (int)(splits > 0 ? splits : 1);
+    return t;
 }
 
-cudaError_t launch_tree_attention(const TreeParams& p, int D, bool f16, cudaStream_t s) {
-    return f16 ? launch_tree_t<__half>(p, D, s) : launch_tree_t<__nv_bfloat16>(p, D, s);
+cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (!plan.mma || !launch_tree_mma(p, D, f16, s, &e))
+        e = f16 ? launch_rows<__half>(p, D, s) : launch_rows<__nv_bfloat16>(p, D, s);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return f16 ? launch_join<__half>(p, D, s) : launch_join<__nv_bfloat16>(p, D, s);
 }
 
 }  // namespace kda

@@ -70,12 +70,33 @@ struct TreeParams {
     int row_blocks;           // set by the launcher
     float scale_log2;         // scale * log2(e)
 };
-// How a call is cut: tokens a split and splits of the longest request.
+// How a call is cut: tokens a split, splits of the longest request, and which
+// kernel takes the rows.
 struct TreePlan {
     int chunk, splits;
+    bool mma;
 };
-TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, int num_sms);
-cudaError_t launch_tree_attention(const TreeParams& p, int D, bool f16, cudaStream_t s);
+TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms);
+cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s);
+// The kernel for many rows; false if the caches' layout has no tensor map.
+bool launch_tree_mma(const TreeParams& p, int D, bool f16, cudaStream_t s, cudaError_t* e);
+
+// n / page for n < 2^32: the magic product is short by at most one.
+__device__ __forceinline__ uint32_t page_div(uint32_t n, uint32_t page, uint32_t magic) {
+    uint32_t q = __umulhi(n, magic);
+    if (n - q * page >= page) ++q;
+    return q;
+}
+
+// Context and drafted tokens of a request; false (and no tokens) if they do
+// not fit the call.
+__device__ __forceinline__ bool tree_lengths(const TreeParams& p, int r, int& ctx, int& n) {
+    ctx = p.ctx[r];
+    n = p.nodes ? p.nodes[r] : p.N;
+    const bool ok = ctx >= 0 && n >= 0 && n <= p.N && (int64_t)ctx + n <= p.max_len;
+    if (!ok) ctx = n = 0;
+    return ok;
+}
 
 // ---------------------------------------------------------------- element types
 template <typename T> struct Elem;
