@@ -61,9 +61,7 @@ TreePlan plan_of(const kda_tree_attention_args* a, int64_t max_len) {
 }
 
 size_t tree_workspace(const kda_tree_attention_args* a, const TreePlan& plan) {
-    if (plan.splits <= 1) return 0;
-    const size_t rows = (size_t)a->num_requests * a->num_q_heads * a->max_nodes * plan.splits;
-    return rows * ((size_t)a->head_dim + 1) * sizeof(float);
+    return plan.parts * sizeof(int4) + plan.part_rows * ((size_t)a->head_dim + 1) * sizeof(float);
 }
 
 }  // namespace
@@ -183,10 +181,13 @@ kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
     p.R = (int)a->num_requests; p.N = (int)a->max_nodes; p.Hq = (int)a->num_q_heads; p.Hk = (int)a->num_k_heads;
     p.G = p.Hq / p.Hk; p.rows = p.N * p.G; p.words = (p.N + 63) / 64;
     p.P = (int)a->num_pages; p.page = (int)a->page_size; p.max_len = max_len;
-    p.page_magic = p.page == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)p.page);
+    auto magic = [](int d) { return d == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)d); };
+    p.page_magic = magic(p.page);
+    p.group_magic = magic(p.G);
     p.chunk = plan.chunk; p.splits = plan.splits;
-    p.part_o = static_cast<float*>(a->workspace);
-    p.part_lse = p.part_o + (need ? (size_t)p.R * p.Hk * p.splits * p.rows * a->head_dim : 0);
+    p.parts = static_cast<int4*>(a->workspace);
+    p.part_o = reinterpret_cast<float*>(p.parts + plan.parts);
+    p.part_lse = p.part_o + plan.part_rows * a->head_dim;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     return status_of(launch_tree_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
                                            static_cast<cudaStream_t>(stream)));

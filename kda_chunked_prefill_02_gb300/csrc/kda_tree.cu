@@ -446,33 +446,37 @@ cudaError_t launch_join(const TreeParams& p, int D, cudaStream_t s) {
 TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms) {
     TreePlan t;
     // More rows than the warp-level kernel takes at a time: the 128-row products,
-    // where pages are whole 8-row groups of a tile.
-    t.mma = rows > 32 && D <= 128 && page >= 8 && (page & (page - 1)) == 0 && scale > 0.f;
-    const int block = t.mma ? 256 : rows_per_block(rows, D);
-    const int unit = t.mma ? 128 : kTile;
+    // where pages are whole 8-row groups of a tile (and the line of work, in key
+    // tiles, stays inside 32 bits).
+    t.mma = rows > 32 && D <= 128 && page >= 8 && (page & (page - 1)) == 0 && scale > 0.f &&
+            max_len / 128 + 1 < (1 << 22);
+    // The rows kernel's splits (also for a cache without a tensor map): CTAs of the
+    // longest contexts for four waves of two an SM, at least 256 tokens a split and
+    // at most 1024 pages.
+    const int block = rows_per_block(rows, D);
     const int64_t items = (int64_t)R * Hk * ((rows + block - 1) / block);
-    // CTAs of the longest contexts: four waves of two an SM (rows kernel); one
-    // wave of one an SM for one request, whose splits are all alike, else four.
-    const int64_t target = t.mma ? (R == 1 ? 1LL : 4LL) * num_sms : 8LL * num_sms;
-    int64_t splits = target / items;
-    // at least 256 (1024) tokens a split, and at most 1024 pages
-    const int64_t least = t.mma ? 1024 : 256, most = (max_len + least - 1) / least;
+    const int64_t most = (max_len + 255) / 256;
+    int64_t splits = 8LL * num_sms / items;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
     int64_t chunk = (max_len + splits - 1) / splits;
     if (chunk > 1024LL * page) chunk = 1024LL * page;
-    chunk = (chunk + unit - 1) / unit * unit;
-    if (chunk < unit) chunk = unit;
+    chunk = (chunk + kTile - 1) / kTile * kTile;
+    if (chunk < kTile) chunk = kTile;
     splits = (max_len + chunk - 1) / chunk;
     t.chunk = (int)chunk;
     t.splits = (int)(splits > 0 ? splits : 1);
+    t.grid = num_sms;
+    t.parts = t.mma ? (size_t)2 * t.grid : 0;
+    t.part_rows = t.splits > 1 ? (size_t)R * Hk * rows * t.splits : 0;
+    if (t.mma && t.part_rows < (size_t)2 * t.grid * 256) t.part_rows = (size_t)2 * t.grid * 256;
     return t;
 }
 
 cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
-    if (!plan.mma || !launch_tree_mma(p, D, f16, s, &e))
-        e = f16 ? launch_rows<__half>(p, D, s) : launch_rows<__nv_bfloat16>(p, D, s);
+    if (plan.mma && launch_tree_mma(p, D, f16, plan.grid, s, &e)) return e;
+    e = f16 ? launch_rows<__half>(p, D, s) : launch_rows<__nv_bfloat16>(p, D, s);
     if (e != cudaSuccess || p.splits == 1) return e;
     return f16 ? launch_join<__half>(p, D, s) : launch_join<__nv_bfloat16>(p, D, s);
 }

@@ -2,20 +2,30 @@
 // (a tree of nodes times the query heads of a key head): 128-row tiles on
 // tcgen05 tensor cores, S and O in TMEM, K and V pages by TMA.
 //
-// From about 32 rows on, the products and not the memory bound the warp-level
+// From about 16 rows on, the products and not the memory bound the warp-level
 // kernel of kda_tree.cu; here a tile of 128 rows and 128 keys costs 16
-// tcgen05.mma (S = Q K^T, then O += P V).  One CTA an SM, ten warps:
+// tcgen05.mma (S = Q K^T, then O += P V).  Persistent CTAs, one an SM:
 //   warps 0-3, 4-7  two softmax streams: thread = row (TMEM lane), the whole row
 //                   of S in registers, so maximum and sum need no exchange; P
 //                   goes back over S's columns as 16-bit pairs, the A operand of
 //                   the second product;
 //   warp 8          the loader: a ring of kBufs tiles, K and V in turn;
-//   warp 9          issues the products.
+//   warp 9          issues the products;
+//   warp 10         deals out the work, item by item.
 // The streams alternate, so that one's softmax runs under the other's
 // products.  With more than 128 rows they are two row tiles over the same keys
 // (each K and V tile is read for 256 rows); with fewer they are the even and
-// odd key tiles of one row tile, joined at the end.  Long contexts are cut into
-// splits as in kda_tree.cu, joined by the same kernel.
+// odd key tiles of one row tile, joined at the end.
+//
+// The work of a call is one line of key tiles, ordered by request, key head and
+// pair of row tiles, and every CTA takes an equal stretch of it (a tile for two
+// row tiles counts 5, for one 4, as measured: 1.92 and 1.52 us), so that ragged
+// contexts leave no SM idle.  A stretch cuts at most two items; the parts of a
+// cut item leave normalised rows and their log-sum in the workspace (slot 0 of
+// a CTA: a later part of an item, slot 1: the first), joined in the CTAs' order
+// by tree_mma_join_kernel.  The loader and the issuer run from
+// one item into the next without a halt; only the rows' way out and the next
+// queries' way in are between two items.
 //
 // The running maximum moves only when a row's scores exceed it by 2^8 (l and O
 // stay far inside fp32 and P inside fp16 until then), so that O in TMEM is
@@ -30,6 +40,10 @@
 // zero), and remembers their nodes; the rows that do see such a node take its
 // elements at the end.
 //
+// The third warpgroup gives most of its registers to the softmax warps (56 of
+// 168 kept, 224 taken: 4 x 56 + 8 x 224 = 12 x 168), whose threads hold a row of
+// 128 scores.
+//
 // Every wait is bounded (sm103.cuh); one that runs out sets the abort flag, the
 // roles fall through to the end, copies and products in flight are waited for,
 // and the status word reports KDA_ERR_TIMEOUT.
@@ -41,18 +55,29 @@
 namespace kda {
 namespace {
 
-constexpr int kMmaThreads = 320;
+constexpr int kMmaThreads = 384;   // three warpgroups: two softmax streams, loader and issuer
 constexpr int kKeys = 128;               // keys a tile
-constexpr uint32_t kBlock = 128 * 128;   // bytes of 128 rows of 64 elements
+constexpr uint32_t kBlock = 128 * 128;   // Q: bytes of 128 rows of 64 elements
 constexpr int kMaxBufs = 8;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 256 + 128 s
+// Floats of the rows' way out: a patch a warp, 32 columns of stream 1, its maxima and sums.
+constexpr int kPatch = 32 * 36, kWayOut = 8 * kPatch + 34 * 128;
+constexpr int kMmaSlice = 256;            // requests a launch
+constexpr int kCostTwo = 5, kCostOne = 4;  // cost of a key tile for two row tiles, for one
 constexpr float kLazy = 8.f;             // log2 units by which scores may exceed the running maximum
 
 template <int D> struct MmaShape {
     static constexpr uint32_t kTileBytes = (D / 64) * kBlock;
+    // K and V tiles as the copies leave them: groups of 8 keys, in a group 64 channels
+    // after the other, 8 rows of 128 bytes each.
+    static constexpr uint32_t kGroupBytes = (D / 64) * 1024;
     static constexpr int kBufs = D == 128 ? 5 : 8;
-    static constexpr uint32_t kSmem = (2 + kBufs) * kTileBytes + 1024;   // Q of both streams, the ring, alignment
+    // the queries of both streams, where the rows also pass on their way out
+    static constexpr uint32_t kFront = D == 128 ? 2 * kTileBytes : 56 * 1024;
+    static constexpr uint32_t kSmem = kFront + kBufs * kTileBytes + 1024;   // and the ring, and alignment
 };
+
+static_assert(kWayOut * 4 <= MmaShape<64>::kFront && kWayOut * 4 <= MmaShape<128>::kFront, "the way out fits the front");
 
 template <typename T> struct MmaTypes;
 template <> struct MmaTypes<__nv_bfloat16> {
@@ -64,33 +89,62 @@ template <> struct MmaTypes<__half> {
     static __host__ __device__ constexpr uint32_t pv(uint32_t n) { return idesc_f16_f32_bmn(128, n); }
 };
 
+// One CTA's part of an item (request, key head, pair of row tiles).
+struct Item {
+    int r, h, rb;      // request, key head, row tiles 2 rb and 2 rb + 1
+    int t0, t1;        // key tiles (t1 < 0: no more items)
+    int ctx, n;        // the request's context and nodes
+    bool two, whole;   // two row tiles; all of the item's key tiles
+};
+constexpr int kItems = 4;   // items dealt out ahead
+
+// K-major operand in the 128-byte swizzle with its 8-row groups `group` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_keys(uint32_t saddr, uint32_t group) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(group >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     tree_mma_kernel(const TreeParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     constexpr uint32_t kTileBytes = MmaShape<D>::kTileBytes;
+    constexpr uint32_t kGroupBytes = MmaShape<D>::kGroupBytes;
     constexpr int kBufs = MmaShape<D>::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t kv_full[kMaxBufs], kv_free[kMaxBufs], v_raw, s_full[2], p_ready[2], o_full;
+    __shared__ uint64_t kv_full[kMaxBufs], kv_free[kMaxBufs], v_raw, q_ready, s_full[2], p_ready[2], o_full, o_free;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
-    __shared__ uint32_t s_bad[8];        // drafted nodes with a V element that is not finite
-    __shared__ float s_m[128], s_l[128]; // stream 1's row maxima and sums when the streams are joined
+    // Drafted nodes with a V element that is not finite, for eight items in turn
+    // (the ring holds at most four items' tiles ahead of the rows' way out).
+    __shared__ uint32_t s_bad[8][8];
+    __shared__ int32_t s_start[kMmaSlice + 1];   // where every request begins on the line, in key tiles
+    __shared__ Item s_item[kItems];
+    __shared__ uint64_t item_full[kItems], item_free[kItems];
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int split = blockIdx.x / p.row_blocks, rb = blockIdx.x - split * p.row_blocks;
-    const int kvh = blockIdx.y, r = blockIdx.z, row0 = rb * 256;
-    int ctx, n;
-    if (!tree_lengths(p, r, ctx, n) && p.status && tid == 0) atomicExch(p.status, 1);
-    const int len = ctx + n;
-    const int nsplit = max(1, (len + p.chunk - 1) / p.chunk);
-    if (split >= nsplit) return;
-    const int lo = split * p.chunk, hi = min(lo + p.chunk, len);
-    const int ntiles = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
-    const bool two = p.rows - row0 > 128;             // two row tiles, or one with its key tiles in turn
-    const int units = two ? 2 * ntiles : ntiles;      // unit u: stream u & 1, tile two ? u >> 1 : u
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int* abort = &abort_flag;
-    uint8_t* ring = sm + 2 * kTileBytes;
+    uint8_t* ring = sm + MmaShape<D>::kFront;
     auto fail = [&]() {
         *abort = 1;
         if (p.status) atomicExch(p.status, 4);
@@ -101,336 +155,525 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_free[i], 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_free[i], 3);   // loader, issuer, softmax
+        }
         mbar_init(&v_raw, 1);
+        mbar_init(&q_ready, 256);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_ready[s], 128);
         }
         mbar_init(&o_full, 1);
+        mbar_init(&o_free, 256);
         abort_flag = 0;
         fence_mbar_init();
     }
-    if (tid < 8) s_bad[tid] = 0;
+    if (tid < 64) s_bad[tid >> 3][tid & 7] = 0;
     if (warp == 9) {
         tmem_alloc(&tmem_base_sh, 512);
         tmem_relinquish();
-    }
-    const int stream = warp >> 2;   // of the softmax warps
-    const int row = (two ? row0 + stream * 128 : row0) + (tid & 127);
-    if (warp < 8 && (two || stream == 0)) {
-        // the query rows as K-major operands in the 128-byte swizzle
-        const int i = row / p.G, h = kvh * p.G + (row - i * p.G);
-        const T* src = static_cast<const T*>(p.q) + r * p.qs[0] + i * p.qs[1] + h * p.qs[2];
-        uint8_t* dst = sm + stream * kTileBytes;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = row < p.rows ? ldg16(src + c * 8) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * kBlock + sw128_off(tid & 127, (c & 7) * 8)) = v;
-        }
-        fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = tmem_base_sh;
+    // The k-th item of this CTA; false after the last (or on an abort).
+    auto take = [&](int k, Item& x, bool& ok) -> bool {
+        ok = ok && mbar_wait(&item_full[k % kItems], (k / kItems) & 1, abort);
+        if (!ok) return false;
+        x = s_item[k % kItems];
+        return x.t1 >= 0;
+    };
 
-    if (warp == 8) {
-        // ---------------------------------------------------------------- loader
-        if (lane == 0) {
-            tma_prefetch_desc(&kmap);
-            tma_prefetch_desc(&vmap);
-        }
-        const int box = min(p.page, kKeys), per_tile = kKeys / box;
-        const int bt = lane / (D / 64), bc = lane % (D / 64);   // this lane's box: tokens bt * box.., columns bc * 64..
-        const int shift = 31 - __clz(p.page);
-        auto page_of = [&](int tile) -> int {
-            const int tok = lo + tile * kKeys + bt * box;
-            if (bt >= per_tile || tok >= hi) return -1;
-            int id = p.table[r * p.table_stride + (tok >> shift)];
-            if (id < 0 || id >= p.P) {
-                if (p.status) atomicExch(p.status, 1);
-                id = p.P;   // past the map's pages: the copy fills in zeros
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 8) {
+            // ------------------------------------------------------------ loader
+            if (lane == 0) {
+                tma_prefetch_desc(&kmap);
+                tma_prefetch_desc(&vmap);
             }
-            return id;
-        };
-        int id = ntiles > 0 ? page_of(0) : -1, issued = 0;
-        uint32_t raw_uses = 0;
-        bool ok = true;
-        for (int tile = 0; tile < ntiles && ok; ++tile) {
-            const int next = tile + 1 < ntiles ? page_of(tile + 1) : -1;
-            const int base = lo + tile * kKeys;
-            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128u;
-            for (int v = 0; v < 2 && ok; ++v) {
-                const int i = 2 * tile + v, slot = i % kBufs, round = i / kBufs;
-                if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&kv_free[slot], (round - 1) & 1, abort));
-                if (!ok) break;
-                uint8_t* dst = ring + slot * kTileBytes;
-                const bool special = v == 1 && base + kKeys > ctx;
-                uint64_t* bar = special ? &v_raw : &kv_full[slot];
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                __syncwarp();
-                if (id >= 0)
-                    tma_load_4d(dst + bc * kBlock + bt * box * 128, v ? &vmap : &kmap, bc * 64,
-                                (base + bt * box) & (p.page - 1), kvh, id, bar);
-                issued = i + 1;
-                if (special) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raw_uses & 1, abort));
-                    ++raw_uses;
-                    constexpr uint32_t kExp = Elem<T>::kExpMask;
-                    const int first = max(0, ctx - base);
-                    for (int e = first * (D / 8) + lane; e < kKeys * (D / 8); e += 32) {
-                        const int krow = e / (D / 8), c = e % (D / 8), tok = base + krow;
-                        uint4* at = reinterpret_cast<uint4*>(dst + (c >> 3) * kBlock + krow * 128 + (c & 7) * 16);
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (tok < hi) {
-                            x = *at;
-                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const int box = min(p.page, kKeys), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
+            const int shift = 31 - __clz(p.page);
+            int issued = 0, item = 0;   // tiles asked for, items begun
+            uint32_t raw_uses = 0;
+            bool ok = true;
+            Item x;
+            for (; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
+                if (lane == 0) mbar_arrive(&item_free[item % kItems]);
+                const int ctx = x.ctx, hi = ctx + x.n;
+                const int32_t* table = p.table + x.r * p.table_stride;
+                auto page_of = [&](int tile) -> int {
+                    const int tok = tile * kKeys + lane * box;
+                    if (lane >= per_tile || tok >= hi) return -1;
+                    int id = table[tok >> shift];
+                    if (id < 0 || id >= p.P) {
+                        if (p.status) atomicExch(p.status, 1);
+                        id = p.P;   // past the map's pages: the copy fills in zeros (p.P * p.Hk + h too)
+                    }
+                    return id;
+                };
+                int id = page_of(x.t0);
+                for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
+                    const int next = tile + 1 < x.t1 ? page_of(tile + 1) : -1;
+                    const int base = tile * kKeys;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * D * 2u;
+                    for (int v = 0; v < 2; ++v) {
+                        const int slot = issued % kBufs, round = issued / kBufs;
+                        if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&kv_free[slot], (round - 1) & 1, abort));
+                        if (!ok) break;
+                        uint8_t* dst = ring + slot * kTileBytes;
+                        const bool special = v == 1 && base + kKeys > ctx;
+                        uint64_t* bar = special ? &v_raw : &kv_full[slot];
+                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (id >= 0)
+                            tma_load_5d(dst + lane * box * D * 2, v ? &vmap : &kmap, 0, 0,
+                                        (v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64),
+                                        ((base + lane * box) & (p.page - 1)) / 8,
+                                        (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
+                        ++issued;
+                        if (!special) continue;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raw_uses & 1, abort));
+                        ++raw_uses;
+                        constexpr uint32_t kExp = Elem<T>::kExpMask;
+                        constexpr int kPieces = D / 8;
+                        auto piece = [&](int e) -> uint4* {   // 16-byte piece e of the tile, rows in order
+                            const int c = e % kPieces, krow = e / kPieces;
+                            return reinterpret_cast<uint4*>(dst + (krow >> 3) * kGroupBytes + (c >> 3) * 1024 +
+                                                            (krow & 7) * 128 + (c & 7) * 16);
+                        };
+                        const int drafted = max(0, ctx - base), past = max(0, min(hi - base, kKeys));
+                        for (int e = past * kPieces + lane; e < kKeys * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+                        for (int e = drafted * kPieces + lane; e < past * kPieces; e += 32) {
+                            const uint4 y = *piece(e);
+                            uint32_t w[4] = {y.x, y.y, y.z, y.w};
                             bool bad = false;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 if ((w[k] & kExp) == kExp) { bad = true; w[k] &= 0xffff0000u; }
                                 if (((w[k] >> 16) & kExp) == kExp) { bad = true; w[k] &= 0xffffu; }
                             }
-                            if (!bad) continue;
-                            atomicOr(&s_bad[(tok - ctx) >> 5], 1u << ((tok - ctx) & 31));
-                            x = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (bad) {
+                                const int j = base + e / kPieces - ctx;
+                                atomicOr(&s_bad[item & 7][j >> 5], 1u << (j & 31));
+                                *piece(e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
                         }
-                        *at = x;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&kv_full[slot]);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&kv_full[slot]);
+                    id = next;
                 }
             }
-            id = next;
-        }
-        if (!ok) {
-            if (lane == 0) fail();
-            // copies still on their way into this CTA's memory
-            for (int i = max(0, issued - kBufs); i < issued; ++i) mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1, nullptr);
-        }
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(D);
-            auto tile_of = [&](int u) { return two ? u >> 1 : u; };
-            auto landed = [&](int i) { return mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1, abort); };
-            bool ok = true;
-            auto scores = [&](int u) {
-                const int s = u & 1, i = 2 * tile_of(u);
-                ok = ok && landed(i);
-                if (!ok) return;
-                tc_fence_after();
-                umma_tile(tb + kTmemS + 128 * s, smem_u32(sm + (two ? s : 0) * kTileBytes), kBlock,
-                          smem_u32(ring + (i % kBufs) * kTileBytes), kBlock, D, id_qk, false);
-                umma_commit(&s_full[s]);
-                if (!two || s == 1) umma_commit(&kv_free[i % kBufs]);
-            };
-            if (units > 0) scores(0);
-            if (units > 1) scores(1);
-            for (int u = 0; u < units && ok; ++u) {
-                const int s = u & 1, i = 2 * tile_of(u) + 1;
-                ok = mbar_wait(&p_ready[s], (u >> 1) & 1, abort) && landed(i);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t bd = sdesc_mnmajor_sw128(smem_u32(ring + (i % kBufs) * kTileBytes), kBlock, 1024);
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    umma_bf16_ta(tb + kTmemO + 128 * s, tb + kTmemS + 128 * s + 8 * k, bd + k * (2048 >> 4), id_pv,
-                                 (u > 1 || k > 0) ? 1u : 0u);
-                if (!two || s == 1) umma_commit(&kv_free[i % kBufs]);
-                if (u + 2 < units) scores(u + 2);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) fail();
+                // copies still on their way into this CTA's memory
+                for (int i = max(0, issued - kBufs); i < issued; ++i)
+                    mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1, nullptr);
             }
-            if (!ok) fail();
-            umma_commit(&o_full);
-            if (!ok) mbar_wait(&o_full, 0, nullptr);   // products still in flight
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ products
+            // The whole warp walks the loop and one elected lane issues, with every
+            // operand a warp-uniform value (taken from lane 0 where it comes from
+            // memory): the products' operands live in uniform registers, and a lone
+            // thread that has to bring them there issues a product in about 105 cycles,
+            // whatever its size.
+            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(D);
+            const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
+            const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sm), 0),
+                           ring_at = q_at + MmaShape<D>::kFront;
+            bool ok = true;
+            int item = 0;
+            int base = 0;                      // ring tiles before this item
+            int done0 = 0, done1 = 0;          // P tiles taken, by stream
+            auto landed = [&](int i) { return mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1, abort); };
+            Item x;
+            for (; __all_sync(0xffffffffu, take(item, x, ok)); ++item) {
+                if (lane == 0) mbar_arrive(&item_free[item % kItems]);
+                const bool two = __shfl_sync(0xffffffffu, (int)x.two, 0) != 0;
+                const int tiles = __shfl_sync(0xffffffffu, x.t1 - x.t0, 0);
+                const int units = (two ? 2 : 1) * tiles;   // unit u: stream u & 1, tile two ? u >> 1 : u
+                auto scores = [&](int u) {
+                    const int s = u & 1, i = base + 2 * (two ? u >> 1 : u);
+                    ok = __all_sync(0xffffffffu, ok && landed(i));
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_kmajor_sw128(q_at + (two ? s : 0) * kTileBytes),
+                                   bd = sdesc_keys(ring_at + (i % kBufs) * kTileBytes, kGroupBytes);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            umma_bf16(tbu + kTmemS + 128 * s, ad + (k >> 2) * (kBlock >> 4) + (k & 3) * 2,
+                                      bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, k > 0 ? 1u : 0u);
+                        umma_commit(&s_full[s]);
+                        if (!two || s == 1) umma_commit(&kv_free[i % kBufs]);
+                    }
+                    __syncwarp();
+                };
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(&q_ready, item & 1, abort));
+                scores(0);
+                if (units > 1) scores(1);
+                for (int u = 0; u < units && ok; ++u) {
+                    const int s = u & 1, i = base + 2 * (two ? u >> 1 : u) + 1;
+                    // O still holds the item before until its rows are out
+                    if (u == 0 && item > 0) ok = mbar_wait(&o_free, (item - 1) & 1, abort);
+                    ok = ok && mbar_wait(&p_ready[s], (s ? done1 : done0) & 1, abort) && landed(i);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (s) ++done1; else ++done0;
+                    tc_fence_after();
+                    const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % kBufs) * kTileBytes, 1024, kGroupBytes);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            umma_bf16_ta(tbu + kTmemO + 128 * s, tbu + kTmemS + 128 * s + 8 * k, bd + k * (kGroupBytes >> 3),
+                                         id_pv, (u > 1 || k > 0) ? 1u : 0u);
+                        if (!two || s == 1) umma_commit(&kv_free[i % kBufs]);
+                    }
+                    __syncwarp();
+                    if (u + 2 < units) scores(u + 2);
+                }
+                if (elect_one()) umma_commit(&o_full);
+                __syncwarp();
+                if (!ok) mbar_wait(&o_full, item & 1, nullptr);   // products still in flight
+                base += 2 * tiles;
+            }
+            if (!ok && lane == 0) fail();
+            __syncwarp();
+        } else if (warp == 10) {
+            // ------------------------------------------------------------ work
+            // where every request begins on the line: at least one tile each, so that
+            // rows that see nothing are written too
+            int64_t at = 0;
+            for (int r0 = 0; r0 < p.count; r0 += 32) {
+                const int r = r0 + lane;
+                int ctx, n, t = 0;
+                if (r < p.count) {
+                    if (!tree_lengths(p, p.r0 + r, ctx, n) && p.status) atomicExch(p.status, 1);
+                    t = max(1, (ctx + n + kKeys - 1) / kKeys);
+                }
+                int sum = t;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                if (r < p.count) s_start[r] = (int)at + sum - t;
+                at += __shfl_sync(0xffffffffu, sum, 31);
+            }
+            if (lane == 0) s_start[p.count] = (int)at;
+            __syncwarp();
+            if (lane == 0) {
+                const int pairs = (p.rows + 255) / 256;
+                const bool odd = (p.rows - 1) % 256 < 128;   // the last pair has one row tile
+                const int head_cost = pairs * kCostTwo - (odd ? kCostTwo - kCostOne : 0);   // of a key tile
+                const int64_t tile_cost = (int64_t)head_cost * p.Hk, total = at * tile_cost;
+                // at least two key tiles a CTA
+                const int64_t most = total / (2 * kCostTwo);
+                const int ctas = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
+                int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+                int k = 0;
+                bool ok = true;
+                auto deal = [&](const Item& x) {
+                    if (k >= kItems) ok = mbar_wait(&item_free[k % kItems], (k / kItems - 1) & 1, abort);
+                    if (!ok) return;
+                    s_item[k % kItems] = x;
+                    mbar_arrive(&item_full[k % kItems]);
+                    ++k;
+                };
+                Item x{};
+                if ((int)blockIdx.x < ctas) {
+                    const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+                    // the item that holds the stretch's begin
+                    int lo = 0, hi = p.count;
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (s_start[mid] * tile_cost <= begin) lo = mid; else hi = mid;
+                    }
+                    int r = lo, tiles = s_start[r + 1] - s_start[r];
+                    int64_t item = s_start[r] * tile_cost, off = begin - item;
+                    const int64_t per_head = (int64_t)tiles * head_cost, per_pair = (int64_t)tiles * kCostTwo;
+                    x.h = (int)(off / per_head);
+                    off -= x.h * per_head;
+                    x.rb = min((int)(off / per_pair), pairs - 1);
+                    off -= x.rb * per_pair;
+                    item = begin - off;
+                    tree_lengths(p, p.r0 + r, x.ctx, x.n);
+                    while (item < end && ok) {
+                        x.two = !(odd && x.rb == pairs - 1);
+                        const int cost = x.two ? kCostTwo : kCostOne;
+                        const int64_t next = item + (int64_t)tiles * cost;
+                        x.r = p.r0 + r;
+                        x.t0 = item < begin ? (int)((begin - item + cost - 1) / cost) : 0;
+                        x.t1 = next <= end ? tiles : (int)((end - item + cost - 1) / cost);
+                        x.whole = x.t0 == 0 && x.t1 == tiles;
+                        if (x.t1 > x.t0) {
+                            if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, x.rb);
+                            deal(x);
+                        }
+                        item = next;
+                        if (++x.rb == pairs) {
+                            x.rb = 0;
+                            if (++x.h == p.Hk) {
+                                x.h = 0;
+                                if (++r == p.count) break;
+                                tiles = s_start[r + 1] - s_start[r];
+                                tree_lengths(p, p.r0 + r, x.ctx, x.n);
+                            }
+                        }
+                    }
+                }
+                x.t1 = -1;
+                deal(x);
+                // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
+                p.parts[2 * blockIdx.x] = slots[0];
+                p.parts[2 * blockIdx.x + 1] = slots[1];
+                if (!ok) fail();
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int stream = warp >> 2, row_in = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tb + lane_base + kTmemS + 128 * stream, to = tb + lane_base + kTmemO + 128 * stream;
-        const int node = min(row / p.G, p.N - 1);
-        const bool live = row - (tid & 31) < p.rows;   // some row of the warp is a row of the call
         const float c = p.scale_log2, lazy = kLazy / c;
-        float m = -INFINITY, l = 0.f;
         bool ok = true;
+        int item = 0, seen_s = 0;   // items begun, score tiles taken
+        for (;; ++item) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&item_full[item % kItems], (item / kItems) & 1, abort));
+            if (!ok && lane == 0) fail();
+            const Item& x = s_item[item % kItems];
+            if (named_bar_or(1, 256, !ok || x.t1 < 0)) break;   // all stop if one has given up
+            const bool two = x.two;
+            const int row0 = x.rb * 256, r = x.r, kvh = x.h;
+            {
+                // the query rows as K-major operands in the 128-byte swizzle, D / 8 lanes a
+                // row; all of them are on their way at once
+                constexpr int kPieces = D / 8, kRowsPass = 256 / kPieces, kPasses = 256 / kRowsPass;
+                const int piece = tid % kPieces;
+                const T* src = static_cast<const T*>(p.q) + r * p.qs[0] + kvh * p.G * p.qs[2] + piece * 8;
+#pragma unroll 2
+                for (int k = 0; k < (two ? kPasses : kPasses / 2); ++k) {
+                    const int in = k * kRowsPass + tid / kPieces, q = row0 + in;   // row of the pair of tiles, of the call
+                    const int i = (int)page_div((uint32_t)q, p.G, p.group_magic);
+                    uint8_t* dst = sm + (in >> 7) * kTileBytes + (piece >> 3) * kBlock + sw128_off(in & 127, (piece & 7) * 8);
+                    if (q < p.rows) cp_async16(dst, src + i * p.qs[1] + (q - i * p.G) * p.qs[2]);
+                    else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+                }
+                cp_async_commit();
+            }
+            const int ctx = x.ctx, hi = ctx + x.n;
+            const int row = row0 + (two ? stream * 128 : 0) + row_in;
+            const int node = min((int)page_div((uint32_t)row, p.G, p.group_magic), p.N - 1);
+            const bool live = row - lane < p.rows;   // some row of the warp is a row of the call
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            mbar_arrive(&q_ready);
 
-        // 32 drafted nodes' visibility to this row, from node 32 w on
-        const uint32_t* mask = p.mask ? reinterpret_cast<const uint32_t*>(p.mask + ((int64_t)r * p.N + node) * p.words)
-                                      : nullptr;
-        auto node_bits = [&](int w) -> uint32_t {
-            if (w >= 2 * p.words) return 0u;
-            if (mask) return mask[w];
-            const int d = node - 32 * w;
-            return d >= 31 ? 0xffffffffu : d < 0 ? 0u : (2u << d) - 1u;
-        };
-        // visibility of positions tok .. tok + 31
-        auto seen = [&](int tok) -> uint32_t {
-            const int rel = tok - ctx, left = hi - tok;
-            uint32_t b = 0xffffffffu;
-            if (rel >= 0) b = __funnelshift_r(node_bits(rel >> 5), node_bits((rel >> 5) + 1), rel & 31);
-            else if (rel > -32) b = (node_bits(0) << -rel) | ((1u << -rel) - 1u);
-            return left >= 32 ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
-        };
+            // 32 drafted nodes' visibility to this row, from node 32 w on
+            const uint32_t* mask =
+                p.mask ? reinterpret_cast<const uint32_t*>(p.mask + ((int64_t)r * p.N + node) * p.words) : nullptr;
+            auto node_bits = [&](int w) -> uint32_t {
+                if (w >= 2 * p.words) return 0u;
+                if (mask) return mask[w];
+                const int d = node - 32 * w;
+                return d >= 31 ? 0xffffffffu : d < 0 ? 0u : (2u << d) - 1u;
+            };
+            // visibility of positions tok .. tok + 31
+            auto seen = [&](int tok) -> uint32_t {
+                const int rel = tok - ctx, left = hi - tok;
+                uint32_t b = 0xffffffffu;
+                if (rel >= 0) b = __funnelshift_r(node_bits(rel >> 5), node_bits((rel >> 5) + 1), rel & 31);
+                else if (rel > -32) b = (node_bits(0) << -rel) | ((1u << -rel) - 1u);
+                return left >= 32 ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
+            };
 
-        for (int u = stream; u < units; u += 2) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[stream], (u >> 1) & 1, abort));
-            if (!ok) break;
-            tc_fence_after();
-            if (live) {
-                uint32_t raw[8][16];
-                float x[128];
+            float m = -INFINITY, l = 0.f;
+            const int units = (two ? 2 : 1) * (x.t1 - x.t0);
+            for (int u = stream; u < units; u += 2) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[stream], seen_s & 1, abort));
+                if (!ok) break;
+                ++seen_s;
+                tc_fence_after();
+                if (live) {
+                    uint32_t raw[8][16];
+                    float v[128];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) tmem_ld16_issue(ts + 16 * k, raw[k]);
-                tmem_wait_ld();
+                    for (int k = 0; k < 8; ++k) tmem_ld16_issue(ts + 16 * k, raw[k]);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) tmem_take16(raw[k], &x[16 * k]);
-                const int base = lo + (two ? u >> 1 : u) * kKeys;
-                if (base + kKeys > ctx) {
+                    for (int k = 0; k < 8; ++k) tmem_take16(raw[k], &v[16 * k]);
+                    const int base = (x.t0 + (two ? u >> 1 : u)) * kKeys;
+                    if (base + kKeys > ctx) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t b = seen(base + 32 * k);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((b >> e) & 1u)) v[32 * k + e] = -INFINITY;
+                        }
+                    }
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    float alpha = 1.f;
+                    if (top > m + lazy || m == -INFINITY) {
+                        if (m != -INFINITY) alpha = ex2_approx((m - top) * c);
+                        m = fmaxf(m, top);
+                        l *= alpha;
+                    }
+                    if (u > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                        for (int k = 0; k < D / 32; ++k) {
+                            float o[32];
+                            uint32_t w[32];
+                            tmem_ld32(to + 32 * k, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                            tmem_st32(to + 32 * k, w);
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : -m * c;
+                    const F2 c2 = f2(c, c), m2 = f2(mc, mc);
+                    F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t b = seen(base + 32 * k);
+                        uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((b >> e) & 1u)) x[32 * k + e] = -INFINITY;
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = f2_parts(f2_fma(f2(v[32 * k + 2 * e], v[32 * k + 2 * e + 1]), c2, m2));
+                            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                            sum[e & 1] = f2_add(sum[e & 1], f2(p0, p1));
+                            w[e] = Elem<T>::pack(p0, p1);
+                        }
+                        tmem_st16_issue(ts + 16 * k, w);
                     }
+                    const float2 q = f2_parts(f2_add(sum[0], sum[1]));
+                    l += q.x + q.y;
+                    tmem_wait_st();
                 }
-                float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (top > m + lazy || m == -INFINITY) {
-                    const float alpha = m == -INFINITY ? 1.f : ex2_approx((m - top) * c);
-                    m = fmaxf(m, top);
-                    l *= alpha;
-                    mx[0] = alpha;
-                } else {
-                    mx[0] = 1.f;
-                }
-                if (u > 1 && __any_sync(0xffffffffu, mx[0] != 1.f)) {
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        uint32_t w[32];
-                        tmem_ld32(to + 32 * k, o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * mx[0]);
-                        tmem_st32(to + 32 * k, w);
-                    }
-                }
-                const float mc = m == -INFINITY ? 0.f : -m * c;
-                const F2 c2 = f2(c, c), m2 = f2(mc, mc);
-                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y = f2_parts(f2_fma(f2(x[32 * k + 2 * e], x[32 * k + 2 * e + 1]), c2, m2));
-                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-                        sum[e & 1] = f2_add(sum[e & 1], f2(p0, p1));
-                        w[e] = Elem<T>::pack(p0, p1);
-                    }
-                    tmem_st16_issue(ts + 16 * k, w);
-                }
-                const float2 q = f2_parts(f2_add(sum[0], sum[1]));
-                l += q.x + q.y;
-                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_ready[stream]);
             }
-            tc_fence_before();
-            mbar_arrive(&p_ready[stream]);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full, 0, abort)) && ok;
-        if (!ok && lane == 0) fail();
-        tc_fence_after();
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full, item & 1, abort)) && ok;
+            if (!ok && lane == 0) fail();
+            tc_fence_after();
 
-        // the joined rows of an even / odd pair of streams leave through stream 0
-        float* so = reinterpret_cast<float*>(ring);   // [D][128]: every tile has been consumed
-        float f0 = 1.f, f1 = 0.f;
-        if (!two) {
-            if (stream == 1) {
-                s_m[tid & 127] = m;
-                s_l[tid & 127] = l;
-                if (units > 1 && ok && live) {
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        tmem_ld32(to + 32 * k, o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) so[(32 * k + e) * 128 + (tid & 127)] = o[e];
-                    }
+            // The rows' way out.  The products are done, so the queries' memory is free:
+            // a patch a warp (32 rows at a pitch of 36 floats) through which the stores
+            // to memory become whole sectors, and behind the patches 32 columns of
+            // stream 1's rows on their way to stream 0 when the two are joined.
+            float* const patch = reinterpret_cast<float*>(sm) + warp * kPatch;
+            float* const other = reinterpret_cast<float*>(sm) + 8 * kPatch;   // [32][128], then m and l
+            float f0 = 1.f, f1 = 0.f;
+            const bool joined = !two && units > 1;
+            if (joined) {
+                if (stream == 1) {
+                    other[32 * 128 + row_in] = m;
+                    other[33 * 128 + row_in] = l;
+                }
+                named_bar_sync(1, 256);
+                if (stream == 0) {
+                    const float m1 = other[32 * 128 + row_in], mj = fmaxf(m, m1), mu = mj == -INFINITY ? 0.f : mj;
+                    f0 = ex2_approx((m - mu) * c);
+                    f1 = ex2_approx((m1 - mu) * c);
+                    l = l * f0 + other[33 * 128 + row_in] * f1;
+                    m = mj;
                 }
             }
-            named_bar_sync(1, 256);
-            if (stream == 0 && units > 1) {
-                const float m1 = s_m[tid], mj = fmaxf(m, m1), mu = mj == -INFINITY ? 0.f : mj;
-                f0 = ex2_approx((m - mu) * c);
-                f1 = ex2_approx((m1 - mu) * c);
-                l = l * f0 + s_l[tid] * f1;
-                m = mj;
-            }
-        }
-        if (ok && live && units > 0 && (two || stream == 0)) {
-            const int i = row / p.G, h = kvh * p.G + (row - i * p.G);
-            const bool mine = row < p.rows;
-            const bool empty = i >= n || l == 0.f;
+            const bool empty = node >= x.n || l == 0.f, whole = x.whole;
             const float inv = empty ? 0.f : 1.f / l;
-            const int64_t at = (((int64_t)r * p.Hk + kvh) * p.splits + split) * p.rows + row;
-            T* dst = static_cast<T*>(p.out) + r * p.os[0] + i * p.os[1] + h * p.os[2];
+            f0 *= inv;
+            f1 *= inv;
+            const int64_t part = ((int64_t)(2 * blockIdx.x + (x.t0 > 0 ? 0 : 1)) * 256 + (row - row0));
+            const bool out = ok && live && (two || stream == 0);
             uint32_t any_bad = 0;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) any_bad |= s_bad[w];
-            const bool joined = !two && units > 1;
-#pragma unroll
+            for (int w = 0; w < 8; ++w) any_bad |= s_bad[item & 7][w];
+            // rolled: the code runs once an item, and fetching it costs more than running it
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
                 float o[32];
-                tmem_ld32(to + 32 * k, o);
+                if (live && ok && (out || joined)) tmem_ld32(to + 32 * k, o);
+                if (joined) {
+                    if (stream == 1) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float y = o[e] * f0;
-                    if (joined) y = fmaf(so[(32 * k + e) * 128 + (tid & 127)], f1, y);
-                    o[e] = empty ? 0.f : y * inv;
+                        for (int e = 0; e < 32; ++e) other[e * 128 + row_in] = o[e];
+                    }
+                    named_bar_sync(1, 256);
                 }
-                if (any_bad && !empty) {
-                    for (int j = max(0, lo - ctx); j < hi - ctx; ++j) {
-                        if (!((s_bad[j >> 5] >> (j & 31)) & 1u) || !(seen(ctx + j) & 1u)) continue;
-                        const int tok = ctx + j, id = p.table[r * p.table_stride + tok / p.page];
-                        if (id < 0 || id >= p.P) continue;
-                        const T* v = static_cast<const T*>(p.vc) + id * p.vs[0] + (tok % p.page) * p.vs[1] +
-                                     kvh * p.vs[2] + 32 * k;
+                if (out) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float x = Elem<T>::one(v[e]);
-                            if (!isfinite(x)) o[e] += x;
+                    for (int e = 0; e < 32; ++e) o[e] = empty ? 0.f : o[e] * f0;
+                    if (joined && !empty) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(other[e * 128 + row_in], f1, o[e]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(patch + lane * 36 + 4 * e) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    if (any_bad && !empty) {
+                        for (int j = max(0, x.t0 * kKeys - ctx); j < min(hi, x.t1 * kKeys) - ctx; ++j) {
+                            if (!((s_bad[item & 7][j >> 5] >> (j & 31)) & 1u) || !(seen(ctx + j) & 1u)) continue;
+                            const int tok = ctx + j, id = p.table[r * p.table_stride + tok / p.page];
+                            if (id < 0 || id >= p.P) continue;
+                            const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (tok % p.page) * p.vs[1] +
+                                           kvh * p.vs[2] + 32 * k;
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = Elem<T>::one(src[e]);
+                                if (!isfinite(y)) patch[lane * 36 + e] += y;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (whole) {
+#pragma unroll 1
+                        for (int g = 0; g < 4; ++g) {
+                            const int pr = 8 * g + (lane >> 2), q = row - lane + pr, col = (lane & 3) * 8;
+                            const float4 y0 = *reinterpret_cast<const float4*>(patch + pr * 36 + col),
+                                         y1 = *reinterpret_cast<const float4*>(patch + pr * 36 + col + 4);
+                            const int qi = (int)page_div((uint32_t)q, p.G, p.group_magic), qh = kvh * p.G + (q - qi * p.G);
+                            if (q < p.rows)
+                                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + r * p.os[0] + qi * p.os[1] +
+                                                          qh * p.os[2] + 32 * k + col) =
+                                    make_uint4(Elem<T>::pack(y0.x, y0.y), Elem<T>::pack(y0.z, y0.w),
+                                               Elem<T>::pack(y1.x, y1.y), Elem<T>::pack(y1.z, y1.w));
+                        }
+                    } else {
+#pragma unroll 2
+                        for (int g = 0; g < 8; ++g) {
+                            const int pr = 4 * g + (lane >> 3), col = (lane & 7) * 4;
+                            if (row - lane + pr < p.rows)
+                                *reinterpret_cast<float4*>(p.part_o + (part - lane + pr) * D + 32 * k + col) =
+                                    *reinterpret_cast<const float4*>(patch + pr * 36 + col);
                         }
                     }
                 }
-                if (!mine) continue;
-                if (nsplit == 1) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(dst + 32 * k + e) =
-                            make_uint4(Elem<T>::pack(o[e], o[e + 1]), Elem<T>::pack(o[e + 2], o[e + 3]),
-                                       Elem<T>::pack(o[e + 4], o[e + 5]), Elem<T>::pack(o[e + 6], o[e + 7]));
-                } else {
-                    float4* po = reinterpret_cast<float4*>(p.part_o + at * D + 32 * k);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) po[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                }
+                if (joined) named_bar_sync(1, 256);   // stream 1's columns are taken
             }
-            const float lse = empty ? -INFINITY : m * c + log2f(l);
-            if (mine && nsplit > 1) p.part_lse[at] = lse;
-            else if (mine && p.lse) p.lse[((int64_t)r * p.N + i) * p.Hq + h] = lse * 0.6931471805599453f;
-        } else if (ok && units == 0 && row < p.rows && (two || stream == 0)) {
-            // nothing to see at all
-            const int i = row / p.G, h = kvh * p.G + (row - i * p.G);
-            T* dst = static_cast<T*>(p.out) + r * p.os[0] + i * p.os[1] + h * p.os[2];
-#pragma unroll
-            for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(dst + e) = make_uint4(0, 0, 0, 0);
-            if (p.lse) p.lse[((int64_t)r * p.N + i) * p.Hq + h] = -INFINITY;
+            if (out && row < p.rows) {
+                const float lse = empty ? -INFINITY : m * c + log2f(l);
+                if (!whole) p.part_lse[part] = lse;
+                else if (p.lse)
+                    p.lse[((int64_t)r * p.N + node) * p.Hq + kvh * p.G + (row - node * p.G)] = lse * 0.6931471805599453f;
+            }
+            tc_fence_before();
+            named_bar_sync(1, 256);   // every warp's patch and s_bad have been read
+            if (tid < 8) s_bad[item & 7][tid] = 0;
+            if (tid == 0) mbar_arrive(&item_free[item % kItems]);
+            mbar_arrive(&o_free);
         }
-        tc_fence_before();
     }
     __syncthreads();
     if (warp == 9) {
@@ -439,36 +682,100 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
 }
 
+// Joins the parts of a cut item: out = sum_c 2^(lse_c - M) o_c / sum_c 2^(lse_c - M)
+// over the CTAs c that hold one, in their order: slot 1 of CTA blockIdx.x, then
+// slot 0 of those behind it up to the item's last part.  One warp a row.
 template <typename T, int D>
-cudaError_t launch_mma_t(const TreeParams& q, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-    TreeParams p = q;
-    p.row_blocks = (p.rows + 255) / 256;
-    static std::atomic<uint64_t> smem_set;
-    cudaError_t e = set_smem_limit_once((const void*)tree_mma_kernel<T, D>, (int)MmaShape<D>::kSmem, smem_set);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.splits * p.row_blocks), (unsigned)p.Hk, (unsigned)p.R);
-    tree_mma_kernel<T, D><<<grid, kMmaThreads, MmaShape<D>::kSmem, s>>>(p, kmap, vmap);
-    return cudaGetLastError();
+__global__ void __launch_bounds__(256) tree_mma_join_kernel(const TreeParams p) {
+    constexpr int kVec = D / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, in = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int4 item = p.parts[2 * blockIdx.x + 1];   // state, request, key head, pair of row tiles
+    const int row = item.w * 256 + in;
+    if (item.x == 0 || row >= p.rows) return;
+    float mx = -INFINITY, sum = 0.f, y[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) y[i] = 0.f;
+    int slot = 2 * blockIdx.x + 1;
+    for (int state = item.x;;) {
+        const int64_t part = (int64_t)slot * 256 + in;
+        const float lse = p.part_lse[part];
+        const float* src = p.part_o + part * D + lane * kVec;
+        float o[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) o[i] = src[i];
+        const float mn = fmaxf(mx, lse), mu = mn == -INFINITY ? 0.f : mn;
+        const float fo = ex2_approx(mx - mu), fn = ex2_approx(lse - mu);
+        sum = sum * fo + fn;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) y[i] = y[i] * fo + o[i] * fn;
+        mx = mn;
+        if (state == 2) break;
+        slot = (slot + 2) & ~1;
+        if (slot >= p.slots) break;
+        state = p.parts[slot].x;
+        if (state == 0) break;
+    }
+    const int r = item.y, i = (int)page_div((uint32_t)row, p.G, p.group_magic), h = item.z * p.G + (row - i * p.G);
+    const bool empty = sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + r * p.os[0] + i * p.os[1] + h * p.os[2] +
+                                                lane * kVec);
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
+    if (p.lse && lane == 0)
+        p.lse[((int64_t)r * p.N + i) * p.Hq + h] = empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Tensor map of a cache as [channel, row of a page, head, page]; a box is the
-// rows of a page that a tile takes, 64 channels wide.
-bool cache_map(CUtensorMap* map, const void* base, const int64_t (&st)[3], const TreeParams& p, int D, bool f16) {
-    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.page, (uint64_t)p.Hk, (uint64_t)p.P};
-    const uint64_t strides[3] = {(uint64_t)st[1] * 2, (uint64_t)st[2] * 2, (uint64_t)st[0] * 2};
-    const uint32_t box[4] = {64, (uint32_t)(p.page < kKeys ? p.page : kKeys), 1, 1};
-    return make_tensor_map(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+template <typename T, int D>
+cudaError_t launch_mma_t(const TreeParams& q, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+    static std::atomic<uint64_t> smem_set;
+    cudaError_t e = set_smem_limit_once((const void*)tree_mma_kernel<T, D>, (int)MmaShape<D>::kSmem, smem_set);
+    const int rows = q.rows < 256 ? q.rows : 256;
+    for (int r0 = 0; r0 < q.R && e == cudaSuccess; r0 += kMmaSlice) {
+        TreeParams p = q;
+        p.r0 = r0;
+        p.slots = 2 * grid;
+        p.count = q.R - r0 < kMmaSlice ? q.R - r0 : kMmaSlice;
+        tree_mma_kernel<T, D><<<grid, kMmaThreads, MmaShape<D>::kSmem, s>>>(p, kmap, vmap);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && grid > 1)
+            e = launch_maybe_pdl(tree_mma_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)((rows + 7) / 8)),
+                                 dim3(256), 0, s, true, p);
+    }
+    return e;
+}
+
+// Tensor map of a cache as [64 channels, 8 rows, blocks of 64 channels, groups of 8
+// rows, pages], a box the rows of a page that a tile takes with all their channels
+// of one head: one copy a page (a copy costs about 120 cycles, whatever its size,
+// which with pages of 16 is what bounds copies of 64 channels).  The head is part
+// of the block dimension where a row's heads follow one another, of the page
+// dimension (*paged) where a page's heads do.  False for any other layout.
+bool cache_map(CUtensorMap* map, const void* base, const int64_t (&st)[3], const TreeParams& p, int D, bool f16,
+               int* paged) {
+    const bool rows = p.Hk == 1 || st[2] == D;
+    if (!rows && st[0] != st[2] * p.Hk) return false;
+    *paged = !rows;
+    const uint64_t dims[5] = {64, 8, (uint64_t)(rows ? p.Hk : 1) * (D / 64), (uint64_t)p.page / 8,
+                              (uint64_t)p.P * (rows ? 1 : p.Hk)};
+    const uint64_t strides[4] = {(uint64_t)st[1] * 2, 128, (uint64_t)st[1] * 16, (uint64_t)(rows ? st[0] : st[2]) * 2};
+    const uint32_t box[5] = {64, 8, (uint32_t)D / 64, (uint32_t)(p.page < kKeys ? p.page : kKeys) / 8, 1};
+    if (dims[4] > INT32_MAX) return false;
+    return make_tensor_map(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims,
                            strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
 
-bool launch_tree_mma(const TreeParams& p, int D, bool f16, cudaStream_t s, cudaError_t* e) {
+bool launch_tree_mma(const TreeParams& q, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e) {
     CUtensorMap kmap, vmap;
-    if (!cache_map(&kmap, p.kc, p.ks, p, D, f16) || !cache_map(&vmap, p.vc, p.vs, p, D, f16)) return false;
-    if (f16) *e = D == 64 ? launch_mma_t<__half, 64>(p, kmap, vmap, s) : launch_mma_t<__half, 128>(p, kmap, vmap, s);
-    else *e = D == 64 ? launch_mma_t<__nv_bfloat16, 64>(p, kmap, vmap, s)
-                      : launch_mma_t<__nv_bfloat16, 128>(p, kmap, vmap, s);
+    TreeParams p = q;
+    if (!cache_map(&kmap, p.kc, p.ks, p, D, f16, &p.k_paged) || !cache_map(&vmap, p.vc, p.vs, p, D, f16, &p.v_paged))
+        return false;
+    if (f16) *e = D == 64 ? launch_mma_t<__half, 64>(p, kmap, vmap, grid, s) : launch_mma_t<__half, 128>(p, kmap, vmap, grid, s);
+    else *e = D == 64 ? launch_mma_t<__nv_bfloat16, 64>(p, kmap, vmap, grid, s)
+                      : launch_mma_t<__nv_bfloat16, 128>(p, kmap, vmap, grid, s);
     return true;
 }
 

@@ -59,29 +59,34 @@ struct TreeParams {
     const int32_t* nodes;
     const uint64_t* mask;
     int32_t* status;
-    float* part_o;            // [R, Hk, splits, rows, D]
-    float* part_lse;          // [R, Hk, splits, rows], base 2
+    float* part_o;            // partial rows: [R, Hk, splits, rows, D], or [2 CTAs, 256, D] (mma)
+    float* part_lse;          // their log-sums, base 2
+    int4* parts;              // mma: what the partial rows belong to, [2 CTAs]
     int64_t qs[3], os[3], ks[3], vs[3], table_stride;
     int R, N, Hq, Hk, G, rows, words;   // rows = N * G, words of a mask row
     int P, page;
     int64_t max_len;          // longest context and nodes of a request (at most what its page row holds)
-    uint32_t page_magic;      // floor(2^32 / page) (2^32 - 1 for page 1)
+    uint32_t page_magic, group_magic;   // floor(2^32 / page), floor(2^32 / G) (2^32 - 1 for 1)
     int chunk, splits;        // tokens a split; splits of the longest request
     int row_blocks;           // set by the launcher
+    int k_paged, v_paged;     // mma: the head is part of the map's page coordinate
+    int r0, count, slots;     // mma: the requests of a launch, 2 x its CTAs (set by the launcher)
     float scale_log2;         // scale * log2(e)
 };
-// How a call is cut: tokens a split, splits of the longest request, and which
-// kernel takes the rows.
+// How a call is cut.
 struct TreePlan {
-    int chunk, splits;
-    bool mma;
+    bool mma;            // the kernel for many rows
+    int chunk, splits;   // rows kernel: tokens a split, splits of the longest request
+    int grid;            // mma: CTAs
+    size_t part_rows;    // partial rows in the workspace (D values and a log-sum each)
+    size_t parts;        // int4 behind them, for what they belong to
 };
 TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms);
 cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s);
 // The kernel for many rows; false if the caches' layout has no tensor map.
-bool launch_tree_mma(const TreeParams& p, int D, bool f16, cudaStream_t s, cudaError_t* e);
+bool launch_tree_mma(const TreeParams& p, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e);
 
-// n / page for n < 2^32: the magic product is short by at most one.
+// n / page for n < 2^32 and magic = floor(2^32 / page): the product is short by at most one.
 __device__ __forceinline__ uint32_t page_div(uint32_t n, uint32_t page, uint32_t magic) {
     uint32_t q = __umulhi(n, magic);
     if (n - q * page >= page) ++q;
