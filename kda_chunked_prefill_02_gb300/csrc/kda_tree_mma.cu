@@ -11,7 +11,8 @@
 //                   the second product;
 //   warp 8          the loader: a ring of kBufs tiles, K and V in turn;
 //   warp 9          issues the products;
-//   warp 10         deals out the work, item by item.
+//   warp 10         deals out the work, item by item;
+//   warp 11         cleans the V tiles that need it.
 // The streams alternate, so that one's softmax runs under the other's
 // products.  With more than 128 rows they are two row tiles over the same keys
 // (each K and V tile is read for 256 rows); with fewer they are the even and
@@ -35,7 +36,7 @@
 //
 // Keys that a row does not see: only the last tiles hold drafted tokens or
 // positions past the end; there every row forms its 128 visibility bits.  In
-// those tiles the loader clears V rows past the end and V elements that are not
+// those tiles a warp of its own clears V rows past the end and V elements that are not
 // finite before the product sees them (0 * NaN is NaN, also for a row whose P is
 // zero), and remembers their nodes; the rows that do see such a node take its
 // elements at the end.
@@ -65,6 +66,21 @@ constexpr int kPatch = 32 * 36, kWayOut = 8 * kPatch + 34 * 128;
 constexpr int kMmaSlice = 256;            // requests a launch
 constexpr int kCostTwo = 5, kCostOne = 4;  // cost of a key tile for two row tiles, for one
 constexpr float kLazy = 8.f;             // log2 units by which scores may exceed the running maximum
+
+// mbar_wait (sm103.cuh) with the clock and the abort flag looked at every 64th time
+// only: between a phase's end and this thread's next step there is then nothing but
+// the try_wait itself, where a look at the global timer takes longer than the wait.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (i % 64) continue;
+        if (abort && *abort) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > kWaitLimitNs) return false;
+    }
+}
 
 template <int D> struct MmaShape {
     static constexpr uint32_t kTileBytes = (D / 64) * kBlock;
@@ -132,7 +148,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     constexpr int kBufs = MmaShape<D>::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t kv_full[kMaxBufs], kv_free[kMaxBufs], v_raw, q_ready, s_full[2], p_ready[2], o_full, o_free;
+    __shared__ uint64_t kv_full[kMaxBufs], kv_free[kMaxBufs], kv_raw[kMaxBufs], q_ready, s_full[2], p_half[2], p_ready[2], o_full, o_free;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     // Drafted nodes with a V element that is not finite, for eight items in turn
@@ -154,19 +170,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_free[i], 1);
+            mbar_init(&kv_raw[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_free[i], 3);   // loader, issuer, softmax
+            mbar_init(&item_free[i], 4);   // loader, issuer, cleaner, softmax
         }
-        mbar_init(&v_raw, 1);
-        mbar_init(&q_ready, 256);
+        mbar_init(&q_ready, 8);   // one arrival a warp
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_ready[s], 128);
+            mbar_init(&p_half[s], 4);
+            mbar_init(&p_ready[s], 4);
         }
         mbar_init(&o_full, 1);
-        mbar_init(&o_free, 256);
+        mbar_init(&o_free, 8);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -181,7 +198,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const uint32_t tb = tmem_base_sh;
     // The k-th item of this CTA; false after the last (or on an abort).
     auto take = [&](int k, Item& x, bool& ok) -> bool {
-        ok = ok && mbar_wait(&item_full[k % kItems], (k / kItems) & 1, abort);
+        ok = ok && wait_for(&item_full[k % kItems], (k / kItems) & 1, abort);
         if (!ok) return false;
         x = s_item[k % kItems];
         return x.t1 >= 0;
@@ -198,35 +215,34 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int box = min(p.page, kKeys), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
             const int shift = 31 - __clz(p.page);
             int issued = 0, item = 0;   // tiles asked for, items begun
-            uint32_t raw_uses = 0;
+            uint32_t raw = 0, raw_phases = ~0u;   // slots whose last copy was a raw one, those copies' phases
             bool ok = true;
             Item x;
             for (; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
                 if (lane == 0) mbar_arrive(&item_free[item % kItems]);
                 const int ctx = x.ctx, hi = ctx + x.n;
                 const int32_t* table = p.table + x.r * p.table_stride;
-                auto page_of = [&](int tile) -> int {
+                // this lane's page of a tile, -1: none (asked for a tile ahead, looked at later)
+                auto page_of = [&](int tile) -> int64_t {
                     const int tok = tile * kKeys + lane * box;
-                    if (lane >= per_tile || tok >= hi) return -1;
-                    int id = table[tok >> shift];
-                    if (id < 0 || id >= p.P) {
-                        if (p.status) atomicExch(p.status, 1);
-                        id = p.P;   // past the map's pages: the copy fills in zeros (p.P * p.Hk + h too)
-                    }
-                    return id;
+                    return tile < x.t1 && lane < per_tile && tok < hi ? (int64_t)(uint32_t)table[tok >> shift] : -1;
                 };
-                int id = page_of(x.t0);
+                int64_t ahead = page_of(x.t0);
                 for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
-                    const int next = tile + 1 < x.t1 ? page_of(tile + 1) : -1;
+                    const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
+                    if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
+                    ahead = page_of(tile + 1);
                     const int base = tile * kKeys;
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * D * 2u;
                     for (int v = 0; v < 2; ++v) {
                         const int slot = issued % kBufs, round = issued / kBufs;
-                        if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&kv_free[slot], (round - 1) & 1, abort));
+                        if (round > 0) ok = __all_sync(0xffffffffu, wait_for(&kv_free[slot], (round - 1) & 1, abort));
                         if (!ok) break;
                         uint8_t* dst = ring + slot * kTileBytes;
                         const bool special = v == 1 && base + kKeys > ctx;
-                        uint64_t* bar = special ? &v_raw : &kv_full[slot];
+                        uint64_t* bar = special ? &kv_raw[slot] : &kv_full[slot];   // raw: to warp 11 first
+                        raw = special ? raw | 1u << slot : raw & ~(1u << slot);
+                        if (special) raw_phases ^= 1u << slot;
                         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                         __syncwarp();
                         if (id >= 0)
@@ -235,46 +251,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                         ((base + lane * box) & (p.page - 1)) / 8,
                                         (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
                         ++issued;
-                        if (!special) continue;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raw_uses & 1, abort));
-                        ++raw_uses;
-                        constexpr uint32_t kExp = Elem<T>::kExpMask;
-                        constexpr int kPieces = D / 8;
-                        auto piece = [&](int e) -> uint4* {   // 16-byte piece e of the tile, rows in order
-                            const int c = e % kPieces, krow = e / kPieces;
-                            return reinterpret_cast<uint4*>(dst + (krow >> 3) * kGroupBytes + (c >> 3) * 1024 +
-                                                            (krow & 7) * 128 + (c & 7) * 16);
-                        };
-                        const int drafted = max(0, ctx - base), past = max(0, min(hi - base, kKeys));
-                        for (int e = past * kPieces + lane; e < kKeys * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-                        for (int e = drafted * kPieces + lane; e < past * kPieces; e += 32) {
-                            const uint4 y = *piece(e);
-                            uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                            bool bad = false;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if ((w[k] & kExp) == kExp) { bad = true; w[k] &= 0xffff0000u; }
-                                if (((w[k] >> 16) & kExp) == kExp) { bad = true; w[k] &= 0xffffu; }
-                            }
-                            if (bad) {
-                                const int j = base + e / kPieces - ctx;
-                                atomicOr(&s_bad[item & 7][j >> 5], 1u << (j & 31));
-                                *piece(e) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&kv_full[slot]);
                     }
-                    id = next;
                 }
             }
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) fail();
                 // copies still on their way into this CTA's memory
                 for (int i = max(0, issued - kBufs); i < issued; ++i)
-                    mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1, nullptr);
+                    if (!((raw >> (i % kBufs)) & 1)) wait_for(&kv_full[i % kBufs], (i / kBufs) & 1, nullptr);
+                    else wait_for(&kv_raw[i % kBufs], (raw_phases >> (i % kBufs)) & 1, nullptr);
             }
         } else if (warp == 9) {
             // ------------------------------------------------------------ products
@@ -291,7 +276,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             int item = 0;
             int base = 0;                      // ring tiles before this item
             int done0 = 0, done1 = 0;          // P tiles taken, by stream
-            auto landed = [&](int i) { return mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1, abort); };
+            auto landed = [&](int i) { return wait_for(&kv_full[i % kBufs], (i / kBufs) & 1, abort); };
             Item x;
             for (; __all_sync(0xffffffffu, take(item, x, ok)); ++item) {
                 if (lane == 0) mbar_arrive(&item_free[item % kItems]);
@@ -300,7 +285,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 const int units = (two ? 2 : 1) * tiles;   // unit u: stream u & 1, tile two ? u >> 1 : u
                 auto scores = [&](int u) {
                     const int s = u & 1, i = base + 2 * (two ? u >> 1 : u);
-                    ok = __all_sync(0xffffffffu, ok && landed(i));
+                    if (!two) ok = __all_sync(0xffffffffu, ok && landed(i));
                     if (!ok) return;
                     tc_fence_after();
                     const uint64_t ad = sdesc_kmajor_sw128(q_at + (two ? s : 0) * kTileBytes),
@@ -315,32 +300,43 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                     __syncwarp();
                 };
-                ok = __all_sync(0xffffffffu, ok && mbar_wait(&q_ready, item & 1, abort));
+                ok = __all_sync(0xffffffffu, ok && wait_for(&q_ready, item & 1, abort));
+                if (two) ok = __all_sync(0xffffffffu, ok && landed(base));
                 scores(0);
                 if (units > 1) scores(1);
                 for (int u = 0; u < units && ok; ++u) {
                     const int s = u & 1, i = base + 2 * (two ? u >> 1 : u) + 1;
                     // O still holds the item before until its rows are out
-                    if (u == 0 && item > 0) ok = mbar_wait(&o_free, (item - 1) & 1, abort);
-                    ok = ok && mbar_wait(&p_ready[s], (s ? done1 : done0) & 1, abort) && landed(i);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    if (u == 0 && item > 0) ok = wait_for(&o_free, (item - 1) & 1, abort);
+                    // This tile's V, and with two row tiles the next K before P is there (the
+                    // second stream's tiles are the first's); with one row tile memory is the
+                    // bound, and waiting for a K would hold up the V before it.
+                    if (!two || s == 0) ok = ok && landed(i) && (!two || u + 2 >= units || landed(i + 1));
+                    const uint32_t phase = (s ? done1 : done0) & 1;
                     if (s) ++done1; else ++done0;
-                    tc_fence_after();
                     const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % kBufs) * kTileBytes, 1024, kGroupBytes);
-                    if (elect_one()) {
+                    // the two halves of P as they come
+                    auto product = [&](int k0, uint64_t* ready) {
+                        ok = __all_sync(0xffffffffu, ok && wait_for(ready, phase, abort));
+                        if (!ok) return;
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            umma_bf16_ta(tbu + kTmemO + 128 * s, tbu + kTmemS + 128 * s + 8 * k, bd + k * (kGroupBytes >> 3),
-                                         id_pv, (u > 1 || k > 0) ? 1u : 0u);
-                        if (!two || s == 1) umma_commit(&kv_free[i % kBufs]);
-                    }
-                    __syncwarp();
+                            for (int k = 0; k < kKeys / 32; ++k)
+                                umma_bf16_ta(tbu + kTmemO + 128 * s, tbu + kTmemS + 128 * s + 8 * (k0 + k),
+                                             bd + (k0 + k) * (kGroupBytes >> 3), id_pv, (u > 1 || k0 + k > 0) ? 1u : 0u);
+                            if (k0 && (!two || s == 1)) umma_commit(&kv_free[i % kBufs]);
+                        }
+                        __syncwarp();
+                    };
+                    product(0, &p_half[s]);
+                    product(kKeys / 32, &p_ready[s]);
+                    if (!ok) break;
                     if (u + 2 < units) scores(u + 2);
                 }
                 if (elect_one()) umma_commit(&o_full);
                 __syncwarp();
-                if (!ok) mbar_wait(&o_full, item & 1, nullptr);   // products still in flight
+                if (!ok) wait_for(&o_full, item & 1, nullptr);   // products still in flight
                 base += 2 * tiles;
             }
             if (!ok && lane == 0) fail();
@@ -380,7 +376,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 int k = 0;
                 bool ok = true;
                 auto deal = [&](const Item& x) {
-                    if (k >= kItems) ok = mbar_wait(&item_free[k % kItems], (k / kItems - 1) & 1, abort);
+                    if (k >= kItems) ok = wait_for(&item_free[k % kItems], (k / kItems - 1) & 1, abort);
                     if (!ok) return;
                     s_item[k % kItems] = x;
                     mbar_arrive(&item_full[k % kItems]);
@@ -436,6 +432,55 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (!ok) fail();
             }
             __syncwarp();
+        } else {
+            // ------------------------------------------------------------ cleaning
+            // V tiles with drafted tokens or positions past the end, between their copy
+            // and the products, so that the loader can go on.
+            int base_kv = 0, item = 0;      // ring tiles before this item, items begun
+            uint32_t phases = 0;            // of the slots' raw barriers
+            bool ok = true;
+            Item x;
+            for (; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
+                if (lane == 0) mbar_arrive(&item_free[item % kItems]);
+                const int ctx = x.ctx, hi = ctx + x.n;
+                for (int tile = max(x.t0, ctx / kKeys); tile < x.t1 && ok; ++tile) {
+                    const int i = base_kv + 2 * (tile - x.t0) + 1, slot = i % kBufs, base = tile * kKeys;
+                    uint8_t* const dst = ring + slot * kTileBytes;
+                    ok = __all_sync(0xffffffffu, wait_for(&kv_raw[slot], (phases >> slot) & 1, abort));
+                    if (!ok) break;
+                    phases ^= 1u << slot;
+                    constexpr uint32_t kExp = Elem<T>::kExpMask;
+                    constexpr int kPieces = D / 8;
+                    auto piece = [&](int e) -> uint4* {   // 16-byte piece e of the tile, rows in order
+                        const int c = e % kPieces, krow = e / kPieces;
+                        return reinterpret_cast<uint4*>(dst + (krow >> 3) * kGroupBytes + (c >> 3) * 1024 +
+                                                        (krow & 7) * 128 + (c & 7) * 16);
+                    };
+                    const int drafted = max(0, ctx - base), past = max(0, min(hi - base, kKeys));
+                    for (int e = past * kPieces + lane; e < kKeys * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+                    for (int e = drafted * kPieces + lane; e < past * kPieces; e += 32) {
+                        const uint4 y = *piece(e);
+                        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                        bool bad = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((w[k] & kExp) == kExp) { bad = true; w[k] &= 0xffff0000u; }
+                            if (((w[k] >> 16) & kExp) == kExp) { bad = true; w[k] &= 0xffffu; }
+                        }
+                        if (bad) {
+                            const int j = base + e / kPieces - ctx;
+                            atomicOr(&s_bad[item & 7][j >> 5], 1u << (j & 31));
+                            *piece(e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kv_full[slot]);
+                }
+                base_kv += 2 * (x.t1 - x.t0);
+            }
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
         }
     } else {
         // ---------------------------------------------------------------- softmax
@@ -447,7 +492,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         bool ok = true;
         int item = 0, seen_s = 0;   // items begun, score tiles taken
         for (;; ++item) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&item_full[item % kItems], (item / kItems) & 1, abort));
+            ok = __all_sync(0xffffffffu, wait_for(&item_full[item % kItems], (item / kItems) & 1, abort));
             if (!ok && lane == 0) fail();
             const Item& x = s_item[item % kItems];
             if (named_bar_or(1, 256, !ok || x.t1 < 0)) break;   // all stop if one has given up
@@ -475,7 +520,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const bool live = row - lane < p.rows;   // some row of the warp is a row of the call
             cp_async_wait<0>();
             fence_proxy_async_smem();
-            mbar_arrive(&q_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready);
 
             // 32 drafted nodes' visibility to this row, from node 32 w on
             const uint32_t* mask =
@@ -495,10 +541,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 return left >= 32 ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
             };
 
+            const int tile0 = x.t0, ctx_in = x.ctx;
             float m = -INFINITY, l = 0.f;
             const int units = (two ? 2 : 1) * (x.t1 - x.t0);
             for (int u = stream; u < units; u += 2) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[stream], seen_s & 1, abort));
+                ok = __all_sync(0xffffffffu, wait_for(&s_full[stream], seen_s & 1, abort));
                 if (!ok) break;
                 ++seen_s;
                 tc_fence_after();
@@ -510,8 +557,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) tmem_take16(raw[k], &v[16 * k]);
-                    const int base = (x.t0 + (two ? u >> 1 : u)) * kKeys;
-                    if (base + kKeys > ctx) {
+                    const int base = (tile0 + (two ? u >> 1 : u)) * kKeys;
+                    if (base + kKeys > ctx_in) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t b = seen(base + 32 * k);
@@ -520,10 +567,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                 if (!((b >> e) & 1u)) v[32 * k + e] = -INFINITY;
                         }
                     }
-                    float mx[4] = {v[0], v[1], v[2], v[3]};
+                    float mx[8];
 #pragma unroll
-                    for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int e = 0; e < 8; ++e) mx[e] = v[e];
+#pragma unroll
+                    for (int e = 8; e < 128; ++e) mx[e & 7] = fmaxf(mx[e & 7], v[e]);
+                    const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                            fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                     float alpha = 1.f;
                     if (top > m + lazy || m == -INFINITY) {
                         if (m != -INFINITY) alpha = ex2_approx((m - top) * c);
@@ -555,15 +605,24 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             w[e] = Elem<T>::pack(p0, p1);
                         }
                         tmem_st16_issue(ts + 16 * k, w);
+                        if (k == 1) {   // half of P: its product may start
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_half[stream]);
+                        }
                     }
                     const float2 q = f2_parts(f2_add(sum[0], sum[1]));
                     l += q.x + q.y;
                     tmem_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&p_half[stream]);
                 }
                 tc_fence_before();
-                mbar_arrive(&p_ready[stream]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[stream]);
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full, item & 1, abort)) && ok;
+            ok = __all_sync(0xffffffffu, wait_for(&o_full, item & 1, abort)) && ok;
             if (!ok && lane == 0) fail();
             tc_fence_after();
 
@@ -598,6 +657,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             uint32_t any_bad = 0;
 #pragma unroll
             for (int w = 0; w < 8; ++w) any_bad |= s_bad[item & 7][w];
+            // Where this lane stores: whole rows 4 lanes a row (8 elements each), partial ones
+            // 8 lanes a row (4 floats each).
+            T* dst[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int q = row - lane + 8 * g + (lane >> 2), qi = (int)page_div((uint32_t)q, p.G, p.group_magic);
+                dst[g] = q < p.rows ? static_cast<T*>(p.out) + r * p.os[0] + qi * p.os[1] +
+                                          (kvh * p.G + q - qi * p.G) * p.os[2] + (lane & 3) * 8
+                                    : nullptr;
+            }
+            float* const pdst = p.part_o + (part - lane + (lane >> 3)) * D + (lane & 7) * 4;
             // rolled: the code runs once an item, and fetching it costs more than running it
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
@@ -638,26 +708,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                     __syncwarp();
                     if (whole) {
-#pragma unroll 1
+                        const float* src = patch + (lane >> 2) * 36 + (lane & 3) * 8;
+#pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            const int pr = 8 * g + (lane >> 2), q = row - lane + pr, col = (lane & 3) * 8;
-                            const float4 y0 = *reinterpret_cast<const float4*>(patch + pr * 36 + col),
-                                         y1 = *reinterpret_cast<const float4*>(patch + pr * 36 + col + 4);
-                            const int qi = (int)page_div((uint32_t)q, p.G, p.group_magic), qh = kvh * p.G + (q - qi * p.G);
-                            if (q < p.rows)
-                                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + r * p.os[0] + qi * p.os[1] +
-                                                          qh * p.os[2] + 32 * k + col) =
+                            const float4 y0 = *reinterpret_cast<const float4*>(src + 8 * g * 36),
+                                         y1 = *reinterpret_cast<const float4*>(src + 8 * g * 36 + 4);
+                            if (dst[g])
+                                *reinterpret_cast<uint4*>(dst[g] + 32 * k) =
                                     make_uint4(Elem<T>::pack(y0.x, y0.y), Elem<T>::pack(y0.z, y0.w),
                                                Elem<T>::pack(y1.x, y1.y), Elem<T>::pack(y1.z, y1.w));
                         }
                     } else {
-#pragma unroll 2
-                        for (int g = 0; g < 8; ++g) {
-                            const int pr = 4 * g + (lane >> 3), col = (lane & 7) * 4;
-                            if (row - lane + pr < p.rows)
-                                *reinterpret_cast<float4*>(p.part_o + (part - lane + pr) * D + 32 * k + col) =
-                                    *reinterpret_cast<const float4*>(patch + pr * 36 + col);
-                        }
+                        const float* src = patch + (lane >> 3) * 36 + (lane & 7) * 4;
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            if (row - lane + 4 * g + (lane >> 3) < p.rows)
+                                *reinterpret_cast<float4*>(pdst + 4 * g * D + 32 * k) =
+                                    *reinterpret_cast<const float4*>(src + 4 * g * 36);
                     }
                 }
                 if (joined) named_bar_sync(1, 256);   // stream 1's columns are taken
@@ -672,7 +739,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             named_bar_sync(1, 256);   // every warp's patch and s_bad have been read
             if (tid < 8) s_bad[item & 7][tid] = 0;
             if (tid == 0) mbar_arrive(&item_free[item % kItems]);
-            mbar_arrive(&o_free);
+            if (lane == 0) mbar_arrive(&o_free);
         }
     }
     __syncthreads();
