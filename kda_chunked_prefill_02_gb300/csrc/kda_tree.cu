@@ -445,18 +445,23 @@ cudaError_t launch_join(const TreeParams& p, int D, cudaStream_t s) {
 
 TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms) {
     TreePlan t;
-    // More rows than the warp-level kernel takes at a time: the 128-row products,
-    // where pages are whole 8-row groups of a tile (and the line of work, in key
-    // tiles, stays inside 32 bits).
-    t.mma = rows > 32 && D <= 128 && page >= 8 && (page & (page - 1)) == 0 && scale > 0.f &&
-            max_len / 128 + 1 < (1 << 22);
-    // The rows kernel's splits (also for a cache without a tensor map): CTAs of the
-    // longest contexts for four waves of two an SM, at least 256 tokens a split and
-    // at most 1024 pages.
+    // The 128-row products where there are more rows than one product of the
+    // warp-level kernel takes and enough work to outlast their longer way in (about
+    // 10 us): 38 requests x 4 key heads x 32 rows over 1024 tokens 21 us against 48,
+    // 8 x 2 x 512 rows over 300 28 against 37; but 16 x 8 x 32 over 500 24 against 22
+    // and 1 x 8 x 32 over 1000 21 against 17.  Pages have to be whole 8-row groups of a
+    // tile (and the line of work, in key tiles, stays inside 32 bits).
+    const int64_t blocks = (rows + 31) / 32;
+    t.mma = rows > 16 && (int64_t)R * Hk * blocks * max_len > 65536 && D <= 128 && page >= 8 &&
+            (page & (page - 1)) == 0 && scale > 0.f && max_len / 128 + 1 < (1 << 22);
+    // The rows kernel's splits (also for a cache without a tensor map): as many CTAs
+    // as run at once (two an SM), so that no context's end is alone on the GPU, at
+    // least 128 tokens a split and at most 1024 pages.  One request, 8 key heads, 64000
+    // tokens: 56 us with these splits, 78 with twice as many, 112 with four times.
     const int block = rows_per_block(rows, D);
     const int64_t items = (int64_t)R * Hk * ((rows + block - 1) / block);
-    const int64_t most = (max_len + 255) / 256;
-    int64_t splits = 8LL * num_sms / items;
+    const int64_t most = (max_len + 127) / 128;
+    int64_t splits = 2LL * num_sms / items;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
     int64_t chunk = (max_len + splits - 1) / splits;

@@ -249,11 +249,14 @@ def test_rope_zero_rows():
 
 
 # ---------------------------------------------------------------- tree attention
-def _pages(g, need_tokens, page, spare=2):
+ROOM = 300000   # tokens a page table has room for: enough for the kernel for many rows
+
+
+def _pages(g, need_tokens, page, spare=2, room=0):
     need = [(t + page - 1) // page for t in need_tokens]
     total = sum(need) + spare
     order = torch.randperm(total, generator=g).to(torch.int32)
-    table = torch.full((len(need), max(max(need), 1)), 0, dtype=torch.int32)
+    table = torch.full((len(need), max(max(need), 1, room // page)), 0, dtype=torch.int32)
     at = 0
     for r, n in enumerate(need):
         table[r, :n] = order[at:at + n]
@@ -280,10 +283,10 @@ def _sees(parents):
 
 
 def _tree_case(seed, ctx, N, Hq, Hk, D, page, dtype, *, form="tree", nodes=None, heads_first=False, q_scale=1.0,
-               scale=None, max_context=None, poison=True, parents=None):
+               scale=None, max_context=None, poison=True, parents=None, room=0):
     g = _gen(seed)
     R = len(ctx)
-    table, total = _pages(g, [c + N for c in ctx], page)
+    table, total = _pages(g, [c + N for c in ctx], page, room=room)
     shape = (total, Hk, page, D) if heads_first else (total, page, Hk, D)
     kc, vc = _rand(g, shape, dtype), _rand(g, shape, dtype)
     if heads_first:
@@ -323,26 +326,62 @@ def _tree_case(seed, ctx, N, Hq, Hk, D, page, dtype, *, form="tree", nodes=None,
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("N,Hq,Hk", [(1, 4, 4), (1, 8, 1), (3, 6, 2), (4, 16, 4), (13, 10, 2), (40, 4, 1)])
-def test_tree_shapes(dtype, D, N, Hq, Hk):
-    """Contexts around the tile size, an empty and a one-token one, one that is split."""
-    _tree_case(N + Hq, [0, 1, 63, 64, 65, 200, 700], N, Hq, Hk, D, 16, dtype)
+@pytest.mark.parametrize("N,Hq,Hk", [(1, 4, 4), (1, 8, 1), (3, 6, 2), (4, 16, 4), (13, 10, 2), (40, 4, 1), (17, 16, 2)])
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_tree_shapes(dtype, D, N, Hq, Hk, room):
+    """Contexts around the tile sizes, an empty and a one-token one, one that is split."""
+    _tree_case(N + Hq, [0, 1, 63, 64, 65, 128, 200, 700], N, Hq, Hk, D, 16, dtype, room=room)
 
 
 @pytest.mark.parametrize("page,heads_first", [(1, False), (7, True), (8, False), (24, False), (64, True), (100, False),
                                               (4096, False)])
-@pytest.mark.parametrize("N,G", [(2, 4), (30, 8)])
-def test_tree_pages(page, heads_first, N, G):
-    _tree_case(page, [130, 0, 900, 31], N, 2 * G, 2, 128, page, BF16, heads_first=heads_first)
+@pytest.mark.parametrize("N,G,room", [(2, 4, 0), (30, 8, 0), (5, 4, ROOM), (40, 8, ROOM)])
+def test_tree_pages(page, heads_first, N, G, room):
+    _tree_case(page, [130, 0, 900, 31], N, 2 * G, 2, 128, page, BF16, heads_first=heads_first, room=room)
+
+
+@pytest.mark.parametrize("page", [8, 16, 128, 512])
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_pages_of_the_kernel_for_many_rows(page, heads_first, D):
+    _tree_case(page, [513, 2, 127, 300, 0], 20, 12, 3, D, page, F16, heads_first=heads_first, room=ROOM)
+
+
+def test_tree_cache_layouts_without_a_tensor_map():
+    """Keys and values in one page, heads neither a row's nor a page's neighbours."""
+    g = _gen(77)
+    R, N, Hk, G, D, page = 2, 9, 3, 4, 64, 16
+    table, total = _pages(g, [300, 64], page, room=ROOM)
+    both = _rand(g, (total, page, Hk, 2, D), BF16)      # head stride 2 D
+    q = _rand(g, (R, N, Hk * G, D), BF16)
+    out, ob, _, _ = tree_reference(q, both[:, :, :, 0], both[:, :, :, 1], table, [291, 55])
+    d = both.cuda()
+    got = K.kda_tree_attention(q.cuda(), d[:, :, :, 0], d[:, :, :, 1], table.cuda(), _i32([291, 55]).cuda())
+    within(got, out, ob)
+    pages = _rand(g, (total, 2, page, Hk, D), BF16)     # a page's keys, then its values
+    out, ob, _, _ = tree_reference(q, pages[:, 0], pages[:, 1], table, [291, 55])
+    d = pages.cuda()
+    got = K.kda_tree_attention(q.cuda(), d[:, 0], d[:, 1], table.cuda(), _i32([291, 55]).cuda())
+    within(got, out, ob)
 
 
 @pytest.mark.parametrize("N,form", [(1, "chain"), (5, "chain"), (64, "tree"), (65, "tree"), (130, "tree"),
                                     (256, "chain")])
-def test_tree_node_counts(N, form):
-    _tree_case(N, [77, 5], N, 2, 1, 64, 32, F16, form=form)
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_tree_node_counts(N, form, room):
+    _tree_case(N, [77, 5], N, 2, 1, 64, 32, F16, form=form, room=room)
 
 
-def test_tree_unused_nodes_and_nodes_outside_the_tree():
+def test_tree_many_requests():
+    """More requests than one launch of the kernel for many rows takes (256), most of
+    them short, some empty, some long enough to be cut."""
+    ctx = [(i * 37) % 90 if i % 50 else 700 + i for i in range(300)]
+    nodes = _i32([(i * 7) % 10 for i in range(300)])
+    _tree_case(50, ctx, 9, 4, 2, 64, 16, BF16, nodes=nodes, room=2048)
+
+
+@pytest.mark.parametrize("G,room", [(2, 0), (12, ROOM)])
+def test_tree_unused_nodes_and_nodes_outside_the_tree(G, room):
     """num_nodes below the call's, and nodes with parent -2 (their keys and values
     hold NaN): zero rows, no trace in the others."""
     g = _gen(3)
@@ -353,16 +392,16 @@ def test_tree_unused_nodes_and_nodes_outside_the_tree():
             if parents[r, i] >= 0 and parents[r, int(parents[r, i])] == -2:
                 parents[r, i] = -1
     for ctx in ([70, 0, 300, 5], [0, 0, 0, 0]):
-        _tree_case(11, ctx, 9, 4, 2, 128, 16, BF16, nodes=_i32([9, 0, 9, 4]), parents=parents)
+        _tree_case(11, ctx, 9, 2 * G, 2, 128, 16, BF16, nodes=_i32([9, 0, 9, 4]), parents=parents, room=room)
 
 
 def test_tree_values_that_only_some_rows_see_may_be_nan():
     """A node whose V holds NaN and infinity reaches its own descendants only."""
     g = _gen(5)
-    for N, Hq in ((6, 4), (24, 16)):
+    for N, Hq, room in ((6, 4, 0), (24, 16, 0), (24, 16, ROOM), (70, 16, ROOM)):
         parents = torch.full((1, N), -1)
         parents[0, 2] = 1       # node 2 follows node 1, the rest follow the context
-        table, total = _pages(g, [50 + N], 16)
+        table, total = _pages(g, [50 + N], 16, room=room)
         kc, vc = _rand(g, (total, 16, 2, 128), BF16), _rand(g, (total, 16, 2, 128), BF16)
         q = _rand(g, (1, N, Hq, 128), BF16)
         out, ob, _, _ = tree_reference(q, kc, vc, table, [50], sees=_sees(parents))
@@ -381,11 +420,30 @@ def test_tree_large_scores_and_scales():
     _tree_case(21, [300, 64], 4, 4, 2, 128, 16, BF16, q_scale=30.0)
     _tree_case(22, [300, 64], 4, 4, 2, 128, 16, F16, scale=-0.1)
     _tree_case(23, [300, 64], 4, 4, 2, 64, 16, F16, scale=0.0)
+    for dtype in (BF16, F16):
+        _tree_case(24, [900, 64, 300], 12, 8, 2, 128, 16, dtype, q_scale=30.0, room=ROOM)
 
 
-@pytest.mark.parametrize("N,G", [(1, 8), (16, 4)])
-def test_tree_long_context(N, G):
-    _tree_case(31, [20011, 3], N, 2 * G, 2, 128, 64, BF16, poison=False)
+def test_tree_a_maximum_that_grows():
+    """Scores that climb along the context: the running maximum has to move again and again."""
+    for dtype, N, G, room in ((BF16, 3, 2, 0), (BF16, 20, 8, ROOM), (F16, 40, 8, ROOM), (F16, 6, 8, ROOM)):
+        g = _gen(N)
+        table, total = _pages(g, [1500], 16, room=room)
+        kc, vc = _rand(g, (total, 16, 1, 128), dtype), _rand(g, (total, 16, 1, 128), dtype)
+        q = _rand(g, (1, N, G, 128), dtype)
+        q[..., 0] = 4.0
+        for p in range(1500):
+            kc[int(table[0, p // 16]), p % 16, 0, 0] = p / 10.0
+        out, ob, lse, lb = tree_reference(q, kc, vc, table, [1500 - N], scale=0.3)
+        got, glse = K.kda_tree_attention(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), _i32([1500 - N]).cuda(),
+                                         scale=0.3, return_lse=True)
+        within(got, out, ob)
+        within(glse, lse, lb)
+
+
+@pytest.mark.parametrize("N,G,form", [(1, 8, "chain"), (16, 4, "tree"), (33, 8, "tree")])
+def test_tree_long_context(N, G, form):
+    _tree_case(31, [20011, 3], N, 2 * G, 2, 128, 64, BF16, poison=False, form=form)
 
 
 def test_tree_max_context_changes_the_cut_only():
@@ -407,11 +465,12 @@ def test_tree_strided_queries_and_outputs():
     assert bool((res[:, 1::2] == 5.0).all()) and bool((res[:, :, 7] == 5.0).all())
 
 
-def test_tree_reports_what_only_the_device_sees():
+@pytest.mark.parametrize("G,room", [(4, 0), (24, 0), (24, ROOM)])
+def test_tree_reports_what_only_the_device_sees(G, room):
     g = _gen(34)
-    table, total = _pages(g, [70, 70, 70], 16, spare=0)
+    table, total = _pages(g, [70, 70, 70], 16, spare=0, room=room)
     kc, vc = _rand(g, (total, 16, 1, 64), BF16).cuda(), _rand(g, (total, 16, 1, 64), BF16).cuda()
-    q = _rand(g, (3, 2, 4, 64), BF16).cuda()
+    q = _rand(g, (3, 2, G, 64), BF16).cuda()
     good = K.kda_tree_attention(q, kc, vc, table.cuda(), _i32([68, 60, 50]).cuda())
 
     def run(ctx, tab=table, **kw):
@@ -421,7 +480,8 @@ def test_tree_reports_what_only_the_device_sees():
         assert status.item() == 1
         return out, lse
 
-    for ctx, kw in (([68, -1, 50], {}), ([68, 79, 50], {}), ([68, 60, 50], dict(num_nodes=_i32([2, 3, 2]).cuda())),
+    too_long = table.shape[1] * 16 - 1
+    for ctx, kw in (([68, -1, 50], {}), ([68, too_long, 50], {}), ([68, 60, 50], dict(num_nodes=_i32([2, 3, 2]).cuda())),
                     ([68, 60, 50], dict(num_nodes=_i32([2, -1, 2]).cuda()))):
         out, lse = run(ctx, **kw)
         assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
