@@ -19,10 +19,12 @@
 // accumulator layout is the next product's operand layout), and the warps meet
 // once, at the end, to join their (m, l, o).
 //
-// A context is cut into splits of `chunk` tokens (one CTA each) when there are
-// too few (request, head) pairs to fill the GPU; the splits leave normalised
-// rows and their log-sum in the workspace, joined in a fixed order by
-// tree_join_kernel.
+// Where there are too few (request, head) pairs to fill the GPU, a context is the
+// work of a cluster of up to 8 CTAs, an equal stretch of its tiles each (of the
+// length that the device sees), which join their rows through distributed shared
+// memory: no second launch and no workspace.  Longer contexts are first cut into
+// splits of `chunk` tokens, one cluster each; the splits leave normalised rows and
+// their log-sum in the workspace, joined in a fixed order by tree_join_kernel.
 //
 // Keys that a row does not see are taken out of the scores by a select, and
 // rows of V past the end are zero-filled in shared memory.  V of a drafted
@@ -41,6 +43,28 @@ constexpr int kStages = 3;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of the cluster's CTA `rank` at this CTA's address `addr`.
+__device__ __forceinline__ uint32_t remote_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 remote_ld4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 remote_ld2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 // 16 bytes global -> shared, or 16 zero bytes.
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
@@ -82,7 +106,7 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
     return (uint32_t)r * (D * 2) + (uint32_t)((c ^ (r & 7)) << 4);
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, bool kCluster>
 __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParams p) {
     constexpr int kRows = 16 * MT;
     constexpr uint32_t kKV = kTile * D * 2, kStage = 2 * kKV;
@@ -91,14 +115,17 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
     int* spage = reinterpret_cast<int*>(sq + kRows * D * 2);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
-    const int split = blockIdx.x / p.row_blocks, rb = blockIdx.x - split * p.row_blocks;
+    const int cluster = kCluster ? p.cluster : 1, rank = kCluster ? blockIdx.x % cluster : 0, bx = blockIdx.x / cluster;
+    const int split = bx / p.row_blocks, rb = bx - split * p.row_blocks;
     const int kvh = blockIdx.y, r = blockIdx.z, row0 = rb * kRows;
     int ctx, n;
     if (!tree_lengths(p, r, ctx, n) && p.status && tid == 0) atomicExch(p.status, 1);
     const int len = ctx + n;
     const int nsplit = max(1, (len + p.chunk - 1) / p.chunk);
-    if (split >= nsplit) return;
-    const int lo = split * p.chunk, hi = min(lo + p.chunk, len);
+    if (split >= nsplit) return;   // the whole cluster
+    // this CTA's tiles of the split
+    const int lo0 = split * p.chunk, hi0 = min(lo0 + p.chunk, len), tiles0 = max(0, hi0 - lo0 + kTile - 1) / kTile;
+    const int lo = lo0 + tiles0 * rank / cluster * kTile, hi = min(lo0 + tiles0 * (rank + 1) / cluster * kTile, hi0);
 
     // this split's pages
     const int pg0 = lo / p.page;
@@ -328,24 +355,64 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
                     make_float2(o[a][b][2 * h], o[a][b][2 * h + 1]);
         }
     __syncthreads();
-    for (int e = tid; e < kRows * kPieces; e += kTreeThreads) {
-        const int row = e / kPieces, c = e - row * kPieces, q = row0 + row;
-        if (q >= p.rows) break;
+    // the four warps' rows joined: the running maximum (0 if there is none), the sum, and
+    // 8 values of the row
+    auto joined = [&](int row, int c, float& mu, float& sum, float (&y)[8]) {
         float mw[4], mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             mw[w] = sml[(w * kRows + row) * 2];
             mx = fmaxf(mx, mw[w]);
         }
-        const float mu = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        mu = mx == -INFINITY ? 0.f : mx;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const float f = ex2_approx(mw[w] - mu);
             sum = fmaf(sml[(w * kRows + row) * 2 + 1], f, sum);
             const float* src = so + (w * kRows + row) * D + c * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(src[i], f, y[i]);
+            for (int k = 0; k < 8; ++k) y[k] = fmaf(src[k], f, y[k]);
+        }
+    };
+    float* const sx = sml + 4 * kRows * 2;      // cluster: this CTA's rows [kRows][D], then (maximum, sum) [kRows]
+    if (kCluster) {
+        for (int e = tid; e < kRows * kPieces; e += kTreeThreads) {
+            const int row = e / kPieces, c = e - row * kPieces;
+            float mu, sum, y[8];
+            joined(row, c, mu, sum, y);
+            float4* dst = reinterpret_cast<float4*>(sx + row * D + c * 8);
+            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+            if (c == 0) *reinterpret_cast<float2*>(sx + kRows * D + 2 * row) = make_float2(sum == 0.f ? -INFINITY : mu, sum);
+        }
+        cluster_sync();
+    }
+    const uint32_t sx_at = smem_addr(sx);
+    for (int e = rank * kTreeThreads + tid; e < kRows * kPieces; e += cluster * kTreeThreads) {
+        const int row = e / kPieces, c = e - row * kPieces, q = row0 + row;
+        if (q >= p.rows) break;
+        float mu, sum, y[8];
+        if (!kCluster) {
+            joined(row, c, mu, sum, y);
+        } else {
+            float mx = -INFINITY;
+            for (int w = 0; w < cluster; ++w) mx = fmaxf(mx, remote_ld2(remote_addr(sx_at + (kRows * D + 2 * row) * 4, w)).x);
+            mu = mx == -INFINITY ? 0.f : mx;
+            sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = 0.f;
+            for (int w = 0; w < cluster; ++w) {
+                const float2 ml = remote_ld2(remote_addr(sx_at + (kRows * D + 2 * row) * 4, w));
+                const uint32_t src = remote_addr(sx_at + (row * D + c * 8) * 4, w);
+                const float4 a = remote_ld4(src), b = remote_ld4(src + 16);
+                const float f = ex2_approx(ml.x - mu);
+                sum = fmaf(ml.y, f, sum);
+                y[0] = fmaf(a.x, f, y[0]); y[1] = fmaf(a.y, f, y[1]); y[2] = fmaf(a.z, f, y[2]); y[3] = fmaf(a.w, f, y[3]);
+                y[4] = fmaf(b.x, f, y[4]); y[5] = fmaf(b.y, f, y[5]); y[6] = fmaf(b.z, f, y[6]); y[7] = fmaf(b.w, f, y[7]);
+            }
         }
         const int i = q / p.G;
         const bool empty = i >= n || sum == 0.f;
@@ -366,6 +433,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
             if (c == 0) p.part_lse[at] = lse;
         }
     }
+    if (kCluster) cluster_sync();   // the others have read this CTA's rows
 }
 
 // Joins the splits of a row: out = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M).
@@ -410,20 +478,34 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeParams p) {
 
 int rows_per_block(int rows, int D) { return rows <= 16 || D > 128 ? 16 : 32; }
 
-template <typename T, int D, int MT>
-cudaError_t launch_rows_t(const TreeParams& q, cudaStream_t s) {
-    TreeParams p = q;
-    p.row_blocks = (p.rows + 16 * MT - 1) / (16 * MT);
+template <typename T, int D, int MT, bool kCluster>
+cudaError_t launch_rows_c(const TreeParams& p, cudaStream_t s) {
     const size_t pages = (size_t)p.chunk / p.page + 2;
     const size_t smem = (size_t)kStages * 2 * kTile * D * 2 + 16 * MT * D * 2 + pages * sizeof(int);
     static std::atomic<uint64_t> smem_set;
     // the largest page list (see tree_plan)
     const int limit = kStages * 2 * kTile * D * 2 + 16 * MT * D * 2 + 1026 * (int)sizeof(int);
-    cudaError_t e = set_smem_limit_once((const void*)tree_rows_kernel<T, D, MT>, limit, smem_set);
+    const auto kernel = tree_rows_kernel<T, D, MT, kCluster>;
+    cudaError_t e = set_smem_limit_once((const void*)kernel, limit, smem_set);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.splits * p.row_blocks), (unsigned)p.Hk, (unsigned)p.R);
-    tree_rows_kernel<T, D, MT><<<grid, kTreeThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(p.splits * p.row_blocks * p.cluster), (unsigned)p.Hk, (unsigned)p.R);
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCluster ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <typename T, int D, int MT>
+cudaError_t launch_rows_t(const TreeParams& q, cudaStream_t s) {
+    TreeParams p = q;
+    p.row_blocks = (p.rows + 16 * MT - 1) / (16 * MT);
+    return p.cluster > 1 ? launch_rows_c<T, D, MT, true>(p, s) : launch_rows_c<T, D, MT, false>(p, s);
 }
 
 template <typename T>
@@ -454,16 +536,21 @@ TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, fl
     const int64_t blocks = (rows + 31) / 32;
     t.mma = rows > 16 && (int64_t)R * Hk * blocks * max_len > 65536 && D <= 128 && page >= 8 &&
             (page & (page - 1)) == 0 && scale > 0.f && max_len / 128 + 1 < (1 << 22);
-    // The rows kernel's splits (also for a cache without a tensor map): as many CTAs
-    // as run at once (two an SM), so that no context's end is alone on the GPU, at
-    // least 128 tokens a split and at most 1024 pages.  One request, 8 key heads, 64000
-    // tokens: 56 us with these splits, 78 with twice as many, 112 with four times.
+    // The rows kernel's cut (also for a cache without a tensor map): as many CTAs as run
+    // at once (two an SM), so that no context's end is alone on the GPU, at least 128
+    // tokens each.  Up to 8 are a cluster, which joins its rows itself (one request, 2
+    // key heads, 1000 tokens: 8.5 us against 9.7 with a second launch, and no workspace);
+    // more are splits, of at most 1024 pages (one request, 8 key heads, 131072 tokens: 95
+    // us against 104 in clusters).  One request, 8 key heads, 64000 tokens: 56 us with as
+    // many splits, 78 with twice as many, 112 with four times.
     const int block = rows_per_block(rows, D);
     const int64_t items = (int64_t)R * Hk * ((rows + block - 1) / block);
     const int64_t most = (max_len + 127) / 128;
-    int64_t splits = 2LL * num_sms / items;
-    if (splits > most) splits = most;
-    if (splits < 1) splits = 1;
+    int64_t parts = 2LL * num_sms / items;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    t.cluster = parts >= 16 ? 1 : parts >= 8 ? 8 : parts >= 4 ? 4 : parts >= 2 ? 2 : 1;
+    int64_t splits = parts / t.cluster;
     int64_t chunk = (max_len + splits - 1) / splits;
     if (chunk > 1024LL * page) chunk = 1024LL * page;
     chunk = (chunk + kTile - 1) / kTile * kTile;

@@ -68,6 +68,7 @@ struct TreeParams {
     int64_t max_len;          // longest context and nodes of a request (at most what its page row holds)
     uint32_t page_magic, group_magic;   // floor(2^32 / page), floor(2^32 / G) (2^32 - 1 for 1)
     int chunk, splits;        // tokens a split; splits of the longest request
+    int cluster;              // CTAs that share a split
     int row_blocks;           // set by the launcher
     int k_paged, v_paged;     // mma: the head is part of the map's page coordinate
     int r0, count, slots;     // mma: the requests of a launch, 2 x its CTAs (set by the launcher)
@@ -77,6 +78,7 @@ struct TreeParams {
 struct TreePlan {
     bool mma;            // the kernel for many rows
     int chunk, splits;   // rows kernel: tokens a split, splits of the longest request
+    int cluster;         // and CTAs that share a split
     int grid;            // mma: CTAs
     size_t part_rows;    // partial rows in the workspace (D values and a log-sum each)
     size_t parts;        // int4 behind them, for what they belong to
