@@ -5,6 +5,7 @@
 Compiles csrc/*.cu (one nvcc per translation unit, in parallel) and links
   libkda.so          the product library (C ABI of include/kda.h and include/kda_ops.h)
   libkda_selftest.so test-only checks of the tcgen05 / TMA building blocks
+  _kda_ops.so        the Python binding of include/kda_ops.h (csrc/ops_binding.cpp)
 next to this file.  Objects go to _build/ (git-ignored).
 """
 import concurrent.futures as cf
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -25,10 +27,12 @@ LIB_SOURCES = ["kda_api.cu", "kda_prep.cu", "kda_state.cu", "kda_state_head.cu",
                "kda_verify_wy.cu", "kda_noalloc.cu", "kda_host.cu", "kda_ops_api.cu", "kda_conv.cu",
                "kda_rope.cu", "kda_tree.cu", "kda_tree_mma.cu"]
 SELFTEST_SOURCES = ["selftest.cu"]
+BINDING_SOURCE = "ops_binding.cpp"
 HEADERS = ["sm103.cuh", "kda_internal.h", "ops_internal.h", "tmap.h"]
 
 LIB = os.path.join(HERE, "libkda.so")
 SELFTEST_LIB = os.path.join(HERE, "libkda_selftest.so")
+BINDING = os.path.join(HERE, "_kda_ops.so")
 
 
 def _nvcc():
@@ -63,19 +67,50 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, r.stdout, r.stderr))
+
+
+def _compile_binding():
+    """The Python binding against this interpreter's torch."""
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = [root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    obj = os.path.join(BUILD, "ops_binding.o")
+    _run(["g++", "-O2", "-fPIC", "-std=c++17", "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+          "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj] + ["-I" + i for i in inc], "g++ for " + BINDING_SOURCE)
+    return obj
+
+
+def _link_binding(obj):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    _run(["g++", "-shared", obj, "-o", tmp, "-L" + HERE, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-lc10",
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + lib], "link of " + BINDING)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     todo = []
     for out, srcs in ((LIB, LIB_SOURCES), (SELFTEST_LIB, SELFTEST_SOURCES)):
         if force or not os.path.exists(out) or os.path.getmtime(out) < _newest_input(srcs):
             todo.append((out, srcs))
-    if not todo:
+    binding = force or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < _newest_input([BINDING_SOURCE])
+    if not todo and not binding:
         return LIB
     all_srcs = sorted({s for _, srcs in todo for s in srcs})
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(all_srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(all_srcs) + 1)) as ex:
+        bound = ex.submit(_compile_binding) if binding else None
         objs = dict(zip(all_srcs, ex.map(_compile, all_srcs)))
     for out, srcs in todo:
         _link([objs[s] for s in srcs], out)
+    if bound:
+        _link_binding(bound.result())
     return LIB
 
 
