@@ -37,8 +37,7 @@ extern "C" {
  *     y_t[c] /= sqrt(sum over its head of 128 channels of y_t^2 + norm_eps)
  *                                              (channels c < norm_channels)
  *
- * in fp32, rounded once to the element type of x.  A sigmoid below 2e-19 is
- * evaluated as 2e-19 (z < -43: |y| < 2e-17 |z|).
+ * in fp32, rounded once to the element type of x.
  *
  * Sequences: padded (cu_seqlens NULL): num_seqs sequences of seqlen tokens,
  * element (n, t, c) of x at n*x_stride[0] + t*x_stride[1] + c; packed: device
@@ -59,7 +58,7 @@ extern "C" {
  *
  * C (channels) a multiple of 8, W in 2..4, norm_channels a multiple of 128 of
  * at most C; x and out do not overlap.  weight [C, W] and bias [C] contiguous.
- * Size limits: fewer than 2^31 tokens and channels, num_seqs <= 2^30.
+ * Size limits: fewer than 2^31 tokens, at most 2^24 channels, num_seqs <= 2^30.
  */
 typedef struct kda_short_conv_args {
     const void* x;

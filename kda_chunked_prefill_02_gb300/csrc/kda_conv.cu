@@ -6,14 +6,18 @@
 //
 // y_t[c] = act(bias[c] + sum_j w[c][j] x_{t-W+1+j}[c]): every input is used W
 // times and every output written once, so the kernel streams x once and is
-// bound by HBM bandwidth (4 bytes an element).  Thread = 8 channels (16 bytes a
+// bound by HBM bandwidth (4 bytes an element).  Thread = 4 channels (8 bytes a
 // token), walking down a tile of tokens with the last W - 1 inputs in fp32
-// registers.  The tokens ahead come by 16-byte asynchronous copies into a ring
+// registers.  The tokens ahead come by 8-byte asynchronous copies into a ring
 // of kRing rows in shared memory, of which every thread reads only what it
-// copied itself: the loads in flight cost no registers (so five CTAs fit an SM)
-// and need no barrier.  Arithmetic is in packed fp32 pairs, without which the
-// issue slots, not the memory, set the time.  A head's 128 channels are 16
-// adjacent lanes, so its L2 norm is four shuffles.
+// copied itself: the loads in flight cost no registers and need no barrier.  A
+// token is a chain of some 400 cycles (taps, exponential, reciprocal, the sum
+// over the head), which other warps hide, and the issue slots leave some 85 cycles
+// a warp and token at the memory's rate: so few channels a thread (many warps),
+// packed fp32 pairs, and four tokens at a time, whose norms share one reduction
+// and one root.  Measured, 32768 tokens of 12288 channels, bf16: 246 us, 6.5 TB/s
+// (372 us with 8 channels a thread, plain fp32 and loads in registers; 292 us
+// with everything but the four tokens' shared reduction and the folded log2 e).
 //
 // Tiles cut the flat token range, whatever sequences they meet, so that ragged
 // batches need no host knowledge of cu_seqlens and leave no empty CTA.  The
@@ -29,119 +33,160 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvVec = 8;
+constexpr int kConvVec = 4;         // channels a thread
+constexpr int kPairs = kConvVec / 2;
+using Piece = uint2;                // their elements
 constexpr int kStep = 4;            // tokens a copy group
 constexpr int kRing = 4 * kStep;    // tokens in flight
-constexpr int kTokenSeqs = 4;       // sequences a CTA of the single-token kernel takes
+constexpr int kTokenSeqs = 2;       // sequences a CTA of the single-token kernel takes (256 of them: 9.7 us; 10.6 with 1, 11.7 with 4)
 
-// z sigmoid(z) of 8 values.  Two values share one reciprocal (1/(ab) times b
-// and a), which takes the special-function work from 2 to 1.5 operations a
-// value; the exponent is clamped at 2^62 so that the product stays finite.
-__device__ __forceinline__ void silu8(F2 (&z)[4]) {
-    constexpr float kLog2e = 1.4426950408889634f;
-    const F2 m = f2(-kLog2e, -kLog2e), one = f2(1.f, 1.f);
-    F2 a[4];
+template <typename T>
+__device__ __forceinline__ void unpack(const Piece& r, F2 (&f)[kPairs]) {
+    const float2 a = Elem<T>::unpack(r.x), b = Elem<T>::unpack(r.y);
+    f[0] = f2(a.x, a.y);
+    f[1] = f2(b.x, b.y);
+}
+template <typename T>
+__device__ __forceinline__ Piece pack(const F2 (&f)[kPairs]) {
+    const float2 a = f2_parts(f[0]), b = f2_parts(f[1]);
+    return make_uint2(Elem<T>::pack(a.x, a.y), Elem<T>::pack(b.x, b.y));
+}
+__device__ __forceinline__ Piece load(const void* p) { return __ldg(static_cast<const Piece*>(p)); }
+__device__ __forceinline__ void copy_async(Piece* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// z sigmoid(z) of 4 values from u = z log2 e (the weights carry the factor):
+// u / (log2 e + log2 e 2^-u); far below zero the denominator is infinite and the
+// quotient 0.
+__device__ __forceinline__ void silu(F2 (&u)[kPairs]) {
+    const F2 l = f2(kLog2e, kLog2e);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = f2_parts(f2_mul(z[i], m));
-        a[i] = f2_add(f2(ex2_approx(fminf(u.x, 62.f)), ex2_approx(fminf(u.y, 62.f))), one);
+    for (int i = 0; i < kPairs; ++i) {
+        const float2 v = f2_parts(u[i]);
+        const float2 a = f2_parts(f2_fma(f2(ex2_approx(-v.x), ex2_approx(-v.y)), l, l));
+        u[i] = f2_mul(u[i], f2(rcp_approx(a.x), rcp_approx(a.y)));
     }
+}
+
+// The sums of a[0..3] over the warp's 32 lanes, each to every lane as
+// 1 / sqrt(sum + eps): two halving steps leave lane l with a quarter of the sum of
+// value (l >> 3), so that one reduction and one root serve all four.
+__device__ __forceinline__ void inverse_norms(float (&a)[4], float eps, int lane) {
+    const bool h = lane & 16, q = lane & 8;
+    const float b0 = (h ? a[2] : a[0]) + __shfl_xor_sync(0xffffffffu, h ? a[0] : a[2], 16);
+    const float b1 = (h ? a[3] : a[1]) + __shfl_xor_sync(0xffffffffu, h ? a[1] : a[3], 16);
+    float s = (q ? b1 : b0) + __shfl_xor_sync(0xffffffffu, q ? b0 : b1, 8);
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        const float2 ab = f2_parts(f2_mul(a[i], a[i + 1]));
-        const F2 r = f2(rcp_approx(ab.x), rcp_approx(ab.y));
-        z[i] = f2_mul(z[i], f2_mul(r, a[i + 1]));
-        z[i + 1] = f2_mul(z[i + 1], f2_mul(r, a[i]));
-    }
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float r = rsqrt_approx(s + eps);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = __shfl_sync(0xffffffffu, r, 8 * k);
 }
 
 // A thread's channels: its weights by tap, bias, and the step from inputs to outputs.
 template <typename T, int W, bool kWF32>
 struct Channels {
-    F2 w[W][4], bias[4];
-    bool warp_norm, lane_norm;
+    F2 w[W][kPairs], bias[kPairs];
+    bool warp_norm;   // a warp is a head
 
     __device__ __forceinline__ Channels(const ConvParams& p, int c0, int cc) {
-        warp_norm = c0 - (int)(threadIdx.x & 31) * kConvVec < p.norm_c;
-        lane_norm = c0 < p.norm_c;
-        float f[8 * W];
+        warp_norm = c0 < p.norm_c;
+        const float factor = p.silu ? kLog2e : 1.f;   // see silu
+        float f[kConvVec * W];
         if (kWF32) {
             const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + (int64_t)cc * W);
 #pragma unroll
-            for (int i = 0; i < 2 * W; ++i) {
+            for (int i = 0; i < W; ++i) {
                 const float4 v = __ldg(src + i);
                 f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
             }
         } else {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.w) + (int64_t)cc * W);
+            const uint2* src = reinterpret_cast<const uint2*>(static_cast<const T*>(p.w) + (int64_t)cc * W);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const uint4 v = __ldg(src + i);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x = Elem<T>::unpack(u[k]);
-                    f[8 * i + 2 * k] = x.x;
-                    f[8 * i + 2 * k + 1] = x.y;
-                }
+                const uint2 v = __ldg(src + i);
+                const float2 x = Elem<T>::unpack(v.x), y = Elem<T>::unpack(v.y);
+                f[4 * i] = x.x; f[4 * i + 1] = x.y; f[4 * i + 2] = y.x; f[4 * i + 3] = y.y;
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kPairs; ++i) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = f2(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+            for (int j = 0; j < W; ++j) w[j][i] = f2(f[2 * i * W + j] * factor, f[(2 * i + 1) * W + j] * factor);
             bias[i] = f2(0.f, 0.f);
         }
         if (p.bias) {
-            const float4 b0 = __ldg(reinterpret_cast<const float4*>(p.bias + cc)),
-                         b1 = __ldg(reinterpret_cast<const float4*>(p.bias + cc + 4));
-            bias[0] = f2(b0.x, b0.y); bias[1] = f2(b0.z, b0.w);
-            bias[2] = f2(b1.x, b1.y); bias[3] = f2(b1.z, b1.w);
+            const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + cc));
+            bias[0] = f2(b.x * factor, b.y * factor);
+            bias[1] = f2(b.z * factor, b.w * factor);
         }
     }
-    // One output row from the window (oldest first) and the current input.
-    __device__ __forceinline__ uint4 row(const ConvParams& p, const F2 (&win)[W - 1][4], const F2 (&x)[4]) const {
-        F2 y[4];
+    // The activation of one token from the window (oldest first) and the current input.
+    __device__ __forceinline__ void taps(const ConvParams& p, const F2 (&win)[W - 1][kPairs], const F2 (&x)[kPairs],
+                                         F2 (&y)[kPairs]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kPairs; ++i) {
             y[i] = f2_fma(w[W - 1][i], x[i], bias[i]);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) y[i] = f2_fma(w[j][i], win[j][i], y[i]);
         }
-        if (p.silu) silu8(y);
+        if (p.silu) silu(y);
+    }
+    static __device__ __forceinline__ float squares(const F2 (&y)[kPairs]) {
+        const float2 s = f2_parts(f2_fma(y[1], y[1], f2_mul(y[0], y[0])));
+        return s.x + s.y;
+    }
+    static __device__ __forceinline__ void scale(F2 (&y)[kPairs], float r) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) y[i] = f2_mul(y[i], f2(r, r));
+    }
+    // One output row.
+    __device__ __forceinline__ Piece row(const ConvParams& p, const F2 (&win)[W - 1][kPairs], const F2 (&x)[kPairs]) const {
+        F2 y[kPairs];
+        taps(p, win, x, y);
         if (warp_norm) {
-            F2 s2 = f2_mul(y[0], y[0]);
+            float ss = squares(y);
 #pragma unroll
-            for (int i = 1; i < 4; ++i) s2 = f2_fma(y[i], y[i], s2);
-            const float2 s = f2_parts(s2);
-            float ss = s.x + s.y;
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = lane_norm ? rsqrt_approx(ss + p.eps) : 1.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = f2_mul(y[i], f2(r, r));
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            scale(y, rsqrt_approx(ss + p.eps));
         }
-        return pack8<T>(y);
+        return pack<T>(y);
     }
 };
 
+template <typename T, int W>
+__device__ __forceinline__ void shift(F2 (&win)[W - 1][kPairs], const F2 (&x)[kPairs]) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+#pragma unroll
+        for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
+        win[W - 2][i] = x[i];
+    }
+}
+
 template <typename T, int W, bool kWF32>
-__global__ void __launch_bounds__(kConvThreads, 5) short_conv_kernel(const ConvParams p) {
-    __shared__ uint4 ring[kRing][kConvThreads];
-    const int tid = threadIdx.x, c0 = (blockIdx.y * kConvThreads + tid) * kConvVec;
+__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvParams p) {
+    __shared__ Piece ring[kRing][kConvThreads];
+    const int cb = blockIdx.x % p.cblocks, tile = blockIdx.x / p.cblocks;
+    const int tid = threadIdx.x, c0 = (cb * kConvThreads + tid) * kConvVec;
     if (c0 - (tid & 31) * kConvVec >= p.C) return;  // the whole warp is past the channels
     const bool act = c0 < p.C;
     const int cc = act ? c0 : 0;
     const Channels<T, W, kWF32> ch(p, c0, cc);
 
     const int total = (int)p.total;
-    const int t0 = (int)blockIdx.x * p.tile, t1 = min(t0 + p.tile, total);
+    const int t0 = tile * p.tile, t1 = min(t0 + p.tile, total);
     const bool last = t1 == total;
     auto start = [&](int n) -> int { return p.cu ? p.cu[n] : n * p.T; };
     auto report = [&]() {
         if (p.status && tid == 0) atomicExch(p.status, 1);
     };
-    if (p.cu && blockIdx.x == 0 && (p.cu[0] != 0 || p.cu[p.N] != total)) report();
+    if (p.cu && tile == 0 && (p.cu[0] != 0 || p.cu[p.N] != total)) report();
 
     // first sequence that starts at or after t0, or the one that runs into it
     int n;
@@ -176,34 +221,34 @@ __global__ void __launch_bounds__(kConvThreads, 5) short_conv_kernel(const ConvP
         const int64_t step = p.xs[1];
         const T* xf = xb + tb * step;                 // next token to ask for
         int left = te - tb;                           // tokens not yet asked for
-        auto fetch = [&](uint4* rows) {               // kStep tokens into their rows of the ring
+        auto fetch = [&](Piece* rows) {               // kStep tokens into their rows of the ring
             if (left >= kStep) {
 #pragma unroll
                 for (int u = 0; u < kStep; ++u) {
-                    cp_async16(rows + u * kConvThreads, xf);
+                    copy_async(rows + u * kConvThreads, xf);
                     xf += step;
                 }
             } else {
 #pragma unroll
                 for (int u = 0; u < kStep - 1; ++u) {
-                    if (u < left) cp_async16(rows + u * kConvThreads, xf);
+                    if (u < left) copy_async(rows + u * kConvThreads, xf);
                     xf += step;
                 }
             }
             left -= kStep;
             cp_async_commit();
         };
-        uint4* const mine = &ring[0][tid];
+        Piece* const mine = &ring[0][tid];
         constexpr int kGroup = kStep * kConvThreads;  // pieces of a copy group
 #pragma unroll
         for (int g = 0; g < kRing / kStep - 1; ++g) fetch(mine + g * kGroup);
-        F2 win[W - 1][4];
+        F2 win[W - 1][kPairs];
         if (owner) {
-            uint4 old[W - 1];
+            Piece old[W - 1];
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) old[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < W - 1; ++i) old[i] = make_uint2(0, 0);
             if (p.pool) {
-                uint4* pool = reinterpret_cast<uint4*>(static_cast<T*>(p.pool) + (int64_t)slot * (W - 1) * p.C + cc);
+                Piece* pool = reinterpret_cast<Piece*>(static_cast<T*>(p.pool) + (int64_t)slot * (W - 1) * p.C + cc);
                 const int64_t row = p.C / kConvVec;
                 if (!p.has_state || p.has_state[n] != 0) {
 #pragma unroll
@@ -212,9 +257,9 @@ __global__ void __launch_bounds__(kConvThreads, 5) short_conv_kernel(const ConvP
                 // inputs a .. a + W - 2 of [old state, tokens]
 #pragma unroll
                 for (int i = 0; i < W - 1; ++i) {
-                    uint4 r;
+                    Piece r;
                     if (a + i >= W - 1) {
-                        r = ldg16(xb + (int64_t)(a + i - (W - 1)) * p.xs[1]);
+                        r = load(xb + (int64_t)(a + i - (W - 1)) * p.xs[1]);
                     } else {
                         r = old[i];
 #pragma unroll
@@ -225,40 +270,53 @@ __global__ void __launch_bounds__(kConvThreads, 5) short_conv_kernel(const ConvP
                 }
             }
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) unpack8<T>(old[i], win[i]);
+            for (int i = 0; i < W - 1; ++i) unpack<T>(old[i], win[i]);
         } else if (tb < te) {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) unpack8<T>(ldg16(xb + (int64_t)(tb - (W - 1) + i) * p.xs[1]), win[i]);
+            for (int i = 0; i < W - 1; ++i) unpack<T>(load(xb + (int64_t)(tb - (W - 1) + i) * p.xs[1]), win[i]);
         }
         T* o = static_cast<T*>(p.out) + (p.cu ? (int64_t)s * p.os[1] : (int64_t)n * p.os[0]) + tb * p.os[1] + cc;
-        auto token = [&](const uint4* piece) {
-            F2 x[4];
-            unpack8<T>(*piece, x);
-            const uint4 y = ch.row(p, win, x);
-            if (act) *reinterpret_cast<uint4*>(o) = y;
-            o += p.os[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
-                win[W - 2][i] = x[i];
-            }
-        };
+        const int64_t ostep = p.os[1];
         int g = 0;
         int t = tb;
         for (; t + kStep <= te; t += kStep) {
             cp_async_wait<kRing / kStep - 2>();
             // the group that comes in goes to the rows that the last round emptied
             fetch(mine + ((g + kRing / kStep - 1) % (kRing / kStep)) * kGroup);
-            const uint4* rows = mine + g * kGroup;
+            const Piece* rows = mine + g * kGroup;
             g = (g + 1) % (kRing / kStep);
+            F2 y[kStep][kPairs];
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) token(rows + u * kConvThreads);
+            for (int u = 0; u < kStep; ++u) {
+                F2 x[kPairs];
+                unpack<T>(rows[u * kConvThreads], x);
+                ch.taps(p, win, x, y[u]);
+                shift<T, W>(win, x);
+            }
+            if (ch.warp_norm) {
+                float ss[kStep];
+#pragma unroll
+                for (int u = 0; u < kStep; ++u) ss[u] = ch.squares(y[u]);
+                inverse_norms(ss, p.eps, tid & 31);
+#pragma unroll
+                for (int u = 0; u < kStep; ++u) ch.scale(y[u], ss[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                if (act) *reinterpret_cast<Piece*>(o) = pack<T>(y[u]);
+                o += ostep;
+            }
         }
         if (t < te) {
             cp_async_wait<0>();
-            const uint4* rows = mine + g * kGroup;
-            for (int u = 0; t + u < te; ++u) token(rows + u * kConvThreads);
+            const Piece* rows = mine + g * kGroup;
+            for (; t < te; ++t, rows += kConvThreads, o += ostep) {
+                F2 x[kPairs];
+                unpack<T>(*rows, x);
+                const Piece y = ch.row(p, win, x);
+                if (act) *reinterpret_cast<Piece*>(o) = y;
+                shift<T, W>(win, x);
+            }
         }
         cp_async_wait<0>();   // groups past the end hold nothing, but the next sequence counts anew
     }
@@ -274,8 +332,8 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_token_kernel(const Co
     const bool act = c0 < p.C;
     const int cc = act ? c0 : 0;
     const int64_t row = p.C / kConvVec;
-    uint4 raw[kTokenSeqs][W];
-    uint4* pool[kTokenSeqs];
+    Piece raw[kTokenSeqs][W];
+    Piece* pool[kTokenSeqs];
     int a[kTokenSeqs];
     bool ok[kTokenSeqs];
 #pragma unroll
@@ -293,10 +351,10 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_token_kernel(const Co
             continue;
         }
         const bool keep = p.pool && (!p.has_state || p.has_state[n] != 0);
-        if (p.pool) pool[u] = reinterpret_cast<uint4*>(static_cast<T*>(p.pool) + (int64_t)slot * (W - 1) * p.C + cc);
-        raw[u][W - 1] = ldg16(static_cast<const T*>(p.x) + (int64_t)n * p.xs[0] + cc);
+        if (p.pool) pool[u] = reinterpret_cast<Piece*>(static_cast<T*>(p.pool) + (int64_t)slot * (W - 1) * p.C + cc);
+        raw[u][W - 1] = load(static_cast<const T*>(p.x) + (int64_t)n * p.xs[0] + cc);
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) raw[u][i] = keep ? pool[u][i * row] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < W - 1; ++i) raw[u][i] = keep ? pool[u][i * row] : make_uint2(0, 0);
     }
     const Channels<T, W, kWF32> ch(p, c0, cc);
 #pragma unroll
@@ -307,13 +365,13 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_token_kernel(const Co
             for (int i = 0; i < W - 1; ++i) pool[u][i * row] = a[u] ? raw[u][i + 1] : raw[u][i];
         }
         if (!p.out) continue;
-        F2 win[W - 1][4], x[4];
+        F2 win[W - 1][kPairs], x[kPairs];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) unpack8<T>(raw[u][i], win[i]);
-        unpack8<T>(raw[u][W - 1], x);
-        const uint4 y = ch.row(p, win, x);
+        for (int i = 0; i < W - 1; ++i) unpack<T>(raw[u][i], win[i]);
+        unpack<T>(raw[u][W - 1], x);
+        const Piece y = ch.row(p, win, x);
         const int64_t n = blockIdx.x * kTokenSeqs + u;
-        if (act) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + n * p.os[0] + cc) = y;
+        if (act) *reinterpret_cast<Piece*>(static_cast<T*>(p.out) + n * p.os[0] + cc) = y;
     }
 }
 
@@ -325,12 +383,23 @@ cudaError_t launch_conv_t(ConvParams& p, int num_sms, cudaStream_t s) {
         short_conv_token_kernel<T, W, kWF32><<<grid, kConvThreads, 0, s>>>(p);
         return cudaGetLastError();
     }
-    // The longest tile (at most 64 tokens) that still gives every SM eight CTAs.
-    int tile = 64;
-    while (tile > 1 && (p.total + tile - 1) / tile * cblocks < 8LL * num_sms) tile >>= 1;
-    p.tile = tile;
+    // Tiles of about 64 tokens (the W - 1 inputs before a tile are read twice), cut so
+    // that the CTAs fill a whole number of the GPU's waves, where there is work for one.
+    int per_sm = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, short_conv_kernel<T, W, kWF32>, kConvThreads, 0);
+    if (e != cudaSuccess) return e;
+    const int64_t wave = (int64_t)num_sms * per_sm / cblocks;   // tiles a wave
+    int64_t tile = 1;
+    if (wave > 0) {
+        const int64_t waves = (p.total + 64 * wave - 1) / (64 * wave);
+        tile = waves > 0 ? (p.total + waves * wave - 1) / (waves * wave) : 1;
+    } else if (p.total > 0) {
+        tile = p.total < 64 ? p.total : 64;
+    }
+    p.tile = (int)tile;
     const int64_t tiles = p.total > 0 ? (p.total + tile - 1) / tile : 1;
-    short_conv_kernel<T, W, kWF32><<<dim3((unsigned)tiles, cblocks), kConvThreads, 0, s>>>(p);
+    p.cblocks = (int)cblocks;
+    short_conv_kernel<T, W, kWF32><<<(unsigned)(tiles * cblocks), kConvThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 template <typename T, int W>

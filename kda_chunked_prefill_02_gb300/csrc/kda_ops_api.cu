@@ -74,7 +74,7 @@ kda_status kda_short_conv(const kda_short_conv_args* a, void* stream) {
         a->norm_channels > a->channels || a->pool_size < 0 || !(a->norm_eps >= 0.f))
         return KDA_ERR_INVALID_ARG;
     if (a->width < 2 || a->width > 4 || a->channels % 8 || a->norm_channels % kHeadDim || !elem_type(a->dtype) ||
-        (a->weight_dtype != a->dtype && a->weight_dtype != KDA_DTYPE_F32) || a->channels > (1 << 26) ||
+        (a->weight_dtype != a->dtype && a->weight_dtype != KDA_DTYPE_F32) || a->channels > (1 << 24) ||
         a->num_seqs > (1 << 30) || a->pool_size > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
     if (a->num_seqs == 0) return a->cu_seqlens && a->seqlen > 0 ? KDA_ERR_INVALID_ARG : KDA_OK;

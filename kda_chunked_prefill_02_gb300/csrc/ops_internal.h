@@ -26,7 +26,7 @@ struct ConvParams {
     int64_t total;            // tokens in all
     int C, norm_c, P;
     int silu;
-    int tile;                 // tokens a tile (set by the launcher)
+    int tile, cblocks;        // tokens a tile, blocks of channels (set by the launcher)
     float eps;
 };
 cudaError_t launch_short_conv(const ConvParams& p, int width, bool f16, bool w_f32, int num_sms, cudaStream_t s);
