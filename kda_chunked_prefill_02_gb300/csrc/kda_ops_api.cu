@@ -61,7 +61,8 @@ TreePlan plan_of(const kda_tree_attention_args* a, int64_t max_len) {
 }
 
 size_t tree_workspace(const kda_tree_attention_args* a, const TreePlan& plan) {
-    return plan.parts * sizeof(int4) + plan.part_rows * ((size_t)a->head_dim + 1) * sizeof(float);
+    return plan.parts * sizeof(int4) + plan.part_rows * ((size_t)a->head_dim + 1) * sizeof(float) +
+           plan.order * sizeof(int32_t);
 }
 
 }  // namespace
@@ -188,6 +189,7 @@ kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
     p.parts = static_cast<int4*>(a->workspace);
     p.part_o = reinterpret_cast<float*>(p.parts + plan.parts);
     p.part_lse = p.part_o + plan.part_rows * a->head_dim;
+    p.order = plan.order ? reinterpret_cast<int32_t*>(p.part_lse + plan.part_rows) : nullptr;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     return status_of(launch_tree_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
                                            static_cast<cudaStream_t>(stream)));

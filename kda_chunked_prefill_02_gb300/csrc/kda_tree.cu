@@ -26,6 +26,10 @@
 // splits of `chunk` tokens, one cluster each; the splits leave normalised rows and
 // their log-sum in the workspace, joined in a fixed order by tree_join_kernel.
 //
+// Where one CTA an item is more than the GPU runs at once, the requests go longest
+// first (tree_order_kernel ranks them, as the chunk table ranks prefill's
+// sequences), so that the last CTAs are short ones.
+//
 // Keys that a row does not see are taken out of the scores by a select, and
 // rows of V past the end are zero-filled in shared memory.  V of a drafted
 // token is seen by some rows only, and 0 * NaN is NaN: a tile that holds
@@ -40,6 +44,7 @@ namespace {
 constexpr int kTreeThreads = 128;
 constexpr int kTile = 64;      // tokens a tile, 16 a warp
 constexpr int kStages = 3;
+constexpr int kOrderMax = 1024;   // requests that are ranked
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -117,7 +122,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int cluster = kCluster ? p.cluster : 1, rank = kCluster ? blockIdx.x % cluster : 0, bx = blockIdx.x / cluster;
     const int split = bx / p.row_blocks, rb = bx - split * p.row_blocks;
-    const int kvh = blockIdx.y, r = blockIdx.z, row0 = rb * kRows;
+    if (p.order) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int kvh = blockIdx.y, r = p.order ? p.order[blockIdx.z] : blockIdx.z, row0 = rb * kRows;
     int ctx, n;
     if (!tree_lengths(p, r, ctx, n) && p.status && tid == 0) atomicExch(p.status, 1);
     const int len = ctx + n;
@@ -436,6 +442,22 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
     if (kCluster) cluster_sync();   // the others have read this CTA's rows
 }
 
+// order[k]: the request of rank k by descending length (ties by index).
+__global__ void __launch_bounds__(1024) tree_order_kernel(const TreeParams p) {
+    __shared__ int len[kOrderMax];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid's end themselves
+    const int r = threadIdx.x;
+    int ctx = 0, n = 0;
+    if (r < p.R) tree_lengths(p, r, ctx, n);
+    const int mine = ctx + n;
+    len[r] = mine;
+    __syncthreads();
+    if (r >= p.R) return;
+    int rank = 0;
+    for (int i = 0; i < p.R; ++i) rank += len[i] > mine || (len[i] == mine && i < r);
+    p.order[rank] = r;
+}
+
 // Joins the splits of a row: out = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M).
 // One warp a row, in a fixed order of the splits.
 template <typename T, int D>
@@ -490,21 +512,31 @@ cudaError_t launch_rows_c(const TreeParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    if (kCluster) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)p.cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // right after tree_order_kernel
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.gridDim = dim3((unsigned)(p.splits * p.row_blocks * p.cluster), (unsigned)p.Hk, (unsigned)p.R);
     cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = kCluster ? 1 : 0;
+    cfg.numAttrs = kCluster || p.order ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 template <typename T, int D, int MT>
 cudaError_t launch_rows_t(const TreeParams& q, cudaStream_t s) {
     TreeParams p = q;
     p.row_blocks = (p.rows + 16 * MT - 1) / (16 * MT);
+    if (p.order) {
+        tree_order_kernel<<<1, kOrderMax, 0, s>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     return p.cluster > 1 ? launch_rows_c<T, D, MT, true>(p, s) : launch_rows_c<T, D, MT, false>(p, s);
 }
 
@@ -558,6 +590,9 @@ TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, fl
     splits = (max_len + chunk - 1) / chunk;
     t.chunk = (int)chunk;
     t.splits = (int)(splits > 0 ? splits : 1);
+    // Ranked where the items outnumber the CTAs that run at once: 256 requests x 8 key heads
+    // of 0.2 to 1 times 4096 tokens 406 us against 437.
+    t.order = !t.mma && t.splits == 1 && t.cluster == 1 && R > 1 && R <= kOrderMax && items > 2LL * num_sms ? R : 0;
     t.grid = num_sms;
     t.parts = t.mma ? (size_t)2 * t.grid : 0;
     t.part_rows = t.splits > 1 ? (size_t)R * Hk * rows * t.splits : 0;

@@ -69,6 +69,7 @@ struct TreeParams {
     uint32_t page_magic, group_magic;   // floor(2^32 / page), floor(2^32 / G) (2^32 - 1 for 1)
     int chunk, splits;        // tokens a split; splits of the longest request
     int cluster;              // CTAs that share a split
+    int32_t* order;           // the requests, longest first; nullptr: in their order
     int row_blocks;           // set by the launcher
     int k_paged, v_paged;     // mma: the head is part of the map's page coordinate
     int r0, count, slots;     // mma: the requests of a launch, 2 x its CTAs (set by the launcher)
@@ -81,7 +82,8 @@ struct TreePlan {
     int cluster;         // and CTAs that share a split
     int grid;            // mma: CTAs
     size_t part_rows;    // partial rows in the workspace (D values and a log-sum each)
-    size_t parts;        // int4 behind them, for what they belong to
+    size_t parts;        // int4, for what they belong to
+    size_t order;        // int32, for the requests' order
 };
 TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms);
 cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s);

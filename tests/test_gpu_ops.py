@@ -372,12 +372,14 @@ def test_tree_node_counts(N, form, room):
     _tree_case(N, [77, 5], N, 2, 1, 64, 32, F16, form=form, room=room)
 
 
-def test_tree_many_requests():
+@pytest.mark.parametrize("N,room", [(9, 2048), (1, 0), (3, 0)])
+def test_tree_many_requests(N, room):
     """More requests than one launch of the kernel for many rows takes (256), most of
-    them short, some empty, some long enough to be cut."""
+    them short, some empty, some long enough to be cut; for few rows, more of them than
+    the GPU runs at once, longest first."""
     ctx = [(i * 37) % 90 if i % 50 else 700 + i for i in range(300)]
-    nodes = _i32([(i * 7) % 10 for i in range(300)])
-    _tree_case(50, ctx, 9, 4, 2, 64, 16, BF16, nodes=nodes, room=2048)
+    nodes = _i32([(i * 7) % (N + 1) for i in range(300)])
+    _tree_case(50, ctx, N, 4, 2, 64, 16, BF16, nodes=nodes, room=room)
 
 
 @pytest.mark.parametrize("G,room", [(2, 0), (12, ROOM)])
