@@ -502,15 +502,30 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 // the query rows as K-major operands in the 128-byte swizzle, D / 8 lanes a
                 // row; all of them are on their way at once
                 constexpr int kPieces = D / 8, kRowsPass = 256 / kPieces, kPasses = 256 / kRowsPass;
-                const int piece = tid % kPieces;
-                const T* src = static_cast<const T*>(p.q) + r * p.qs[0] + kvh * p.G * p.qs[2] + piece * 8;
-#pragma unroll 2
-                for (int k = 0; k < (two ? kPasses : kPasses / 2); ++k) {
-                    const int in = k * kRowsPass + tid / kPieces, q = row0 + in;   // row of the pair of tiles, of the call
-                    const int i = (int)page_div((uint32_t)q, p.G, p.group_magic);
-                    uint8_t* dst = sm + (in >> 7) * kTileBytes + (piece >> 3) * kBlock + sw128_off(in & 127, (piece & 7) * 8);
-                    if (q < p.rows) cp_async16(dst, src + i * p.qs[1] + (q - i * p.G) * p.qs[2]);
-                    else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+                const int piece = tid % kPieces, in0 = tid / kPieces;
+                // node and head of the thread's rows, kRowsPass rows on each time
+                const int di = (int)page_div(kRowsPass, p.G, p.group_magic), dg = kRowsPass - di * p.G;
+                const int64_t step = di * p.qs[1] + dg * p.qs[2], wrap = p.qs[1] - p.G * p.qs[2];
+                const int i0 = (int)page_div((uint32_t)(row0 + in0), p.G, p.group_magic);
+                int left = p.rows - row0 - in0, g = row0 + in0 - i0 * p.G;
+                const T* src = static_cast<const T*>(p.q) + r * p.qs[0] + i0 * p.qs[1] + (kvh * p.G + g) * p.qs[2] +
+                               piece * 8;
+                uint8_t* const dst = sm + (piece >> 3) * kBlock;
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) {
+                    const int in = k * kRowsPass + in0;   // row of the pair of tiles
+                    if (k < kPasses / 2 || two) {
+                        uint8_t* at = dst + (k * kRowsPass >> 7) * kTileBytes + sw128_off(in & 127, (piece & 7) * 8);
+                        if (left > 0) cp_async16(at, src);
+                        else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+                    }
+                    left -= kRowsPass;
+                    g += dg;
+                    src += step;
+                    if (g >= p.G) {
+                        g -= p.G;
+                        src += wrap;
+                    }
                 }
                 cp_async_commit();
             }
