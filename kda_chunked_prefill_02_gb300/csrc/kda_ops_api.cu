@@ -185,7 +185,7 @@ kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
     auto magic = [](int d) { return d == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)d); };
     p.page_magic = magic(p.page);
     p.group_magic = magic(p.G);
-    p.chunk = plan.chunk; p.splits = plan.splits; p.cluster = plan.cluster;
+    p.cluster = plan.cluster;
     p.parts = static_cast<int4*>(a->workspace);
     p.part_o = reinterpret_cast<float*>(p.parts + plan.parts);
     p.part_lse = p.part_o + plan.part_rows * a->head_dim;

@@ -24,7 +24,7 @@
 // contexts leave no SM idle.  A stretch cuts at most two items; the parts of a
 // cut item leave normalised rows and their log-sum in the workspace (slot 0 of
 // a CTA: a later part of an item, slot 1: the first), joined in the CTAs' order
-// by tree_mma_join_kernel.  The loader and the issuer run from
+// by tree_join_kernel (kda_tree.cu).  The loader and the issuer run from
 // one item into the next without a halt; only the rows' way out and the next
 // queries' way in are between two items.
 //
@@ -104,6 +104,10 @@ template <> struct MmaTypes<__half> {
     static __host__ __device__ constexpr uint32_t qk(uint32_t n) { return idesc_f16_f32(128, n); }
     static __host__ __device__ constexpr uint32_t pv(uint32_t n) { return idesc_f16_f32_bmn(128, n); }
 };
+
+// Rows a copy brings: the largest power of two that divides the page, a tile's at most,
+// so that no copy goes past a tile's or a page's end.
+__host__ __device__ constexpr int box_of(int page) { return page % kKeys == 0 ? kKeys : page & -page; }
 
 // One CTA's part of an item (request, key head, pair of row tiles).
 struct Item {
@@ -212,8 +216,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 tma_prefetch_desc(&kmap);
                 tma_prefetch_desc(&vmap);
             }
-            const int box = min(p.page, kKeys), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
-            const int shift = 31 - __clz(p.page);
+            const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
             int issued = 0, item = 0;   // tiles asked for, items begun
             uint32_t raw = 0, raw_phases = ~0u;   // slots whose last copy was a raw one, those copies' phases
             bool ok = true;
@@ -222,15 +225,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (lane == 0) mbar_arrive(&item_free[item % kItems]);
                 const int ctx = x.ctx, hi = ctx + x.n;
                 const int32_t* table = p.table + x.r * p.table_stride;
-                // this lane's page of a tile, -1: none (asked for a tile ahead, looked at later)
+                // this lane's page of a tile, -1: none (asked for a tile ahead, looked at
+                // later), and its first row there
+                int row_ahead = 0;
                 auto page_of = [&](int tile) -> int64_t {
                     const int tok = tile * kKeys + lane * box;
-                    return tile < x.t1 && lane < per_tile && tok < hi ? (int64_t)(uint32_t)table[tok >> shift] : -1;
+                    const int at = (int)page_div((uint32_t)tok, p.page, p.page_magic);
+                    row_ahead = tok - at * p.page;
+                    return tile < x.t1 && lane < per_tile && tok < hi ? (int64_t)(uint32_t)table[at] : -1;
                 };
                 int64_t ahead = page_of(x.t0);
                 for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
                     const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
                     if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
+                    const int row = row_ahead;
                     ahead = page_of(tile + 1);
                     const int base = tile * kKeys;
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * D * 2u;
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         if (id >= 0)
                             tma_load_5d(dst + lane * box * D * 2, v ? &vmap : &kmap, 0, 0,
                                         (v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64),
-                                        ((base + lane * box) & (p.page - 1)) / 8,
+                                        row / 8,
                                         (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
                         ++issued;
                     }
@@ -369,8 +377,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 const bool odd = (p.rows - 1) % 256 < 128;   // the last pair has one row tile
                 const int head_cost = pairs * kCostTwo - (odd ? kCostTwo - kCostOne : 0);   // of a key tile
                 const int64_t tile_cost = (int64_t)head_cost * p.Hk, total = at * tile_cost;
-                // at least two key tiles a CTA
-                const int64_t most = total / (2 * kCostTwo);
+                // at least a key tile a CTA
+                const int64_t most = total / kCostTwo;
                 const int ctas = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
                 int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
                 int k = 0;
@@ -538,23 +546,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_ready);
 
-            // 32 drafted nodes' visibility to this row, from node 32 w on
-            const uint32_t* mask =
-                p.mask ? reinterpret_cast<const uint32_t*>(p.mask + ((int64_t)r * p.N + node) * p.words) : nullptr;
-            auto node_bits = [&](int w) -> uint32_t {
-                if (w >= 2 * p.words) return 0u;
-                if (mask) return mask[w];
-                const int d = node - 32 * w;
-                return d >= 31 ? 0xffffffffu : d < 0 ? 0u : (2u << d) - 1u;
-            };
-            // visibility of positions tok .. tok + 31
-            auto seen = [&](int tok) -> uint32_t {
-                const int rel = tok - ctx, left = hi - tok;
-                uint32_t b = 0xffffffffu;
-                if (rel >= 0) b = __funnelshift_r(node_bits(rel >> 5), node_bits((rel >> 5) + 1), rel & 31);
-                else if (rel > -32) b = (node_bits(0) << -rel) | ((1u << -rel) - 1u);
-                return left >= 32 ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
-            };
+            // visibility of positions tok .. tok + 31 to this row
+            const uint32_t* mask = tree_mask_row(p, r, node);
+            auto seen = [&](int tok) -> uint32_t { return tree_seen(p, mask, node, ctx, hi, tok); };
 
             const int tile0 = x.t0, ctx_in = x.ctx;
             float m = -INFINITY, l = 0.f;
@@ -764,66 +758,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
 }
 
-// Joins the parts of a cut item: out = sum_c 2^(lse_c - M) o_c / sum_c 2^(lse_c - M)
-// over the CTAs c that hold one, in their order: slot 1 of CTA blockIdx.x, then
-// slot 0 of those behind it up to the item's last part.  One warp a row.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) tree_mma_join_kernel(const TreeParams p) {
-    constexpr int kVec = D / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, in = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int4 item = p.parts[2 * blockIdx.x + 1];   // state, request, key head, pair of row tiles
-    const int row = item.w * 256 + in;
-    if (item.x == 0 || row >= p.rows) return;
-    float mx = -INFINITY, sum = 0.f, y[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) y[i] = 0.f;
-    int slot = 2 * blockIdx.x + 1;
-    for (int state = item.x;;) {
-        const int64_t part = (int64_t)slot * 256 + in;
-        const float lse = p.part_lse[part];
-        const float* src = p.part_o + part * D + lane * kVec;
-        float o[kVec];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) o[i] = src[i];
-        const float mn = fmaxf(mx, lse), mu = mn == -INFINITY ? 0.f : mn;
-        const float fo = ex2_approx(mx - mu), fn = ex2_approx(lse - mu);
-        sum = sum * fo + fn;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) y[i] = y[i] * fo + o[i] * fn;
-        mx = mn;
-        if (state == 2) break;
-        slot = (slot + 2) & ~1;
-        if (slot >= p.slots) break;
-        state = p.parts[slot].x;
-        if (state == 0) break;
-    }
-    const int r = item.y, i = (int)page_div((uint32_t)row, p.G, p.group_magic), h = item.z * p.G + (row - i * p.G);
-    const bool empty = sum == 0.f;
-    const float inv = empty ? 0.f : 1.f / sum;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + r * p.os[0] + i * p.os[1] + h * p.os[2] +
-                                                lane * kVec);
-#pragma unroll
-    for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[((int64_t)r * p.N + i) * p.Hq + h] = empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
-}
-
 template <typename T, int D>
 cudaError_t launch_mma_t(const TreeParams& q, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
     static std::atomic<uint64_t> smem_set;
     cudaError_t e = set_smem_limit_once((const void*)tree_mma_kernel<T, D>, (int)MmaShape<D>::kSmem, smem_set);
-    const int rows = q.rows < 256 ? q.rows : 256;
     for (int r0 = 0; r0 < q.R && e == cudaSuccess; r0 += kMmaSlice) {
         TreeParams p = q;
         p.r0 = r0;
         p.slots = 2 * grid;
+        p.slot_rows = 256;
         p.count = q.R - r0 < kMmaSlice ? q.R - r0 : kMmaSlice;
         tree_mma_kernel<T, D><<<grid, kMmaThreads, MmaShape<D>::kSmem, s>>>(p, kmap, vmap);
         e = cudaGetLastError();
-        if (e == cudaSuccess && grid > 1)
-            e = launch_maybe_pdl(tree_mma_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)((rows + 7) / 8)),
-                                 dim3(256), 0, s, true, p);
+        if (e == cudaSuccess) e = launch_tree_join(p, D, std::is_same<T, __half>::value, s);
     }
     return e;
 }
@@ -842,7 +789,7 @@ bool cache_map(CUtensorMap* map, const void* base, const int64_t (&st)[3], const
     const uint64_t dims[5] = {64, 8, (uint64_t)(rows ? p.Hk : 1) * (D / 64), (uint64_t)p.page / 8,
                               (uint64_t)p.P * (rows ? 1 : p.Hk)};
     const uint64_t strides[4] = {(uint64_t)st[1] * 2, 128, (uint64_t)st[1] * 16, (uint64_t)(rows ? st[0] : st[2]) * 2};
-    const uint32_t box[5] = {64, 8, (uint32_t)D / 64, (uint32_t)(p.page < kKeys ? p.page : kKeys) / 8, 1};
+    const uint32_t box[5] = {64, 8, (uint32_t)D / 64, (uint32_t)box_of(p.page) / 8, 1};
     if (dims[4] > INT32_MAX) return false;
     return make_tensor_map(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims,
                            strides, box, CU_TENSOR_MAP_SWIZZLE_128B);

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace kda {
 
 struct ConvParams {
@@ -59,27 +61,29 @@ struct TreeParams {
     const int32_t* nodes;
     const uint64_t* mask;
     int32_t* status;
-    float* part_o;            // partial rows: [R, Hk, splits, rows, D], or [2 CTAs, 256, D] (mma)
+    float* part_o;            // partial rows [2 CTAs, slot_rows, D] of items that are cut
     float* part_lse;          // their log-sums, base 2
-    int4* parts;              // mma: what the partial rows belong to, [2 CTAs]
+    int4* parts;              // what they belong to, [2 CTAs]: state (0 nothing, 1 a part, 2 an item's
+                              // last), request, key head, block of slot_rows rows
     int64_t qs[3], os[3], ks[3], vs[3], table_stride;
     int R, N, Hq, Hk, G, rows, words;   // rows = N * G, words of a mask row
     int P, page;
     int64_t max_len;          // longest context and nodes of a request (at most what its page row holds)
     uint32_t page_magic, group_magic;   // floor(2^32 / page), floor(2^32 / G) (2^32 - 1 for 1)
-    int chunk, splits;        // tokens a split; splits of the longest request
-    int cluster;              // CTAs that share a split
+    int cluster;              // rows kernel: CTAs that share an item
     int32_t* order;           // the requests, longest first; nullptr: in their order
-    int row_blocks;           // set by the launcher
+    int row_blocks, stages;   // set by the launcher
     int k_paged, v_paged;     // mma: the head is part of the map's page coordinate
-    int r0, count, slots;     // mma: the requests of a launch, 2 x its CTAs (set by the launcher)
+    int r0, count;            // mma: the requests of a launch (set by the launcher)
+    int slots, slot_rows;     // 2 x the CTAs over a line of items, rows of a slot (set by the launcher)
     float scale_log2;         // scale * log2(e)
 };
 // How a call is cut.
 struct TreePlan {
     bool mma;            // the kernel for many rows
-    int chunk, splits;   // rows kernel: tokens a split, splits of the longest request
-    int cluster;         // and CTAs that share a split
+    bool line;           // rows kernel: CTAs over equal stretches of the line of items
+    int row_grid;        // and their number
+    int cluster;         // rows kernel: CTAs that share an item
     int grid;            // mma: CTAs
     size_t part_rows;    // partial rows in the workspace (D values and a log-sum each)
     size_t parts;        // int4, for what they belong to
@@ -87,6 +91,7 @@ struct TreePlan {
 };
 TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, float scale, int num_sms);
 cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s);
+cudaError_t launch_tree_join(const TreeParams& p, int D, bool f16, cudaStream_t s);
 // The kernel for many rows; false if the caches' layout has no tensor map.
 bool launch_tree_mma(const TreeParams& p, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e);
 
@@ -105,6 +110,26 @@ __device__ __forceinline__ bool tree_lengths(const TreeParams& p, int r, int& ct
     const bool ok = ctx >= 0 && n >= 0 && n <= p.N && (int64_t)ctx + n <= p.max_len;
     if (!ok) ctx = n = 0;
     return ok;
+}
+
+// Which of the positions tok .. tok + 31 of a request with `ctx` cached tokens and
+// positions below `hi` its node sees, a bit each; mask: the node's words, nullptr: a chain.
+__device__ __forceinline__ const uint32_t* tree_mask_row(const TreeParams& p, int r, int node) {
+    return p.mask ? reinterpret_cast<const uint32_t*>(p.mask + ((int64_t)r * p.N + node) * p.words) : nullptr;
+}
+__device__ __forceinline__ uint32_t tree_seen(const TreeParams& p, const uint32_t* mask, int node, int ctx, int hi,
+                                              int tok) {
+    auto node_bits = [&](int w) -> uint32_t {   // drafted nodes 32 w ..
+        if (w >= 2 * p.words) return 0u;
+        if (mask) return mask[w];
+        const int d = node - 32 * w;
+        return d >= 31 ? 0xffffffffu : d < 0 ? 0u : (2u << d) - 1u;
+    };
+    const int rel = tok - ctx, left = hi - tok;
+    uint32_t b = 0xffffffffu;
+    if (rel >= 0) b = __funnelshift_r(node_bits(rel >> 5), node_bits((rel >> 5) + 1), rel & 31);
+    else if (rel > -32) b = (node_bits(0) << -rel) | ((1u << -rel) - 1u);
+    return left >= 32 ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
 }
 
 // ---------------------------------------------------------------- element types

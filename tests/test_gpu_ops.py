@@ -340,11 +340,38 @@ def test_tree_pages(page, heads_first, N, G, room):
     _tree_case(page, [130, 0, 900, 31], N, 2 * G, 2, 128, page, BF16, heads_first=heads_first, room=room)
 
 
-@pytest.mark.parametrize("page", [8, 16, 128, 512])
+@pytest.mark.parametrize("page", [8, 16, 24, 48, 128, 160, 512])
 @pytest.mark.parametrize("heads_first", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
 def test_tree_pages_of_the_kernel_for_many_rows(page, heads_first, D):
     _tree_case(page, [513, 2, 127, 300, 0], 20, 12, 3, D, page, F16, heads_first=heads_first, room=ROOM)
+
+
+@pytest.mark.parametrize("D,Hq,Hk,N", [(64, 4, 2, 3), (128, 8, 2, 1), (128, 12, 3, 8), (256, 16, 2, 1), (256, 2, 1, 20)])
+@pytest.mark.parametrize("page", [3, 24, 64])
+def test_tree_long_and_short_contexts_together(D, Hq, Hk, N, page):
+    """Equal stretches of work that meet many requests, and a request that meets many stretches."""
+    _tree_case(D + N, [6000, 0, 17, 2600, 1, 64, 3000, 127], N, Hq, Hk, D, page, BF16)
+
+
+def test_tree_one_context_over_every_multiprocessor():
+    _tree_case(5, [40000], 2, 4, 1, 128, 16, F16)
+
+
+def test_tree_one_token_pages_of_a_long_context():
+    """More pages in a stretch of work than are listed at a time."""
+    _tree_case(6, [60000, 30000], 1, 4, 4, 64, 1, BF16)
+
+
+def test_tree_many_requests_with_small_pages():
+    """A CTA each, with more pages than are listed at a time."""
+    _tree_case(7, [700 - 9 * i for i in range(40)], 1, 16, 8, 128, 2, BF16)
+
+
+@pytest.mark.parametrize("rows", [40, 160])
+def test_tree_few_items_in_many_parts(rows):
+    """The joins of few and of many rows over many parts."""
+    _tree_case(rows, [20000, 3], rows // 8, 8, 1, 128, 32, BF16)
 
 
 def test_tree_cache_layouts_without_a_tensor_map():

@@ -108,12 +108,12 @@ def test_tree_workspace_query(ops):
     size = lambda **kw: ops._fn().kda_tree_attention_workspace_size(ctypes.byref(_tree_args(ops, **kw)))  # noqa: E731
     assert ops._fn().kda_tree_attention_workspace_size(None) == 0
     assert size(head_dim=96) == 0 and size(num_requests=0) == 0
-    # contexts of a tile need no splits; a longer context needs at least two partial rows
+    # contexts of a tile are not cut; a longer context needs at least two partial rows
     # (128 values and their log-sum in fp32) per query row, 2 requests x 4 nodes x 8 heads
     assert size(pages_per_request=4) == 0
     rows = 2 * 4 * 8
     n = size(pages_per_request=1000)
-    assert n > 0 and n % (rows * 129 * 4) == 0 and n >= 2 * rows * 129 * 4
+    assert n >= 2 * rows * 129 * 4
     # a bound of the contexts cuts the work as so many pages would
     assert size(pages_per_request=1000, max_context=60) == 0
     assert size(pages_per_request=1000, max_context=1596) == size(pages_per_request=100)
