@@ -1,6 +1,6 @@
 // kda_tree.cu -- attention of drafted tokens over a paged cache
-// (kda_tree_attention in include/kda_ops.h): the kernel for few query rows and
-// the kernel that joins the splits of a long context.
+// (kda_tree_attention in include/kda_ops.h): the kernel for few query rows, the
+// kernel that joins the parts of long contexts, and the choice between the kernels.
 //
 // The rows of one (request, key head) are its nodes times the G query heads
 // that share the key head, so that a key is read once for all of them.  One
@@ -720,19 +720,23 @@ TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, fl
     TreePlan t;
     // The 128-row products where there are more rows than one product of the warp-level
     // kernel takes and enough work to outlast their longer way in and out (some 15 us).
-    // Up to 32 rows the rows kernel reads a key once too, and what decides is the context
-    // (152 items x 20 rows over 1000 tokens 32 us against 24, over 4000 51 against 60; 8
-    // items 21 against 12 and 17.5 against 20); with more it reads a key once for 32 rows
-    // (304 x 248 over 120 tokens 36 us against 91, 16 x 248 over 500 26 against 20, 8 x 64
-    // over 1000 24 against 15).  Pages have to be whole 8-row groups of a tile (and the line
-    // of work, in key tiles, stays inside 32 bits).
-    const int64_t blocks = (rows + 31) / 32, work = (int64_t)R * Hk * blocks * (max_len + 128);
-    t.mma = rows > 16 && D <= 128 && page % 8 == 0 && scale > 0.f && max_len / 128 + 1 < (1 << 22) &&
-            (blocks == 1 ? max_len >= 4096 : blocks == 2 ? max_len >= 1024 && work >= 65536 : work >= 131072);
+    // In one block of 32 rows the rows kernel reads a key once too, and what decides is the
+    // context (152 items x 20 rows over up to 1000 tokens 32 us against 24, over 4000 51
+    // against 60; 8 items 21 against 12 and 17.5 against 20); in more it reads a key once a
+    // block (304 x 248 over 120 tokens 36 us against 91, 16 x 248 over 500 26 against 20, 8 x
+    // 64 over 1000 24 against 15; head size 256, blocks of 16: 40 x 128 over 120 23 us both
+    // ways, 152 x 64 over 4000 125 against 275, 306 x 40 over 10 47 against 25, 304 x 512 over 4000 653 against 4421).  Pages
+    // have to be whole 8-row groups of a tile (and the line of work, in key tiles, stays
+    // inside 32 bits).
+    const int block = rows_per_block(rows, D);
+    const int64_t row_blocks = (rows + block - 1) / block, items = (int64_t)R * Hk * row_blocks;
+    const int64_t work = items * (max_len + 64);
+    t.mma = rows > 16 && page % 8 == 0 && num_sms > 1 && scale > 0.f && max_len / 128 + 1 < (1 << 22) &&
+            (row_blocks == 1 ? max_len >= 4096
+                             : row_blocks == 2 ? max_len >= 1024 && work >= 65536 : work >= 98304);
     // The rows kernel's cut (also for a cache without a tensor map); at_once is what the
     // tiles in flight leave room for, or for D 64 the registers.
-    const int block = rows_per_block(rows, D), at_once = num_sms * (D == 64 ? 4 : D == 128 ? 2 : 1);
-    const int64_t row_blocks = (rows + block - 1) / block, items = (int64_t)R * Hk * row_blocks;
+    const int at_once = num_sms * (D == 64 ? 4 : D == 128 ? 2 : 1);
     const int64_t tiles = (max_len + kTile - 1) / kTile;
     // Fewer items than CTAs at once: clusters of up to 8, at least 128 tokens a CTA (one
     // request, 2 key heads, 1000 tokens: 6.8 us, 9 as a line), until a CTA's tiles outweigh
@@ -753,9 +757,10 @@ TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, fl
     // 202 requests of up to 41 (and 34 both ways with 150 of up to 250).
     t.order = !t.mma && !t.line && t.cluster == 1 && R > 1 && R <= kOrderMax && items > at_once && tiles > 4 ? R : 0;
     t.grid = num_sms;
-    t.parts = (size_t)2 * (t.mma && t.grid > t.row_grid ? t.grid : t.row_grid);
+    const int stretches = t.mma ? D == 256 ? t.grid / 2 : t.grid : 0;   // with head size 256 two CTAs share one
+    t.parts = (size_t)2 * (stretches > t.row_grid ? stretches : t.row_grid);
     t.part_rows = (size_t)2 * t.row_grid * block;
-    if (t.mma && t.part_rows < (size_t)2 * t.grid * 256) t.part_rows = (size_t)2 * t.grid * 256;
+    if (t.part_rows < (size_t)2 * stretches * 256) t.part_rows = (size_t)2 * stretches * 256;
     return t;
 }
 

@@ -9,7 +9,7 @@
 //                   of S in registers, so maximum and sum need no exchange; P
 //                   goes back over S's columns as 16-bit pairs, the A operand of
 //                   the second product;
-//   warp 8          the loader: a ring of kBufs tiles, K and V in turn;
+//   warp 8          the loader: a ring of K and V tiles in turn;
 //   warp 9          issues the products;
 //   warp 10         deals out the work, item by item;
 //   warp 11         cleans the V tiles that need it.
@@ -27,6 +27,17 @@
 // by tree_join_kernel (kda_tree.cu).  The loader and the issuer run from
 // one item into the next without a halt; only the rows' way out and the next
 // queries' way in are between two items.
+//
+// Head size 256: S of two row tiles and a whole O (256 columns each) do not fit TMEM,
+// so two neighbouring CTAs take the same stretch, both with all of S and each with
+// one half of V's columns.  That is 3 products where 2 are due, but the keys are read
+// for 256 rows at a time (a whole O would leave room for 128) and come out of L2 the
+// second time.
+//
+// Measured: 19 requests x 4 key heads x 512 rows of 128 over 16384 tokens 216 us, 1.51
+// PFLOP/s; 38 x 4 x 256 over 8192 122 us, 1.34 PFLOP/s and 5.2 TB/s; head size 256, 152 x 2
+// x 512 rows over 0.2 to 1 times 16000 2.24 ms, 1.14 PFLOP/s (15.8 ms in the kernel for
+// few rows).
 //
 // The running maximum moves only when a row's scores exceed it by 2^8 (l and O
 // stay far inside fp32 and P inside fp16 until then), so that O in TMEM is
@@ -83,17 +94,25 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const v
 }
 
 template <int D> struct MmaShape {
-    static constexpr uint32_t kTileBytes = (D / 64) * kBlock;
+    static constexpr int kV = D == 256 ? 128 : D;   // value columns a CTA
+    static constexpr int kHalves = D / kV;          // CTAs that share a stretch, each with its columns
+    static constexpr int kPer = kHalves + 1;        // ring slots a key tile: K by kV channels, V
+    static constexpr uint32_t kSlotBytes = (kV / 64) * kBlock, kQBytes = (D / 64) * kBlock;
     // K and V tiles as the copies leave them: groups of 8 keys, in a group 64 channels
     // after the other, 8 rows of 128 bytes each.
-    static constexpr uint32_t kGroupBytes = (D / 64) * 1024;
-    static constexpr int kBufs = D == 128 ? 5 : 8;
-    // the queries of both streams, where the rows also pass on their way out
-    static constexpr uint32_t kFront = D == 128 ? 2 * kTileBytes : 56 * 1024;
-    static constexpr uint32_t kSmem = kFront + kBufs * kTileBytes + 1024;   // and the ring, and alignment
+    static constexpr uint32_t kGroupBytes = (kV / 64) * 1024;
+    // The queries, where the rows also pass on their way out, and the ring of K and V.  With
+    // head size 256 one row tile's queries leave room for more of the ring.
+    static __host__ __device__ constexpr uint32_t front(int rows) {
+        return D == 64 ? 56 * 1024 : D == 256 && rows <= 128 ? kQBytes : 2 * kQBytes;
+    }
+    static __host__ __device__ constexpr int bufs(int rows) { return D == 64 ? 8 : D == 256 && rows > 128 ? 3 : 5; }
+    static constexpr uint32_t smem(int rows) { return front(rows) + bufs(rows) * kSlotBytes + 1024; }   // and alignment
 };
 
-static_assert(kWayOut * 4 <= MmaShape<64>::kFront && kWayOut * 4 <= MmaShape<128>::kFront, "the way out fits the front");
+static_assert(kWayOut * 4 <= MmaShape<64>::front(1) && kWayOut * 4 <= MmaShape<128>::front(1) &&
+                  kWayOut * 4 <= MmaShape<256>::front(1),
+              "the way out fits the front");
 
 template <typename T> struct MmaTypes;
 template <> struct MmaTypes<__nv_bfloat16> {
@@ -147,9 +166,11 @@ __device__ __forceinline__ bool elect_one() {
 template <typename T, int D>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     tree_mma_kernel(const TreeParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    constexpr uint32_t kTileBytes = MmaShape<D>::kTileBytes;
-    constexpr uint32_t kGroupBytes = MmaShape<D>::kGroupBytes;
-    constexpr int kBufs = MmaShape<D>::kBufs;
+    using Shape = MmaShape<D>;
+    constexpr uint32_t kSlotBytes = Shape::kSlotBytes, kQBytes = Shape::kQBytes, kGroupBytes = Shape::kGroupBytes;
+    constexpr int kV = Shape::kV, kHalves = Shape::kHalves, kPer = Shape::kPer;
+    const int bufs = Shape::bufs(p.rows);
+    const int cta = (int)blockIdx.x / kHalves, half = (int)blockIdx.x % kHalves;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t kv_full[kMaxBufs], kv_free[kMaxBufs], kv_raw[kMaxBufs], q_ready, s_full[2], p_half[2], p_ready[2], o_full, o_free;
@@ -164,14 +185,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int* abort = &abort_flag;
-    uint8_t* ring = sm + MmaShape<D>::kFront;
+    uint8_t* ring = sm + Shape::front(p.rows);
     auto fail = [&]() {
         *abort = 1;
         if (p.status) atomicExch(p.status, 4);
     };
 
     if (tid == 0) {
-        for (int i = 0; i < kBufs; ++i) {
+        for (int i = 0; i < bufs; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_free[i], 1);
             mbar_init(&kv_raw[i], 1);
@@ -241,21 +262,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     const int row = row_ahead;
                     ahead = page_of(tile + 1);
                     const int base = tile * kKeys;
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * D * 2u;
-                    for (int v = 0; v < 2; ++v) {
-                        const int slot = issued % kBufs, round = issued / kBufs;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * kV * 2u;
+                    for (int part = 0; part < kPer; ++part) {   // K by kV channels, then V
+                        const bool v = part == kHalves;
+                        const int slot = issued % bufs, round = issued / bufs;
                         if (round > 0) ok = __all_sync(0xffffffffu, wait_for(&kv_free[slot], (round - 1) & 1, abort));
                         if (!ok) break;
-                        uint8_t* dst = ring + slot * kTileBytes;
-                        const bool special = v == 1 && base + kKeys > ctx;
+                        uint8_t* dst = ring + slot * kSlotBytes;
+                        const bool special = v && base + kKeys > ctx;
                         uint64_t* bar = special ? &kv_raw[slot] : &kv_full[slot];   // raw: to warp 11 first
                         raw = special ? raw | 1u << slot : raw & ~(1u << slot);
                         if (special) raw_phases ^= 1u << slot;
                         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                         __syncwarp();
                         if (id >= 0)
-                            tma_load_5d(dst + lane * box * D * 2, v ? &vmap : &kmap, 0, 0,
-                                        (v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64),
+                            tma_load_5d(dst + lane * box * kV * 2, v ? &vmap : &kmap, 0, 0,
+                                        ((v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64)) +
+                                            (v ? half : part) * (kV / 64),
                                         row / 8,
                                         (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
                         ++issued;
@@ -265,9 +288,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) fail();
                 // copies still on their way into this CTA's memory
-                for (int i = max(0, issued - kBufs); i < issued; ++i)
-                    if (!((raw >> (i % kBufs)) & 1)) wait_for(&kv_full[i % kBufs], (i / kBufs) & 1, nullptr);
-                    else wait_for(&kv_raw[i % kBufs], (raw_phases >> (i % kBufs)) & 1, nullptr);
+                for (int i = max(0, issued - bufs); i < issued; ++i)
+                    if (!((raw >> (i % bufs)) & 1)) wait_for(&kv_full[i % bufs], (i / bufs) & 1, nullptr);
+                    else wait_for(&kv_raw[i % bufs], (raw_phases >> (i % bufs)) & 1, nullptr);
             }
         } else if (warp == 9) {
             // ------------------------------------------------------------ products
@@ -276,53 +299,64 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             // memory): the products' operands live in uniform registers, and a lone
             // thread that has to bring them there issues a product in about 105 cycles,
             // whatever its size.
-            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(D);
+            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(kV);
             const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
             const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sm), 0),
-                           ring_at = q_at + MmaShape<D>::kFront;
+                           ring_at = q_at + Shape::front(p.rows);
             bool ok = true;
             int item = 0;
             int base = 0;                      // ring tiles before this item
             int done0 = 0, done1 = 0;          // P tiles taken, by stream
-            auto landed = [&](int i) { return wait_for(&kv_full[i % kBufs], (i / kBufs) & 1, abort); };
+            auto landed = [&](int i) { return wait_for(&kv_full[i % bufs], (i / bufs) & 1, abort); };
             Item x;
             for (; __all_sync(0xffffffffu, take(item, x, ok)); ++item) {
                 if (lane == 0) mbar_arrive(&item_free[item % kItems]);
                 const bool two = __shfl_sync(0xffffffffu, (int)x.two, 0) != 0;
                 const int tiles = __shfl_sync(0xffffffffu, x.t1 - x.t0, 0);
                 const int units = (two ? 2 : 1) * tiles;   // unit u: stream u & 1, tile two ? u >> 1 : u
+                auto keys_landed = [&](int i) {
+                    bool all = true;
+#pragma unroll
+                    for (int part = 0; part < kHalves; ++part) all = all && landed(i + part);
+                    return all;
+                };
                 auto scores = [&](int u) {
-                    const int s = u & 1, i = base + 2 * (two ? u >> 1 : u);
-                    if (!two) ok = __all_sync(0xffffffffu, ok && landed(i));
+                    const int s = u & 1, i = base + kPer * (two ? u >> 1 : u);
+                    if (!two) ok = __all_sync(0xffffffffu, ok && keys_landed(i));
                     if (!ok) return;
                     tc_fence_after();
-                    const uint64_t ad = sdesc_kmajor_sw128(q_at + (two ? s : 0) * kTileBytes),
-                                   bd = sdesc_keys(ring_at + (i % kBufs) * kTileBytes, kGroupBytes);
-                    if (elect_one()) {
+                    const uint64_t ad = sdesc_kmajor_sw128(q_at + (two ? s : 0) * kQBytes);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            umma_bf16(tbu + kTmemS + 128 * s, ad + (k >> 2) * (kBlock >> 4) + (k & 3) * 2,
-                                      bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, k > 0 ? 1u : 0u);
-                        umma_commit(&s_full[s]);
-                        if (!two || s == 1) umma_commit(&kv_free[i % kBufs]);
+                    for (int part = 0; part < kHalves; ++part) {   // kV channels of K
+                        const int slot = (i + part) % bufs;
+                        const uint64_t bd = sdesc_keys(ring_at + slot * kSlotBytes, kGroupBytes);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < kV / 16; ++k)
+                                umma_bf16(tbu + kTmemS + 128 * s,
+                                          ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
+                                          bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, part + k > 0 ? 1u : 0u);
+                            if (part == kHalves - 1) umma_commit(&s_full[s]);
+                            if (!two || s == 1) umma_commit(&kv_free[slot]);
+                        }
                     }
                     __syncwarp();
                 };
                 ok = __all_sync(0xffffffffu, ok && wait_for(&q_ready, item & 1, abort));
-                if (two) ok = __all_sync(0xffffffffu, ok && landed(base));
+                if (two) ok = __all_sync(0xffffffffu, ok && keys_landed(base));
                 scores(0);
                 if (units > 1) scores(1);
                 for (int u = 0; u < units && ok; ++u) {
-                    const int s = u & 1, i = base + 2 * (two ? u >> 1 : u) + 1;
+                    const int s = u & 1, i = base + kPer * (two ? u >> 1 : u) + kHalves;
                     // O still holds the item before until its rows are out
                     if (u == 0 && item > 0) ok = wait_for(&o_free, (item - 1) & 1, abort);
                     // This tile's V, and with two row tiles the next K before P is there (the
                     // second stream's tiles are the first's); with one row tile memory is the
                     // bound, and waiting for a K would hold up the V before it.
-                    if (!two || s == 0) ok = ok && landed(i) && (!two || u + 2 >= units || landed(i + 1));
+                    if (!two || s == 0) ok = ok && landed(i) && (!two || u + 2 >= units || keys_landed(i + 1));
                     const uint32_t phase = (s ? done1 : done0) & 1;
                     if (s) ++done1; else ++done0;
-                    const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % kBufs) * kTileBytes, 1024, kGroupBytes);
+                    const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % bufs) * kSlotBytes, 1024, kGroupBytes);
                     // the two halves of P as they come
                     auto product = [&](int k0, uint64_t* ready) {
                         ok = __all_sync(0xffffffffu, ok && wait_for(ready, phase, abort));
@@ -333,7 +367,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             for (int k = 0; k < kKeys / 32; ++k)
                                 umma_bf16_ta(tbu + kTmemO + 128 * s, tbu + kTmemS + 128 * s + 8 * (k0 + k),
                                              bd + (k0 + k) * (kGroupBytes >> 3), id_pv, (u > 1 || k0 + k > 0) ? 1u : 0u);
-                            if (k0 && (!two || s == 1)) umma_commit(&kv_free[i % kBufs]);
+                            if (k0 && (!two || s == 1)) umma_commit(&kv_free[i % bufs]);
                         }
                         __syncwarp();
                     };
@@ -345,7 +379,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (elect_one()) umma_commit(&o_full);
                 __syncwarp();
                 if (!ok) wait_for(&o_full, item & 1, nullptr);   // products still in flight
-                base += 2 * tiles;
+                base += kPer * tiles;
             }
             if (!ok && lane == 0) fail();
             __syncwarp();
@@ -379,7 +413,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 const int64_t tile_cost = (int64_t)head_cost * p.Hk, total = at * tile_cost;
                 // at least a key tile a CTA
                 const int64_t most = total / kCostTwo;
-                const int ctas = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
+                const int room = (int)gridDim.x / kHalves, ctas = most < 1 ? 1 : most < room ? (int)most : room;
                 int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
                 int k = 0;
                 bool ok = true;
@@ -391,8 +425,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     ++k;
                 };
                 Item x{};
-                if ((int)blockIdx.x < ctas) {
-                    const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+                if (cta < ctas) {
+                    const int64_t begin = total * cta / ctas, end = total * (cta + 1) / ctas;
                     // the item that holds the stretch's begin
                     int lo = 0, hi = p.count;
                     while (hi - lo > 1) {
@@ -435,8 +469,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 x.t1 = -1;
                 deal(x);
                 // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
-                p.parts[2 * blockIdx.x] = slots[0];
-                p.parts[2 * blockIdx.x + 1] = slots[1];
+                if (half == 0) {
+                    p.parts[2 * cta] = slots[0];
+                    p.parts[2 * cta + 1] = slots[1];
+                }
                 if (!ok) fail();
             }
             __syncwarp();
@@ -452,13 +488,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (lane == 0) mbar_arrive(&item_free[item % kItems]);
                 const int ctx = x.ctx, hi = ctx + x.n;
                 for (int tile = max(x.t0, ctx / kKeys); tile < x.t1 && ok; ++tile) {
-                    const int i = base_kv + 2 * (tile - x.t0) + 1, slot = i % kBufs, base = tile * kKeys;
-                    uint8_t* const dst = ring + slot * kTileBytes;
+                    const int i = base_kv + kPer * (tile - x.t0) + kHalves, slot = i % bufs, base = tile * kKeys;
+                    uint8_t* const dst = ring + slot * kSlotBytes;
                     ok = __all_sync(0xffffffffu, wait_for(&kv_raw[slot], (phases >> slot) & 1, abort));
                     if (!ok) break;
                     phases ^= 1u << slot;
                     constexpr uint32_t kExp = Elem<T>::kExpMask;
-                    constexpr int kPieces = D / 8;
+                    constexpr int kPieces = kV / 8;
                     auto piece = [&](int e) -> uint4* {   // 16-byte piece e of the tile, rows in order
                         const int c = e % kPieces, krow = e / kPieces;
                         return reinterpret_cast<uint4*>(dst + (krow >> 3) * kGroupBytes + (c >> 3) * 1024 +
@@ -486,7 +522,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&kv_full[slot]);
                 }
-                base_kv += 2 * (x.t1 - x.t0);
+                base_kv += kPer * (x.t1 - x.t0);
             }
             if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
         }
@@ -523,7 +559,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 for (int k = 0; k < kPasses; ++k) {
                     const int in = k * kRowsPass + in0;   // row of the pair of tiles
                     if (k < kPasses / 2 || two) {
-                        uint8_t* at = dst + (k * kRowsPass >> 7) * kTileBytes + sw128_off(in & 127, (piece & 7) * 8);
+                        uint8_t* at = dst + (k * kRowsPass >> 7) * kQBytes + sw128_off(in & 127, (piece & 7) * 8);
                         if (left > 0) cp_async16(at, src);
                         else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
                     }
@@ -591,7 +627,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                     if (u > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
+                        for (int k = 0; k < kV / 32; ++k) {
                             float o[32];
                             uint32_t w[32];
                             tmem_ld32(to + 32 * k, o);
@@ -661,7 +697,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const float inv = empty ? 0.f : 1.f / l;
             f0 *= inv;
             f1 *= inv;
-            const int64_t part = ((int64_t)(2 * blockIdx.x + (x.t0 > 0 ? 0 : 1)) * 256 + (row - row0));
+            const int64_t part = ((int64_t)(2 * cta + (x.t0 > 0 ? 0 : 1)) * 256 + (row - row0));
             const bool out = ok && live && (two || stream == 0);
             uint32_t any_bad = 0;
 #pragma unroll
@@ -673,13 +709,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             for (int g = 0; g < 4; ++g) {
                 const int q = row - lane + 8 * g + (lane >> 2), qi = (int)page_div((uint32_t)q, p.G, p.group_magic);
                 dst[g] = q < p.rows ? static_cast<T*>(p.out) + r * p.os[0] + qi * p.os[1] +
-                                          (kvh * p.G + q - qi * p.G) * p.os[2] + (lane & 3) * 8
+                                          (kvh * p.G + q - qi * p.G) * p.os[2] + half * kV + (lane & 3) * 8
                                     : nullptr;
             }
-            float* const pdst = p.part_o + (part - lane + (lane >> 3)) * D + (lane & 7) * 4;
+            float* const pdst = p.part_o + (part - lane + (lane >> 3)) * D + half * kV + (lane & 7) * 4;
             // rolled: the code runs once an item, and fetching it costs more than running it
 #pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
+            for (int k = 0; k < kV / 32; ++k) {
                 float o[32];
                 if (live && ok && (out || joined)) tmem_ld32(to + 32 * k, o);
                 if (joined) {
@@ -707,7 +743,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             const int tok = ctx + j, id = p.table[r * p.table_stride + tok / p.page];
                             if (id < 0 || id >= p.P) continue;
                             const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (tok % p.page) * p.vs[1] +
-                                           kvh * p.vs[2] + 32 * k;
+                                           kvh * p.vs[2] + half * kV + 32 * k;
 #pragma unroll 1
                             for (int e = 0; e < 32; ++e) {
                                 const float y = Elem<T>::one(src[e]);
@@ -738,7 +774,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
                 if (joined) named_bar_sync(1, 256);   // stream 1's columns are taken
             }
-            if (out && row < p.rows) {
+            if (out && row < p.rows && half == 0) {
                 const float lse = empty ? -INFINITY : m * c + log2f(l);
                 if (!whole) p.part_lse[part] = lse;
                 else if (p.lse)
@@ -760,19 +796,29 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
 template <typename T, int D>
 cudaError_t launch_mma_t(const TreeParams& q, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+    using Shape = MmaShape<D>;
     static std::atomic<uint64_t> smem_set;
-    cudaError_t e = set_smem_limit_once((const void*)tree_mma_kernel<T, D>, (int)MmaShape<D>::kSmem, smem_set);
+    constexpr uint32_t most = Shape::smem(1) > Shape::smem(256) ? Shape::smem(1) : Shape::smem(256);
+    cudaError_t e = set_smem_limit_once((const void*)tree_mma_kernel<T, D>, (int)most, smem_set);
+    grid -= grid % Shape::kHalves;
     for (int r0 = 0; r0 < q.R && e == cudaSuccess; r0 += kMmaSlice) {
         TreeParams p = q;
         p.r0 = r0;
-        p.slots = 2 * grid;
+        p.slots = 2 * (grid / Shape::kHalves);
         p.slot_rows = 256;
         p.count = q.R - r0 < kMmaSlice ? q.R - r0 : kMmaSlice;
-        tree_mma_kernel<T, D><<<grid, kMmaThreads, MmaShape<D>::kSmem, s>>>(p, kmap, vmap);
+        tree_mma_kernel<T, D><<<grid, kMmaThreads, Shape::smem(p.rows), s>>>(p, kmap, vmap);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = launch_tree_join(p, D, std::is_same<T, __half>::value, s);
     }
     return e;
+}
+
+template <typename T>
+cudaError_t launch_mma(const TreeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int D, int grid,
+                       cudaStream_t s) {
+    return D == 64 ? launch_mma_t<T, 64>(p, kmap, vmap, grid, s)
+                   : D == 128 ? launch_mma_t<T, 128>(p, kmap, vmap, grid, s) : launch_mma_t<T, 256>(p, kmap, vmap, grid, s);
 }
 
 // Tensor map of a cache as [64 channels, 8 rows, blocks of 64 channels, groups of 8
@@ -789,7 +835,7 @@ bool cache_map(CUtensorMap* map, const void* base, const int64_t (&st)[3], const
     const uint64_t dims[5] = {64, 8, (uint64_t)(rows ? p.Hk : 1) * (D / 64), (uint64_t)p.page / 8,
                               (uint64_t)p.P * (rows ? 1 : p.Hk)};
     const uint64_t strides[4] = {(uint64_t)st[1] * 2, 128, (uint64_t)st[1] * 16, (uint64_t)(rows ? st[0] : st[2]) * 2};
-    const uint32_t box[5] = {64, 8, (uint32_t)D / 64, (uint32_t)box_of(p.page) / 8, 1};
+    const uint32_t box[5] = {64, 8, (uint32_t)(D == 256 ? 128 : D) / 64, (uint32_t)box_of(p.page) / 8, 1};
     if (dims[4] > INT32_MAX) return false;
     return make_tensor_map(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims,
                            strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -802,9 +848,8 @@ bool launch_tree_mma(const TreeParams& q, int D, bool f16, int grid, cudaStream_
     TreeParams p = q;
     if (!cache_map(&kmap, p.kc, p.ks, p, D, f16, &p.k_paged) || !cache_map(&vmap, p.vc, p.vs, p, D, f16, &p.v_paged))
         return false;
-    if (f16) *e = D == 64 ? launch_mma_t<__half, 64>(p, kmap, vmap, grid, s) : launch_mma_t<__half, 128>(p, kmap, vmap, grid, s);
-    else *e = D == 64 ? launch_mma_t<__nv_bfloat16, 64>(p, kmap, vmap, grid, s)
-                      : launch_mma_t<__nv_bfloat16, 128>(p, kmap, vmap, grid, s);
+    if (f16) *e = launch_mma<__half>(p, kmap, vmap, D, grid, s);
+    else *e = launch_mma<__nv_bfloat16>(p, kmap, vmap, D, grid, s);
     return true;
 }
 

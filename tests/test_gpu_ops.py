@@ -342,7 +342,7 @@ def test_tree_pages(page, heads_first, N, G, room):
 
 @pytest.mark.parametrize("page", [8, 16, 24, 48, 128, 160, 512])
 @pytest.mark.parametrize("heads_first", [False, True])
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_tree_pages_of_the_kernel_for_many_rows(page, heads_first, D):
     _tree_case(page, [513, 2, 127, 300, 0], 20, 12, 3, D, page, F16, heads_first=heads_first, room=ROOM)
 
