@@ -18,10 +18,12 @@
 //
 // All of a warp's pieces are asked for at once by 16-byte asynchronous copies into
 // shared memory (up to kMaxPasses of 512 bytes), and A and B are formed while they
-// fly.  The arithmetic is near the issue limit (a pass of 32 pieces has some 90
+// fly: every angle by one lane, the cosines and sines through shared memory (formed by
+// every lane that needs them they cost 0.5 us of a small call's 3.8, 41 us against 37 with
+// 18318 tokens of 12 + 3 heads of 96, 36.5 against 35.3 with wide heads).  The arithmetic is near the issue limit (a pass of 32 pieces has some 90
 // cycles of a scheduler at the memory's rate), and it takes 20 warps an SM to keep
 // up: two passes go together, whose sums of squares share one reduction and one
-// root.  Measured: 32768 tokens of 32 + 8 heads of 128, fp16, 105 us (6.4 TB/s; 171
+// root.  Measured: 32768 tokens of 32 + 8 heads of 128, fp16, 104 us (6.4 TB/s; 171
 // with the loads in registers, 118 with a reduction a pass, 103 with four passes
 // together, but then 8191 tokens of 16 + 2 heads of 256 take 38 us against 36; 153
 // with persistent warps and two buffers, which leave 8 warps an SM).
@@ -40,10 +42,11 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kMaxPasses = 20;   // of an item
-constexpr int kSlack = 1;        // rows read (not used) past an item's last pass, two passes at a time
-// Rows of 32 pieces a warp has: its passes, and zeros.
-__host__ __device__ constexpr int warp_rows(int passes) { return passes + kSlack + 1; }
-static_assert(kRopeThreads / 32 * warp_rows(kMaxPasses) * 512 <= 48 * 1024, "fits without an opt-in");
+// Rows of 512 bytes a warp has: its passes, the token's cosines and sines (which are also
+// read, and not used, past an odd number of passes, two at a time), and zeros.
+__host__ __device__ constexpr int turn_rows(int rot) { return rot > 128 ? 2 : 1; }
+__host__ __device__ constexpr int warp_rows(int passes, int rot) { return passes + turn_rows(rot) + 1; }
+static_assert(kRopeThreads / 32 * warp_rows(kMaxPasses, 256) * 512 <= 48 * 1024, "fits without an opt-in");
 
 // position * f modulo 2 pi, in about [-5, 5], within 1e-6.
 __device__ __forceinline__ float reduced_angle(int pos, float f) {
@@ -85,8 +88,9 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
     const int cc = act ? c0 : 0;
     const int P = p.chunk_passes;
     extern __shared__ __align__(16) uint4 pieces[];
-    uint4* const mine = pieces + (threadIdx.x >> 5) * warp_rows(P) * 32;
-    uint4* const zeros = mine + (P + kSlack) * 32;
+    uint4* const mine = pieces + (threadIdx.x >> 5) * warp_rows(P, p.rot) * 32;
+    float2* const turn = reinterpret_cast<float2*>(mine + P * 32);
+    uint4* const zeros = mine + (P + turn_rows(p.rot)) * 32;
     zeros[lane] = make_uint4(0, 0, 0, 0);
 
     // passes of a token: its query heads, its key heads, its value heads
@@ -172,24 +176,34 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
             kc_off = page * p.kcs[0] + row * p.kcs[1];
             vc_off = page * p.vcs[0] + row * p.vcs[1];
         }
+        // every angle once, to all lanes that turn by it
         float cs[8], sn[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cs[i] = 1.f;
+            sn[i] = 0.f;
+        }
         if (cur.first < qp + kp) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cs[i] = 1.f;
-                sn[i] = 0.f;
-                if (rotates && !(p.interleaved && (i & 1))) {
-                    const int pair = p.interleaved ? (c0 + i) >> 1 : (low ? c0 + i : c0 + i - half);
-                    const float a = reduced_angle(cur.pos, __ldg(p.inv_freq + pair));
-                    cs[i] = p.scale * __cosf(a);
-                    sn[i] = p.scale * __sinf(a);
-                }
+            for (int j = lane; j < half; j += 32) {
+                const float a = reduced_angle(cur.pos, __ldg(p.inv_freq + j));
+                turn[j] = make_float2(p.scale * __cosf(a), p.scale * __sinf(a));
             }
-            if (rotates && p.interleaved) {
+            __syncwarp();
+            if (rotates) {
+                const float4* src = reinterpret_cast<const float4*>(turn + (p.interleaved ? c0 / 2 : low ? c0 : c0 - half));
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    cs[i + 1] = cs[i];
-                    sn[i + 1] = sn[i];
+                for (int i = 0; i < 4; ++i) {
+                    if (p.interleaved) {
+                        const float2 y = reinterpret_cast<const float2*>(src)[i];
+                        cs[2 * i] = cs[2 * i + 1] = y.x;
+                        sn[2 * i] = sn[2 * i + 1] = y.y;
+                    } else {
+                        const float4 y = src[i];
+                        cs[2 * i] = y.x;
+                        sn[2 * i] = y.y;
+                        cs[2 * i + 1] = y.z;
+                        sn[2 * i + 1] = y.w;
+                    }
                 }
             }
         }
@@ -303,7 +317,7 @@ cudaError_t launch_rope_t(RopeParams& p, int num_sms, cudaStream_t s) {
     while (p.tokens * chunks < 8LL * num_sms && chunks * 2 < passes) chunks <<= 1;
     p.chunk_passes = (passes + chunks - 1) / chunks;
     p.chunks = (passes + p.chunk_passes - 1) / p.chunk_passes;
-    const size_t smem = (size_t)(kRopeThreads / 32) * warp_rows(p.chunk_passes) * 512;
+    const size_t smem = (size_t)(kRopeThreads / 32) * warp_rows(p.chunk_passes, p.rot) * 512;
     const int64_t blocks = (p.tokens * p.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     const auto kernel = lanes == 8 ? qk_norm_rope_kernel<T, 8> : lanes == 16 ? qk_norm_rope_kernel<T, 16>
                                                                              : qk_norm_rope_kernel<T, 32>;
