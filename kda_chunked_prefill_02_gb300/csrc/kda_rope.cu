@@ -18,15 +18,16 @@
 //
 // All of a warp's pieces are asked for at once by 16-byte asynchronous copies into
 // shared memory (up to kMaxPasses of 512 bytes), and A and B are formed while they
-// fly: every angle by one lane, the cosines and sines through shared memory (formed by
-// every lane that needs them they cost 0.5 us of a small call's 3.8, 41 us against 37 with
-// 18318 tokens of 12 + 3 heads of 96, 36.5 against 35.3 with wide heads).  The arithmetic is near the issue limit (a pass of 32 pieces has some 90
-// cycles of a scheduler at the memory's rate), and it takes 20 warps an SM to keep
-// up: two passes go together, whose sums of squares share one reduction and one
-// root.  Measured: 32768 tokens of 32 + 8 heads of 128, fp16, 104 us (6.4 TB/s; 171
-// with the loads in registers, 118 with a reduction a pass, 103 with four passes
-// together, but then 8191 tokens of 16 + 2 heads of 256 take 38 us against 36; 153
-// with persistent warps and two buffers, which leave 8 warps an SM).
+// fly: every angle by one lane, the cosines and sines through shared memory (formed
+// by every lane that turns by them they take 0.5 us of a small call's 3.8; 41 us
+// against 37 with 18318 tokens of 12 + 3 heads of 96, 36.5 against 35.3 with 8191
+// tokens of 16 + 2 heads of 256).  The arithmetic is near the issue limit (a pass of
+// 32 pieces has some 90 cycles of a scheduler at the memory's rate), and it takes 20
+// warps an SM to keep up: two passes go together, whose sums of squares share one
+// reduction and one root.  Measured: 32768 tokens of 32 + 8 heads of 128, fp16, 104
+// us (6.4 TB/s; 171 with the loads in registers, 118 with a reduction a pass, 103
+// with four passes together, but then the wide heads take 38 us against 36; 153 with
+// persistent warps and two buffers, which leave 8 warps an SM).
 //
 // The angle.  t = position * f reaches 1e5 and more in a long context, where a
 // rounded fp32 product is off by 1e-2.  The product is kept in two fp32 parts
