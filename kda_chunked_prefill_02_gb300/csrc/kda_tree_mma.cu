@@ -20,8 +20,9 @@
 //
 // The work of a call is one line of key tiles, ordered by request, key head and
 // pair of row tiles, and every CTA takes an equal stretch of it (a tile for two
-// row tiles counts 5, for one 4, as measured: 1.92 and 1.52 us), so that ragged
-// contexts leave no SM idle.  A stretch cuts at most two items; the parts of a
+// row tiles counts 5, for one 4, as measured: 1.92 and 1.52 us; an item's way in and
+// out as much as several tiles: 24 requests of 4 key heads and 488 rows over up to
+// 9000 tokens 136 us without, 124 with), so that ragged contexts leave no SM idle.  A stretch cuts at most two items; the parts of a
 // cut item leave normalised rows and their log-sum in the workspace (slot 0 of
 // a CTA: a later part of an item, slot 1: the first), joined in the CTAs' order
 // by tree_join_kernel (kda_tree.cu).  The loader and the issuer run from
@@ -97,6 +98,8 @@ template <int D> struct MmaShape {
     static constexpr int kV = D == 256 ? 128 : D;   // value columns a CTA
     static constexpr int kHalves = D / kV;          // CTAs that share a stretch, each with its columns
     static constexpr int kPer = kHalves + 1;        // ring slots a key tile: K by kV channels, V
+    // Cost of an item's way in and out (some 9 us) beside a key tile's kCostTwo.
+    static constexpr int kCostItem = D == 256 ? 12 : D == 128 ? 24 : 16;
     static constexpr uint32_t kSlotBytes = (kV / 64) * kBlock, kQBytes = (D / 64) * kBlock;
     // K and V tiles as the copies leave them: groups of 8 keys, in a group 64 channels
     // after the other, 8 rows of 128 bytes each.
@@ -150,6 +153,12 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
         " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
         : "memory");
+}
+
+// a / b of numbers that hardly ever need 64 bits: the division that does takes some
+// 500 cycles of the way to a CTA's first item.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // One lane of a converged warp.
@@ -410,9 +419,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 const int pairs = (p.rows + 255) / 256;
                 const bool odd = (p.rows - 1) % 256 < 128;   // the last pair has one row tile
                 const int head_cost = pairs * kCostTwo - (odd ? kCostTwo - kCostOne : 0);   // of a key tile
-                const int64_t tile_cost = (int64_t)head_cost * p.Hk, total = at * tile_cost;
+                const int pairs_cost = pairs * Shape::kCostItem;
+                // where request r begins on the line
+                const auto start = [&](int r) { return ((int64_t)s_start[r] * head_cost + (int64_t)r * pairs_cost) * p.Hk; };
+                const int64_t total = start(p.count);
                 // at least a key tile a CTA
-                const int64_t most = total / kCostTwo;
+                const int64_t most = quotient(at * head_cost * p.Hk, kCostTwo);
                 const int room = (int)gridDim.x / kHalves, ctas = most < 1 ? 1 : most < room ? (int)most : room;
                 int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
                 int k = 0;
@@ -426,29 +438,30 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 };
                 Item x{};
                 if (cta < ctas) {
-                    const int64_t begin = total * cta / ctas, end = total * (cta + 1) / ctas;
+                    const int64_t begin = quotient(total * cta, ctas), end = quotient(total * (cta + 1), ctas);
                     // the item that holds the stretch's begin
                     int lo = 0, hi = p.count;
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) >> 1;
-                        if (s_start[mid] * tile_cost <= begin) lo = mid; else hi = mid;
+                        if (start(mid) <= begin) lo = mid; else hi = mid;
                     }
                     int r = lo, tiles = s_start[r + 1] - s_start[r];
-                    int64_t item = s_start[r] * tile_cost, off = begin - item;
-                    const int64_t per_head = (int64_t)tiles * head_cost, per_pair = (int64_t)tiles * kCostTwo;
-                    x.h = (int)(off / per_head);
+                    int64_t item = start(r), off = begin - item;
+                    const int64_t per_head = (int64_t)tiles * head_cost + pairs_cost;
+                    const int64_t per_pair = (int64_t)tiles * kCostTwo + Shape::kCostItem;
+                    x.h = (int)quotient(off, per_head);
                     off -= x.h * per_head;
-                    x.rb = min((int)(off / per_pair), pairs - 1);
+                    x.rb = min((int)quotient(off, per_pair), pairs - 1);
                     off -= x.rb * per_pair;
                     item = begin - off;
                     tree_lengths(p, p.r0 + r, x.ctx, x.n);
                     while (item < end && ok) {
                         x.two = !(odd && x.rb == pairs - 1);
                         const int cost = x.two ? kCostTwo : kCostOne;
-                        const int64_t next = item + (int64_t)tiles * cost;
+                        const int64_t first = item + Shape::kCostItem, next = first + (int64_t)tiles * cost;
                         x.r = p.r0 + r;
-                        x.t0 = item < begin ? (int)((begin - item + cost - 1) / cost) : 0;
-                        x.t1 = next <= end ? tiles : (int)((end - item + cost - 1) / cost);
+                        x.t0 = first < begin ? (int)quotient(begin - first + cost - 1, cost) : 0;
+                        x.t1 = next <= end ? tiles : first < end ? (int)quotient(end - first + cost - 1, cost) : 0;
                         x.whole = x.t0 == 0 && x.t1 == tiles;
                         if (x.t1 > x.t0) {
                             if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, x.rb);
