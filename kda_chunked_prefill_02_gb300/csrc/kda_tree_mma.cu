@@ -98,7 +98,10 @@ template <int D> struct MmaShape {
     static constexpr int kV = D == 256 ? 128 : D;   // value columns a CTA
     static constexpr int kHalves = D / kV;          // CTAs that share a stretch, each with its columns
     static constexpr int kPer = kHalves + 1;        // ring slots a key tile: K by kV channels, V
-    // Cost of an item's way in and out (some 9 us) beside a key tile's kCostTwo.
+    // Cost of an item's way in and out (some 9 us) beside a key tile's kCostTwo.  With 0, 12,
+    // 16, 24, 32: head size 128, 24 requests x 4 key heads x 488 rows over up to 9000 tokens
+    // 136, 128, 126, 124, 125 us; 256, 20 x 2 x 248 over up to 6555 100, 93, 94, 97, 98; 64,
+    // 20 x 16 x 64 over up to 9286 134, 127, 127, 130, 135.
     static constexpr int kCostItem = D == 256 ? 12 : D == 128 ? 24 : 16;
     static constexpr uint32_t kSlotBytes = (kV / 64) * kBlock, kQBytes = (D / 64) * kBlock;
     // K and V tiles as the copies leave them: groups of 8 keys, in a group 64 channels
