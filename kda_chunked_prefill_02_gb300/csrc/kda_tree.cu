@@ -730,35 +730,34 @@ TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, fl
     // The 128-row products where there are more rows than one product of the warp-level
     // kernel takes and enough work to outlast their longer way in and out (some 15 us).
     // In one block of 32 rows the rows kernel reads a key once too, and what decides is the
-    // context (152 items x 20 rows over up to 1000 tokens 32 us against 24, over 4000 51
-    // against 60; 8 items 21 against 12 and 17.5 against 20); in more it reads a key once a
-    // block (304 x 248 over 120 tokens 36 us against 91, 16 x 248 over 500 26 against 20, 8 x
-    // 64 over 1000 24 against 15; head size 256, blocks of 16: 40 x 128 over 120 23 us both
-    // ways, 152 x 64 over 4000 125 against 275, 306 x 40 over 10 47 against 25, 304 x 512 over 4000 653 against 4421).  Pages
-    // have to be whole 8-row groups of a tile (and the line of work, in key tiles, stays
-    // inside 32 bits).
+    // context (20 rows, 8 items over up to 1000 tokens 17 us against 11, over 4000 17 against
+    // 19; 304 items 37 against 33 and 77 against 84); in more it reads a key once a block (80
+    // items x 64 rows over up to 1000 tokens 21 us against 24, over 120 20 against 12; 16 x 64
+    // over 2000 21 against 17; 304 x 248 over 120 34 against 79, 16 x 248 over 500 26 against
+    // 18; head size 256, blocks of 16: 152 x 64 over 4000 125 against 275, 306 x 40 over 10 47
+    // against 25, 304 x 512 over 4000 653 against 4421).  Pages have to be whole 8-row groups
+    // of a tile (and the line of work, in key tiles, stays inside 32 bits).
     const int block = rows_per_block(rows, D);
     const int64_t row_blocks = (rows + block - 1) / block, items = (int64_t)R * Hk * row_blocks;
     const int64_t work = items * (max_len + 64);
     t.mma = rows > 16 && page % 8 == 0 && num_sms > 1 && scale > 0.f && max_len / 128 + 1 < (1 << 22) &&
-            (row_blocks == 1 ? max_len >= 4096
-                             : row_blocks == 2 ? max_len >= 1024 && work >= 65536 : work >= 98304);
+            (row_blocks == 1 ? max_len >= 2560 : work >= 98304 && (row_blocks > 2 || max_len >= 512));
     // The rows kernel's cut (also for a cache without a tensor map); at_once is what the
     // tiles in flight leave room for, or for D 64 the registers.
     const int at_once = num_sms * (D == 64 ? 4 : D == 128 ? 2 : 1);
     const int64_t tiles = (max_len + kTile - 1) / kTile;
     // Fewer items than CTAs at once: clusters of up to 8, at least 128 tokens a CTA (one
-    // request, 2 key heads, 1000 tokens: 6.8 us, 9 as a line), until a CTA's tiles outweigh
-    // the line's second launch: 48 items of up to 1000 tokens 12.3 us and 13.8 as a line,
-    // 2000 17.1 and 16.6, 4000 27 and 21, 160 items of up to 4000 79 and 47, 80 of head size
-    // 256 107 and 55; head size 64 72 items of up to 4000 15.5 and 18, 240 37 and 37.  Where
-    // clusters of one fill the GPU nearly as well, the line pays late (304 items, up to 2000
-    // tokens: 45 us and 47, 4000: 82 and 73).
+    // request, 2 key heads, 1000 tokens: 8.5 us, 10.2 as a line), until a CTA's tiles outweigh
+    // the line's second launch: 8 rows, 48 items of up to 1000 tokens 11.0 us and 12.1 as a
+    // line, 1500 13.3 and 12.5, 4000 25 and 18, 160 items of up to 4000 81 and 43, 80 of head
+    // size 256 107 and 50; head size 64, 72 items of up to 4000 14.5 and 15.6, 8000 22.6 and
+    // 22.0.  Where a CTA an item fills the GPU nearly as well, the line pays late (304 items
+    // of up to 4000 tokens 82 us and 69).
     int64_t parts = items > 0 ? at_once / items : 1;
     if (parts > (tiles + 1) / 2) parts = (tiles + 1) / 2;
     t.cluster = parts >= 8 ? 8 : parts >= 4 ? 4 : parts >= 2 ? 2 : 1;
     t.line = R <= kLineMax && items <= at_once && items * tiles < (1 << 30) &&
-             tiles > t.cluster * (items * 4 > at_once * 3 ? 40 : D == 64 ? 16 : 8);
+             tiles > t.cluster * (items * 8 > at_once * 7 ? 24 : D == 64 ? 12 : 5);
     if (t.line) t.cluster = 1;
     t.row_grid = t.line ? at_once : 0;
     // Ranked where the items outnumber the CTAs that run at once: 100 requests x 8 key heads
