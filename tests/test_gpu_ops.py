@@ -347,6 +347,13 @@ def test_tree_pages_of_the_kernel_for_many_rows(page, heads_first, D):
     _tree_case(page, [513, 2, 127, 300, 0], 20, 12, 3, D, page, F16, heads_first=heads_first, room=ROOM)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("N", [34, 48, 49, 100])
+def test_tree_a_last_row_tile_by_itself(D, N):
+    """Rows a little past 256, 384 and 768: the last pair of 128-row tiles full, half or hardly used."""
+    _tree_case(N, [700, 5, 130], N, 8, 1, D, 16, BF16, room=ROOM)
+
+
 @pytest.mark.parametrize("D,Hq,Hk,N", [(64, 4, 2, 3), (128, 8, 2, 1), (128, 12, 3, 8), (256, 16, 2, 1), (256, 2, 1, 20)])
 @pytest.mark.parametrize("page", [3, 24, 64])
 def test_tree_long_and_short_contexts_together(D, Hq, Hk, N, page):
