@@ -90,7 +90,7 @@ kda_status kda_short_conv(const kda_short_conv_args* args, void* stream);
  * RMS norm of every query and key head and the rotation by the token's
  * position, in one pass over q and k:
  *
- *     y = x / sqrt(mean(x^2) + norm_eps) * weight        (norm = 1; else y = x)
+ *     y = x / sqrt(mean(x^2) + norm_eps) * weight   (norm = 1; else y = x, the weights unread)
  *     (a, b) -> s (a cos t - b sin t, a sin t + b cos t),   t = position * inv_freq[i],
  *
  * for i < rot_dim / 2, s = rope_scale, on the pairs (a, b) = (y[i], y[i + rot_dim/2])

@@ -137,7 +137,8 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, void* stream) {
     memset(&p, 0, sizeof(p));
     p.q = a->q; p.k = a->k; p.v = a->v; p.q_out = a->q_out; p.k_out = a->k_out;
     p.k_cache = a->k_cache; p.v_cache = a->v_cache; p.slots = a->slots; p.positions = a->positions;
-    p.inv_freq = a->inv_freq; p.q_w = a->q_weight; p.k_w = a->k_weight; p.status = a->device_status;
+    p.inv_freq = a->inv_freq; p.status = a->device_status;
+    if (a->norm) { p.q_w = a->q_weight; p.k_w = a->k_weight; }   // the weights are the norm's
     for (int i = 0; i < 3; ++i) {
         p.qs[i] = a->q_stride[i]; p.ks[i] = a->k_stride[i]; p.vs[i] = a->v_stride[i];
         p.qos[i] = a->q_out_stride[i]; p.kos[i] = a->k_out_stride[i];

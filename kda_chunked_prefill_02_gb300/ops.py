@@ -135,7 +135,7 @@ def kda_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
     q [T, Hq, D] and k [T, Hk, D] (or [B, T, H, D]) bf16 or fp16; positions int32
     [T] ([B, T]); inv_freq fp32 [rot_dim / 2] (rope_frequencies) or None for the
     norm alone; weights [D] in q's type or fp32 (None: ones); norm=False
-    rotates only.  With k_cache [pages, page_size, Hk, D] and slots int64 [T]
+    rotates only and leaves the weights unread.  With k_cache [pages, page_size, Hk, D] and slots int64 [T]
     (page * page_size + row, negative: none) the keys go to the cache, and v to
     v_cache; keys are then returned only if k_out is given.  q_out and k_out may
     be q and k themselves.  Returns (q_out, k_out).
