@@ -52,9 +52,10 @@ extern "C" {
  * entry holds the last W - 1 inputs up to and including the sequence's first
  * accepted[n] tokens (device int32 [num_seqs], 0 .. length; NULL: all tokens).
  * out == NULL: only the states are updated (the commit of accepted drafts).
- * A slot or accepted entry out of range, or cu_seqlens not running from 0 to
- * seqlen without decreasing, is reported in device_status and the sequence is
- * left out.
+ * A slot or accepted entry out of range is reported in device_status and the
+ * sequence is left out.  cu_seqlens that does not run from 0 to seqlen without
+ * decreasing is reported too, and which of the call's sequences are computed is
+ * then not defined (rows of x and out and pool entries of the call alone are used).
  *
  * C (channels) a multiple of 8, W in 2..4, norm_channels a multiple of 128 of
  * at most C; x and out do not overlap.  weight [C, W] and bias [C] contiguous.

@@ -174,19 +174,28 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvPara
     __shared__ Piece ring[kRing][kConvThreads];
     const int cb = blockIdx.x % p.cblocks, tile = blockIdx.x / p.cblocks;
     const int tid = threadIdx.x, c0 = (cb * kConvThreads + tid) * kConvVec;
+    const int total = (int)p.total;
+    if (p.cu && cb == 0 && p.status) {
+        // Every pair of cu is looked at once: the tiles below search cu as a sorted
+        // array, and need not meet the places where it is not.
+        const int64_t step = (int64_t)(gridDim.x / p.cblocks) * kConvThreads;
+        for (int64_t n = (int64_t)tile * kConvThreads + tid; n < p.N; n += step) {
+            const int s = p.cu[n], e = p.cu[n + 1];
+            if (s < 0 || e < s || e > total || (n == 0 && s != 0) || (n == p.N - 1 && e != total))
+                atomicExch(p.status, 1);
+        }
+    }
     if (c0 - (tid & 31) * kConvVec >= p.C) return;  // the whole warp is past the channels
     const bool act = c0 < p.C;
     const int cc = act ? c0 : 0;
     const Channels<T, W, kWF32> ch(p, c0, cc);
 
-    const int total = (int)p.total;
     const int t0 = tile * p.tile, t1 = min(t0 + p.tile, total);
     const bool last = t1 == total;
     auto start = [&](int n) -> int { return p.cu ? p.cu[n] : n * p.T; };
     auto report = [&]() {
         if (p.status && tid == 0) atomicExch(p.status, 1);
     };
-    if (p.cu && tile == 0 && (p.cu[0] != 0 || p.cu[p.N] != total)) report();
 
     // first sequence that starts at or after t0, or the one that runs into it
     int n;

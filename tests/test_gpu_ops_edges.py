@@ -21,6 +21,38 @@ def _i32(v):
     return torch.tensor(v, dtype=torch.int32)
 
 
+# ---------------------------------------------------------------- short convolution
+def _inversions():
+    even = list(range(0, 1401))                  # one token each, two neighbours' bounds the wrong way round
+    swapped = even[:700] + [even[701], even[700]] + even[702:]
+    return {"skipped by a search": [0, 100, 10, 20, 200],
+            "skipped by a search, long": [0, 100000, 10000, 20000, 200000],
+            "one pair of many": swapped,
+            "long, at the end": [0, 60000, 60001, 60000, 130000],
+            "below zero": [0, -5, 50, 200], "past the tokens": [0, 300, 150, 200],
+            "from one": [1, 50, 200], "short of the tokens": [0, 50, 199]}
+
+
+@pytest.mark.parametrize("what", sorted(_inversions()))
+@pytest.mark.parametrize("C", [8, 1536])
+def test_conv_reports_every_decrease_of_cu_seqlens(what, C):
+    """Wherever the tiles' own search looks, a cu_seqlens that does not run from 0 to the
+    token count without decreasing is reported; the sorted one of the same length is not."""
+    cu = _inversions()[what]
+    total = max(200, max(cu[:-1]) if what == "one pair of many" else 0, cu[-1] if cu[-1] > 200 else 0)
+    g = _gen(102)
+    x, w = _rand(g, (total, C), BF16).cuda(), _rand(g, (C, 4), torch.float32).cuda()
+    st = torch.zeros(len(cu) - 1, 3, C, dtype=BF16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kda_short_conv(x, w, conv_state=st, cu_seqlens=_i32(cu).cuda(), device_status=status)
+    assert status.item() == 1
+    status.zero_()
+    good = sorted(min(max(c, 0), total) for c in cu)
+    good[0], good[-1] = 0, total
+    K.kda_short_conv(x, w, conv_state=st, cu_seqlens=_i32(good).cuda(), device_status=status)
+    assert status.item() == 0
+
+
 # ---------------------------------------------------------------- norm and rotation
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("wdtype", [torch.float32, BF16])
