@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvPara
     const int cc = act ? c0 : 0;
     const Channels<T, W, kWF32> ch(p, c0, cc);
 
-    const int t0 = tile * p.tile, t1 = min(t0 + p.tile, total);
+    const int t0 = tile * p.tile, t1 = (int)min((unsigned)t0 + p.tile, (unsigned)total);   // total may be 2^31 - 1
     const bool last = t1 == total;
     auto start = [&](int n) -> int { return p.cu ? p.cu[n] : n * p.T; };
     auto report = [&]() {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvPara
         const int64_t ostep = p.os[1];
         int g = 0;
         int t = tb;
-        for (; t + kStep <= te; t += kStep) {
+        for (const int last_step = te - kStep; t <= last_step; t += kStep) {   // te may be 2^31 - 1
             cp_async_wait<kRing / kStep - 2>();
             // the group that comes in goes to the rows that the last round emptied
             fetch(mine + ((g + kRing / kStep - 1) % (kRing / kStep)) * kGroup);

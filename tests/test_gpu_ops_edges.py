@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import kda_chunked_prefill_02_gb300 as K
-from ops_test_util import rope_reference, within
+from ops_test_util import conv_reference, rope_reference, within
 
 pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
@@ -51,6 +51,35 @@ def test_conv_reports_every_decrease_of_cu_seqlens(what, C):
     good[0], good[-1] = 0, total
     K.kda_short_conv(x, w, conv_state=st, cu_seqlens=_i32(good).cuda(), device_status=status)
     assert status.item() == 0
+
+
+MOST = (1 << 31) - 1   # tokens of a call
+
+
+def test_conv_state_of_a_sequence_in_the_last_tile_of_the_longest_call():
+    """Sums of token numbers near 2^31: the tile that holds the last tokens still owns its
+    sequence.  x is one row seen 2^31 - 1 times."""
+    g = _gen(103)
+    row, w = _rand(g, (1, 8), BF16).cuda(), _rand(g, (8, 4), torch.float32).cuda()
+    st = _rand(g, (2, 3, 8), BF16).cuda()
+    K.kda_short_conv(row.expand(MOST, 8), w, conv_state=st, cu_seqlens=_i32([0, MOST - 5, MOST]).cuda(),
+                     state_only=True)
+    assert torch.equal(st, row.expand(2, 3, 8))
+
+
+def test_conv_outputs_of_the_longest_sequence():
+    """One sequence of 2^31 - 1 equal tokens: from the fourth on all outputs are equal, up
+    to the last, and nothing is written behind them."""
+    g = _gen(104)
+    row, w = _rand(g, (1, 8), BF16).cuda(), _rand(g, (8, 4), torch.float32).cuda()
+    buf = torch.empty(MOST + 4097, 8, dtype=BF16, device="cuda")
+    buf[-8192:] = 7.0
+    K.kda_short_conv(row.expand(MOST, 8), w, cu_seqlens=_i32([0, MOST]).cuda(), out=buf[:MOST])
+    y, bound, _ = conv_reference(row.cpu().expand(6, 8), w.cpu(), starts=[0], lengths=[6])
+    within(buf[:6], y, bound)
+    assert torch.equal(buf[MOST - 4095:MOST], buf[5:6].expand(4095, 8))
+    assert torch.equal(buf[MOST // 2:MOST // 2 + 64], buf[5:6].expand(64, 8))
+    assert bool((buf[MOST:] == 7.0).all())
 
 
 # ---------------------------------------------------------------- norm and rotation
