@@ -3,9 +3,11 @@
 // only; ops.py holds the documented functions and calls these with every
 // argument in place.  It is native because for a single token the call is the
 // host's time: 13 us in Python for a convolution of one token, most of it looking
-// at tensors.  Everything runs on the current stream of the tensors' device.
+// at tensors.  Everything runs on the current stream of the device that all of a
+// call's tensors are on.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -46,8 +48,18 @@ const at::Tensor* tensor(const char* name, PyObject* o, bool optional = false) {
     if (o == Py_None && optional) return nullptr;
     refuse(PyExc_TypeError, std::string(name) + " must be a tensor");
 }
-void need_cuda(const char* name, const at::Tensor& t, c10::ScalarType dtype) {
+// What a call's tensors have in common: the device of its first one.
+struct Call {
+    c10::Device device;
+};
+void need_device(const Call& c, const char* name, const at::Tensor& t) {
     if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + " must be a CUDA tensor");
+    if (t.device() != c.device)
+        refuse(PyExc_ValueError, std::string(name) + " is on " + t.device().str() + ", the call's first tensor on " +
+                                     c.device.str());
+}
+void need_cuda(const Call& c, const char* name, const at::Tensor& t, c10::ScalarType dtype) {
+    need_device(c, name, t);
     if (t.scalar_type() != dtype)
         refuse(PyExc_TypeError, std::string(name) + " must be " + text(dtype) + ", got " + text(t.scalar_type()));
 }
@@ -60,41 +72,42 @@ int32_t elem(const char* name, const at::Tensor& t) {
 }
 // Address of a contiguous CUDA tensor of one type and shape (None: null).
 template <typename T = void>
-T* flat(const char* name, PyObject* o, c10::ScalarType dtype, at::IntArrayRef shape) {
+T* flat(const Call& c, const char* name, PyObject* o, c10::ScalarType dtype, at::IntArrayRef shape) {
     const at::Tensor* t = tensor(name, o, true);
     if (!t) return nullptr;
-    need_cuda(name, *t, dtype);
+    need_cuda(c, name, *t, dtype);
     if (t->sizes() != shape || !t->is_contiguous())
         refuse(PyExc_ValueError, std::string(name) + " must be contiguous of shape " + text(shape) + ", got " +
                                      text(t->sizes()));
     return static_cast<T*>(t->data_ptr());
 }
-int32_t* status_word(PyObject* o) {
+int32_t* status_word(const Call& c, PyObject* o) {
     const at::Tensor* t = tensor("device_status", o, true);
     if (!t) return nullptr;
-    need_cuda("device_status", *t, at::kInt);
+    need_cuda(c, "device_status", *t, at::kInt);
     if (t->numel() < 1) refuse(PyExc_ValueError, "device_status must hold an int32");
     return static_cast<int32_t*>(t->data_ptr());
 }
 // A strided operand of a given shape with a channel dim of stride 1.
-void strided(const char* name, const at::Tensor& t, at::IntArrayRef shape, c10::ScalarType dtype) {
-    need_cuda(name, t, dtype);
+void strided(const Call& c, const char* name, const at::Tensor& t, at::IntArrayRef shape, c10::ScalarType dtype) {
+    need_cuda(c, name, t, dtype);
     if (t.sizes() != shape || t.stride(-1) != 1)
         refuse(PyExc_ValueError, std::string(name) + " must have shape " + text(shape) +
                                      " and a channel dim of stride 1, got " + text(t.sizes()));
 }
 // (batch, token, head) strides of a [T, H, D] or [B, T, H, D] tensor.
-void heads(const char* name, const at::Tensor& t, at::IntArrayRef shape, c10::ScalarType dtype, int64_t (&s)[3]) {
-    strided(name, t, shape, dtype);
+void heads(const Call& c, const char* name, const at::Tensor& t, at::IntArrayRef shape, c10::ScalarType dtype,
+           int64_t (&s)[3]) {
+    strided(c, name, t, shape, dtype);
     const bool batched = shape.size() == 4;
     s[0] = batched ? t.stride(0) : 0;
     s[1] = t.stride(batched);
     s[2] = t.stride(1 + batched);
 }
 // (page, row, head) strides of a cache.
-void cache(const char* name, const at::Tensor& t, int64_t num_heads, int64_t dim, c10::ScalarType dtype,
-           int64_t (&s)[3]) {
-    need_cuda(name, t, dtype);
+void cache(const Call& c, const char* name, const at::Tensor& t, int64_t num_heads, int64_t dim,
+           c10::ScalarType dtype, int64_t (&s)[3]) {
+    need_cuda(c, name, t, dtype);
     if (t.dim() != 4 || t.size(2) != num_heads || t.size(3) != dim || t.stride(3) != 1)
         refuse(PyExc_ValueError, std::string(name) + " must be [pages, page_size, " + std::to_string(num_heads) + ", " +
                                      std::to_string(dim) + "] with a channel dim of stride 1");
@@ -146,6 +159,7 @@ PyObject* short_conv(PyObject* const* o) {
     const at::Tensor &x = *tensor("x", o[0]), &w = *tensor("weight", o[1]);
     kda_short_conv_args a{};
     a.dtype = elem("x", x);
+    const Call c{x.device()};
     const auto dt = x.scalar_type();
     const at::Tensor *pool = tensor("conv_state", o[3], true), *cu = tensor("cu_seqlens", o[6], true);
     if (x.dim() != (cu ? 2 : 3) || x.stride(-1) != 1)
@@ -156,7 +170,7 @@ PyObject* short_conv(PyObject* const* o) {
         a.num_seqs = cu->size(0) - 1;
         a.seqlen = x.size(0);
         a.x_stride[1] = x.stride(0);
-        a.cu_seqlens = flat<int32_t>("cu_seqlens", o[6], at::kInt, {a.num_seqs + 1});
+        a.cu_seqlens = flat<int32_t>(c, "cu_seqlens", o[6], at::kInt, {a.num_seqs + 1});
     } else {
         a.num_seqs = x.size(0);
         a.seqlen = x.size(1);
@@ -168,36 +182,34 @@ PyObject* short_conv(PyObject* const* o) {
     const bool f32 = w.scalar_type() == at::kFloat;
     const bool state_only = truth(o[12]);
     a.x = x.data_ptr();
-    a.weight = flat("weight", o[1], f32 ? at::kFloat : dt, {C, W});
-    a.bias = flat<float>("bias", o[2], at::kFloat, {C});
+    a.weight = flat(c, "weight", o[1], f32 ? at::kFloat : dt, {C, W});
+    a.bias = flat<float>(c, "bias", o[2], at::kFloat, {C});
     if (pool) {
         if (pool->dim() < 1) refuse(PyExc_ValueError, "conv_state must be [P, W-1, C]");
         a.pool_size = pool->size(0);
-        a.conv_state = flat("conv_state", o[3], dt, {a.pool_size, W - 1, C});
+        a.conv_state = flat(c, "conv_state", o[3], dt, {a.pool_size, W - 1, C});
         if (o[4] == Py_None && a.pool_size < a.num_seqs)
             refuse(PyExc_ValueError, "conv_state has " + std::to_string(a.pool_size) + " entries for " +
                                          std::to_string(a.num_seqs) + " sequences");
     } else if (state_only) {
         refuse(PyExc_ValueError, "state_only needs conv_state");
     }
-    a.slot = flat<int32_t>("slot", o[4], at::kInt, {a.num_seqs});
-    a.has_state = flat<int32_t>("has_state", o[5], at::kInt, {a.num_seqs});
-    a.accepted = flat<int32_t>("accepted", o[7], at::kInt, {a.num_seqs});
-    a.device_status = status_word(o[13]);
+    a.slot = flat<int32_t>(c, "slot", o[4], at::kInt, {a.num_seqs});
+    a.has_state = flat<int32_t>(c, "has_state", o[5], at::kInt, {a.num_seqs});
+    a.accepted = flat<int32_t>(c, "accepted", o[7], at::kInt, {a.num_seqs});
+    a.device_status = status_word(c, o[13]);
     a.channels = C;
     a.norm_channels = integer(o[9]);
     a.width = (int32_t)W;
     a.weight_dtype = f32 ? KDA_DTYPE_F32 : a.dtype;
     a.silu = truth(o[8]);
     a.norm_eps = real(o[10]);
+    const at::Tensor* given = state_only ? nullptr : tensor("out", o[11], true);
+    if (given) strided(c, "out", *given, x.sizes(), dt);
+    const c10::cuda::CUDAGuard guard(c.device);   // the library launches on the current device
     at::Tensor out;
     if (!state_only) {
-        if (const at::Tensor* given = tensor("out", o[11], true)) {
-            strided("out", *given, x.sizes(), dt);
-            out = *given;
-        } else {
-            out = at::empty(x.sizes(), x.options());
-        }
+        out = given ? *given : at::empty(x.sizes(), x.options());
         a.out = out.data_ptr();
         a.out_stride[0] = cu ? 0 : out.stride(0);
         a.out_stride[1] = out.stride(cu ? 0 : 1);
@@ -214,6 +226,7 @@ PyObject* qk_norm_rope(PyObject* const* o) {
                      *kc = tensor("k_cache", o[13], true), *vc = tensor("v_cache", o[14], true);
     kda_qk_norm_rope_args a{};
     a.dtype = elem("q", q);
+    const Call c{q.device()};
     const auto dt = q.scalar_type();
     const int64_t nd = q.dim();
     if (nd != 3 && nd != 4) refuse(PyExc_ValueError, "q must be [T, H, D] or [B, T, H, D]");
@@ -228,8 +241,8 @@ PyObject* qk_norm_rope(PyObject* const* o) {
     if (freq) {
         if (freq->dim() != 1) refuse(PyExc_ValueError, "inv_freq must be fp32 [rot_dim / 2]");
         a.rot_dim = 2 * freq->size(0);
-        a.inv_freq = flat<float>("inv_freq", o[3], at::kFloat, {freq->size(0)});
-        a.positions = flat<int32_t>("positions", o[2], at::kInt, lead);
+        a.inv_freq = flat<float>(c, "inv_freq", o[3], at::kFloat, {freq->size(0)});
+        a.positions = flat<int32_t>(c, "positions", o[2], at::kInt, lead);
     }
     const at::Tensor *qw = tensor("q_weight", o[4], true), *kw = tensor("k_weight", o[5], true);
     if (qw && kw && qw->scalar_type() != kw->scalar_type())
@@ -237,45 +250,48 @@ PyObject* qk_norm_rope(PyObject* const* o) {
     const at::Tensor* any = qw ? qw : kw;
     const bool f32 = !any || any->scalar_type() == at::kFloat;
     a.weight_dtype = f32 ? KDA_DTYPE_F32 : a.dtype;
-    a.q_weight = flat("q_weight", o[4], f32 ? at::kFloat : dt, {a.head_dim});
-    a.k_weight = flat("k_weight", o[5], f32 ? at::kFloat : dt, {a.head_dim});
-    heads("q", q, q.sizes(), dt, a.q_stride);
-    heads("k", k, k.sizes(), dt, a.k_stride);
+    a.q_weight = flat(c, "q_weight", o[4], f32 ? at::kFloat : dt, {a.head_dim});
+    a.k_weight = flat(c, "k_weight", o[5], f32 ? at::kFloat : dt, {a.head_dim});
+    heads(c, "q", q, q.sizes(), dt, a.q_stride);
+    heads(c, "k", k, k.sizes(), dt, a.k_stride);
     a.q = q.data_ptr();
     a.k = k.data_ptr();
     if (kc) {
-        cache("k_cache", *kc, a.num_k_heads, a.head_dim, dt, a.k_cache_stride);
+        cache(c, "k_cache", *kc, a.num_k_heads, a.head_dim, dt, a.k_cache_stride);
         a.k_cache = kc->data_ptr();
         a.num_pages = kc->size(0);
         a.page_size = kc->size(1);
-        a.slots = flat<int64_t>("slots", o[15], at::kLong, lead);
-        if (!a.slots && a.batch * a.seqlen > 0) refuse(PyExc_ValueError, "k_cache needs slots");
+        a.slots = flat<int64_t>(c, "slots", o[15], at::kLong, lead);
+        if (o[15] == Py_None && a.batch * a.seqlen > 0) refuse(PyExc_ValueError, "k_cache needs slots");
         if (vc) {
-            cache("v_cache", *vc, a.num_k_heads, a.head_dim, dt, a.v_cache_stride);
+            cache(c, "v_cache", *vc, a.num_k_heads, a.head_dim, dt, a.v_cache_stride);
             if (!v || vc->sizes() != kc->sizes()) refuse(PyExc_ValueError, "v_cache needs v, and k_cache's shape");
-            heads("v", *v, k.sizes(), dt, a.v_stride);
+            heads(c, "v", *v, k.sizes(), dt, a.v_stride);
             a.v = v->data_ptr();
             a.v_cache = vc->data_ptr();
         }
     } else if (vc || o[15] != Py_None) {
         refuse(PyExc_ValueError, "slots and v_cache need k_cache");
     }
+    const at::Tensor *q_given = tensor("q_out", o[10], true), *k_given = tensor("k_out", o[11], true);
+    if (q_given) heads(c, "q_out", *q_given, q.sizes(), dt, a.q_out_stride);
+    if (k_given) heads(c, "k_out", *k_given, k.sizes(), dt, a.k_out_stride);
+    a.device_status = status_word(c, o[16]);
+    const c10::cuda::CUDAGuard guard(c.device);
     at::Tensor q_out, k_out;
-    if (const at::Tensor* given = tensor("q_out", o[10], true)) q_out = *given;
-    else q_out = at::empty(q.sizes(), q.options());
-    heads("q_out", q_out, q.sizes(), dt, a.q_out_stride);
+    q_out = q_given ? *q_given : at::empty(q.sizes(), q.options());
+    if (!q_given) heads(c, "q_out", q_out, q.sizes(), dt, a.q_out_stride);
     a.q_out = q_out.data_ptr();
-    if (const at::Tensor* given = tensor("k_out", o[11], true)) k_out = *given;
+    if (k_given) k_out = *k_given;
     else if (!kc) k_out = at::empty(k.sizes(), k.options());
     if (k_out.defined()) {
-        heads("k_out", k_out, k.sizes(), dt, a.k_out_stride);
+        if (!k_given) heads(c, "k_out", k_out, k.sizes(), dt, a.k_out_stride);
         a.k_out = k_out.data_ptr();
     }
     a.norm = truth(o[6]);
     a.norm_eps = real(o[7]);
     a.interleaved = truth(o[8]);
     a.rope_scale = real(o[9]);
-    a.device_status = status_word(o[16]);
     done(kda_qk_norm_rope(&a, stream_of(q)));
     PyObject* qo = o[10] != Py_None ? Py_NewRef(o[10]) : THPVariable_Wrap(q_out);
     PyObject* ko = o[11] != Py_None ? Py_NewRef(o[11]) : k_out.defined() ? THPVariable_Wrap(k_out) : none();
@@ -292,26 +308,36 @@ PyObject* tree_attention(PyObject* const* o) {
                      &table = *tensor("page_table", o[3]);
     kda_tree_attention_args a{};
     a.dtype = elem("q", q);
+    const Call c{q.device()};
     const auto dt = q.scalar_type();
     if (q.dim() != 4 || q.stride(3) != 1)
         refuse(PyExc_ValueError, "q must be [R, N, Hq, D] with a channel dim of stride 1");
     const int64_t R = q.size(0), N = q.size(1), Hq = q.size(2), D = q.size(3);
-    if (!kc.is_cuda() || kc.dim() != 4) refuse(PyExc_ValueError, "k_cache must be a CUDA tensor [pages, page_size, Hk, D]");
+    need_device(c, "k_cache", kc);
+    if (kc.dim() != 4) refuse(PyExc_ValueError, "k_cache must be [pages, page_size, Hk, D]");
     a.num_k_heads = kc.size(2);
-    cache("k_cache", kc, a.num_k_heads, D, dt, a.k_cache_stride);
-    cache("v_cache", vc, a.num_k_heads, D, dt, a.v_cache_stride);
+    cache(c, "k_cache", kc, a.num_k_heads, D, dt, a.k_cache_stride);
+    cache(c, "v_cache", vc, a.num_k_heads, D, dt, a.v_cache_stride);
     if (vc.sizes() != kc.sizes()) refuse(PyExc_ValueError, "k_cache and v_cache must have the same shape");
-    need_cuda("page_table", table, at::kInt);
+    need_cuda(c, "page_table", table, at::kInt);
     if (table.dim() != 2 || table.size(0) != R || (table.size(1) > 1 && table.stride(1) != 1))
         refuse(PyExc_ValueError, "page_table must be int32 [R, pages] with contiguous rows");
-    at::Tensor out, lse, ws;
-    if (const at::Tensor* given = tensor("out", o[9], true)) {
-        strided("out", *given, q.sizes(), dt);
-        out = *given;
-    } else {
-        out = at::empty(q.sizes(), q.options());
+    if (o[4] == Py_None) refuse(PyExc_TypeError, "context_lens must be a tensor");
+    a.context_lens = flat<int32_t>(c, "context_lens", o[4], at::kInt, {R});
+    a.tree_mask = flat<uint64_t>(c, "tree_mask", o[5], at::kLong, {R, N, (N + 63) / 64});
+    a.num_nodes = flat<int32_t>(c, "num_nodes", o[6], at::kInt, {R});
+    a.device_status = status_word(c, o[12]);
+    const at::Tensor *given = tensor("out", o[9], true), *given_ws = tensor("workspace", o[11], true);
+    if (given) strided(c, "out", *given, q.sizes(), dt);
+    if (given_ws) {
+        need_cuda(c, "workspace", *given_ws, at::kByte);
+        if (!given_ws->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
     }
+    a.max_context = o[8] == Py_None ? 0 : integer(o[8]);
+    a.scale = o[7] == Py_None ? (D > 0 ? 1.f / sqrtf((float)D) : 1.f) : real(o[7]);
     const bool want_lse = truth(o[10]);
+    const c10::cuda::CUDAGuard guard(c.device);
+    at::Tensor out = given ? *given : at::empty(q.sizes(), q.options()), lse, ws;
     if (want_lse) {
         lse = at::empty({R, N, Hq}, q.options().dtype(at::kFloat));
         a.lse = static_cast<float*>(lse.data_ptr());
@@ -321,11 +347,6 @@ PyObject* tree_attention(PyObject* const* o) {
     a.v_cache = vc.data_ptr();
     a.out = out.data_ptr();
     a.page_table = static_cast<int32_t*>(table.data_ptr());
-    if (o[4] == Py_None) refuse(PyExc_TypeError, "context_lens must be a tensor");
-    a.context_lens = flat<int32_t>("context_lens", o[4], at::kInt, {R});
-    a.tree_mask = flat<uint64_t>("tree_mask", o[5], at::kLong, {R, N, (N + 63) / 64});
-    a.num_nodes = flat<int32_t>("num_nodes", o[6], at::kInt, {R});
-    a.device_status = status_word(o[12]);
     for (int i = 0; i < 3; ++i) {
         a.q_stride[i] = q.stride(i);
         a.out_stride[i] = out.stride(i);
@@ -338,15 +359,9 @@ PyObject* tree_attention(PyObject* const* o) {
     a.num_pages = kc.size(0);
     a.page_size = kc.size(1);
     a.pages_per_request = table.size(1);
-    a.max_context = o[8] == Py_None ? 0 : integer(o[8]);
-    a.scale = o[7] == Py_None ? (D > 0 ? 1.f / sqrtf((float)D) : 1.f) : real(o[7]);
-    if (const at::Tensor* given = tensor("workspace", o[11], true)) {
-        need_cuda("workspace", *given, at::kByte);
-        if (!given->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
-        ws = *given;
-    } else if (const size_t need = kda_tree_attention_workspace_size(&a)) {
+    if (given_ws) ws = *given_ws;
+    else if (const size_t need = kda_tree_attention_workspace_size(&a))
         ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-    }
     if (ws.defined()) {
         a.workspace = ws.data_ptr();
         a.workspace_bytes = (size_t)ws.numel();

@@ -1,0 +1,80 @@
+"""Host side of the operators in include/kda_ops.h at the edges (no GPU): refusals of the
+Python binding, the helpers' formulas, sizes near the ends of their types."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from kda_chunked_prefill_02_gb300 import build, ops as o
+    build.build()
+    o._fn()
+    return o
+
+
+# ---------------------------------------------------------------- tensors on two devices
+def _fake(make):
+    """Tensors of a device and a shape without memory: what a check may look at."""
+    if 0 < torch.cuda.device_count() < 2:
+        pytest.skip("one GPU: torch makes a tensor without memory only for a GPU that is there")
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        return make()
+
+
+@pytest.mark.filterwarnings("ignore")
+@pytest.mark.parametrize("arg", ["weight", "bias", "conv_state", "slot", "has_state", "accepted", "out",
+                                 "device_status"])
+def test_conv_tensors_on_one_device(ops, arg):
+    def make():
+        d = {a: "cuda:1" if a == arg else "cuda:0" for a in
+             ("weight", "bias", "conv_state", "slot", "has_state", "accepted", "out", "device_status")}
+        i32 = dict(dtype=torch.int32)
+        return (torch.empty(2, 3, 256, dtype=BF16, device="cuda:0"), torch.empty(256, 4, device=d["weight"]),
+                dict(bias=torch.empty(256, device=d["bias"]),
+                     conv_state=torch.empty(2, 3, 256, dtype=BF16, device=d["conv_state"]),
+                     slot=torch.empty(2, device=d["slot"], **i32), has_state=torch.empty(2, device=d["has_state"], **i32),
+                     accepted=torch.empty(2, device=d["accepted"], **i32),
+                     out=torch.empty(2, 3, 256, dtype=BF16, device=d["out"]),
+                     device_status=torch.empty(1, device=d["device_status"], **i32)))
+    x, w, kw = _fake(make)
+    with pytest.raises(ValueError, match=arg + " is on cuda:1"):
+        ops.kda_short_conv(x, w, **kw)
+
+
+@pytest.mark.filterwarnings("ignore")
+@pytest.mark.parametrize("arg", ["k", "positions", "inv_freq", "q_weight", "v", "k_cache", "v_cache", "slots", "q_out",
+                                 "k_out", "device_status"])
+def test_rope_tensors_on_one_device(ops, arg):
+    def make():
+        def t(name, *shape, dtype=BF16):
+            return torch.empty(*shape, dtype=dtype, device="cuda:1" if name == arg else "cuda:0")
+        return (t("q", 5, 4, 128), t("k", 5, 2, 128), t("positions", 5, dtype=torch.int32),
+                t("inv_freq", 32, dtype=torch.float32),
+                dict(q_weight=t("q_weight", 128), v=t("v", 5, 2, 128), k_cache=t("k_cache", 3, 16, 2, 128),
+                     v_cache=t("v_cache", 3, 16, 2, 128), slots=t("slots", 5, dtype=torch.int64),
+                     q_out=t("q_out", 5, 4, 128), k_out=t("k_out", 5, 2, 128),
+                     device_status=t("device_status", 1, dtype=torch.int32)))
+    q, k, pos, freq, kw = _fake(make)
+    with pytest.raises(ValueError, match=arg + " is on cuda:1"):
+        ops.kda_qk_norm_rope(q, k, pos, freq, **kw)
+
+
+@pytest.mark.filterwarnings("ignore")
+@pytest.mark.parametrize("arg", ["k_cache", "v_cache", "page_table", "context_lens", "tree_mask", "num_nodes", "out",
+                                 "workspace", "device_status"])
+def test_tree_tensors_on_one_device(ops, arg):
+    def make():
+        def t(name, *shape, dtype=BF16):
+            return torch.empty(*shape, dtype=dtype, device="cuda:1" if name == arg else "cuda:0")
+        i32 = torch.int32
+        return (t("q", 2, 3, 4, 128), t("k_cache", 9, 16, 2, 128), t("v_cache", 9, 16, 2, 128),
+                t("page_table", 2, 4, dtype=i32), t("context_lens", 2, dtype=i32),
+                dict(tree_mask=t("tree_mask", 2, 3, 1, dtype=torch.int64), num_nodes=t("num_nodes", 2, dtype=i32),
+                     out=t("out", 2, 3, 4, 128), workspace=t("workspace", 4096, dtype=torch.uint8),
+                     device_status=t("device_status", 1, dtype=i32)))
+    q, kc, vc, table, ctx, kw = _fake(make)
+    with pytest.raises(ValueError, match=arg + " is on cuda:1"):
+        ops.kda_tree_attention(q, kc, vc, table, ctx, **kw)
