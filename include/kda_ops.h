@@ -172,7 +172,9 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  * q and out element (r, i, h, c) at r*s[0] + i*s[1] + h*s[2] + c; cache element
  * (page, row, h, c) likewise; tree_mask contiguous [R, max_nodes, ceil(max_nodes/64)];
  * lse contiguous fp32 [R, max_nodes, Hq] or NULL; page_table row r at
- * r*page_table_stride.
+ * r*page_table_stride.  out may be q itself (same pointer and strides; head size
+ * 256 then takes the kernel for few rows whatever their number), otherwise no
+ * overlap.
  * head_dim 64, 128 or 256; Hq a multiple of Hk; max_nodes <= 256.
  * max_context: an upper bound of context_lens that the host knows (<= 0: what
  * the page table can address); it sets how the work is cut, not the result's

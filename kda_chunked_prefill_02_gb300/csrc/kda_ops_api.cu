@@ -38,6 +38,10 @@ kda_status check_tree(const kda_tree_attention_args* a) {
         !strides8(a->q_stride) || !strides8(a->out_stride) || !strides8(a->k_cache_stride) ||
         !strides8(a->v_cache_stride))
         return KDA_ERR_UNSUPPORTED;
+    // results over the queries: each row over its own
+    const int64_t sizes[3] = {a->num_requests, a->max_nodes, a->num_q_heads};
+    for (int i = 0; i < 3; ++i)
+        if (a->out == a->q && sizes[i] > 1 && a->out_stride[i] != a->q_stride[i]) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
 

@@ -778,7 +778,10 @@ cudaError_t launch_tree_join(const TreeParams& p, int D, bool f16, cudaStream_t 
 
 cudaError_t launch_tree_attention(const TreeParams& p, const TreePlan& plan, int D, bool f16, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
-    if (plan.mma && launch_tree_mma(p, D, f16, plan.grid, s, &e)) return e;
+    // With head size 256 the two CTAs of an item both read all of its queries and each
+    // writes a half of its results, in no order: not where the results replace the queries.
+    const bool in_place = p.out == p.q;
+    if (plan.mma && !(in_place && D == 256) && launch_tree_mma(p, D, f16, plan.grid, s, &e)) return e;
     return f16 ? launch_rows<__half>(p, plan, D, s) : launch_rows<__nv_bfloat16>(p, plan, D, s);
 }
 

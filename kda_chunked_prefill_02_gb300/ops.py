@@ -215,7 +215,8 @@ def kda_tree_attention(q, k_cache, v_cache, page_table, context_lens, *, tree_ma
     [R, N, ceil(N/64)]: which nodes a node sees besides the whole context
     (tree_mask(parents); None: a chain, N = 1 a single token); num_nodes int32
     [R]: nodes in use; scale defaults to D^-0.5; max_context: a host upper bound
-    of context_lens (None: what the page table can address).  Returns out, or
+    of context_lens (None: what the page table can address); out may be q
+    itself.  Returns out, or
     (out, lse) with lse fp32 [R, N, Hq].
     """
     return _run((_binding or _native()).tree_attention, stream,

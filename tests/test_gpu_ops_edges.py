@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import kda_chunked_prefill_02_gb300 as K
-from ops_test_util import conv_reference, rope_reference, within
+from ops_test_util import conv_reference, rope_reference, tree_reference, within
 
 pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
@@ -107,3 +107,38 @@ def test_rope_without_the_norm_leaves_the_weights_alone(interleaved, wdtype):
         assert torch.equal(a, b)
     within(weighted[0], *rope_reference(q, pos, freq, None, norm=False, interleaved=interleaved))
     within(weighted[1], *rope_reference(k, pos, freq, None, norm=False, interleaved=interleaved))
+
+
+# ---------------------------------------------------------------- tree attention
+ROOM = 300000   # tokens a page table has room for: enough for the kernel for many rows
+
+
+def _tree_inputs(seed, ctx, N, Hq, Hk, D, page, dtype=BF16, room=0):
+    """q, caches, table, contexts on the host: every request its own pages."""
+    g = _gen(seed)
+    need = [(c + N + page - 1) // page for c in ctx]
+    table = torch.zeros((len(ctx), max(max(need), room // page)), dtype=torch.int32)
+    order, at = torch.randperm(sum(need), generator=g).to(torch.int32), 0
+    for r, n in enumerate(need):
+        table[r, :n] = order[at:at + n]
+        at += n
+    kc, vc = _rand(g, (sum(need), page, Hk, D), dtype), _rand(g, (sum(need), page, Hk, D), dtype)
+    return _rand(g, (len(ctx), N, Hq, D), dtype), kc, vc, table, _i32(ctx)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("N,Hq,Hk,room", [(1, 4, 2, 0), (3, 8, 2, 0), (40, 16, 2, 0), (40, 16, 2, ROOM),
+                                          (5, 8, 2, ROOM)])
+def test_tree_results_over_the_queries(D, N, Hq, Hk, room):
+    """out = q: every cut of both kernels, whole items and parts."""
+    q, kc, vc, table, ctx = _tree_inputs(105, [3000, 0, 17, 900], N, Hq, Hk, D, 16, room=room)
+    out, ob, _, _ = tree_reference(q, kc, vc, table, ctx)
+    dev = [t.cuda() for t in (kc, vc, table, ctx)]
+    qd = q.cuda()
+    apart = K.kda_tree_attention(qd, *dev)
+    assert torch.equal(qd.cpu(), q)
+    over = K.kda_tree_attention(qd, *dev, out=qd)
+    assert over is qd
+    within(over, out, ob)
+    if D != 256:   # the same kernel as apart from the queries: the same bits
+        assert torch.equal(over, apart)

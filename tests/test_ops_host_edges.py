@@ -1,5 +1,7 @@
 """Host side of the operators in include/kda_ops.h at the edges (no GPU): refusals of the
 Python binding, the helpers' formulas, sizes near the ends of their types."""
+import ctypes
+
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -78,3 +80,33 @@ def test_tree_tensors_on_one_device(ops, arg):
     q, kc, vc, table, ctx, kw = _fake(make)
     with pytest.raises(ValueError, match=arg + " is on cuda:1"):
         ops.kda_tree_attention(q, kc, vc, table, ctx, **kw)
+
+
+# ---------------------------------------------------------------- results over the queries
+PTR = 1 << 20   # never dereferenced: the checks fail first
+
+
+def _tree_args(ops, **kw):
+    a = ops.TreeAttentionArgs()
+    a.q = a.k_cache = a.v_cache = a.page_table = a.context_lens = PTR
+    a.out = 2 * PTR
+    for n in ("q", "out", "k_cache", "v_cache"):
+        for i, s in enumerate((8192, 1024, 128)):
+            setattr(a, "%s_stride%d" % (n, i), s)
+    a.num_requests, a.max_nodes, a.num_q_heads, a.num_k_heads, a.head_dim = 2, 4, 8, 2, 128
+    a.num_pages, a.page_size, a.pages_per_request, a.page_table_stride, a.scale = 100, 16, 50, 50, 0.1
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_tree_results_over_other_queries_are_refused(ops):
+    """out at q's address with other strides would put rows over queries that other CTAs read."""
+    run = lambda **kw: ops._fn().kda_tree_attention(ctypes.byref(_tree_args(ops, **kw)), None)  # noqa: E731
+    invalid = 1
+    for kw in (dict(out_stride0=4096), dict(out_stride1=2048), dict(out_stride2=256)):
+        assert run(out=PTR, **kw) == invalid, kw
+        assert run(**kw) != invalid, kw
+    assert run(out=PTR) != invalid
+    # the stride of a dim of size 1 says nothing
+    assert run(out=PTR, num_requests=1, out_stride0=4096) != invalid
