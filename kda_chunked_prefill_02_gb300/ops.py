@@ -175,7 +175,7 @@ def rope_frequencies(rot_dim, *, base=10000.0, scaling=None, factor=1.0, origina
             return rot_dim * math.log(original_context / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
         low = max(math.floor(index(fast_turns)), 0)
-        high = min(math.ceil(index(slow_turns)), rot_dim // 2 - 1)
+        high = min(math.ceil(index(slow_turns)), rot_dim - 1)   # may lie behind the last frequency
         keep = 1.0 - ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
         freq = freq / factor * (1.0 - keep) + freq * keep
         scale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0

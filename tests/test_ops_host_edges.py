@@ -1,6 +1,7 @@
 """Host side of the operators in include/kda_ops.h at the edges (no GPU): refusals of the
 Python binding, the helpers' formulas, sizes near the ends of their types."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -110,3 +111,22 @@ def test_tree_results_over_other_queries_are_refused(ops):
     assert run(out=PTR) != invalid
     # the stride of a dim of size 1 says nothing
     assert run(out=PTR, num_requests=1, out_stride0=4096) != invalid
+
+
+# ---------------------------------------------------------------- frequencies
+def test_frequencies_by_parts_where_all_are_faster_than_slow_turns(ops):
+    """A long original context: the ramp ends behind the last frequency, which is then not
+    divided by the whole factor."""
+    ctx, factor, n = 131072, 16.0, 64
+    f, _ = ops.rope_frequencies(2 * n, device="cpu")
+    g, _ = ops.rope_frequencies(2 * n, scaling="by_parts", factor=factor, original_context=ctx, device="cpu")
+    turns = f.double() * ctx / (2 * math.pi)
+    assert bool((turns > 2).all())
+    # f makes `turns` turns at index n ln(ctx / (2 pi turns)) / ln base
+    index = lambda t: n * math.log(ctx / (2 * math.pi * t)) / math.log(10000.0)  # noqa: E731
+    low, high = math.floor(index(32)), math.ceil(index(1))
+    assert 0 < low < n - 1 < high
+    keep = (1 - (torch.arange(n).double() - low) / (high - low)).clamp(0, 1)
+    assert 0.2 < float(keep[-1]) < 0.3
+    want = f.double() * (keep + (1 - keep) / factor)
+    assert bool(((g.double() / want - 1).abs() < 2 ** -22).all())
