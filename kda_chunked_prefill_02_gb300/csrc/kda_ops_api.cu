@@ -49,7 +49,7 @@ kda_status check_tree(const kda_tree_attention_args* a) {
 int64_t tree_max_len(const kda_tree_attention_args* a) {
     const int64_t room = a->pages_per_request * a->page_size;
     int64_t len = room;
-    if (a->max_context > 0 && a->max_context + a->max_nodes < room) len = a->max_context + a->max_nodes;
+    if (a->max_context > 0 && a->max_context < room - a->max_nodes) len = a->max_context + a->max_nodes;
     return len > (1 << 30) ? -1 : len;
 }
 

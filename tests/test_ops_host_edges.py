@@ -116,6 +116,18 @@ def test_tree_results_over_other_queries_are_refused(ops):
     assert size(out=PTR, num_requests=1, out_stride0=4096) > 0
 
 
+@pytest.mark.parametrize("bound", [(1 << 63) - 1, (1 << 63) - 4, 1 << 62, 1 << 31])
+def test_tree_bound_of_the_contexts_near_the_end_of_its_type(ops, bound):
+    """A bound past what the page table addresses is no bound."""
+    size = lambda **kw: ops._fn().kda_tree_attention_workspace_size(ctypes.byref(_tree_args(ops, **kw)))  # noqa: E731
+    want = size(pages_per_request=1000)
+    assert want > 0 and size(pages_per_request=1000, max_context=bound) == want
+    # and refuses nothing: without a GPU the call gets as far as looking for one
+    unsupported = 2
+    a = _tree_args(ops, pages_per_request=1000, max_context=bound)
+    assert ops._fn().kda_tree_attention(ctypes.byref(a), None) != unsupported
+
+
 # ---------------------------------------------------------------- frequencies
 def test_frequencies_by_parts_where_all_are_faster_than_slow_turns(ops):
     """A long original context: the ramp ends behind the last frequency, which is then not
