@@ -95,14 +95,20 @@ void strided(const Call& c, const char* name, const at::Tensor& t, at::IntArrayR
         refuse(PyExc_ValueError, std::string(name) + " must have shape " + text(shape) +
                                      " and a channel dim of stride 1, got " + text(t.sizes()));
 }
+// Stride of a dim.  That of a dim of size 1 says nothing (torch calls a row of a transposed
+// column contiguous, with a stride of 1): one that the library would refuse is rounded up.
+int64_t step(const at::Tensor& t, int64_t dim) {
+    const int64_t s = t.stride(dim);
+    return t.size(dim) > 1 ? s : (s + 7) / 8 * 8;
+}
 // (batch, token, head) strides of a [T, H, D] or [B, T, H, D] tensor.
 void heads(const Call& c, const char* name, const at::Tensor& t, at::IntArrayRef shape, c10::ScalarType dtype,
            int64_t (&s)[3]) {
     strided(c, name, t, shape, dtype);
     const bool batched = shape.size() == 4;
-    s[0] = batched ? t.stride(0) : 0;
-    s[1] = t.stride(batched);
-    s[2] = t.stride(1 + batched);
+    s[0] = batched ? step(t, 0) : 0;
+    s[1] = step(t, batched);
+    s[2] = step(t, 1 + batched);
 }
 // (page, row, head) strides of a cache.
 void cache(const Call& c, const char* name, const at::Tensor& t, int64_t num_heads, int64_t dim,
@@ -111,7 +117,7 @@ void cache(const Call& c, const char* name, const at::Tensor& t, int64_t num_hea
     if (t.dim() != 4 || t.size(2) != num_heads || t.size(3) != dim || t.stride(3) != 1)
         refuse(PyExc_ValueError, std::string(name) + " must be [pages, page_size, " + std::to_string(num_heads) + ", " +
                                      std::to_string(dim) + "] with a channel dim of stride 1");
-    for (int i = 0; i < 3; ++i) s[i] = t.stride(i);
+    for (int i = 0; i < 3; ++i) s[i] = step(t, i);
 }
 int64_t integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
@@ -169,13 +175,13 @@ PyObject* short_conv(PyObject* const* o) {
         if (cu->dim() != 1 || cu->size(0) < 1) refuse(PyExc_ValueError, "cu_seqlens must be int32 [N+1]");
         a.num_seqs = cu->size(0) - 1;
         a.seqlen = x.size(0);
-        a.x_stride[1] = x.stride(0);
+        a.x_stride[1] = step(x, 0);
         a.cu_seqlens = flat<int32_t>(c, "cu_seqlens", o[6], at::kInt, {a.num_seqs + 1});
     } else {
         a.num_seqs = x.size(0);
         a.seqlen = x.size(1);
-        a.x_stride[0] = x.stride(0);
-        a.x_stride[1] = x.stride(1);
+        a.x_stride[0] = step(x, 0);
+        a.x_stride[1] = step(x, 1);
     }
     if (w.dim() != 2) refuse(PyExc_ValueError, "weight must be [C, W]");
     const int64_t W = w.size(1);
@@ -211,8 +217,8 @@ PyObject* short_conv(PyObject* const* o) {
     if (!state_only) {
         out = given ? *given : at::empty(x.sizes(), x.options());
         a.out = out.data_ptr();
-        a.out_stride[0] = cu ? 0 : out.stride(0);
-        a.out_stride[1] = out.stride(cu ? 0 : 1);
+        a.out_stride[0] = cu ? 0 : step(out, 0);
+        a.out_stride[1] = step(out, cu ? 0 : 1);
     }
     done(kda_short_conv(&a, stream_of(x)));
     return state_only ? none() : THPVariable_Wrap(out);
@@ -348,8 +354,8 @@ PyObject* tree_attention(PyObject* const* o) {
     a.out = out.data_ptr();
     a.page_table = static_cast<int32_t*>(table.data_ptr());
     for (int i = 0; i < 3; ++i) {
-        a.q_stride[i] = q.stride(i);
-        a.out_stride[i] = out.stride(i);
+        a.q_stride[i] = step(q, i);
+        a.out_stride[i] = step(out, i);
     }
     a.page_table_stride = table.stride(0);
     a.num_requests = R;

@@ -142,3 +142,42 @@ def test_tree_results_over_the_queries(D, N, Hq, Hk, room):
     within(over, out, ob)
     if D != 256:   # the same kernel as apart from the queries: the same bits
         assert torch.equal(over, apart)
+
+
+# ---------------------------------------------------------------- strides of dims of size 1
+def test_one_token_as_a_transposed_column():
+    """The row of a transposed column has strides (1, 1): what a matrix times a column
+    leaves behind.  Every operator takes it as the contiguous row that it is."""
+    g = _gen(106)
+
+    def row(n):
+        r = _rand(g, (n, 1), BF16).cuda().t()
+        assert r.stride() == (1, 1) and r.is_contiguous()
+        return r
+
+    x = row(384)
+    w = _rand(g, (384, 4), torch.float32).cuda()
+    cu = _i32([0, 1]).cuda()
+    st = [torch.zeros(1, 3, 384, dtype=BF16, device="cuda") for _ in range(3)]
+    want = K.kda_short_conv(x.as_strided((1, 384), (384, 1)), w, conv_state=st[0], cu_seqlens=cu, norm_channels=256)
+    res = row(384)
+    assert torch.equal(K.kda_short_conv(x, w, conv_state=st[1], cu_seqlens=cu, norm_channels=256), want)
+    batch = ((1, 1, 384), (1, 1, 1))
+    K.kda_short_conv(x.as_strided(*batch), w, conv_state=st[2], norm_channels=256, out=res.as_strided(*batch))
+    assert torch.equal(res, want)
+    assert torch.equal(st[1], st[0]) and torch.equal(st[2], st[0])
+
+    qkv = row(8 * 128).as_strided((1, 8, 128), (1, 128, 1))
+    freq, _ = K.rope_frequencies(128)
+    pos = _i32([5]).cuda()
+    q, k = K.kda_qk_norm_rope(qkv[:, :6], qkv[:, 6:], pos, freq)
+    same = qkv.as_strided((1, 8, 128), (1024, 128, 1))
+    q2, k2 = K.kda_qk_norm_rope(same[:, :6], same[:, 6:], pos, freq)
+    assert torch.equal(q, q2) and torch.equal(k, k2)
+
+    for N, room in ((1, 0), (24, ROOM)):
+        q, kc, vc, table, ctx = _tree_inputs(107, [200], N, 4, 2, 128, 16, room=room)
+        dev = [t.cuda() for t in (kc, vc, table, ctx)]
+        qd = q.cuda()
+        odd = qd.as_strided(qd.shape, (1, *qd.stride()[1:]))
+        assert torch.equal(K.kda_tree_attention(odd, *dev), K.kda_tree_attention(qd, *dev))
