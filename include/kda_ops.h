@@ -217,6 +217,12 @@ typedef struct kda_tree_attention_args {
 } kda_tree_attention_args;
 size_t kda_tree_attention_workspace_size(const kda_tree_attention_args* args);
 kda_status kda_tree_attention(const kda_tree_attention_args* args, void* stream);
+/*
+ * The same with overrides for tests (NULL: none): wait_limit_ns and timeout_probe
+ * apply to the kernel for many rows, whose waits are the only ones of these
+ * operators.  A wait that runs out reports KDA_ERR_TIMEOUT in device_status.
+ */
+kda_status kda_tree_attention_ex(const kda_tree_attention_args* args, const kda_overrides* overrides, void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,6 +6,7 @@
 #include "../../include/kda_ops.h"
 #include "kda_internal.h"
 #include "ops_internal.h"
+#include "sm103.cuh"
 
 using namespace kda;
 
@@ -165,6 +166,10 @@ size_t kda_tree_attention_workspace_size(const kda_tree_attention_args* a) {
 }
 
 kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
+    return kda_tree_attention_ex(a, nullptr, stream);
+}
+
+kda_status kda_tree_attention_ex(const kda_tree_attention_args* a, const kda_overrides* overrides, void* stream) {
     const kda_status st = check_tree(a);
     if (st != KDA_OK || a->num_requests == 0) return st;
     const int64_t max_len = tree_max_len(a);
@@ -196,6 +201,8 @@ kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
     p.part_lse = p.part_o + plan.part_rows * a->head_dim;
     p.order = plan.order ? reinterpret_cast<int32_t*>(p.part_lse + plan.part_rows) : nullptr;
     p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.wait_ns = overrides && overrides->wait_limit_ns > 0 ? (uint64_t)overrides->wait_limit_ns : kWaitLimitNs;
+    p.timeout_probe = overrides && overrides->timeout_probe ? 1 : 0;
     return status_of(launch_tree_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
                                            static_cast<cudaStream_t>(stream)));
 }

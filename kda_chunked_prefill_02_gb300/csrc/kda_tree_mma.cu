@@ -57,9 +57,11 @@
 // 168 kept, 224 taken: 4 x 56 + 8 x 224 = 12 x 168), whose threads hold a row of
 // 128 scores.
 //
-// Every wait is bounded (sm103.cuh); one that runs out sets the abort flag, the
-// roles fall through to the end, copies and products in flight are waited for,
-// and the status word reports KDA_ERR_TIMEOUT.
+// Every wait is bounded; one that runs out sets the abort flag, the roles fall
+// through to the end, and the status word reports KDA_ERR_TIMEOUT.  Whatever the
+// others do, the loader and the issuer end by waiting for their last copies and
+// products (with the full kWaitLimitNs), so that none is in flight when the CTA's
+// memory goes to the next.
 #include "kda_internal.h"
 #include "ops_internal.h"
 #include "sm103.cuh"
@@ -82,7 +84,7 @@ constexpr float kLazy = 8.f;             // log2 units by which scores may excee
 // mbar_wait (sm103.cuh) with the clock and the abort flag looked at every 64th time
 // only: between a phase's end and this thread's next step there is then nothing but
 // the try_wait itself, where a look at the global timer takes longer than the wait.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -90,7 +92,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const v
         if (abort && *abort) return false;
         const uint64_t t = globaltimer_ns();
         if (t0 == 0) t0 = t;
-        else if (t - t0 > kWaitLimitNs) return false;
+        else if (t - t0 > limit_ns) return false;
     }
 }
 
@@ -193,10 +195,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     __shared__ uint32_t s_bad[8][8];
     __shared__ int32_t s_start[kMmaSlice + 1];   // where every request begins on the line, in key tiles
     __shared__ Item s_item[kItems];
-    __shared__ uint64_t item_full[kItems], item_free[kItems];
+    __shared__ uint64_t item_full[kItems], item_free[kItems], never;   // never: the probe's, nothing arrives on it
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int* abort = &abort_flag;
+    const uint64_t limit = p.wait_ns;
     uint8_t* ring = sm + Shape::front(p.rows);
     auto fail = [&]() {
         *abort = 1;
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 8);
+        mbar_init(&never, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const uint32_t tb = tmem_base_sh;
     // The k-th item of this CTA; false after the last (or on an abort).
     auto take = [&](int k, Item& x, bool& ok) -> bool {
-        ok = ok && wait_for(&item_full[k % kItems], (k / kItems) & 1, abort);
+        ok = ok && wait_for(&item_full[k % kItems], (k / kItems) & 1, abort, limit);
         if (!ok) return false;
         x = s_item[k % kItems];
         return x.t1 >= 0;
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     for (int part = 0; part < kPer; ++part) {   // K by kV channels, then V
                         const bool v = part == kHalves;
                         const int slot = issued % bufs, round = issued / bufs;
-                        if (round > 0) ok = __all_sync(0xffffffffu, wait_for(&kv_free[slot], (round - 1) & 1, abort));
+                        if (round > 0) ok = __all_sync(0xffffffffu, wait_for(&kv_free[slot], (round - 1) & 1, abort, limit));
                         if (!ok) break;
                         uint8_t* dst = ring + slot * kSlotBytes;
                         const bool special = v && base + kKeys > ctx;
@@ -297,13 +301,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                 }
             }
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) fail();
-                // copies still on their way into this CTA's memory
-                for (int i = max(0, issued - bufs); i < issued; ++i)
-                    if (!((raw >> (i % bufs)) & 1)) wait_for(&kv_full[i % bufs], (i / bufs) & 1, nullptr);
-                    else wait_for(&kv_raw[i % bufs], (raw_phases >> (i % bufs)) & 1, nullptr);
-            }
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+            // the last copies into this CTA's memory
+            for (int i = max(0, issued - bufs); i < issued; ++i)
+                if (!((raw >> (i % bufs)) & 1)) wait_for(&kv_full[i % bufs], (i / bufs) & 1, nullptr, kWaitLimitNs);
+                else wait_for(&kv_raw[i % bufs], (raw_phases >> (i % bufs)) & 1, nullptr, kWaitLimitNs);
         } else if (warp == 9) {
             // ------------------------------------------------------------ products
             // The whole warp walks the loop and one elected lane issues, with every
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             int item = 0;
             int base = 0;                      // ring tiles before this item
             int done0 = 0, done1 = 0;          // P tiles taken, by stream
-            auto landed = [&](int i) { return wait_for(&kv_full[i % bufs], (i / bufs) & 1, abort); };
+            auto landed = [&](int i) { return wait_for(&kv_full[i % bufs], (i / bufs) & 1, abort, limit); };
             Item x;
             for (; __all_sync(0xffffffffu, take(item, x, ok)); ++item) {
                 if (lane == 0) mbar_arrive(&item_free[item % kItems]);
@@ -354,14 +356,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                     __syncwarp();
                 };
-                ok = __all_sync(0xffffffffu, ok && wait_for(&q_ready, item & 1, abort));
+                ok = __all_sync(0xffffffffu, ok && wait_for(&q_ready, item & 1, abort, limit));
                 if (two) ok = __all_sync(0xffffffffu, ok && keys_landed(base));
                 scores(0);
                 if (units > 1) scores(1);
                 for (int u = 0; u < units && ok; ++u) {
                     const int s = u & 1, i = base + kPer * (two ? u >> 1 : u) + kHalves;
                     // O still holds the item before until its rows are out
-                    if (u == 0 && item > 0) ok = wait_for(&o_free, (item - 1) & 1, abort);
+                    if (u == 0 && item > 0) ok = wait_for(&o_free, (item - 1) & 1, abort, limit);
                     // This tile's V, and with two row tiles the next K before P is there (the
                     // second stream's tiles are the first's); with one row tile memory is the
                     // bound, and waiting for a K would hold up the V before it.
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % bufs) * kSlotBytes, 1024, kGroupBytes);
                     // the two halves of P as they come
                     auto product = [&](int k0, uint64_t* ready) {
-                        ok = __all_sync(0xffffffffu, ok && wait_for(ready, phase, abort));
+                        ok = __all_sync(0xffffffffu, ok && wait_for(ready, phase, abort, limit));
                         if (!ok) return;
                         tc_fence_after();
                         if (elect_one()) {
@@ -390,10 +392,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
                 if (elect_one()) umma_commit(&o_full);
                 __syncwarp();
-                if (!ok) wait_for(&o_full, item & 1, nullptr);   // products still in flight
                 base += kPer * tiles;
             }
             if (!ok && lane == 0) fail();
+            if (item > 0) wait_for(&o_full, (item - 1) & 1, nullptr, kWaitLimitNs);   // the last products
             __syncwarp();
         } else if (warp == 10) {
             // ------------------------------------------------------------ work
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 int k = 0;
                 bool ok = true;
                 auto deal = [&](const Item& x) {
-                    if (k >= kItems) ok = wait_for(&item_free[k % kItems], (k / kItems - 1) & 1, abort);
+                    if (k >= kItems) ok = wait_for(&item_free[k % kItems], (k / kItems - 1) & 1, abort, limit);
                     if (!ok) return;
                     s_item[k % kItems] = x;
                     mbar_arrive(&item_full[k % kItems]);
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 for (int tile = max(x.t0, ctx / kKeys); tile < x.t1 && ok; ++tile) {
                     const int i = base_kv + kPer * (tile - x.t0) + kHalves, slot = i % bufs, base = tile * kKeys;
                     uint8_t* const dst = ring + slot * kSlotBytes;
-                    ok = __all_sync(0xffffffffu, wait_for(&kv_raw[slot], (phases >> slot) & 1, abort));
+                    ok = __all_sync(0xffffffffu, wait_for(&kv_raw[slot], (phases >> slot) & 1, abort, limit));
                     if (!ok) break;
                     phases ^= 1u << slot;
                     constexpr uint32_t kExp = Elem<T>::kExpMask;
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         bool ok = true;
         int item = 0, seen_s = 0;   // items begun, score tiles taken
         for (;; ++item) {
-            ok = __all_sync(0xffffffffu, wait_for(&item_full[item % kItems], (item / kItems) & 1, abort));
+            ok = __all_sync(0xffffffffu, wait_for(&item_full[item % kItems], (item / kItems) & 1, abort, limit));
             if (!ok && lane == 0) fail();
             const Item& x = s_item[item % kItems];
             if (named_bar_or(1, 256, !ok || x.t1 < 0)) break;   // all stop if one has given up
@@ -605,8 +607,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int tile0 = x.t0, ctx_in = x.ctx;
             float m = -INFINITY, l = 0.f;
             const int units = (two ? 2 : 1) * (x.t1 - x.t0);
-            for (int u = stream; u < units; u += 2) {
-                ok = __all_sync(0xffffffffu, wait_for(&s_full[stream], seen_s & 1, abort));
+            if (p.timeout_probe && item == 0) ok = __all_sync(0xffffffffu, wait_for(&never, 0, abort, limit));
+            for (int u = stream; u < units && ok; u += 2) {
+                ok = __all_sync(0xffffffffu, wait_for(&s_full[stream], seen_s & 1, abort, limit));
                 if (!ok) break;
                 ++seen_s;
                 tc_fence_after();
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[stream]);
             }
-            ok = __all_sync(0xffffffffu, wait_for(&o_full, item & 1, abort)) && ok;
+            ok = __all_sync(0xffffffffu, wait_for(&o_full, item & 1, abort, limit)) && ok;
             if (!ok && lane == 0) fail();
             tc_fence_after();
 

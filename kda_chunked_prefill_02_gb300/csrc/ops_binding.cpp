@@ -308,7 +308,7 @@ PyObject* qk_norm_rope(PyObject* const* o) {
 }
 
 // q, k_cache, v_cache, page_table, context_lens, tree_mask, num_nodes, scale,
-// max_context, out, return_lse, workspace, device_status
+// max_context, out, return_lse, workspace, device_status, address of a kda_overrides
 PyObject* tree_attention(PyObject* const* o) {
     const at::Tensor &q = *tensor("q", o[0]), &kc = *tensor("k_cache", o[1]), &vc = *tensor("v_cache", o[2]),
                      &table = *tensor("page_table", o[3]);
@@ -372,7 +372,9 @@ PyObject* tree_attention(PyObject* const* o) {
         a.workspace = ws.data_ptr();
         a.workspace_bytes = (size_t)ws.numel();
     }
-    done(kda_tree_attention(&a, stream_of(q)));
+    const auto* overrides = o[13] == Py_None ? nullptr : static_cast<const kda_overrides*>(PyLong_AsVoidPtr(o[13]));
+    if (PyErr_Occurred()) throw Refused();
+    done(kda_tree_attention_ex(&a, overrides, stream_of(q)));
     PyObject* ro = o[9] != Py_None ? Py_NewRef(o[9]) : THPVariable_Wrap(out);
     if (!want_lse) return ro;
     PyObject* rl = THPVariable_Wrap(lse);
@@ -403,7 +405,7 @@ PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(counted<F, kArgs>)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<short_conv, 14>("short_conv"), method<qk_norm_rope, 17>("qk_norm_rope"),
-                         method<tree_attention, 13>("tree_attention"), method<set_error, 1>("set_error"),
+                         method<tree_attention, 14>("tree_attention"), method<set_error, 1>("set_error"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

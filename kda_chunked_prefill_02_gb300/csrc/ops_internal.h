@@ -77,6 +77,8 @@ struct TreeParams {
     int r0, count;            // mma: the requests of a launch (set by the launcher)
     int slots, slot_rows;     // 2 x the CTAs over a line of items, rows of a slot (set by the launcher)
     float scale_log2;         // scale * log2(e)
+    uint64_t wait_ns;         // mma: bound of the working waits (set by the entry; a wind-down's are kWaitLimitNs)
+    int timeout_probe;        // mma: the softmax warps' first wait runs out (tests)
 };
 // How a call is cut.
 struct TreePlan {

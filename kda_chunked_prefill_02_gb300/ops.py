@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from .kda import KdaError, lib
+from .kda import KdaError, _overrides_var, lib
 
 KDA_DTYPE_BF16, KDA_DTYPE_F16, KDA_DTYPE_F32 = range(3)
 
@@ -219,6 +219,7 @@ def kda_tree_attention(q, k_cache, v_cache, page_table, context_lens, *, tree_ma
     itself.  Returns out, or
     (out, lse) with lse fp32 [R, N, Hq].
     """
+    given = _overrides_var.get()
     return _run((_binding or _native()).tree_attention, stream,
                 (q, k_cache, v_cache, page_table, context_lens, tree_mask, num_nodes, scale, max_context, out,
-                 return_lse, workspace, device_status))
+                 return_lse, workspace, device_status, None if given is None else ctypes.addressof(given)))

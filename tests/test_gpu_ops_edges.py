@@ -144,6 +144,38 @@ def test_tree_results_over_the_queries(D, N, Hq, Hk, room):
         assert torch.equal(over, apart)
 
 
+# ---------------------------------------------------------------- waits that run out
+KDA_ERR_TIMEOUT = 4
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("N,Hq,ctx", [(24, 4, [3000, 0, 900, 17]),             # one row tile: two streams over one item
+                                      (40, 16, [20000, 5, 300, 700] * 20)])    # two row tiles, many items a CTA
+def test_tree_wait_that_runs_out_is_reported_and_the_context_survives(D, N, Hq, ctx):
+    """The first wait of the softmax warps is for a barrier that nothing arrives on, so that it
+    runs out with copies and products in flight.  The call returns and says so, and the next
+    one on the same stream and workspace gives the usual bits."""
+    pages = 4000   # the requests share them
+    kc = torch.randn(pages, 16, 2, D, device="cuda").to(BF16)
+    vc = torch.randn_like(kc)
+    g = _gen(108)
+    table = torch.randint(0, pages, (len(ctx), ROOM // 16), generator=g).to(torch.int32).cuda()
+    q, lens = _rand(g, (len(ctx), N, Hq, D), BF16).cuda(), _i32(ctx).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    usual = K.kda_tree_attention(q, kc, vc, table, lens, device_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for limit in (2000, 200000):
+        with K.overrides(wait_limit_ns=limit, timeout_probe=True):
+            K.kda_tree_attention(q, kc, vc, table, lens, device_status=status)
+        torch.cuda.synchronize()            # returns: no hang, no fault
+        assert status.item() == KDA_ERR_TIMEOUT
+        status.zero_()
+        again = K.kda_tree_attention(q, kc, vc, table, lens, device_status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0 and torch.equal(again, usual)
+
+
 # ---------------------------------------------------------------- strides of dims of size 1
 def test_one_token_as_a_transposed_column():
     """The row of a transposed column has strides (1, 1): what a matrix times a column
