@@ -220,7 +220,9 @@ kda_status kda_tree_attention(const kda_tree_attention_args* args, void* stream)
 /*
  * The same with overrides for tests (NULL: none): wait_limit_ns and timeout_probe
  * apply to the kernel for many rows, whose waits are the only ones of these
- * operators.  A wait that runs out reports KDA_ERR_TIMEOUT in device_status.
+ * operators: bounded by wait_limit_ns (200 ms by default) and 0.1 ms for every 128
+ * tokens of the longest context, since some last as long as a context's work.  A
+ * wait that runs out reports KDA_ERR_TIMEOUT in device_status.
  */
 kda_status kda_tree_attention_ex(const kda_tree_attention_args* args, const kda_overrides* overrides, void* stream);
 

@@ -144,6 +144,10 @@ struct Item {
     bool two, whole;   // two row tiles; all of the item's key tiles
 };
 constexpr int kItems = 4;   // items dealt out ahead
+// What a wait may take beside its bound, a key tile of the longest context: the cleaner waits
+// for an item's last tiles from its first on, and the other roles and the dealer for what the
+// kItems items before are done with.  A tile takes some 2 us.
+constexpr uint64_t kTileWaitNs = 20000 * (kItems + 1);
 
 // K-major operand in the 128-byte swizzle with its 8-row groups `group` bytes apart.
 __device__ __forceinline__ uint64_t sdesc_keys(uint32_t saddr, uint32_t group) {
@@ -865,6 +869,7 @@ bool cache_map(CUtensorMap* map, const void* base, const int64_t (&st)[3], const
 bool launch_tree_mma(const TreeParams& q, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e) {
     CUtensorMap kmap, vmap;
     TreeParams p = q;
+    p.wait_ns += (uint64_t)((p.max_len + kKeys - 1) / kKeys) * kTileWaitNs;
     if (!cache_map(&kmap, p.kc, p.ks, p, D, f16, &p.k_paged) || !cache_map(&vmap, p.vc, p.vs, p, D, f16, &p.v_paged))
         return false;
     if (f16) *e = launch_mma<__half>(p, kmap, vmap, D, grid, s);

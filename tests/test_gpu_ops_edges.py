@@ -176,6 +176,22 @@ def test_tree_wait_that_runs_out_is_reported_and_the_context_survives(D, N, Hq, 
         assert status.item() == 0 and torch.equal(again, usual)
 
 
+def test_tree_waits_that_last_as_long_as_an_item_do_not_run_out():
+    """Some roles wait for an item's last tile from its first on, or for a free place among the
+    items dealt out.  An item of 8192 key tiles takes a CTA some 16 ms; the bound of a wait
+    here is 1 ms beside what the contexts themselves may take."""
+    g = _gen(109)
+    R, pages = 38, 600   # the requests share their pages
+    kc, vc = (torch.randn(pages, 64, 4, 128, device="cuda").to(BF16) for _ in range(2))
+    table = torch.randint(0, pages, (R, (1 << 14) + 1), generator=g).to(torch.int32).cuda()
+    q, lens = _rand(g, (R, 32, 32, 128), BF16).cuda(), torch.full((R,), 1 << 20, dtype=torch.int32).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    usual = K.kda_tree_attention(q, kc, vc, table, lens)
+    with K.overrides(wait_limit_ns=1000000):
+        got = K.kda_tree_attention(q, kc, vc, table, lens, device_status=status)
+    assert status.item() == 0 and torch.equal(got, usual)
+
+
 # ---------------------------------------------------------------- strides of dims of size 1
 def test_one_token_as_a_transposed_column():
     """The row of a transposed column has strides (1, 1): what a matrix times a column
