@@ -225,6 +225,24 @@ kda_status kda_tree_attention(const kda_tree_attention_args* args, void* stream)
  * wait that runs out reports KDA_ERR_TIMEOUT in device_status.
  */
 kda_status kda_tree_attention_ex(const kda_tree_attention_args* args, const kda_overrides* overrides, void* stream);
+/*
+ * How kda_tree_attention cuts these arguments on a GPU with num_sms SMs (host only:
+ * no device call, pointers are not followed).  kernel: KDA_TREE_ITEMS, one CTA a
+ * (request, key head, block of rows), the requests longest first where ordered is 1;
+ * KDA_TREE_CLUSTERS, `cluster` CTAs each; KDA_TREE_LINE, equal stretches of all of
+ * them in a row; KDA_TREE_MANY_ROWS, the kernel for many rows in `launches` launches
+ * of up to 256 requests (a cache without a tensor map and results over queries of
+ * head size 256 take KDA_TREE_ITEMS or _LINE all the same).  KDA_ERR_INVALID_ARG for
+ * NULL or num_sms < 1, otherwise what kda_tree_attention would refuse.
+ */
+#define KDA_TREE_ITEMS 0
+#define KDA_TREE_CLUSTERS 1
+#define KDA_TREE_LINE 2
+#define KDA_TREE_MANY_ROWS 3
+typedef struct kda_tree_schedule {
+    int32_t kernel, ordered, cluster, launches;
+} kda_tree_schedule;
+kda_status kda_tree_attention_schedule(const kda_tree_attention_args* args, int num_sms, kda_tree_schedule* schedule);
 
 #ifdef __cplusplus
 }

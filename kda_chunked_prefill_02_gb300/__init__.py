@@ -11,4 +11,4 @@ from .kda import (CHUNK, HEAD_DIM, KdaError, host_staging_size, kda_prefill,  # 
                   kda_prefill_host, kda_verify, lib, status_string, workspace_layout,
                   workspace_size)
 from .ops import (kda_qk_norm_rope, kda_short_conv, kda_tree_attention,  # noqa: F401
-                  rope_frequencies, tree_mask)
+                  rope_frequencies, tree_attention_schedule, tree_mask)

@@ -59,10 +59,10 @@ int sm_count_or_default() {
     return n > 0 ? n : 152;   // no device (a host-only query of the workspace)
 }
 
-TreePlan plan_of(const kda_tree_attention_args* a, int64_t max_len) {
+TreePlan plan_of(const kda_tree_attention_args* a, int64_t max_len, int num_sms) {
     return tree_plan((int)a->num_requests, (int)a->num_k_heads,
                      (int)(a->max_nodes * (a->num_q_heads / a->num_k_heads)), (int)a->head_dim, max_len,
-                     (int)a->page_size, a->scale, sm_count_or_default());
+                     (int)a->page_size, a->scale, num_sms);
 }
 
 size_t tree_workspace(const kda_tree_attention_args* a, const TreePlan& plan) {
@@ -162,7 +162,23 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, void* stream) {
 size_t kda_tree_attention_workspace_size(const kda_tree_attention_args* a) {
     if (check_tree(a) != KDA_OK || a->num_requests == 0) return 0;
     const int64_t max_len = tree_max_len(a);
-    return max_len < 0 ? 0 : tree_workspace(a, plan_of(a, max_len));
+    return max_len < 0 ? 0 : tree_workspace(a, plan_of(a, max_len, sm_count_or_default()));
+}
+
+kda_status kda_tree_attention_schedule(const kda_tree_attention_args* a, int num_sms, kda_tree_schedule* schedule) {
+    if (!schedule || num_sms < 1) return KDA_ERR_INVALID_ARG;
+    memset(schedule, 0, sizeof(*schedule));
+    const kda_status st = check_tree(a);
+    if (st != KDA_OK || a->num_requests == 0) return st;
+    const int64_t max_len = tree_max_len(a);
+    if (max_len < 0) return KDA_ERR_UNSUPPORTED;
+    const TreePlan plan = plan_of(a, max_len, num_sms);
+    schedule->kernel = plan.mma ? KDA_TREE_MANY_ROWS
+                                : plan.line ? KDA_TREE_LINE : plan.cluster > 1 ? KDA_TREE_CLUSTERS : KDA_TREE_ITEMS;
+    schedule->ordered = plan.order > 0 ? 1 : 0;
+    schedule->cluster = plan.mma ? 1 : plan.cluster;
+    schedule->launches = plan.mma ? (int)((a->num_requests + kTreeSlice - 1) / kTreeSlice) : 1;
+    return KDA_OK;
 }
 
 kda_status kda_tree_attention(const kda_tree_attention_args* a, void* stream) {
@@ -175,7 +191,7 @@ kda_status kda_tree_attention_ex(const kda_tree_attention_args* a, const kda_ove
     const int64_t max_len = tree_max_len(a);
     if (max_len < 0) return KDA_ERR_UNSUPPORTED;
     if (device_sm_count() < 1) return KDA_ERR_CUDA;
-    const TreePlan plan = plan_of(a, max_len);
+    const TreePlan plan = plan_of(a, max_len, sm_count_or_default());
     const size_t need = tree_workspace(a, plan);
     if (need && (!a->workspace || a->workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
     if (need && (reinterpret_cast<uintptr_t>(a->workspace) & 255u)) return KDA_ERR_UNSUPPORTED;

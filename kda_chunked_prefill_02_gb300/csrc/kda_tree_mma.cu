@@ -77,7 +77,6 @@ constexpr int kMaxBufs = 8;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 256 + 128 s
 // Floats of the rows' way out: a patch a warp, 32 columns of stream 1, its maxima and sums.
 constexpr int kPatch = 32 * 36, kWayOut = 8 * kPatch + 34 * 128;
-constexpr int kMmaSlice = 256;            // requests a launch
 constexpr int kCostTwo = 5, kCostOne = 4;  // cost of a key tile for two row tiles, for one
 constexpr float kLazy = 8.f;             // log2 units by which scores may exceed the running maximum
 
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     // Drafted nodes with a V element that is not finite, for eight items in turn
     // (the ring holds at most four items' tiles ahead of the rows' way out).
     __shared__ uint32_t s_bad[8][8];
-    __shared__ int32_t s_start[kMmaSlice + 1];   // where every request begins on the line, in key tiles
+    __shared__ int32_t s_start[kTreeSlice + 1];   // where every request begins on the line, in key tiles
     __shared__ Item s_item[kItems];
     __shared__ uint64_t item_full[kItems], item_free[kItems], never;   // never: the probe's, nothing arrives on it
 
@@ -824,12 +823,12 @@ cudaError_t launch_mma_t(const TreeParams& q, const CUtensorMap& kmap, const CUt
     constexpr uint32_t most = Shape::smem(1) > Shape::smem(256) ? Shape::smem(1) : Shape::smem(256);
     cudaError_t e = set_smem_limit_once((const void*)tree_mma_kernel<T, D>, (int)most, smem_set);
     grid -= grid % Shape::kHalves;
-    for (int r0 = 0; r0 < q.R && e == cudaSuccess; r0 += kMmaSlice) {
+    for (int r0 = 0; r0 < q.R && e == cudaSuccess; r0 += kTreeSlice) {
         TreeParams p = q;
         p.r0 = r0;
         p.slots = 2 * (grid / Shape::kHalves);
         p.slot_rows = 256;
-        p.count = q.R - r0 < kMmaSlice ? q.R - r0 : kMmaSlice;
+        p.count = q.R - r0 < kTreeSlice ? q.R - r0 : kTreeSlice;
         tree_mma_kernel<T, D><<<grid, kMmaThreads, Shape::smem(p.rows), s>>>(p, kmap, vmap);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = launch_tree_join(p, D, std::is_same<T, __half>::value, s);

@@ -80,6 +80,7 @@ struct TreeParams {
     uint64_t wait_ns;         // mma: bound of the working waits (set by the entry; a wind-down's are kWaitLimitNs)
     int timeout_probe;        // mma: the softmax warps' first wait runs out (tests)
 };
+constexpr int kTreeSlice = 256;   // requests a launch of the kernel for many rows takes
 // How a call is cut.
 struct TreePlan {
     bool mma;            // the kernel for many rows

@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from .kda import KdaError, _overrides_var, lib
+from .kda import KdaError, _check, _overrides_var, lib
 
 KDA_DTYPE_BF16, KDA_DTYPE_F16, KDA_DTYPE_F32 = range(3)
 
@@ -62,6 +62,10 @@ class TreeAttentionArgs(ctypes.Structure):
         f32: scale""")
 
 
+class TreeSchedule(ctypes.Structure):
+    _fields_ = _fields("i32: kernel ordered cluster launches")
+
+
 _funcs = None
 
 
@@ -76,6 +80,8 @@ def _fn():
             f.argtypes = [_p, _p]
         L.kda_tree_attention_workspace_size.restype = ctypes.c_size_t
         L.kda_tree_attention_workspace_size.argtypes = [_p]
+        L.kda_tree_attention_schedule.restype = ctypes.c_int
+        L.kda_tree_attention_schedule.argtypes = [_p, ctypes.c_int, _p]
         _funcs = L
     return _funcs
 
@@ -223,3 +229,24 @@ def kda_tree_attention(q, k_cache, v_cache, page_table, context_lens, *, tree_ma
     return _run((_binding or _native()).tree_attention, stream,
                 (q, k_cache, v_cache, page_table, context_lens, tree_mask, num_nodes, scale, max_context, out,
                  return_lse, workspace, device_status, None if given is None else ctypes.addressof(given)))
+
+
+def tree_attention_schedule(q, k_cache, page_table, *, scale=None, max_context=None, num_sms=None):
+    """How kda_tree_attention cuts a call (kda_tree_attention_schedule): dict(kernel,
+    ordered, cluster, launches), kernel "items", "clusters", "line" or "many rows".  Host
+    only; the tensors may live anywhere (only their types and shapes are read).  num_sms
+    defaults to the current CUDA device's SM count."""
+    a = TreeAttentionArgs()
+    a.q = a.out = a.k_cache = a.v_cache = a.page_table = a.context_lens = 16   # not followed
+    a.dtype = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_F16}.get(q.dtype, KDA_DTYPE_F32)
+    a.num_requests, a.max_nodes, a.num_q_heads, a.head_dim = q.shape
+    a.num_pages, a.page_size, a.num_k_heads, _ = k_cache.shape
+    a.pages_per_request = page_table.shape[1]
+    a.max_context = max_context or 0
+    a.scale = q.shape[3] ** -0.5 if scale is None else scale
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    s = TreeSchedule()
+    _check(_fn().kda_tree_attention_schedule(ctypes.byref(a), int(num_sms), ctypes.byref(s)))
+    return dict(kernel=("items", "clusters", "line", "many rows")[s.kernel], ordered=bool(s.ordered),
+                cluster=s.cluster, launches=s.launches)

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import kda_chunked_prefill_02_gb300 as K
+from test_gpu_ops import _tree_case
 from ops_test_util import conv_reference, rope_reference, tree_reference, within
 
 pytestmark = pytest.mark.gpu
@@ -142,6 +143,34 @@ def test_tree_results_over_the_queries(D, N, Hq, Hk, room):
     within(over, out, ob)
     if D != 256:   # the same kernel as apart from the queries: the same bits
         assert torch.equal(over, apart)
+
+
+def _cut(ctx, N, Hq, Hk, D, page, room):
+    """How _tree_case's call is cut on this GPU."""
+    empty = lambda *shape: torch.empty(shape, dtype=BF16, device="meta")  # noqa: E731
+    width = max(max((c + N + page - 1) // page for c in ctx), 1, room // page)
+    return K.tree_attention_schedule(empty(len(ctx), N, Hq, D), empty(1, page, Hk, D), empty(len(ctx), width))
+
+
+@pytest.mark.parametrize("D,N,Hq,Hk", [(64, 9, 4, 2), (128, 34, 16, 2), (256, 20, 4, 2)])
+def test_tree_more_requests_than_a_launch_of_the_kernel_for_many_rows(D, N, Hq, Hk):
+    """Two launches, the second over the requests from 256 on in the same workspace: one and
+    two row tiles, most contexts short, some empty, some long enough to be cut, in both."""
+    ctx = [(i * 37) % 90 if i % 50 else 700 + 9 * i for i in range(300)]
+    nodes = _i32([(i * 7) % (N + 1) for i in range(300)])
+    cut = _cut(ctx, N, Hq, Hk, D, 16, ROOM)
+    assert cut["kernel"] == "many rows" and cut["launches"] == 2
+    _tree_case(110, ctx, N, Hq, Hk, D, 16, BF16, nodes=nodes, room=ROOM)
+
+
+@pytest.mark.parametrize("D,R,N,Hk", [(64, 330, 1, 2), (64, 220, 3, 3), (128, 170, 3, 2), (256, 160, 1, 1)])
+def test_tree_more_items_than_run_at_once(D, R, N, Hk):
+    """A CTA an item, the requests longest first."""
+    ctx = [(i * 37) % 90 if i % 50 else 700 + i for i in range(R)]
+    nodes = _i32([(i * 7) % (N + 1) for i in range(R)])
+    cut = _cut(ctx, N, 2 * Hk, Hk, D, 16, 0)
+    assert cut["kernel"] == "items" and cut["ordered"]
+    _tree_case(111, ctx, N, 2 * Hk, Hk, D, 16, BF16, nodes=nodes)
 
 
 # ---------------------------------------------------------------- waits that run out

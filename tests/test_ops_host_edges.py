@@ -104,9 +104,9 @@ def _tree_args(ops, **kw):
 def test_tree_results_over_other_queries_are_refused(ops):
     """out at q's address with other strides would put rows over queries that other CTAs read.
     (What is not refused is asked for its workspace alone, so that nothing can be launched.)"""
-    run = lambda **kw: ops._fn().kda_tree_attention(ctypes.byref(_tree_args(ops, **kw)), None)  # noqa: E731
-    size = lambda **kw: ops._fn().kda_tree_attention_workspace_size(  # noqa: E731
-        ctypes.byref(_tree_args(ops, pages_per_request=1000, **kw)))
+    args = lambda **kw: ctypes.byref(_tree_args(ops, pages_per_request=1000, **kw))  # noqa: E731
+    run = lambda **kw: ops._fn().kda_tree_attention(args(**kw), None)  # noqa: E731
+    size = lambda **kw: ops._fn().kda_tree_attention_workspace_size(args(**kw))  # noqa: E731
     invalid = 1
     for kw in (dict(out_stride0=4096), dict(out_stride1=2048), dict(out_stride2=256)):
         assert run(out=PTR, **kw) == invalid, kw
@@ -126,6 +126,35 @@ def test_tree_bound_of_the_contexts_near_the_end_of_its_type(ops, bound):
     unsupported = 2
     a = _tree_args(ops, pages_per_request=1000, max_context=bound)
     assert ops._fn().kda_tree_attention(ctypes.byref(a), None) != unsupported
+
+
+# ---------------------------------------------------------------- how tree attention is cut
+def _schedule(ops, R, N, Hq, Hk, D, tokens, page=16, num_sms=152, dtype=BF16, **kw):
+    empty = lambda *shape: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    return ops.tree_attention_schedule(empty(R, N, Hq, D), empty(10, page, Hk, D), empty(R, tokens // page),
+                                       num_sms=num_sms, **kw)
+
+
+def test_tree_schedule(ops):
+    """One clear case of every cut."""
+    assert _schedule(ops, 1, 1, 8, 2, 128, 1008) == dict(kernel="clusters", ordered=False, cluster=8, launches=1)
+    assert _schedule(ops, 1, 1, 8, 2, 128, 131072)["kernel"] == "line"
+    assert _schedule(ops, 400, 1, 8, 2, 128, 4096) == dict(kernel="items", ordered=True, cluster=1, launches=1)
+    assert _schedule(ops, 256, 61, 32, 4, 128, 8192) == dict(kernel="many rows", ordered=False, cluster=1, launches=1)
+    assert _schedule(ops, 257, 61, 32, 4, 128, 8192)["launches"] == 2
+    # the bound of the contexts counts, not the table's width
+    assert _schedule(ops, 1, 1, 8, 2, 128, 131072, max_context=1000)["kernel"] == "clusters"
+    # pages that are no multiple of 8, and scales that are not above zero, stay with few rows
+    assert _schedule(ops, 24, 61, 32, 4, 128, 8190, page=10)["kernel"] != "many rows"
+    assert _schedule(ops, 24, 61, 32, 4, 128, 8192, scale=0.0)["kernel"] != "many rows"
+
+
+def test_tree_schedule_refusals(ops):
+    from kda_chunked_prefill_02_gb300 import KdaError
+    for kw in (dict(D=96), dict(dtype=torch.float32), dict(N=257), dict(num_sms=0), dict(Hq=7)):
+        with pytest.raises(KdaError):
+            _schedule(ops, **{**dict(R=2, N=4, Hq=8, Hk=2, D=128, tokens=800), **kw})
+    assert _schedule(ops, 0, 4, 8, 2, 128, 800)["launches"] == 0
 
 
 # ---------------------------------------------------------------- frequencies
