@@ -1,12 +1,14 @@
 """Build the KDA CUDA library in-tree for sm_103a.
 
-    python -m kda_chunked_prefill_02_gb300.build [--force]
+    python -m kda_chunked_prefill_02_gb300.build [--force] [--no-binding]
 
 Compiles csrc/*.cu (one nvcc per translation unit, in parallel) and links
   libkda.so          the product library (C ABI of include/kda.h and include/kda_ops.h)
   libkda_selftest.so test-only checks of the tcgen05 / TMA building blocks
   _kda_ops.so        the Python binding of include/kda_ops.h (csrc/ops_binding.cpp)
-next to this file.  Objects go to _build/ (git-ignored).
+next to this file.  Objects go to _build/ (git-ignored).  The first two need nvcc
+alone; the binding, which only Python callers use, needs torch with its headers
+and g++, and is left out with --no-binding or where there is no torch.
 """
 import concurrent.futures as cf
 import os
@@ -94,13 +96,24 @@ def _link_binding(obj):
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False) -> str:
+def _torch_is_there() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("no torch: %s is left out (the C library is complete)" % os.path.basename(BINDING), file=sys.stderr)
+        return False
+    return True
+
+
+def build(force: bool = False, binding: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     todo = []
     for out, srcs in ((LIB, LIB_SOURCES), (SELFTEST_LIB, SELFTEST_SOURCES)):
         if force or not os.path.exists(out) or os.path.getmtime(out) < _newest_input(srcs):
             todo.append((out, srcs))
-    binding = force or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < _newest_input([BINDING_SOURCE])
+    if binding:
+        stale = force or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < _newest_input([BINDING_SOURCE])
+        binding = stale and _torch_is_there()
     if not todo and not binding:
         return LIB
     all_srcs = sorted({s for _, srcs in todo for s in srcs})
@@ -115,4 +128,4 @@ def build(force: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv))
+    print(build(force="--force" in sys.argv, binding="--no-binding" not in sys.argv))

@@ -174,3 +174,18 @@ def test_frequencies_by_parts_where_all_are_faster_than_slow_turns(ops):
     assert 0.2 < float(keep[-1]) < 0.3
     want = f.double() * (keep + (1 - keep) / factor)
     assert bool(((g.double() / want - 1).abs() < 2 ** -22).all())
+
+
+# ---------------------------------------------------------------- the C library without Python's binding
+def test_library_builds_without_torch(ops, monkeypatch, tmp_path, capsys):
+    """A user of the C interface alone needs neither torch nor its headers."""
+    import os
+    import sys
+    from kda_chunked_prefill_02_gb300 import build
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_kda_ops.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setitem(sys.modules, "torch", None)   # import torch: ImportError
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert "left out" in capsys.readouterr().err
+    assert build.build(binding=False) == build.LIB
+    assert not os.path.exists(build.BINDING) and capsys.readouterr().err == ""
