@@ -37,7 +37,9 @@ extern "C" {
  *     y_t[c] /= sqrt(sum over its head of 128 channels of y_t^2 + norm_eps)
  *                                              (channels c < norm_channels)
  *
- * in fp32, rounded once to the element type of x.
+ * in fp32, rounded once to the element type of x.  (With silu z has to be below
+ * 2^127; under the root fp32 numbers below 2^-126 count as 0, which only a norm_eps
+ * below that leaves to be seen.)
  *
  * Sequences: padded (cu_seqlens NULL): num_seqs sequences of seqlen tokens,
  * element (n, t, c) of x at n*x_stride[0] + t*x_stride[1] + c; packed: device
@@ -96,6 +98,7 @@ kda_status kda_short_conv(const kda_short_conv_args* args, void* stream);
  *
  * for i < rot_dim / 2, s = rope_scale, on the pairs (a, b) = (y[i], y[i + rot_dim/2])
  * or, with interleaved = 1, (y[2i], y[2i+1]); channels from rot_dim on keep y.
+ * (The root as in kda_short_conv.)
  * Long contexts are a matter of inv_freq and rope_scale.  The angle is formed
  * and reduced with an error below 1e-6 turns for every int32 position.
  *
