@@ -181,7 +181,10 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  * head_dim 64, 128 or 256; Hq a multiple of Hk; max_nodes <= 256.
  * max_context: an upper bound of context_lens that the host knows (<= 0: what
  * the page table can address); it sets how the work is cut, not the result's
- * definition.  A context length or node count out of range gives the request
+ * definition.  Give it where the table is much wider than the contexts: 4 requests
+ * of 5 drafts and 4 query heads a key head over up to 1000 tokens, in a table for
+ * 131072, take 10.7 us with it and 17.8 without, one token over 1000 tokens 7.5
+ * and 9.5.  A context length or node count out of range gives the request
  * zero rows; a page outside 0 .. num_pages - 1 reads as zeros; both are
  * reported in device_status.
  * workspace: kda_tree_attention_workspace_size(args) bytes, 256-byte aligned,

@@ -42,7 +42,7 @@
 //
 // The running maximum moves only when a row's scores exceed it by 2^8 (l and O
 // stay far inside fp32 and P inside fp16 until then), so that O in TMEM is
-// hardly ever rescaled; that is the softmax threads' work, in the time between
+// hardly ever rescaled (a published refinement of the softmax in one pass); that is the softmax threads' work, in the time between
 // a score tile's arrival (which implies that the product before it is done) and
 // their P's.
 //

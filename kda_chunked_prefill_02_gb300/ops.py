@@ -5,8 +5,8 @@ The operators a serving decoder runs around KDA: the short causal convolution
 (`kda_qk_norm_rope`, frequencies from `rope_frequencies`), and the attention of
 drafted tokens over a paged cache (`kda_tree_attention`, masks from
 `tree_mask`).  The tensors' checks and the calls are in the native binding
-csrc/ops_binding.cpp; the structures below are the C ABI's, for callers of the
-library itself.  As in kda.py, outputs and workspaces come from torch, any status
+csrc/ops_binding.cpp, which also sees to it that a call's tensors are on one
+device; the structures below are the C ABI's, for callers of the library itself.  As in kda.py, outputs and workspaces come from torch, any status
 other than KDA_OK raises KdaError, and there is no fallback.
 """
 import ctypes
@@ -195,7 +195,8 @@ def tree_mask(parents):
 
     parents: int tensor [R, N]; parents[r, i] < i is the node that node i
     follows, -1 for a node right behind the context, -2 for a node that is not
-    in the tree (it sees nothing, not even itself).  Returns int64
+    in the tree (it sees no node, not even itself; the context it sees, as every
+    node does, so that its row is zero only over an empty one).  Returns int64
     [R, N, ceil(N/64)] on the same device: bit j of row i (bit j mod 64 of word
     j // 64) is set for i itself and its ancestors.
     """
@@ -221,8 +222,9 @@ def kda_tree_attention(q, k_cache, v_cache, page_table, context_lens, *, tree_ma
     [R, N, ceil(N/64)]: which nodes a node sees besides the whole context
     (tree_mask(parents); None: a chain, N = 1 a single token); num_nodes int32
     [R]: nodes in use; scale defaults to D^-0.5; max_context: a host upper bound
-    of context_lens (None: what the page table can address); out may be q
-    itself.  Returns out, or
+    of context_lens (None: what the page table can address), by which the kernel and
+    its cut are chosen: with a table much wider than the contexts give it
+    (tree_attention_schedule tells the choice); out may be q itself.  Returns out, or
     (out, lse) with lse fp32 [R, N, Hq].
     """
     given = _overrides_var.get()
