@@ -170,7 +170,8 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  * An empty S_i (and every row past num_nodes[r]) gives out = 0 and lse = -inf.
  * Keys and values that a node does not see have no influence on it, whatever
  * they hold (NaN and infinities too).  Products and sums are fp32; the weights
- * e^{..} enter the product with v in the element type.
+ * e^{..} enter the product with v in the element type (fp16: scaled, so that those
+ * down to 2^-35 of the largest are kept).
  *
  * q and out element (r, i, h, c) at r*s[0] + i*s[1] + h*s[2] + c; cache element
  * (page, row, h, c) likewise; tree_mask contiguous [R, max_nodes, ceil(max_nodes/64)];

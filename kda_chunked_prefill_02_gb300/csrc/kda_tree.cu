@@ -59,6 +59,10 @@ constexpr int kWindow = 256;      // pages listed at a time (a tile has at most 
 constexpr int kByItem = 0, kByCluster = 1, kByLine = 2;
 constexpr int kJoinParts = 4, kJoinRows = 64;   // see launch_join
 template <typename T> constexpr bool elem_is_f16() { return std::is_same<T, __half>::value; }
+// The probabilities meet V in its type.  fp16 ends at 2^-24, and a long context may have its
+// weight in keys far below the largest, so there they are 2^15 times as large (the sum of the
+// softmax too; only the log-sum takes the factor back).
+template <typename T> constexpr float kWeightShift = elem_is_f16<T>() ? 15.f : 0.f;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -333,9 +337,9 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
                     float mx = fmaxf(fmaxf(s[a][0][2 * h], s[a][0][2 * h + 1]), fmaxf(s[a][1][2 * h], s[a][1][2 * h + 1]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float mn = fmaxf(m[a][h], mx), mu = mn == -INFINITY ? 0.f : mn;
+                    const float mn = fmaxf(m[a][h], mx), at0 = mn == -INFINITY ? 0.f : mn, mu = at0 - kWeightShift<T>;
                     moved |= mn != m[a][h];
-                    alpha[a][h] = ex2_approx(m[a][h] - mu);
+                    alpha[a][h] = ex2_approx(m[a][h] - at0);
                     m[a][h] = mn;
                     float sum = 0.f;
 #pragma unroll
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
             const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] = empty ? 0.f : y[k] * inv;
-            const float lse = empty ? -INFINITY : mu + log2f(sum);
+            const float lse = empty ? -INFINITY : mu + log2f(sum) - kWeightShift<T>;
             if (!kLine || whole) {
                 const int h = kvh * p.G + (q - i * p.G);
                 *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + r * p.os[0] + i * p.os[1] + h * p.os[2] + c * 8) =
@@ -736,11 +740,12 @@ TreePlan tree_plan(int R, int Hk, int rows, int D, int64_t max_len, int page, fl
     // over 2000 21 against 17; 304 x 248 over 120 34 against 79, 16 x 248 over 500 26 against
     // 18; head size 256, blocks of 16: 152 x 64 over 4000 125 against 275, 306 x 40 over 10 47
     // against 25, 304 x 512 over 4000 653 against 4421).  Pages have to be whole 8-row groups
-    // of a tile (and the line of work, in key tiles, stays inside 32 bits).
+    // of a tile, the scale's reciprocal finite (and the line of work, in key tiles, stays inside
+    // 32 bits).
     const int block = rows_per_block(rows, D);
     const int64_t row_blocks = (rows + block - 1) / block, items = (int64_t)R * Hk * row_blocks;
     const int64_t work = items * (max_len + 64);
-    t.mma = rows > 16 && page % 8 == 0 && num_sms > 1 && scale > 0.f && max_len / 128 + 1 < (1 << 22) &&
+    t.mma = rows > 16 && page % 8 == 0 && num_sms > 1 && scale > 1e-30f && max_len / 128 + 1 < (1 << 22) &&
             (row_blocks == 1 ? max_len >= 2560 : work >= 98304 && (row_blocks > 2 || max_len >= 512));
     // The rows kernel's cut (also for a cache without a tensor map); at_once is what the
     // tiles in flight leave room for, or for D 64 the registers.

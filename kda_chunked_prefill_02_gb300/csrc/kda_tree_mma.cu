@@ -40,9 +40,9 @@
 // x 512 rows over 0.2 to 1 times 16000 2.24 ms, 1.14 PFLOP/s (15.8 ms in the kernel for
 // few rows).
 //
-// The running maximum moves only when a row's scores exceed it by 2^8 (l and O
-// stay far inside fp32 and P inside fp16 until then), so that O in TMEM is
-// hardly ever rescaled (a published refinement of the softmax in one pass); that is the softmax threads' work, in the time between
+// The running maximum moves only when a row's scores exceed it by a factor of
+// 2^8 (2^4 in fp16; l and O stay far inside fp32 and P inside its type until
+// then), so that O in TMEM is hardly ever rescaled (a published refinement of the softmax in one pass); that is the softmax threads' work, in the time between
 // a score tile's arrival (which implies that the product before it is done) and
 // their P's.
 //
@@ -78,7 +78,13 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 2
 // Floats of the rows' way out: a patch a warp, 32 columns of stream 1, its maxima and sums.
 constexpr int kPatch = 32 * 36, kWayOut = 8 * kPatch + 34 * 128;
 constexpr int kCostTwo = 5, kCostOne = 4;  // cost of a key tile for two row tiles, for one
-constexpr float kLazy = 8.f;             // log2 units by which scores may exceed the running maximum
+// P enters its product in the element type.  bf16: scores may exceed the running maximum by 8
+// log2 units.  fp16 ends at 2^-24, and a long context may have its weight in keys far below the
+// largest, so there the maximum is held 11 units lower than the scores and they may exceed it
+// by 15: P uses fp16's range up to 2^15 (l carries the same factor, the log-sum m c + log2 l
+// none).  A maximum that moves at 4 units instead of 8 is not slower to measure.
+template <typename T> constexpr float kLazy = std::is_same<T, __half>::value ? 15.f : 8.f;
+template <typename T> constexpr float kShift = std::is_same<T, __half>::value ? 11.f : 0.f;
 
 // mbar_wait (sm103.cuh) with the clock and the abort flag looked at every 64th time
 // only: between a phase's end and this thread's next step there is then nothing but
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const int stream = warp >> 2, row_in = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tb + lane_base + kTmemS + 128 * stream, to = tb + lane_base + kTmemO + 128 * stream;
-        const float c = p.scale_log2, lazy = kLazy / c;
+        const float c = p.scale_log2, lazy = kLazy<T> / c;   // in units of the scores
         bool ok = true;
         int item = 0, seen_s = 0;   // items begun, score tiles taken
         for (;; ++item) {
@@ -643,8 +649,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                     float alpha = 1.f;
                     if (top > m + lazy || m == -INFINITY) {
-                        if (m != -INFINITY) alpha = ex2_approx((m - top) * c);
-                        m = fmaxf(m, top);
+                        const float mn = fmaxf(m, kShift<T> == 0.f ? top : fmaf(lazy, -kShift<T> / kLazy<T>, top));
+                        if (m != -INFINITY) alpha = ex2_approx((m - mn) * c);
+                        m = mn;
                         l *= alpha;
                     }
                     if (u > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {

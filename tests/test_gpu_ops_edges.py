@@ -145,6 +145,46 @@ def test_tree_results_over_the_queries(D, N, Hq, Hk, room):
         assert torch.equal(over, apart)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("gap", [13.0, 17.5, 20.0])
+@pytest.mark.parametrize("N,Hq,D,kernel", [(1, 2, 64, "items"), (2, 2, 128, "items"), (1, 2, 256, "items"),
+                                           (20, 2, 64, "many rows"), (20, 2, 128, "many rows"),
+                                           (20, 2, 256, "many rows"), (100, 2, 128, "many rows")])
+def test_tree_weight_in_many_keys_far_below_the_largest(dtype, gap, N, Hq, D, kernel):
+    """One key whose score is `gap` above all others' and whose value is 0, before 200000 keys
+    with values near 1: the result is the many keys' share, 200000 e^-gap of the whole.  As
+    many equal requests as make a CTA take a context whole.  A weight's rounding to fp16 is
+    off by its unit, or where it is smaller by half of 2^-24 at the kernels' scales (2^11 at
+    least)."""
+    g = _gen(114)
+    L, R, page = 200000, 4 * 160, 16
+    q, kc, vc, table, ctx = _tree_inputs(115, [L], N, Hq, 1, D, page, dtype, room=ROOM)
+    q[:], kc[:] = 0, 0
+    q[..., 0] = 1.0
+    vc.copy_(1 + _rand(g, vc.shape, torch.float32, 0.1))
+    at = int(table[0, 77])
+    kc[at, 5, 0, 0], vc[at, 5] = gap, 0
+    # the nodes differ in the last keys that they see, N of 200000: one node stands for all
+    out, ob, lse, lb = tree_reference(q[:, -1:], kc, vc, table, ctx + N - 1, scale=1.0)
+    ob, lb = ob + out.abs() * N / L, lb + N / L
+    if dtype == F16:
+        ob = ob + (L + N) * 2.0 ** -25 * 2.0 ** -11 * vc.abs().max().double()
+    dev = [t.cuda() for t in (q.expand(R, N, Hq, D).contiguous(), kc, vc, table.expand(R, table.shape[1]).contiguous(),
+                              ctx.expand(R).contiguous())]
+    assert K.tree_attention_schedule(dev[0], dev[1], dev[3], scale=1.0)["kernel"] == kernel
+    got, glse = K.kda_tree_attention(*dev, scale=1.0, return_lse=True)
+    for r in (0, 1, R // 2, R - 1):
+        within(got[r], out[0].expand(N, Hq, D), ob[0].expand(N, Hq, D))
+        within(glse[r], lse[0].expand(N, Hq), lb[0].expand(N, Hq))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("scale", [1e-38, 1e-20, 1e10])
+def test_tree_scales_near_the_ends_of_their_type(dtype, scale):
+    """Every key alike, and one key alone, through the rows that would take the kernel for many."""
+    _tree_case(116, [900, 64, 0], 12, 8, 2, 128, 16, dtype, scale=scale, room=ROOM, q_scale=1.0 if scale < 1 else 1e-10)
+
+
 def _cut(ctx, N, Hq, Hk, D, page, room):
     """How _tree_case's call is cut on this GPU."""
     empty = lambda *shape: torch.empty(shape, dtype=BF16, device="meta")  # noqa: E731
