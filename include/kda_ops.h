@@ -100,7 +100,8 @@ kda_status kda_short_conv(const kda_short_conv_args* args, void* stream);
  * or, with interleaved = 1, (y[2i], y[2i+1]); channels from rot_dim on keep y.
  * (The root as in kda_short_conv.)
  * Long contexts are a matter of inv_freq and rope_scale.  The angle is formed
- * and reduced with an error below 1e-6 turns for every int32 position.
+ * and reduced with an error below 1e-6 turns for every int32 position and
+ * frequencies up to 2^20.
  *
  * q element (b, t, h, c) at b*s[0] + t*s[1] + h*s[2] + c, likewise k, v and the
  * outputs; positions (and slots) at b*seqlen + t, contiguous.  q_out / k_out

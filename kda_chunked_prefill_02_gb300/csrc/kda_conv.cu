@@ -15,7 +15,7 @@
 // over the head), which other warps hide, and the issue slots leave some 85 cycles
 // a warp and token at the memory's rate: so few channels a thread (many warps),
 // packed fp32 pairs, and four tokens at a time, whose norms share one reduction
-// and one root.  Measured, 32768 tokens of 12288 channels, bf16: 246 us, 6.5 TB/s
+// and one root.  Measured, 32768 tokens of 12288 channels, bf16: 247 us, 6.5 TB/s
 // (372 us with 8 channels a thread, plain fp32 and loads in registers; 292 us
 // with everything but the four tokens' shared reduction and the folded log2 e).
 //

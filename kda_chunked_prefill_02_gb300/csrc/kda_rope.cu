@@ -34,7 +34,7 @@
 // (hi = round(p f), lo = fma(p, f, -hi), exact while p is) and hi is reduced by
 // the nearest multiple of 2 pi with 2 pi in two parts, each step one FMA whose
 // result is small; positions or products of 2^24 and beyond are reduced in
-// double.
+// the same way in double.
 #include "kda_internal.h"
 #include "ops_internal.h"
 
@@ -60,8 +60,11 @@ __device__ __forceinline__ float reduced_angle(int pos, float f) {
         const float k = rintf(hi * 0.15915494309189535f);
         return fmaf(-k, kTwoPiRest, fmaf(-k, kTwoPi, hi)) + lo;
     }
-    const double a = (double)pos * (double)f;
-    return (float)(a - 6.283185307179586476925 * rint(a * 0.15915494309189533577));
+    // the same in double: the product has up to 55 bits, and its rounding and that of 2 pi count
+    // from frequencies of some 16 on
+    constexpr double kTwoPiD = 6.283185307179586, kTwoPiDRest = 2.4492935982947064e-16;
+    const double d = (double)pos, a = d * (double)f, rest = fma(d, (double)f, -a), k = rint(a * 0.15915494309189533577);
+    return (float)(fma(-k, kTwoPiDRest, fma(-k, kTwoPiD, a)) + rest);
 }
 
 // 1 / sqrt(a[k] / D + eps) of two sums over groups of kLanes lanes, each to all of

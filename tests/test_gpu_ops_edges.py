@@ -1,4 +1,6 @@
 """The operators of include/kda_ops.h on the GPU at the edges of what their headers allow."""
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -8,6 +10,10 @@ from ops_test_util import conv_reference, rope_reference, tree_reference, within
 
 pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
+
+
+# 2 pi to 50 digits
+TWO_PI = "6.2831853071795864769252867665590057683943387987502"
 
 
 def _gen(seed):
@@ -108,6 +114,29 @@ def test_rope_without_the_norm_leaves_the_weights_alone(interleaved, wdtype):
         assert torch.equal(a, b)
     within(weighted[0], *rope_reference(q, pos, freq, None, norm=False, interleaved=interleaved))
     within(weighted[1], *rope_reference(k, pos, freq, None, norm=False, interleaved=interleaved))
+
+
+@pytest.mark.parametrize("lo,hi", [(1 << 22, 1 << 24), ((1 << 24) - 500, (1 << 24) + 500), (1 << 24, 1 << 31),
+                                   (-(1 << 31), -(1 << 24))])
+@pytest.mark.parametrize("factor", [1.0, 3.7, 1000.0, 1e6])
+def test_rope_angles_of_large_positions_and_frequencies(lo, hi, factor):
+    """Products of up to 55 bits, some 3e14 turns.  The reference's angle is formed without
+    rounding, from integers, since doubles do not hold it."""
+    g = _gen(117)
+    T, half = 500, 16
+    q = _rand(g, (T, 2, 64), F16)
+    pos = torch.randint(lo, hi, (T,), generator=g).to(torch.int32)
+    freq = (10000.0 ** (-torch.arange(half).double() / half) * factor).float()
+    turn = Fraction(TWO_PI)
+    angle = torch.tensor([[float(Fraction(int(p)) * Fraction(float(f)) % turn) for f in freq] for p in pos],
+                         dtype=torch.float64)
+    out, _ = K.kda_qk_norm_rope(q.cuda(), q.cuda(), pos.cuda(), freq.cuda(), norm=False)
+    # the reference with these angles: positions 0 .. T - 1 stand for them one by one
+    y = torch.empty(T, 2, 64, dtype=torch.float64)
+    bound = torch.empty_like(y)
+    for t in range(T):
+        y[t:t + 1], bound[t:t + 1] = rope_reference(q[t:t + 1], torch.ones(1), angle[t], None, norm=False)
+    within(out, y, bound)
 
 
 # ---------------------------------------------------------------- tree attention
