@@ -18,6 +18,9 @@
 // and one root.  Measured, 32768 tokens of 12288 channels, bf16: 247 us, 6.5 TB/s
 // (372 us with 8 channels a thread, plain fp32 and loads in registers; 292 us
 // with everything but the four tokens' shared reduction and the folded log2 e).
+// Drafts (256 sequences of 4 tokens of 12288 channels, accepted = 0): 22.1 us, their
+// bytes 13.0; the commit alone 14.1.  A tile walks its seven or so short sequences
+// one after the other.
 //
 // Tiles cut the flat token range, whatever sequences they meet, so that ragged
 // batches need no host knowledge of cu_seqlens and leave no empty CTA.  The
