@@ -19,6 +19,14 @@ bool strides8(const int64_t (&s)[N]) {
         if (s[i] < 0 || s[i] % 8) return false;
     return true;
 }
+// Results at their inputs' address lie over them row by row (dims of size 1 aside).
+template <int N>
+bool in_place_or_apart(const void* in, const int64_t (&is)[N], const void* out, const int64_t (&os)[N],
+                       const int64_t (&sizes)[N]) {
+    for (int i = 0; i < N; ++i)
+        if (in == out && sizes[i] > 1 && is[i] != os[i]) return false;
+    return true;
+}
 bool elem_type(int32_t t) { return t == KDA_DTYPE_BF16 || t == KDA_DTYPE_F16; }
 kda_status status_of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
@@ -39,10 +47,8 @@ kda_status check_tree(const kda_tree_attention_args* a) {
         !strides8(a->q_stride) || !strides8(a->out_stride) || !strides8(a->k_cache_stride) ||
         !strides8(a->v_cache_stride))
         return KDA_ERR_UNSUPPORTED;
-    // results over the queries: each row over its own
     const int64_t sizes[3] = {a->num_requests, a->max_nodes, a->num_q_heads};
-    for (int i = 0; i < 3; ++i)
-        if (a->out == a->q && sizes[i] > 1 && a->out_stride[i] != a->q_stride[i]) return KDA_ERR_INVALID_ARG;
+    if (!in_place_or_apart(a->q, a->q_stride, a->out, a->out_stride, sizes)) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
 
@@ -136,6 +142,10 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, void* stream) {
         (cached && !strides8(a->k_cache_stride)) ||
         (a->v_cache && (!strides8(a->v_stride) || !strides8(a->v_cache_stride))))
         return KDA_ERR_UNSUPPORTED;
+    const int64_t q_sizes[3] = {a->batch, a->seqlen, a->num_q_heads}, k_sizes[3] = {a->batch, a->seqlen, a->num_k_heads};
+    if ((a->num_q_heads > 0 && !in_place_or_apart(a->q, a->q_stride, a->q_out, a->q_out_stride, q_sizes)) ||
+        (a->num_k_heads > 0 && a->k_out && !in_place_or_apart(a->k, a->k_stride, a->k_out, a->k_out_stride, k_sizes)))
+        return KDA_ERR_INVALID_ARG;
     const int sms = device_sm_count();
     if (sms < 1) return KDA_ERR_CUDA;
     RopeParams p;

@@ -116,6 +116,27 @@ def test_tree_results_over_other_queries_are_refused(ops):
     assert size(out=PTR, num_requests=1, out_stride0=4096) > 0
 
 
+def test_rope_results_over_other_heads_are_refused(ops):
+    """The same with q_out at q's address and k_out at k's.  (Only calls that are refused.)"""
+    def run(**kw):
+        a = ops.QkNormRopeArgs()
+        a.q = a.q_out = a.positions = a.inv_freq = PTR
+        a.k = a.k_out = 2 * PTR
+        for n in ("q", "k", "q_out", "k_out"):
+            for i, s in enumerate((4096, 512, 128)):
+                setattr(a, "%s_stride%d" % (n, i), s)
+        a.batch, a.seqlen, a.num_q_heads, a.num_k_heads, a.head_dim, a.rot_dim = 2, 3, 4, 2, 128, 64
+        a.weight_dtype, a.norm, a.norm_eps, a.rope_scale = 2, 1, 1e-6, 1.0
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return ops._fn().kda_qk_norm_rope(ctypes.byref(a), None)
+
+    invalid = 1
+    for kw in (dict(q_out_stride0=8192), dict(q_out_stride1=1024), dict(q_out_stride2=256), dict(k_out_stride0=2048),
+               dict(k_out_stride1=256), dict(k_out_stride2=256)):
+        assert run(**kw) == invalid, kw
+
+
 @pytest.mark.parametrize("bound", [(1 << 63) - 1, (1 << 63) - 4, 1 << 62, 1 << 31])
 def test_tree_bound_of_the_contexts_near_the_end_of_its_type(ops, bound):
     """A bound past what the page table addresses is no bound."""
