@@ -2,8 +2,11 @@
  * kda_ops.h -- the operators a serving decoder runs around Kimi Delta Attention
  * (kda.h): the short causal convolution in front of a KDA layer, the query /
  * key norm with the position rotation in front of a softmax-attention layer,
+ * the attention of chunks of new tokens (prompts, and single tokens among them)
  * and the attention that verifies drafted tokens (a tree, a chain, or one
- * token) over that layer's paged cache.
+ * token) over that layer's paged cache, the norm of the residual stream between
+ * the blocks, and what moves in caches and pools when a tree has been verified or
+ * a request is forked.
  *
  * Conventions are those of kda.h: device pointers owned by the caller, element
  * strides, asynchronous calls on `stream`, host errors returned synchronously
@@ -251,6 +254,185 @@ typedef struct kda_tree_schedule {
     int32_t kernel, ordered, cluster, launches;
 } kda_tree_schedule;
 kda_status kda_tree_attention_schedule(const kda_tree_attention_args* args, int num_sms, kda_tree_schedule* schedule);
+
+/*
+ * Attention of chunks of new tokens over a paged cache: prompts, pieces of prompts
+ * behind what is cached of them, and single tokens among them.  Request r has a
+ * context of context_lens[r] tokens and n_r new tokens, whose keys and values are in
+ * the cache behind the context's: position p < context_lens[r] + n_r is row p mod
+ * page_size of page page_table[r][p / page_size].  New token i of r sees the
+ * positions p <= context_lens[r] + i.  With query head h and key head h / (Hq / Hk):
+ *
+ *     out_i = sum_p e^{scale q_i.k_p - m} v_p / sum_p e^{scale q_i.k_p - m},
+ *     lse_i = ln sum_p e^{scale q_i.k_p}
+ *
+ * Keys and values behind a token's own position have no influence on it, whatever they
+ * hold (NaN and infinities too).  Products and sums are fp32; the weights e^{..} enter
+ * the product with v in the element type (fp16: scaled, so that those down to 2^-35 of
+ * the largest are kept).
+ *
+ * Tokens: padded (cu_seqlens NULL): num_requests chunks of seqlen tokens, element
+ * (r, i, h, c) of q at r*q_stride[0] + i*q_stride[1] + h*q_stride[2] + c; packed: device
+ * int32 cu_seqlens [num_requests + 1] over seqlen tokens in all, stride [0] unused.
+ * cu_seqlens starts at 0, does not decrease and ends at most at seqlen; rows behind the
+ * last request's are left as they were.  out likewise; out may be q itself (same pointer
+ * and strides; head size 256 then takes the kernel for few rows), otherwise no overlap.
+ * lse contiguous fp32 [R, seqlen, Hq] ([seqlen, Hq]) or NULL.
+ * Cache element (page, row, h, c) as in kda_tree_attention; page_table row r at
+ * r*page_table_stride.
+ * head_dim 64, 128 or 256; Hq a multiple of Hk.
+ * max_context: an upper bound of context_lens that the host knows (< 0: what the page
+ * table can address); it sets how the work is cut, not the result's definition.  Give it
+ * where the table is much wider than the contexts.
+ * A request whose context length is below zero, above max_context, or with its new tokens
+ * past what a row of the page table addresses gives zero rows (lse -inf), one whose
+ * cu_seqlens decreases or passes seqlen has none; a page outside 0 .. num_pages - 1 reads
+ * as zeros; all are reported in device_status.
+ * workspace: kda_chunk_attention_workspace_size(args) bytes, 256-byte aligned, used
+ * during the call's kernels only.
+ * Size limits: R <= 65535, Hk <= 65535, Hq / Hk <= 65536, tokens (of a request where padded)
+ * times Hq / Hk below 2^31, contexts with their new tokens up to 2^30.
+ */
+typedef struct kda_chunk_attention_args {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    void* out;
+    float* lse;
+    const int32_t* page_table;
+    const int32_t* context_lens;
+    const int32_t* cu_seqlens;
+    void* workspace;
+    int32_t* device_status;
+    size_t workspace_bytes;
+    int64_t q_stride[3];        /* (request, token, head) element strides */
+    int64_t out_stride[3];
+    int64_t k_cache_stride[3];  /* (page, row, head) element strides */
+    int64_t v_cache_stride[3];
+    int64_t page_table_stride;
+    int64_t num_requests;
+    int64_t seqlen;             /* padded: new tokens a request; packed: new tokens in all */
+    int64_t num_q_heads;
+    int64_t num_k_heads;
+    int64_t head_dim;
+    int64_t num_pages;
+    int64_t page_size;
+    int64_t pages_per_request;  /* columns of page_table */
+    int64_t max_context;
+    int32_t dtype;              /* KDA_DTYPE_BF16 or KDA_DTYPE_F16 */
+    float scale;
+} kda_chunk_attention_args;
+size_t kda_chunk_attention_workspace_size(const kda_chunk_attention_args* args);
+kda_status kda_chunk_attention(const kda_chunk_attention_args* args, void* stream);
+
+/*
+ * The residual stream between two blocks: a block's output y added to the stream x,
+ * with a norm of its own, a gate and a scale, and the norm in front of the next block:
+ *
+ *     u  = y / sqrt(mean(y^2) + norm_eps) * post_weight    (post_norm = 1; else u = y)
+ *     x' = x + alpha * g * u         (g = gate, gate_sigmoid = 1: 1 / (1 + e^{-gate}), NULL: 1)
+ *     h  = x' / sqrt(mean(x'^2) + norm_eps) * weight
+ *
+ * over the channels of a token, in fp32; x' is rounded once to the stream's type and h,
+ * from the x' before that rounding, once to y's.  y == NULL: x' = x, which is not written
+ * (x_out NULL), and h alone.  out == NULL: x' alone, the weight unread.
+ * (The root as in kda_short_conv; mean squares have to stay below 2^128, -gate below 2^6
+ * for the sigmoid's smallest values to be told from 0.)
+ *
+ * Token t's channels at t*stride; gate_stride may be 0 (one gate for all tokens).
+ * x and x_out have type x_dtype (dtype or KDA_DTYPE_F32; strides multiples of 8 elements
+ * all the same), y, gate and out dtype, the weights (contiguous [channels], NULL: ones)
+ * weight_dtype.  out may be y, and x_out may be x (same pointer and stride), otherwise no
+ * overlap.  channels a multiple of 8, at most 16384.  Size limit: fewer than 2^31 tokens.
+ */
+typedef struct kda_residual_norm_args {
+    const void* x;
+    const void* y;              /* or NULL */
+    const void* gate;           /* or NULL */
+    void* out;                  /* h, or NULL */
+    void* x_out;                /* x'; NULL where y is */
+    const void* weight;
+    const void* post_weight;
+    int64_t x_stride;           /* element strides of a token */
+    int64_t y_stride;
+    int64_t gate_stride;
+    int64_t out_stride;
+    int64_t x_out_stride;
+    int64_t tokens;
+    int64_t channels;
+    int32_t dtype;              /* KDA_DTYPE_BF16 or KDA_DTYPE_F16 */
+    int32_t x_dtype;            /* dtype or KDA_DTYPE_F32 */
+    int32_t weight_dtype;       /* dtype or KDA_DTYPE_F32 */
+    int32_t post_norm;
+    int32_t gate_sigmoid;
+    float alpha;
+    float norm_eps;
+} kda_residual_norm_args;
+kda_status kda_residual_norm(const kda_residual_norm_args* args, void* stream);
+
+/*
+ * A pool of equal entries (a cache's pages, the KDA states or convolution states of
+ * requests) as bytes: element (e, i, j) is `bytes` bytes at data + e*stride[0] +
+ * i*stride[1] + j*stride[2], 0 <= e < entries, i < rows, j < cols.  data, bytes and
+ * strides are multiples of 16; an entry has fewer than 2^31 pieces of 16 bytes.
+ */
+typedef struct kda_pool {
+    void* data;
+    int64_t stride[3];          /* (entry, row, col) byte strides */
+    int64_t entries;
+    int64_t rows;
+    int64_t cols;
+    int64_t bytes;
+} kda_pool;
+
+/*
+ * Entry src[i] copied to entry dst[i], or (rows, device int32 [count], not NULL) its
+ * first rows[i] rows, in every pool: what a forked request needs of its parent's (its
+ * last, partly filled page; its KDA and convolution states).  src and dst device int32
+ * [count]; a negative index, or src[i] = dst[i], copies nothing.  A dst is none of the
+ * other indices of the call.  An index or row count past a pool's is reported in
+ * device_status and that copy left out of that pool.  Size limits: count and num_pools
+ * <= 65535.
+ */
+typedef struct kda_pool_copy_args {
+    const kda_pool* pools;      /* host array [num_pools] */
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* rows;        /* or NULL */
+    int32_t* device_status;
+    int64_t num_pools;
+    int64_t count;
+} kda_pool_copy_args;
+kda_status kda_pool_copy(const kda_pool_copy_args* args, void* stream);
+
+/*
+ * The cache rows of a verified tree's accepted nodes moved together behind their
+ * context: with the pages and context of kda_tree_attention, row context_lens[r] +
+ * path[r][j] goes to row context_lens[r] + j, j < accepted[r], in every cache (a layer's
+ * keys or values; the pool's rows are a page's, entries its pages).  path (device int32
+ * [R, max_path], contiguous) holds the accepted nodes in their order and ascends, as the
+ * path from a tree's root does.  context_lens is not changed: the next call's is
+ * context_lens[r] + accepted[r].
+ * A path that does not ascend or leaves the page table's row, an accepted[r] outside 0 ..
+ * max_path or a context below zero leaves the request out, a page outside the pool the
+ * row; both are reported in device_status.  No other request may use the pages that rows
+ * are moved to.  All caches have the same rows (the page size).
+ * Size limits: max_path <= 256, R and num_caches <= 65535, a request's tokens <= 2^30.
+ */
+typedef struct kda_cache_commit_args {
+    const kda_pool* caches;     /* host array [num_caches] */
+    const int32_t* page_table;
+    const int32_t* context_lens;
+    const int32_t* path;
+    const int32_t* accepted;
+    int32_t* device_status;
+    int64_t num_caches;
+    int64_t page_table_stride;
+    int64_t num_requests;
+    int64_t max_path;           /* columns of path */
+    int64_t pages_per_request;  /* columns of page_table */
+} kda_cache_commit_args;
+kda_status kda_cache_commit(const kda_cache_commit_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,485 @@
+// kda_chunk.cu -- attention of chunks of new tokens over a paged cache
+// (kda_chunk_attention in include/kda_ops.h): the kernel for few rows and for caches
+// that have no tensor map, and the choice between the kernels.
+//
+// The rows of one (request, key head) are its new tokens times the G query heads that
+// share the key head.  One pass over the keys with the running maximum m and sum l of
+// the softmax:
+//
+//     m' = max(m, max_p s_p),  o' = o 2^(m - m') + sum_p 2^(s_p - m') v_p,  l' likewise,
+//
+// s in units of log2.  A CTA takes a block of 16 or 32 rows and the keys that its last
+// token sees, in 64-token tiles by 16-byte asynchronous copies, three tiles deep; the
+// four warps split a tile's tokens and join their rows at the end, as in kda_tree.cu.
+// Where the blocks are few, a cluster of up to 8 CTAs shares one, an equal stretch of
+// its tiles each, and joins the rows through distributed shared memory.
+//
+// Which request a block belongs to is found on the device: a call's grid has room for
+// floor(tokens * G / rows) + requests blocks, as many as ragged requests can need.
+//
+// Keys behind a row's own are taken out of the scores by a select; V rows past the
+// request's end are zero-filled, and a tile in which some row does not see a key whose V
+// is not finite takes a scalar product that leaves out what a row does not see
+// (0 * NaN is NaN).
+#include "kda_internal.h"
+#include "ops_internal.h"
+#include "sm103.cuh"
+#include "warp_mma.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kChunkThreads = 128;
+constexpr int kTile = 64;      // tokens a tile, 16 a warp
+constexpr int kStages = 3;
+constexpr int kWindow = 256;   // pages listed at a time (a tile has at most kTile)
+template <typename T> constexpr bool elem_is_f16() { return std::is_same<T, __half>::value; }
+// The probabilities meet V in its type.  fp16 ends at 2^-24, and a long context may have its
+// weight in keys far below the largest, so there they are 2^15 times as large (the sum of the
+// softmax too; only the log-sum takes the factor back).
+template <typename T> constexpr float kWeightShift = elem_is_f16<T>() ? 15.f : 0.f;
+
+template <typename T, int D, int MT, bool kCluster>
+__global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkParams p) {
+    constexpr int kRows = 16 * MT;
+    constexpr uint32_t kKV = kTile * D * 2, kStage = 2 * kKV;
+    extern __shared__ __align__(128) uint8_t smt[];
+    __shared__ int spage[kWindow];
+    __shared__ int s_request, s_block;
+    uint8_t* sq = smt + p.stages * kStage;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+    const int cluster = kCluster ? p.cluster : 1, rank = kCluster ? blockIdx.x % cluster : 0;
+    const int kvh = blockIdx.y;
+    // this CTA's block of rows: the requests' blocks one after the other
+    if (warp == 0) {
+        const int64_t at = blockIdx.x / cluster;
+        int64_t before = 0;
+        int request = -1, block = 0;
+        if (!p.cu) {
+            const int each = (int)(((int64_t)p.T * p.G + kRows - 1) / kRows);
+            request = (int)(at / each);
+            block = (int)(at - (int64_t)request * each);
+        } else {
+            for (int r0 = 0; r0 < p.R; r0 += 32) {
+                int first, n = 0, len, blocks = 0;
+                if (r0 + lane < p.R) {
+                    const bool ok = chunk_request(p, r0 + lane, first, n, len);
+                    if (!ok && p.status && at == 0 && rank == 0 && kvh == 0) atomicExch(p.status, 1);
+                    blocks = (int)(((int64_t)n * p.G + kRows - 1) / kRows);
+                }
+                int upto = blocks;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const int64_t off = at - before - (upto - blocks);
+                const uint32_t here = __ballot_sync(0xffffffffu, off >= 0 && off < blocks);
+                if (here && request < 0) {
+                    const int who = __ffs(here) - 1;
+                    request = r0 + who;
+                    block = __shfl_sync(0xffffffffu, (int)off, who);
+                    if (at > 0) break;   // the first block looks at every request
+                }
+                before += __shfl_sync(0xffffffffu, upto, 31);
+            }
+        }
+        if (lane == 0) {
+            s_request = request;
+            s_block = block;
+        }
+    }
+    __syncthreads();
+    const int r = s_request, row0 = s_block * kRows;
+    if (r < 0) return;   // no such block (all CTAs of a cluster)
+    int first, n, len;
+    if (!chunk_request(p, r, first, n, len) && !p.cu && p.status && tid == 0) atomicExch(p.status, 1);
+    const int rows = n * p.G, ctx = len - n;   // without keys (len 0) no row sees any
+    const int token0 = (int)page_div((uint32_t)row0, p.G, p.group_magic);
+    const int token1 = min((int)page_div((uint32_t)(row0 + kRows - 1), p.G, p.group_magic), n - 1);
+    const int end = len == 0 ? 0 : ctx + token1 + 1;   // keys of the block's last token
+    const int tiles = (end + kTile - 1) / kTile;
+    const int t0 = tiles * rank / cluster, t1 = tiles * (rank + 1) / cluster;
+    const int lo = t0 * kTile, hi = min(t1 * kTile, end);
+    const T* qbase = static_cast<const T*>(p.q) + (p.cu ? first * p.qs[1] : r * p.qs[0]);
+    T* obase = static_cast<T*>(p.out) + (p.cu ? first * p.os[1] : r * p.os[0]);
+
+    // the pages of this part, kWindow at a time
+    int page0 = 0;
+    auto list_pages = [&](int tok) {
+        page0 = (int)page_div((uint32_t)tok, p.page, p.page_magic);
+        const int count = hi > tok ? min(kWindow, (int)page_div((uint32_t)(hi - 1), p.page, p.page_magic) - page0 + 1) : 0;
+        for (int e = tid; e < count; e += kChunkThreads) {
+            int id = p.table[r * p.table_stride + page0 + e];
+            if (id < 0 || id >= p.P) {
+                id = -1;
+                if (p.status) atomicExch(p.status, 1);
+            }
+            spage[e] = id;
+        }
+        __syncthreads();
+    };
+    list_pages(lo);
+
+    const uint32_t s0 = smem_addr(smt);
+    const T* kbase = static_cast<const T*>(p.kc) + kvh * p.ks[2];
+    const T* vbase = static_cast<const T*>(p.vc) + kvh * p.vs[2];
+    constexpr int kPieces = D / 8, kRowsPass = kChunkThreads / kPieces;
+    auto load = [&](int tile) {
+        if (lo + tile * kTile < hi) {
+            const uint32_t dst = s0 + (tile % kStages) * kStage;
+            const int c = tid % kPieces;
+#pragma unroll
+            for (int j = 0; j < kTile / kRowsPass; ++j) {
+                const int row = tid / kPieces + j * kRowsPass;
+                const uint32_t tok = (uint32_t)(lo + tile * kTile + row), pg = page_div(tok, p.page, p.page_magic);
+                const int id = (int)tok < hi ? spage[(int)pg - page0] : -1;
+                const int64_t rem = id < 0 ? 0 : tok - pg * p.page, page = id < 0 ? 0 : id;
+                const uint32_t off = tile_off<D>(row, c);
+                cp_async16_or_zero(dst + off, kbase + page * p.ks[0] + rem * p.ks[1] + c * 8, id >= 0);
+                cp_async16_or_zero(dst + kKV + off, vbase + page * p.vs[0] + rem * p.vs[1] + c * 8, id >= 0);
+            }
+        }
+        cp_async_commit();
+    };
+    const int ntiles = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load(i);
+
+    // query rows
+    for (int e = tid; e < kRows * kPieces; e += kChunkThreads) {
+        const int row = e / kPieces, c = e - row * kPieces, q = row0 + row;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (q < rows) {
+            const int i = (int)page_div((uint32_t)q, p.G, p.group_magic), h = kvh * p.G + (q - i * p.G);
+            v = ldg16(qbase + i * p.qs[1] + h * p.qs[2] + c * 8);
+        }
+        *reinterpret_cast<uint4*>(sq + tile_off<D>(row, c)) = v;
+    }
+
+    float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+#pragma unroll
+        for (int b = 0; b < D / 8; ++b)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[a][b][c] = 0.f;
+        m[a][0] = m[a][1] = -INFINITY;
+        l[a][0] = l[a][1] = 0.f;
+    }
+    // how many of the positions from tok on row `row` of this block sees
+    auto sees = [&](int row, int tok) -> int {
+        const int i = (int)page_div((uint32_t)(row0 + row), p.G, p.group_magic);
+        return min(ctx + i + 1, hi) - tok;
+    };
+
+    for (int tile = 0; tile < ntiles; ++tile) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();   // the tile has landed for every thread; the tile before it is consumed
+        const int next = lo + (tile + kStages - 1) * kTile;
+        if (next < hi && (int)page_div((uint32_t)min(next + kTile, hi) - 1, p.page, p.page_magic) - page0 >= kWindow)
+            list_pages(next);
+        load(tile + kStages - 1);
+        const int tok0 = lo + tile * kTile + warp * 16;
+        if (tok0 >= hi) continue;
+        const uint32_t sk = s0 + (tile % kStages) * kStage, sv = sk + kKV;
+
+        float s[MT][2][4];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[a][b][c] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t kb[4];
+            ldmatrix4(kb, sk + tile_off<D>(warp * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                uint32_t qa[4];
+                ldmatrix4(qa, smem_addr(sq) + tile_off<D>(a * 16 + (lane & 15), ks * 2 + (lane >> 4)));
+                mma16816<T>(s[a][0], qa, kb[0], kb[1]);
+                mma16816<T>(s[a][1], qa, kb[2], kb[3]);
+            }
+        }
+        // some row of the block does not see some of these keys
+        const bool ragged = tok0 + 16 > min(hi, ctx + token0 + 1);
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[a][b][c] *= p.scale_log2;
+        if (ragged) {
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int count = sees(a * 16 + g + 8 * h, tok0 + tq * 2);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (b * 8 + c >= count) s[a][b][2 * h + c] = -INFINITY;
+                }
+        }
+        bool moved = false;
+        float alpha[MT][2];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float mx = fmaxf(fmaxf(s[a][0][2 * h], s[a][0][2 * h + 1]), fmaxf(s[a][1][2 * h], s[a][1][2 * h + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m[a][h], mx), at0 = mn == -INFINITY ? 0.f : mn, mu = at0 - kWeightShift<T>;
+                moved |= mn != m[a][h];
+                alpha[a][h] = ex2_approx(m[a][h] - at0);
+                m[a][h] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float& x = s[a][b][2 * h + c];
+                        x = ex2_approx(x - mu);
+                        sum += x;
+                    }
+                l[a][h] = fmaf(l[a][h], alpha[a][h], sum);
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int b = 0; b < D / 8; ++b)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[a][b][c] *= alpha[a][c >> 1];
+        }
+        bool plain = true;
+        if (ragged) {
+            // is all of their V finite?
+            bool bad = false;
+            constexpr uint32_t kExp = Elem<T>::kExpMask;
+#pragma unroll 8
+            for (int e = lane; e < 16 * kPieces; e += 32) {
+                const uint4 v = *reinterpret_cast<const uint4*>(smt + (sv - s0) + (uint32_t)warp * 16 * (D * 2) + e * 16);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bad |= (w[k] & kExp) == kExp || ((w[k] >> 16) & kExp) == kExp;
+            }
+            plain = !__any_sync(0xffffffffu, bad);
+        }
+        if (plain) {
+            uint32_t pa[MT][4];
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                pa[a][0] = Elem<T>::pack(s[a][0][0], s[a][0][1]);
+                pa[a][1] = Elem<T>::pack(s[a][0][2], s[a][0][3]);
+                pa[a][2] = Elem<T>::pack(s[a][1][0], s[a][1][1]);
+                pa[a][3] = Elem<T>::pack(s[a][1][2], s[a][1][3]);
+            }
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b) {
+                uint32_t vb[4];
+                ldmatrix4_trans(vb, sv + tile_off<D>(warp * 16 + (lane & 15), b * 2 + (lane >> 4)));
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    mma16816<T>(o[a][2 * b], pa[a], vb[0], vb[1]);
+                    mma16816<T>(o[a][2 * b + 1], pa[a], vb[2], vb[3]);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < 16 && tok0 + t < hi; ++t) {
+                const int src = (lane & ~3) | ((t & 7) >> 1);
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    const float lo0 = (t & 1) ? s[a][0][1] : s[a][0][0], hi0 = (t & 1) ? s[a][0][3] : s[a][0][2];
+                    const float lo1 = (t & 1) ? s[a][1][1] : s[a][1][0], hi1 = (t & 1) ? s[a][1][3] : s[a][1][2];
+                    const float p0 = __shfl_sync(0xffffffffu, t < 8 ? lo0 : lo1, src);
+                    const float p1 = __shfl_sync(0xffffffffu, t < 8 ? hi0 : hi1, src);
+                    const bool see0 = sees(a * 16 + g, tok0 + t) > 0, see1 = sees(a * 16 + g + 8, tok0 + t) > 0;
+#pragma unroll
+                    for (int b = 0; b < D / 8; ++b) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                            smt + (sv - s0) + tile_off<D>(warp * 16 + t, b) + tq * 4);
+                        const float2 v = Elem<T>::unpack(w);
+                        if (see0) {
+                            o[a][b][0] = fmaf(p0, v.x, o[a][b][0]);
+                            o[a][b][1] = fmaf(p0, v.y, o[a][b][1]);
+                        }
+                        if (see1) {
+                            o[a][b][2] = fmaf(p1, v.x, o[a][b][2]);
+                            o[a][b][3] = fmaf(p1, v.y, o[a][b][3]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();   // every tile is consumed: its memory takes the warps' (m, l, o)
+
+    float* so = reinterpret_cast<float*>(smt);                  // [4][kRows][D], a row's 8-value pieces c at c ^ (row % 8)
+    float* sml = so + 4 * kRows * D;                            // [4][kRows][2]
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float sum = l[a][h];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const int row = a * 16 + g + 8 * h;
+            if (tq == 0) {
+                sml[(warp * kRows + row) * 2] = m[a][h];
+                sml[(warp * kRows + row) * 2 + 1] = sum;
+            }
+#pragma unroll
+            for (int b = 0; b < D / 8; ++b)
+                *reinterpret_cast<float2*>(so + (warp * kRows + row) * D + ((b ^ (row & 7)) * 8) + tq * 2) =
+                    make_float2(o[a][b][2 * h], o[a][b][2 * h + 1]);
+        }
+    __syncthreads();
+    // the four warps' rows joined: the running maximum (0 if there is none), the sum, and
+    // 8 values of the row
+    auto joined = [&](int row, int c, float& mu, float& sum, float (&y)[8]) {
+        float mw[4], mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            mw[w] = sml[(w * kRows + row) * 2];
+            mx = fmaxf(mx, mw[w]);
+        }
+        mu = mx == -INFINITY ? 0.f : mx;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = ex2_approx(mw[w] - mu);
+            sum = fmaf(sml[(w * kRows + row) * 2 + 1], f, sum);
+            const float* src = so + (w * kRows + row) * D + ((c ^ (row & 7)) * 8);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = fmaf(src[k], f, y[k]);
+        }
+    };
+    float* const sx = sml + 4 * kRows * 2;      // cluster: this CTA's rows [kRows][D], then (maximum, sum) [kRows]
+    if (kCluster) {
+        for (int e = tid; e < kRows * kPieces; e += kChunkThreads) {
+            const int row = e / kPieces, c = e - row * kPieces;
+            float mu, sum, y[8];
+            joined(row, c, mu, sum, y);
+            float4* dst = reinterpret_cast<float4*>(sx + row * D + c * 8);
+            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+            if (c == 0) *reinterpret_cast<float2*>(sx + kRows * D + 2 * row) = make_float2(sum == 0.f ? -INFINITY : mu, sum);
+        }
+        cluster_sync();
+    }
+    const uint32_t sx_at = smem_addr(sx);
+    for (int e = rank * kChunkThreads + tid; e < kRows * kPieces; e += cluster * kChunkThreads) {
+        const int row = e / kPieces, c = e - row * kPieces, q = row0 + row;
+        if (q >= rows) break;
+        float mu, sum, y[8];
+        if (!kCluster) {
+            joined(row, c, mu, sum, y);
+        } else {
+            float mx = -INFINITY;
+            for (int w = 0; w < cluster; ++w) mx = fmaxf(mx, remote_ld2(remote_addr(sx_at + (kRows * D + 2 * row) * 4, w)).x);
+            mu = mx == -INFINITY ? 0.f : mx;
+            sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = 0.f;
+            for (int w = 0; w < cluster; ++w) {
+                const float2 ml = remote_ld2(remote_addr(sx_at + (kRows * D + 2 * row) * 4, w));
+                const uint32_t src = remote_addr(sx_at + (row * D + c * 8) * 4, w);
+                const float4 a = remote_ld4(src), b = remote_ld4(src + 16);
+                const float f = ex2_approx(ml.x - mu);
+                sum = fmaf(ml.y, f, sum);
+                y[0] = fmaf(a.x, f, y[0]); y[1] = fmaf(a.y, f, y[1]); y[2] = fmaf(a.z, f, y[2]); y[3] = fmaf(a.w, f, y[3]);
+                y[4] = fmaf(b.x, f, y[4]); y[5] = fmaf(b.y, f, y[5]); y[6] = fmaf(b.z, f, y[6]); y[7] = fmaf(b.w, f, y[7]);
+            }
+        }
+        const int i = (int)page_div((uint32_t)q, p.G, p.group_magic), h = kvh * p.G + (q - i * p.G);
+        const bool empty = sum == 0.f;
+        const float inv = empty ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = empty ? 0.f : y[k] * inv;
+        *reinterpret_cast<uint4*>(obase + i * p.os[1] + h * p.os[2] + c * 8) = pack8<T>(y);
+        if (p.lse && c == 0)
+            p.lse[((p.cu ? (int64_t)first : (int64_t)r * p.T) + i) * p.Hq + h] =
+                empty ? -INFINITY : (mu + log2f(sum) - kWeightShift<T>) * 0.6931471805599453f;
+    }
+    if (kCluster) cluster_sync();   // the others have read this CTA's rows
+}
+
+int rows_per_block(int64_t rows, int D) { return rows <= 16 || D > 128 ? 16 : 32; }
+// Blocks of rows of all requests: exactly (padded), or at most (packed).
+int64_t row_blocks(int R, int T, bool packed, int G, int block) {
+    const int64_t rows = (int64_t)T * G;
+    return packed ? rows / block + R : (int64_t)R * ((rows + block - 1) / block);
+}
+
+template <typename T, int D, int MT, bool kCluster>
+cudaError_t launch_rows_t(const ChunkParams& q, cudaStream_t s) {
+    ChunkParams p = q;
+    // no more tiles in flight than a CTA has, so that more CTAs of short contexts share an SM
+    const int64_t tiles = ((p.max_len + kTile - 1) / kTile + p.cluster - 1) / p.cluster;
+    p.stages = tiles < 1 ? 1 : tiles < kStages ? (int)tiles : kStages;
+    const auto bytes = [](int stages) -> size_t {
+        const size_t load = (size_t)stages * 2 * kTile * D * 2 + 16 * MT * D * 2;
+        const size_t join = (size_t)16 * MT * (kCluster ? 5 * D + 10 : 4 * D + 8) * sizeof(float);
+        return load > join ? load : join;
+    };
+    const auto kernel = chunk_rows_kernel<T, D, MT, kCluster>;
+    static std::atomic<uint64_t> smem_set;
+    cudaError_t e = set_smem_limit_once((const void*)kernel, (int)bytes(kStages), smem_set);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(row_blocks(p.R, p.T, p.cu != nullptr, p.G, 16 * MT) * p.cluster), (unsigned)p.Hk);
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.dynamicSmemBytes = bytes(p.stages);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCluster ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <typename T, int D, int MT>
+cudaError_t launch_rows_m(const ChunkParams& p, cudaStream_t s) {
+    return p.cluster > 1 ? launch_rows_t<T, D, MT, true>(p, s) : launch_rows_t<T, D, MT, false>(p, s);
+}
+template <typename T>
+cudaError_t launch_rows(const ChunkParams& p, int D, cudaStream_t s) {
+    const bool one = rows_per_block((int64_t)p.T * p.G, D) == 16;
+    if (D == 64) return one ? launch_rows_m<T, 64, 1>(p, s) : launch_rows_m<T, 64, 2>(p, s);
+    if (D == 128) return one ? launch_rows_m<T, 128, 1>(p, s) : launch_rows_m<T, 128, 2>(p, s);
+    return launch_rows_m<T, 256, 1>(p, s);
+}
+
+}  // namespace
+
+ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int num_sms) {
+    ChunkPlan t;
+    // Clusters where the blocks are fewer than the CTAs that run at once (what the tiles in
+    // flight leave room for, or for D 64 the registers), at least 128 tokens a CTA.
+    const int at_once = num_sms * (D == 64 ? 4 : D == 128 ? 2 : 1);
+    const int64_t blocks = row_blocks(R, T, packed, G, rows_per_block((int64_t)T * G, D)) * Hk;
+    const int64_t tiles = (max_len + kTile - 1) / kTile;
+    int64_t parts = blocks > 0 ? at_once / blocks : 1;
+    if (parts > (tiles + 1) / 2) parts = (tiles + 1) / 2;
+    t.cluster = parts >= 8 ? 8 : parts >= 4 ? 4 : parts >= 2 ? 2 : 1;
+    return t;
+}
+
+cudaError_t launch_chunk_attention(const ChunkParams& p, const ChunkPlan& plan, int D, bool f16, cudaStream_t s) {
+    ChunkParams q = p;
+    q.cluster = plan.cluster;
+    return f16 ? launch_rows<__half>(q, D, s) : launch_rows<__nv_bfloat16>(q, D, s);
+}
+
+}  // namespace kda

@@ -76,6 +76,69 @@ size_t tree_workspace(const kda_tree_attention_args* a, const TreePlan& plan) {
            plan.order * sizeof(int32_t);
 }
 
+kda_status check_chunk(const kda_chunk_attention_args* a) {
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (a->num_requests < 0 || a->seqlen < 0 || a->num_q_heads < 1 || a->num_k_heads < 1 || a->num_pages < 0 ||
+        a->page_size < 1 || a->pages_per_request < 0 || a->num_q_heads % a->num_k_heads != 0 || !isfinite(a->scale))
+        return KDA_ERR_INVALID_ARG;
+    const int64_t group = a->num_q_heads / a->num_k_heads;
+    if (!elem_type(a->dtype) || (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256) ||
+        a->num_requests > 65535 || a->num_k_heads > 65535 || group > 65536 || a->num_pages > INT32_MAX ||
+        a->page_size > (1 << 30) || a->pages_per_request > INT32_MAX || a->page_table_stride < 0 ||
+        a->seqlen > INT32_MAX / group)
+        return KDA_ERR_UNSUPPORTED;
+    if (a->num_requests == 0) return a->cu_seqlens && a->seqlen > 0 ? KDA_ERR_INVALID_ARG : KDA_OK;
+    if (a->seqlen == 0) return KDA_OK;
+    if (!a->q || !a->k_cache || !a->v_cache || !a->out || !a->page_table || !a->context_lens || a->num_pages < 1)
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->out) ||
+        !strides8(a->q_stride) || !strides8(a->out_stride) || !strides8(a->k_cache_stride) ||
+        !strides8(a->v_cache_stride))
+        return KDA_ERR_UNSUPPORTED;
+    const int64_t sizes[3] = {a->cu_seqlens ? 1 : a->num_requests, a->seqlen, a->num_q_heads};
+    if (!in_place_or_apart(a->q, a->q_stride, a->out, a->out_stride, sizes)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// Tokens of the longest request the call allows for, or -1 past 2^30.
+int64_t chunk_max_len(const kda_chunk_attention_args* a) {
+    const int64_t room = a->pages_per_request * a->page_size;
+    int64_t len = room;
+    if (a->max_context >= 0 && a->max_context < room - a->seqlen) len = a->max_context + a->seqlen;
+    return len > (1 << 30) ? -1 : len;
+}
+
+ChunkPlan plan_of(const kda_chunk_attention_args* a, int64_t max_len, int num_sms) {
+    return chunk_plan((int)a->num_requests, (int)a->seqlen, a->cu_seqlens != nullptr, (int)a->num_k_heads,
+                      (int)(a->num_q_heads / a->num_k_heads), (int)a->head_dim, max_len, num_sms);
+}
+
+uint32_t magic_of(int64_t d) { return d == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint64_t)d); }
+
+// A pool as the kernels take it.
+kda_status pool_desc(const kda_pool& q, PoolDesc& d) {
+    if (q.entries < 0 || q.rows < 0 || q.cols < 0 || q.bytes < 0) return KDA_ERR_INVALID_ARG;
+    if (q.entries > INT32_MAX || q.rows > INT32_MAX || q.cols > INT32_MAX || q.bytes % 16 || q.bytes / 16 > INT32_MAX ||
+        !aligned16(q.data))
+        return KDA_ERR_UNSUPPORTED;
+    const int64_t runs = q.rows * q.cols, pieces = q.bytes / 16;   // below 2^62
+    if (runs > INT32_MAX || runs * pieces > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    for (int64_t st : q.stride)
+        if (st < 0 || st % 16) return KDA_ERR_UNSUPPORTED;
+    if (!q.data && q.entries * runs * pieces > 0) return KDA_ERR_INVALID_ARG;
+    d.data = static_cast<char*>(q.data);
+    for (int i = 0; i < 3; ++i) d.st[i] = q.stride[i];
+    d.entries = (int32_t)q.entries; d.rows = (int32_t)q.rows;
+    // runs that follow one another are one
+    const bool one = q.cols == 1 || q.stride[2] == q.bytes;
+    d.cols = one ? 1 : (int32_t)q.cols;
+    d.pieces = (int32_t)(one ? q.cols * pieces : pieces);
+    if (d.pieces == 0 || d.cols == 0) d.rows = 0, d.cols = d.pieces = 1;   // nothing to copy
+    d.piece_magic = magic_of(d.pieces);
+    d.col_magic = magic_of(d.cols);
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -231,6 +294,138 @@ kda_status kda_tree_attention_ex(const kda_tree_attention_args* a, const kda_ove
     p.timeout_probe = overrides && overrides->timeout_probe ? 1 : 0;
     return status_of(launch_tree_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_chunk_attention_workspace_size(const kda_chunk_attention_args* a) {
+    return 0;
+}
+
+kda_status kda_chunk_attention(const kda_chunk_attention_args* a, void* stream) {
+    const kda_status st = check_chunk(a);
+    if (st != KDA_OK || a->num_requests == 0 || a->seqlen == 0) return st;
+    const int64_t max_len = chunk_max_len(a);
+    if (max_len < 0) return KDA_ERR_UNSUPPORTED;
+    if (device_sm_count() < 1) return KDA_ERR_CUDA;
+    const ChunkPlan plan = plan_of(a, max_len, sm_count_or_default());
+    ChunkParams p;
+    memset(&p, 0, sizeof(p));
+    p.q = a->q; p.kc = a->k_cache; p.vc = a->v_cache; p.out = a->out; p.lse = a->lse;
+    p.table = a->page_table; p.ctx = a->context_lens; p.cu = a->cu_seqlens; p.status = a->device_status;
+    for (int i = 0; i < 3; ++i) {
+        p.qs[i] = a->q_stride[i]; p.os[i] = a->out_stride[i];
+        p.ks[i] = a->k_cache_stride[i]; p.vs[i] = a->v_cache_stride[i];
+    }
+    p.table_stride = a->page_table_stride;
+    p.R = (int)a->num_requests; p.T = (int)a->seqlen; p.Hq = (int)a->num_q_heads; p.Hk = (int)a->num_k_heads;
+    p.G = p.Hq / p.Hk; p.P = (int)a->num_pages; p.page = (int)a->page_size;
+    p.max_len = max_len;
+    p.max_ctx = a->max_context >= 0 && a->max_context < INT32_MAX ? (int32_t)a->max_context : INT32_MAX;
+    p.page_magic = magic_of(p.page);
+    p.group_magic = magic_of(p.G);
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    return status_of(launch_chunk_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_residual_norm(const kda_residual_norm_args* a, void* stream) {
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (a->tokens < 0 || a->channels < 1 || !(a->norm_eps >= 0.f) || !isfinite(a->alpha)) return KDA_ERR_INVALID_ARG;
+    if (!elem_type(a->dtype) || (a->x_dtype != a->dtype && a->x_dtype != KDA_DTYPE_F32) ||
+        (a->weight_dtype != a->dtype && a->weight_dtype != KDA_DTYPE_F32) || a->channels % 8 || a->channels > 16384 ||
+        a->tokens > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (a->tokens == 0) return KDA_OK;
+    if ((!a->out && !a->x_out) || (a->y ? !a->x_out : (a->x_out || a->gate || a->post_norm))) return KDA_ERR_INVALID_ARG;
+    if (!a->x) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {a->x, a->y, a->gate, a->out, a->x_out, a->weight, a->post_weight};
+    for (const void* ptr : ptrs)
+        if (!aligned16(ptr)) return KDA_ERR_UNSUPPORTED;
+    const int64_t strides[] = {a->x_stride, a->y ? a->y_stride : 0, a->gate ? a->gate_stride : 0,
+                               a->out ? a->out_stride : 0, a->x_out ? a->x_out_stride : 0};
+    for (int64_t st : strides)
+        if (st < 0 || st % 8) return KDA_ERR_UNSUPPORTED;
+    const bool many = a->tokens > 1;
+    if (many && ((a->out && a->out_stride < a->channels) || (a->x_out && a->x_out_stride < a->channels)))
+        return KDA_ERR_INVALID_ARG;   // rows that overlap
+    // a result at an input's address replaces that input alone, row by row
+    if ((a->out && (a->out == a->x || a->out == a->x_out || a->out == a->gate ||
+                    (a->out == a->y && many && a->out_stride != a->y_stride))) ||
+        (a->x_out && (a->x_out == a->y || a->x_out == a->gate ||
+                      (a->x_out == a->x && many && a->x_out_stride != a->x_stride))))
+        return KDA_ERR_INVALID_ARG;
+    ResidualParams p;
+    memset(&p, 0, sizeof(p));
+    p.x = a->x; p.y = a->y; p.gate = a->gate; p.out = a->out; p.x_out = a->x_out;
+    p.w = a->weight; p.post_w = a->post_weight;
+    p.xs = a->x_stride; p.ys = a->y_stride; p.gs = a->gate_stride; p.os = a->out_stride; p.xos = a->x_out_stride;
+    p.tokens = a->tokens; p.E = (int)a->channels; p.post = a->post_norm ? 1 : 0; p.sigmoid = a->gate_sigmoid ? 1 : 0;
+    p.w_f32 = a->weight_dtype == KDA_DTYPE_F32 ? 1 : 0;
+    p.alpha = a->alpha; p.eps = a->norm_eps;
+    const int sms = device_sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
+    return status_of(launch_residual_norm(p, a->dtype == KDA_DTYPE_F16, a->x_dtype == KDA_DTYPE_F32, sms,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_pool_copy(const kda_pool_copy_args* a, void* stream) {
+    if (!a || a->num_pools < 0 || a->count < 0 || (a->num_pools > 0 && !a->pools)) return KDA_ERR_INVALID_ARG;
+    if (a->num_pools > 65535 || a->count > 65535) return KDA_ERR_UNSUPPORTED;
+    PoolCopyParams p;
+    memset(&p, 0, sizeof(p));
+    for (int64_t k = 0; k < a->num_pools; ++k) {   // every pool is looked at before the first launch
+        const kda_status st = pool_desc(a->pools[k], p.pool[0]);
+        if (st != KDA_OK) return st;
+    }
+    if (a->num_pools == 0 || a->count == 0) return KDA_OK;
+    if (!a->src || !a->dst) return KDA_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
+    p.src = a->src; p.dst = a->dst; p.rows = a->rows; p.status = a->device_status;
+    p.count = (int)a->count;
+    for (int64_t k = 0; k < a->num_pools; k += kPoolSlice) {
+        p.pools = (int)(a->num_pools - k < kPoolSlice ? a->num_pools - k : kPoolSlice);
+        for (int i = 0; i < p.pools; ++i) pool_desc(a->pools[k + i], p.pool[i]);
+        const cudaError_t e = launch_pool_copy(p, sms, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}
+
+kda_status kda_cache_commit(const kda_cache_commit_args* a, void* stream) {
+    if (!a || a->num_caches < 0 || a->num_requests < 0 || a->max_path < 0 || a->pages_per_request < 0 ||
+        (a->num_caches > 0 && !a->caches))
+        return KDA_ERR_INVALID_ARG;
+    if (a->num_caches > 65535 || a->num_requests > 65535 || a->max_path > 256 || a->pages_per_request > INT32_MAX ||
+        a->page_table_stride < 0)
+        return KDA_ERR_UNSUPPORTED;
+    CacheCommitParams p;
+    memset(&p, 0, sizeof(p));
+    for (int64_t k = 0; k < a->num_caches; ++k) {
+        const kda_status st = pool_desc(a->caches[k], p.pool[0]);
+        if (st != KDA_OK) return st;
+        if (a->caches[k].rows < 1 || a->caches[k].rows != a->caches[0].rows || a->caches[k].cols < 1 ||
+            a->caches[k].bytes < 16)
+            return KDA_ERR_INVALID_ARG;
+    }
+    if (a->num_caches == 0 || a->num_requests == 0 || a->max_path == 0) return KDA_OK;
+    if (!a->page_table || !a->context_lens || !a->path || !a->accepted) return KDA_ERR_INVALID_ARG;
+    const int64_t page = a->caches[0].rows;
+    if (page > (1 << 30) || a->pages_per_request * page > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    const int sms = device_sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
+    p.table = a->page_table; p.ctx = a->context_lens; p.path = a->path; p.accepted = a->accepted;
+    p.status = a->device_status;
+    p.table_stride = a->page_table_stride;
+    p.room = a->pages_per_request * page;
+    p.R = (int)a->num_requests; p.max_path = (int)a->max_path; p.page = (int)page;
+    p.page_magic = magic_of(page);
+    for (int64_t k = 0; k < a->num_caches; k += kPoolSlice) {
+        p.pools = (int)(a->num_caches - k < kPoolSlice ? a->num_caches - k : kPoolSlice);
+        for (int i = 0; i < p.pools; ++i) pool_desc(a->caches[k + i], p.pool[i]);
+        const cudaError_t e = launch_cache_commit(p, sms, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
 }
 
 }  // extern "C"

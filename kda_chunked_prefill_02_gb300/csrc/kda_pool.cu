@@ -1,0 +1,154 @@
+// kda_pool.cu -- copies between the entries of pools (kda_pool_copy in
+// include/kda_ops.h: cache pages, KDA states, convolution states of requests that are
+// forked) and the rows of a verified tree's accepted nodes moved together behind their
+// context in the caches of all layers (kda_cache_commit).
+//
+// Both move bytes: each is read and written once, and what counts is that many 16-byte
+// loads are on their way before the first store.  All pools of a call (48 a launch) go in
+// one grid, since a layer's share alone would not fill the GPU.
+#include "kda_internal.h"
+#include "ops_internal.h"
+
+namespace kda {
+namespace {
+
+constexpr int kPoolThreads = 256;
+constexpr int kBatch = 8;                             // pieces a thread has on their way
+constexpr int kSlicePieces = kPoolThreads * kBatch;   // pieces a CTA of the copy takes
+
+// Byte offset of piece e of an entry (its rows and columns in order).
+__device__ __forceinline__ int64_t piece_at(const PoolDesc& d, uint32_t e) {
+    const uint32_t run = page_div(e, (uint32_t)d.pieces, d.piece_magic), piece = e - run * (uint32_t)d.pieces;
+    const uint32_t row = page_div(run, (uint32_t)d.cols, d.col_magic), col = run - row * (uint32_t)d.cols;
+    return row * d.st[1] + col * d.st[2] + (int64_t)piece * 16;
+}
+
+__global__ void __launch_bounds__(kPoolThreads) pool_copy_kernel(const __grid_constant__ PoolCopyParams p) {
+    const PoolDesc& d = p.pool[blockIdx.z];
+    const int i = blockIdx.y;
+    const int src = p.src[i], dst = p.dst[i], given = p.rows ? p.rows[i] : d.rows;
+    if (src < 0 || dst < 0 || src == dst) return;
+    if (src >= d.entries || dst >= d.entries || given < 0 || given > d.rows) {
+        if (p.status && threadIdx.x == 0 && blockIdx.x == 0) atomicExch(p.status, 1);
+        return;
+    }
+    const uint32_t total = (uint32_t)given * (uint32_t)d.cols * (uint32_t)d.pieces;
+    const char* from = d.data + src * d.st[0];
+    char* to = d.data + dst * d.st[0];
+    for (uint32_t base = blockIdx.x * (uint32_t)kSlicePieces + threadIdx.x; base < total; base += gridDim.x * (uint32_t)kSlicePieces) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t e = base + k * kPoolThreads;
+            if (e < total) v[k] = *reinterpret_cast<const uint4*>(from + piece_at(d, e));
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t e = base + k * kPoolThreads;
+            if (e < total) *reinterpret_cast<uint4*>(to + piece_at(d, e)) = v[k];
+        }
+    }
+}
+
+constexpr int kPathMax = 256;
+
+// A CTA takes a request's path in one cache (or a split of the rows' pieces).  The path
+// ascends, so path[j] >= j: in the order of j no row is written before it has been read,
+// and a batch of pieces in that order can be read as a whole before it is written.
+__global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
+    __shared__ int2 s_from[kPathMax], s_to[kPathMax];   // page (< 0: none) and row of a moved node and of its new place
+    __shared__ int s_first;
+    const PoolDesc& d = p.pool[blockIdx.z];
+    const int r = blockIdx.y, tid = threadIdx.x;
+    const int ctx = p.ctx[r], n = p.accepted[r];
+    const int32_t* path = p.path + (int64_t)r * p.max_path;
+    const bool report = p.status && blockIdx.x == 0 && blockIdx.z == 0;
+    if (ctx < 0 || n < 0 || n > p.max_path) {
+        if (report && tid == 0) atomicExch(p.status, 1);
+        return;
+    }
+    if (tid == 0) s_first = n;
+    __syncthreads();
+    bool ok = true;
+    if (tid < n) {   // n <= kPathMax = kPoolThreads
+        const int node = path[tid];
+        ok = (tid == 0 ? node >= 0 : node > path[tid - 1]) && (int64_t)ctx + node < p.room;
+        if (ok && node != tid) {
+            const auto place = [&](int at) {
+                const int pg = (int)page_div((uint32_t)at, p.page, p.page_magic);
+                const int id = p.table[r * p.table_stride + pg];
+                const bool in = id >= 0 && id < d.entries;
+                if (!in && report) atomicExch(p.status, 1);
+                return make_int2(in ? id : -1, at - pg * p.page);
+            };
+            s_from[tid] = place(ctx + node);
+            s_to[tid] = place(ctx + tid);
+            atomicMin(&s_first, tid);
+        }
+    }
+    if (!__syncthreads_and(ok)) {
+        if (report && tid == 0) atomicExch(p.status, 1);
+        return;
+    }
+    // path[j] = j up to s_first, and never again behind it
+    const uint32_t row_pieces = (uint32_t)(d.cols * d.pieces);
+    const uint32_t c0 = (uint32_t)((uint64_t)row_pieces * blockIdx.x / gridDim.x),
+                   width = (uint32_t)((uint64_t)row_pieces * (blockIdx.x + 1) / gridDim.x) - c0;
+    const uint32_t total = (uint32_t)(n - s_first) * width;
+    for (uint32_t base = tid; base - tid < total; base += kSlicePieces) {
+        uint4 v[kBatch];
+        char* to[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t e = base + k * kPoolThreads;
+            to[k] = nullptr;
+            if (e < total) {
+                const uint32_t j = e / width, c = c0 + (e - j * width);
+                const int2 a = s_from[s_first + j], b = s_to[s_first + j];
+                const uint32_t col = page_div(c, (uint32_t)d.pieces, d.piece_magic), piece = c - col * (uint32_t)d.pieces;
+                const int64_t in_row = col * d.st[2] + (int64_t)piece * 16;
+                if (a.x >= 0 && b.x >= 0) {
+                    v[k] = *reinterpret_cast<const uint4*>(d.data + a.x * d.st[0] + a.y * d.st[1] + in_row);
+                    to[k] = d.data + b.x * d.st[0] + b.y * d.st[1] + in_row;
+                }
+            }
+        }
+        __syncthreads();   // the batch is read
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (to[k]) *reinterpret_cast<uint4*>(to[k]) = v[k];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_pool_copy(const PoolCopyParams& q, int num_sms, cudaStream_t s) {
+    (void)num_sms;
+    int64_t most = 1;
+    for (int k = 0; k < q.pools; ++k) {
+        const int64_t n = (int64_t)q.pool[k].rows * q.pool[k].cols * q.pool[k].pieces;
+        most = n > most ? n : most;
+    }
+    const int64_t slices = (most + kSlicePieces - 1) / kSlicePieces;
+    const dim3 grid((unsigned)(slices < 65535 ? slices : 65535), (unsigned)q.count, (unsigned)q.pools);
+    pool_copy_kernel<<<grid, kPoolThreads, 0, s>>>(q);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_commit(const CacheCommitParams& q, int num_sms, cudaStream_t s) {
+    // Rows are cut where the (request, cache) pairs are fewer than two CTAs an SM, at least 8
+    // pieces (128 bytes) a CTA.
+    int least = 1 << 30;
+    for (int k = 0; k < q.pools; ++k) {
+        const int n = q.pool[k].cols * q.pool[k].pieces;
+        least = n < least ? n : least;
+    }
+    int64_t splits = 2 * num_sms / ((int64_t)q.R * q.pools);
+    if (splits > least / 8) splits = least / 8;
+    if (splits < 1) splits = 1;
+    const dim3 grid((unsigned)splits, (unsigned)q.R, (unsigned)q.pools);
+    cache_commit_kernel<<<grid, kPoolThreads, 0, s>>>(q);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
+#include <vector>
 
 #include "../../include/kda_ops.h"
 
@@ -146,6 +147,13 @@ void done(kda_status st) {
     throw Refused();
 }
 PyObject* none() { Py_RETURN_NONE; }
+// Two new references as a tuple.
+PyObject* both(PyObject* a, PyObject* b) {
+    PyObject* r = PyTuple_Pack(2, a, b);
+    Py_DECREF(a);
+    Py_DECREF(b);
+    return r;
+}
 
 // Every entry: exceptions of the checks and of torch become Python errors.
 template <PyObject* (*F)(PyObject* const*)>
@@ -384,6 +392,266 @@ PyObject* tree_attention(PyObject* const* o) {
     return r;
 }
 
+// q, k_cache, v_cache, page_table, context_lens, cu_seqlens, scale, max_context, out,
+// return_lse, workspace, device_status, address of a kda_overrides
+PyObject* chunk_attention(PyObject* const* o) {
+    const at::Tensor &q = *tensor("q", o[0]), &kc = *tensor("k_cache", o[1]), &vc = *tensor("v_cache", o[2]),
+                     &table = *tensor("page_table", o[3]);
+    const at::Tensor* cu = tensor("cu_seqlens", o[5], true);
+    kda_chunk_attention_args a{};
+    a.dtype = elem("q", q);
+    const Call c{q.device()};
+    const auto dt = q.scalar_type();
+    if (q.dim() != (cu ? 3 : 4) || q.stride(-1) != 1)
+        refuse(PyExc_ValueError, "q must be [T_total, Hq, D] with cu_seqlens, [R, T, Hq, D] without, its last stride 1");
+    if (cu) {
+        if (cu->dim() != 1 || cu->size(0) < 1) refuse(PyExc_ValueError, "cu_seqlens must be int32 [R+1]");
+        a.num_requests = cu->size(0) - 1;
+        a.seqlen = q.size(0);
+        a.cu_seqlens = flat<int32_t>(c, "cu_seqlens", o[5], at::kInt, {a.num_requests + 1});
+    } else {
+        a.num_requests = q.size(0);
+        a.seqlen = q.size(1);
+    }
+    const int64_t R = a.num_requests, Hq = q.size(-2), D = q.size(-1);
+    need_device(c, "k_cache", kc);
+    if (kc.dim() != 4) refuse(PyExc_ValueError, "k_cache must be [pages, page_size, Hk, D]");
+    a.num_k_heads = kc.size(2);
+    cache(c, "k_cache", kc, a.num_k_heads, D, dt, a.k_cache_stride);
+    cache(c, "v_cache", vc, a.num_k_heads, D, dt, a.v_cache_stride);
+    if (vc.sizes() != kc.sizes()) refuse(PyExc_ValueError, "k_cache and v_cache must have the same shape");
+    need_cuda(c, "page_table", table, at::kInt);
+    if (table.dim() != 2 || table.size(0) != R || (table.size(1) > 1 && table.stride(1) != 1))
+        refuse(PyExc_ValueError, "page_table must be int32 [R, pages] with contiguous rows");
+    if (o[4] == Py_None) refuse(PyExc_TypeError, "context_lens must be a tensor");
+    a.context_lens = flat<int32_t>(c, "context_lens", o[4], at::kInt, {R});
+    a.device_status = status_word(c, o[11]);
+    const at::Tensor *given = tensor("out", o[8], true), *given_ws = tensor("workspace", o[10], true);
+    if (given) strided(c, "out", *given, q.sizes(), dt);
+    if (given_ws) {
+        need_cuda(c, "workspace", *given_ws, at::kByte);
+        if (!given_ws->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+    }
+    a.max_context = o[7] == Py_None ? -1 : integer(o[7]);
+    a.scale = o[6] == Py_None ? (D > 0 ? 1.f / sqrtf((float)D) : 1.f) : real(o[6]);
+    const bool want_lse = truth(o[9]);
+    const c10::cuda::CUDAGuard guard(c.device);
+    at::Tensor out = given ? *given : at::empty(q.sizes(), q.options()), lse, ws;
+    if (want_lse) {
+        lse = at::empty(q.sizes().slice(0, q.dim() - 1), q.options().dtype(at::kFloat));
+        a.lse = static_cast<float*>(lse.data_ptr());
+    }
+    a.q = q.data_ptr();
+    a.k_cache = kc.data_ptr();
+    a.v_cache = vc.data_ptr();
+    a.out = out.data_ptr();
+    a.page_table = static_cast<int32_t*>(table.data_ptr());
+    for (int i = cu ? 1 : 0; i < 3; ++i) {
+        a.q_stride[i] = step(q, cu ? i - 1 : i);
+        a.out_stride[i] = step(out, cu ? i - 1 : i);
+    }
+    a.page_table_stride = table.stride(0);
+    a.num_q_heads = Hq;
+    a.head_dim = D;
+    a.num_pages = kc.size(0);
+    a.page_size = kc.size(1);
+    a.pages_per_request = table.size(1);
+    if (given_ws) ws = *given_ws;
+    else if (const size_t need = kda_chunk_attention_workspace_size(&a))
+        ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
+    if (ws.defined()) {
+        a.workspace = ws.data_ptr();
+        a.workspace_bytes = (size_t)ws.numel();
+    }
+    done(kda_chunk_attention(&a, stream_of(q)));
+    PyObject* ro = o[8] != Py_None ? Py_NewRef(o[8]) : THPVariable_Wrap(out);
+    return want_lse ? both(ro, THPVariable_Wrap(lse)) : ro;
+}
+
+// Stride of a token of a [..., E] operand: its leading dims have to be one.
+int64_t token_step(const char* name, const at::Tensor& t) {
+    int64_t step = -1, size = 1;   // of a token, and of the tokens of the dims looked at
+    for (int64_t d = t.dim() - 2; d >= 0; --d) {
+        if (t.size(d) == 1) continue;
+        if (step < 0) step = t.stride(d);
+        else if (t.stride(d) != step * size)
+            refuse(PyExc_ValueError, std::string(name) + " must have tokens that are equally far apart");
+        size *= t.size(d);
+    }
+    return step < 0 ? 0 : step;
+}
+
+// x, y, weight, post_norm, post_weight, gate, gate_sigmoid, alpha, norm, norm_eps, out, x_out
+PyObject* residual_norm(PyObject* const* o) {
+    const at::Tensor& x = *tensor("x", o[0]);
+    const at::Tensor *y = tensor("y", o[1], true), *w = tensor("weight", o[2], true),
+                     *pw = tensor("post_weight", o[4], true), *gate = tensor("gate", o[5], true),
+                     *out_given = tensor("out", o[10], true), *x_given = tensor("x_out", o[11], true);
+    kda_residual_norm_args a{};
+    const Call c{x.device()};
+    need_device(c, "x", x);
+    const bool norm = truth(o[8]);
+    const bool x32 = x.scalar_type() == at::kFloat;
+    // the type of y and h: y's, or without one that of out or x
+    const at::Tensor& typed = y ? *y : x32 && out_given ? *out_given : x;
+    a.dtype = elem(y ? "y" : x32 && out_given ? "out" : "x", typed);
+    const auto dt = typed.scalar_type();
+    a.x_dtype = x32 ? KDA_DTYPE_F32 : a.dtype;
+    if (x.dim() < 1) refuse(PyExc_ValueError, "x must be [..., E]");
+    const int64_t E = x.size(-1);
+    strided(c, "x", x, x.sizes(), x32 ? at::kFloat : dt);
+    if (y) strided(c, "y", *y, x.sizes(), dt);
+    if (!y && (gate || truth(o[3]) || x_given || !norm))
+        refuse(PyExc_ValueError, "without y there is the norm of x alone");
+    if (gate) strided(c, "gate", *gate, gate->dim() == 1 ? at::IntArrayRef(&E, 1) : x.sizes(), dt);
+    const at::Tensor* any = w ? w : pw;
+    if (w && pw && w->scalar_type() != pw->scalar_type())
+        refuse(PyExc_TypeError, "the weights must have the same type");
+    const bool f32 = !any || any->scalar_type() == at::kFloat;
+    a.weight_dtype = f32 ? KDA_DTYPE_F32 : a.dtype;
+    a.weight = flat(c, "weight", o[2], f32 ? at::kFloat : dt, {E});
+    a.post_weight = flat(c, "post_weight", o[4], f32 ? at::kFloat : dt, {E});
+    if (out_given) strided(c, "out", *out_given, x.sizes(), dt);
+    if (x_given) strided(c, "x_out", *x_given, x.sizes(), x.scalar_type());
+    if (out_given && !norm) refuse(PyExc_ValueError, "out is the norm's");
+    a.post_norm = truth(o[3]);
+    a.gate_sigmoid = truth(o[6]);
+    a.alpha = real(o[7]);
+    a.norm_eps = real(o[9]);
+    a.channels = E;
+    a.tokens = E > 0 ? x.numel() / E : 0;
+    a.x = x.data_ptr();
+    a.x_stride = token_step("x", x);
+    if (y) {
+        a.y = y->data_ptr();
+        a.y_stride = token_step("y", *y);
+    }
+    if (gate) {
+        a.gate = gate->data_ptr();
+        a.gate_stride = token_step("gate", *gate);
+    }
+    const c10::cuda::CUDAGuard guard(c.device);
+    at::Tensor out, x_out;
+    if (norm) {
+        out = out_given ? *out_given : at::empty(x.sizes(), x.options().dtype(dt));
+        a.out = out.data_ptr();
+        a.out_stride = token_step("out", out);
+    }
+    if (y) {
+        x_out = x_given ? *x_given : at::empty(x.sizes(), x.options());
+        a.x_out = x_out.data_ptr();
+        a.x_out_stride = token_step("x_out", x_out);
+    }
+    done(kda_residual_norm(&a, stream_of(x)));
+    PyObject* ro = o[10] != Py_None ? Py_NewRef(o[10]) : norm ? THPVariable_Wrap(out) : none();
+    PyObject* rx = !y ? Py_NewRef(o[0]) : o[11] != Py_None ? Py_NewRef(o[11]) : THPVariable_Wrap(x_out);
+    return both(ro, rx);
+}
+
+// A tensor, or a sequence of tensors, of entries as pools; c takes the first one's device.
+struct Pools {
+    std::vector<kda_pool> list;
+    const at::Tensor* first = nullptr;
+};
+void add_pool(Pools& pools, const char* name, PyObject* o, bool page_rows) {
+    const at::Tensor& t = *tensor(name, o);
+    if (!pools.first) pools.first = &t;
+    need_device(Call{pools.first->device()}, name, t);
+    if (t.dim() < (page_rows ? 3 : 2))
+        refuse(PyExc_ValueError, std::string(name) + (page_rows ? " must be [pages, page_size, ...]" : " must be [entries, ...]"));
+    const bool rows = t.dim() > 2;   // of an entry: its first dim, where it has more than one
+    kda_pool p{};
+    p.data = t.data_ptr();
+    p.entries = t.size(0);
+    p.rows = rows ? t.size(1) : 1;
+    p.cols = 1;
+    p.bytes = t.element_size();
+    const int64_t unit = t.element_size();
+    const auto far = [&](int64_t d) { return t.size(d) > 1 ? t.stride(d) * unit : 0; };   // that of a dim of size 1 says nothing
+    p.stride[0] = far(0);
+    p.stride[1] = rows ? far(1) : 0;
+    bool apart = false;
+    for (int64_t d = t.dim() - 1; d >= (rows ? 2 : 1); --d) {
+        if (t.size(d) == 1) continue;
+        const int64_t s = t.stride(d) * unit;
+        if (!apart && s == p.bytes) {
+            p.bytes *= t.size(d);
+        } else if (!apart) {
+            apart = true;
+            p.cols = t.size(d);
+            p.stride[2] = s;
+        } else if (s == p.stride[2] * p.cols) {
+            p.cols *= t.size(d);
+        } else {
+            refuse(PyExc_ValueError, std::string(name) + " must have rows of at most two strides");
+        }
+    }
+    pools.list.push_back(p);
+}
+Pools pools_of(const char* name, PyObject* o, bool page_rows) {
+    Pools pools;
+    if (THPVariable_Check(o)) {
+        add_pool(pools, name, o, page_rows);
+        return pools;
+    }
+    if (!PyList_Check(o) && !PyTuple_Check(o))
+        refuse(PyExc_TypeError, std::string(name) + " must be a tensor or a list of tensors");
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    pools.list.reserve((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) add_pool(pools, name, PySequence_Fast_GET_ITEM(o, i), page_rows);
+    return pools;
+}
+
+// pools, src, dst, rows, device_status
+PyObject* pool_copy(PyObject* const* o) {
+    const at::Tensor &src = *tensor("src", o[1]), &dst = *tensor("dst", o[2]);
+    const Pools pools = pools_of("pools", o[0], false);
+    const Call c{pools.first ? pools.first->device() : src.device()};
+    need_cuda(c, "src", src, at::kInt);
+    if (src.dim() != 1) refuse(PyExc_ValueError, "src must be int32 [n]");
+    kda_pool_copy_args a{};
+    a.pools = pools.list.data();
+    a.num_pools = (int64_t)pools.list.size();
+    a.count = src.size(0);
+    a.src = flat<int32_t>(c, "src", o[1], at::kInt, {a.count});
+    a.dst = flat<int32_t>(c, "dst", o[2], at::kInt, {a.count});
+    a.rows = flat<int32_t>(c, "rows", o[3], at::kInt, {a.count});
+    a.device_status = status_word(c, o[4]);
+    (void)dst;
+    const c10::cuda::CUDAGuard guard(c.device);
+    done(kda_pool_copy(&a, stream_of(src)));
+    return none();
+}
+
+// caches, page_table, context_lens, path, accepted, device_status
+PyObject* cache_commit(PyObject* const* o) {
+    const at::Tensor &table = *tensor("page_table", o[1]), &path = *tensor("path", o[3]);
+    const Pools caches = pools_of("caches", o[0], true);
+    const Call c{caches.first ? caches.first->device() : table.device()};
+    need_cuda(c, "page_table", table, at::kInt);
+    if (table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
+        refuse(PyExc_ValueError, "page_table must be int32 [R, pages] with contiguous rows");
+    const int64_t R = table.size(0);
+    need_cuda(c, "path", path, at::kInt);
+    if (path.dim() != 2) refuse(PyExc_ValueError, "path must be int32 [R, nodes]");
+    if (o[2] == Py_None || o[4] == Py_None) refuse(PyExc_TypeError, "context_lens and accepted must be tensors");
+    kda_cache_commit_args a{};
+    a.caches = caches.list.data();
+    a.num_caches = (int64_t)caches.list.size();
+    a.num_requests = R;
+    a.max_path = path.size(1);
+    a.page_table = static_cast<int32_t*>(table.data_ptr());
+    a.page_table_stride = table.stride(0);
+    a.pages_per_request = table.size(1);
+    a.path = flat<int32_t>(c, "path", o[3], at::kInt, {R, a.max_path});
+    a.context_lens = flat<int32_t>(c, "context_lens", o[2], at::kInt, {R});
+    a.accepted = flat<int32_t>(c, "accepted", o[4], at::kInt, {R});
+    a.device_status = status_word(c, o[5]);
+    const c10::cuda::CUDAGuard guard(c.device);
+    done(kda_cache_commit(&a, stream_of(table)));
+    return none();
+}
+
 PyObject* set_error(PyObject* const* o) {
     Py_XDECREF(g_error);
     g_error = Py_NewRef(o[0]);
@@ -405,7 +673,9 @@ PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(counted<F, kArgs>)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<short_conv, 14>("short_conv"), method<qk_norm_rope, 17>("qk_norm_rope"),
-                         method<tree_attention, 14>("tree_attention"), method<set_error, 1>("set_error"),
+                         method<tree_attention, 14>("tree_attention"), method<chunk_attention, 13>("chunk_attention"),
+                         method<residual_norm, 12>("residual_norm"), method<pool_copy, 5>("pool_copy"),
+                         method<cache_commit, 6>("cache_commit"), method<set_error, 1>("set_error"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -98,6 +98,91 @@ cudaError_t launch_tree_join(const TreeParams& p, int D, bool f16, cudaStream_t 
 // The kernel for many rows; false if the caches' layout has no tensor map.
 bool launch_tree_mma(const TreeParams& p, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e);
 
+// Attention of chunks of new tokens (kda_chunk.cu, kda_chunk_mma.cu).
+struct ChunkParams {
+    const void *q, *kc, *vc;
+    void* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* ctx;
+    const int32_t* cu;        // nullptr: padded
+    int32_t* status;
+    int64_t qs[3], os[3], ks[3], vs[3], table_stride;   // q, out: (request, token, head); caches: (page, row, head)
+    int R, T;                 // requests; new tokens a request (padded) or in all (packed)
+    int Hq, Hk, G;
+    int P, page;
+    int64_t max_len;          // longest context and new tokens of a request (at most what its page row holds)
+    int32_t max_ctx;          // longest context the call allows for
+    uint32_t page_magic, group_magic;
+    int cluster;              // rows kernel: CTAs that share an item
+    int stages;               // rows kernel: tiles in flight (set by the launcher)
+    float scale_log2;         // scale * log2(e)
+};
+// How a call is cut.
+struct ChunkPlan {
+    int cluster;              // rows kernel: CTAs that share an item
+};
+ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int num_sms);
+cudaError_t launch_chunk_attention(const ChunkParams& p, const ChunkPlan& plan, int D, bool f16, cudaStream_t s);
+
+// Request r of a call: its first row of q (packed: in all, padded: 0), its new tokens and
+// the keys it may see; false if they do not fit the call.  Tokens that lie inside the call
+// keep their rows (their results are zero then), others are none.
+__device__ __forceinline__ bool chunk_request(const ChunkParams& p, int r, int& first, int& n, int& len) {
+    bool ok = true;
+    first = 0;
+    n = p.T;
+    if (p.cu) {
+        const int a = p.cu[r], b = p.cu[r + 1];
+        ok = (r > 0 || a == 0) && a >= 0 && a <= b && b <= p.T;
+        first = ok ? a : 0;
+        n = ok ? b - a : 0;
+    }
+    const int ctx = p.ctx[r];
+    len = 0;
+    if (ctx < 0 || ctx > p.max_ctx || (int64_t)ctx + n > p.max_len) ok = false;
+    else len = ctx + n;
+    return ok;
+}
+
+// The residual stream's norm (kda_residual.cu).
+struct ResidualParams {
+    const void *x, *y, *gate;    // y, gate may be nullptr
+    void *out, *x_out;           // either may be nullptr (x_out is without y)
+    const void *w, *post_w;      // nullptr: ones
+    int64_t xs, ys, gs, os, xos; // element strides of a token
+    int64_t tokens;
+    int E, post, sigmoid, w_f32;
+    float alpha, eps;
+};
+cudaError_t launch_residual_norm(const ResidualParams& p, bool f16, bool x_f32, int num_sms, cudaStream_t s);
+
+// Copies between entries of pools (kda_pool.cu).  A pool's entry is rows x cols runs of
+// `pieces` 16-byte pieces, byte strides st (entry, row, col).
+struct PoolDesc {
+    char* data;
+    int64_t st[3];
+    int32_t entries, rows, cols, pieces;
+    uint32_t piece_magic, col_magic;   // floor(2^32 / pieces), floor(2^32 / cols), as page_magic
+};
+constexpr int kPoolSlice = 48;   // pools a launch takes
+struct PoolCopyParams {
+    PoolDesc pool[kPoolSlice];
+    const int32_t *src, *dst, *rows;
+    int32_t* status;
+    int count, pools, slices;        // copies; pools of this launch; slices of an entry (set by the launcher)
+};
+cudaError_t launch_pool_copy(const PoolCopyParams& p, int num_sms, cudaStream_t s);
+struct CacheCommitParams {
+    PoolDesc pool[kPoolSlice];
+    const int32_t *table, *ctx, *path, *accepted;
+    int32_t* status;
+    int64_t table_stride, room;      // room: tokens a page row holds
+    int R, max_path, page, pools, splits;
+    uint32_t page_magic;
+};
+cudaError_t launch_cache_commit(const CacheCommitParams& p, int num_sms, cudaStream_t s);
+
 // n / page for n < 2^32 and magic = floor(2^32 / page): the product is short by at most one.
 __device__ __forceinline__ uint32_t page_div(uint32_t n, uint32_t page, uint32_t magic) {
     uint32_t q = __umulhi(n, magic);

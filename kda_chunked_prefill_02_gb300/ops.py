@@ -2,9 +2,12 @@
 
 The operators a serving decoder runs around KDA: the short causal convolution
 (`kda_short_conv`), the query / key norm with the position rotation
-(`kda_qk_norm_rope`, frequencies from `rope_frequencies`), and the attention of
-drafted tokens over a paged cache (`kda_tree_attention`, masks from
-`tree_mask`).  The tensors' checks and the calls are in the native binding
+(`kda_qk_norm_rope`, frequencies from `rope_frequencies`), the attention of
+prompts (`kda_chunk_attention`) and of drafted tokens (`kda_tree_attention`, masks
+from `tree_mask`) over a paged cache, the norm of the residual stream
+(`kda_residual_norm`), the commit of a verified tree's cache rows
+(`kda_cache_commit`) and copies between pools' entries for forked requests
+(`kda_pool_copy`).  The tensors' checks and the calls are in the native binding
 csrc/ops_binding.cpp, which also sees to it that a call's tensors are on one
 device; the structures below are the C ABI's, for callers of the library itself.  As in kda.py, outputs and workspaces come from torch, any status
 other than KDA_OK raises KdaError, and there is no fallback.
@@ -62,6 +65,42 @@ class TreeAttentionArgs(ctypes.Structure):
         f32: scale""")
 
 
+class ChunkAttentionArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        p: q k_cache v_cache out lse page_table context_lens cu_seqlens workspace device_status
+        size: workspace_bytes
+        i64: q_stride[3] out_stride[3] k_cache_stride[3] v_cache_stride[3] page_table_stride
+        i64: num_requests seqlen num_q_heads num_k_heads head_dim num_pages page_size pages_per_request max_context
+        i32: dtype
+        f32: scale""")
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        p: x y gate out x_out weight post_weight
+        i64: x_stride y_stride gate_stride out_stride x_out_stride tokens channels
+        i32: dtype x_dtype weight_dtype post_norm gate_sigmoid
+        f32: alpha norm_eps""")
+
+
+class Pool(ctypes.Structure):
+    _fields_ = _fields("""
+        p: data
+        i64: stride[3] entries rows cols bytes""")
+
+
+class PoolCopyArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        p: pools src dst rows device_status
+        i64: num_pools count""")
+
+
+class CacheCommitArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        p: caches page_table context_lens path accepted device_status
+        i64: num_caches page_table_stride num_requests max_path pages_per_request""")
+
+
 class TreeSchedule(ctypes.Structure):
     _fields_ = _fields("i32: kernel ordered cluster launches")
 
@@ -74,12 +113,15 @@ def _fn():
     global _funcs
     if _funcs is None:
         L = lib()
-        for name in ("kda_short_conv", "kda_qk_norm_rope", "kda_tree_attention"):
+        for name in ("kda_short_conv", "kda_qk_norm_rope", "kda_tree_attention", "kda_chunk_attention",
+                     "kda_residual_norm", "kda_pool_copy", "kda_cache_commit"):
             f = getattr(L, name)
             f.restype = ctypes.c_int
             f.argtypes = [_p, _p]
         L.kda_tree_attention_workspace_size.restype = ctypes.c_size_t
         L.kda_tree_attention_workspace_size.argtypes = [_p]
+        L.kda_chunk_attention_workspace_size.restype = ctypes.c_size_t
+        L.kda_chunk_attention_workspace_size.argtypes = [_p]
         L.kda_tree_attention_schedule.restype = ctypes.c_int
         L.kda_tree_attention_schedule.argtypes = [_p, ctypes.c_int, _p]
         _funcs = L
@@ -252,3 +294,66 @@ def tree_attention_schedule(q, k_cache, page_table, *, scale=None, max_context=N
     _check(_fn().kda_tree_attention_schedule(ctypes.byref(a), int(num_sms), ctypes.byref(s)))
     return dict(kernel=("items", "clusters", "line", "many rows")[s.kernel], ordered=bool(s.ordered),
                 cluster=s.cluster, launches=s.launches)
+
+
+def kda_chunk_attention(q, k_cache, v_cache, page_table, context_lens, *, cu_seqlens=None, scale=None,
+                        max_context=None, out=None, return_lse=False, workspace=None, device_status=None, stream=None):
+    """Causal attention of chunks of new tokens over a paged cache (see
+    kda_chunk_attention in include/kda_ops.h): prompts, pieces of prompts, single tokens.
+
+    q [T_total, Hq, D] with cu_seqlens (int32 [R+1] on the device), or [R, T, Hq, D],
+    bf16 or fp16; caches [pages, page_size, Hk, D]; page_table int32 [R,
+    pages_per_request]; context_lens int32 [R], the tokens cached before the chunk.
+    The keys and values of the new tokens follow their request's context in the cache
+    (kda_qk_norm_rope puts them there); token i sees the context and the new tokens up
+    to itself.  Rows of q behind cu_seqlens[R] belong to no request and are left out.
+    scale defaults to D^-0.5; max_context: a host upper bound of context_lens (None:
+    what the page table can address); out may be q itself.  Returns out, or (out, lse)
+    with lse fp32 [T_total, Hq] ([R, T, Hq]).
+    """
+    given = _overrides_var.get()
+    return _run((_binding or _native()).chunk_attention, stream,
+                (q, k_cache, v_cache, page_table, context_lens, cu_seqlens, scale, max_context, out, return_lse,
+                 workspace, device_status, None if given is None else ctypes.addressof(given)))
+
+
+def kda_residual_norm(x, y=None, *, weight=None, post_norm=False, post_weight=None, gate=None, gate_sigmoid=False,
+                      alpha=1.0, norm=True, norm_eps=1e-6, out=None, x_out=None, stream=None):
+    """A block's output added to the residual stream and the norm in front of the next
+    block, in one pass (see kda_residual_norm in include/kda_ops.h).
+
+    x [..., E] the stream, y [..., E] the block's output (bf16 or fp16; x in y's type or
+    fp32).  post_norm: y is RMS-normed first, times post_weight; gate [..., E] or [E] in
+    y's type multiplies it (gate_sigmoid: its sigmoid does), and alpha.  norm=False
+    leaves the norm of the new stream, times weight, out.  Weights [E] in y's type or
+    fp32 (None: ones).  Without y the norm of x alone (an fp32 x then needs out).
+    out may be y, x_out x itself.  Returns (h, new x): h in y's type (None with
+    norm=False), the new x in x's (x itself without y).
+    """
+    return _run((_binding or _native()).residual_norm, stream,
+                (x, y, weight, post_norm, post_weight, gate, gate_sigmoid, alpha, norm, norm_eps, out, x_out))
+
+
+def kda_pool_copy(pools, src, dst, *, rows=None, device_status=None, stream=None):
+    """Entry src[i] copied to entry dst[i] in every pool (see kda_pool_copy in
+    include/kda_ops.h): what a forked request needs of its parent's.
+
+    pools: a tensor [entries, ...] or a list of them (caches of pages, pools of KDA or
+    convolution states), of any type; src and dst int32 [n] on the device, negative:
+    nothing.  rows int32 [n]: only the first rows[i] rows of an entry (its rows are dim 1
+    of a pool of 3 dims and more).
+    """
+    return _run((_binding or _native()).pool_copy, stream, (pools, src, dst, rows, device_status))
+
+
+def kda_cache_commit(caches, page_table, context_lens, path, accepted, *, device_status=None, stream=None):
+    """The cache rows of verified trees' accepted nodes moved together behind their
+    context (see kda_cache_commit in include/kda_ops.h).
+
+    caches: a tensor [pages, page_size, ...] or a list of them (every layer's keys and
+    values); page_table and context_lens as the trees were verified with; path int32
+    [R, N]: a request's accepted nodes, ascending, the first accepted[r] (int32 [R]) of
+    them.  Row context + path[r, j] goes to row context + j.
+    """
+    return _run((_binding or _native()).cache_commit, stream,
+                (caches, page_table, context_lens, path, accepted, device_status))
