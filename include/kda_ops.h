@@ -324,6 +324,8 @@ typedef struct kda_chunk_attention_args {
 } kda_chunk_attention_args;
 size_t kda_chunk_attention_workspace_size(const kda_chunk_attention_args* args);
 kda_status kda_chunk_attention(const kda_chunk_attention_args* args, void* stream);
+/* The same with overrides for tests, as kda_tree_attention_ex. */
+kda_status kda_chunk_attention_ex(const kda_chunk_attention_args* args, const kda_overrides* overrides, void* stream);
 
 /*
  * The residual stream between two blocks: a block's output y added to the stream x,

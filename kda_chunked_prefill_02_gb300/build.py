@@ -27,10 +27,11 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 LIB_SOURCES = ["kda_api.cu", "kda_prep.cu", "kda_state.cu", "kda_state_head.cu", "kda_verify.cu",
                "kda_verify_wy.cu", "kda_noalloc.cu", "kda_host.cu", "kda_ops_api.cu", "kda_conv.cu",
-               "kda_rope.cu", "kda_tree.cu", "kda_tree_mma.cu", "kda_chunk.cu", "kda_residual.cu", "kda_pool.cu"]
+               "kda_rope.cu", "kda_tree.cu", "kda_tree_mma.cu", "kda_chunk.cu",
+               "kda_chunk_mma.cu", "kda_residual.cu", "kda_pool.cu"]
 SELFTEST_SOURCES = ["selftest.cu"]
 BINDING_SOURCE = "ops_binding.cpp"
-HEADERS = ["sm103.cuh", "kda_internal.h", "ops_internal.h", "warp_mma.cuh", "tmap.h"]
+HEADERS = ["sm103.cuh", "kda_internal.h", "ops_internal.h", "warp_mma.cuh", "attn_mma.cuh", "tmap.h"]
 
 LIB = os.path.join(HERE, "libkda.so")
 SELFTEST_LIB = os.path.join(HERE, "libkda_selftest.so")

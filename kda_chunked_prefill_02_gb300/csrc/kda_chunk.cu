@@ -414,6 +414,111 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
     if (kCluster) cluster_sync();   // the others have read this CTA's rows
 }
 
+// Joins the parts of an item that kda_chunk_mma.cu has cut: out = sum_c 2^(lse_c - M) o_c /
+// sum_c 2^(lse_c - M) over the CTAs c that hold one, in their order: slot 1 of CTA
+// blockIdx.x, then slot 0 of those behind it up to the item's last part.  A row is the work
+// of one warp that takes part after part, or of W > 1 warps, of every W-th part each (the
+// order of the sums is fixed all the same).
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p) {
+    constexpr int kVec = D / 32;
+    __shared__ float sy[W > 1 ? 8 : 1][W > 1 ? D : 1], ssum[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = blockIdx.y * (8 / W) + warp / W;
+    const int cta = blockIdx.x, ctas = p.ctas;
+    const int4 item = p.parts[2 * cta + 1];   // state, request, key head, pair of row tiles
+    if (item.x == 0 || in >= 256) return;     // all of a row's warps
+    int first, n, len;
+    chunk_request(p, item.y, first, n, len);
+    const int tile = in >> 7, row = in & 127, in_token = (int)page_div((uint32_t)row, p.G, p.group_magic);
+    const int token = (2 * item.w + tile) * p.tile_tokens + in_token;
+    if (in_token >= p.tile_tokens || token >= n) return;
+    const auto part = [&](int k) { return (int64_t)(k ? 2 * (cta + k) : 2 * cta + 1) * 256 + in; };
+    float mx = -INFINITY, sum = 0.f, y[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) y[i] = 0.f;
+    if (W == 1) {
+        for (int k = 0, state = item.x;;) {
+            const float lse = p.part_lse[part(k)];
+            const float* src = p.part_o + part(k) * D + lane * kVec;
+            float o[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) o[i] = src[i];
+            const float mn = fmaxf(mx, lse), mu = mn == -INFINITY ? 0.f : mn;
+            const float fo = ex2_approx(mx - mu), fn = ex2_approx(lse - mu);
+            sum = sum * fo + fn;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) y[i] = y[i] * fo + o[i] * fn;
+            mx = mn;
+            if (state == 2 || cta + ++k >= ctas) break;
+            state = p.parts[2 * (cta + k)].x;
+            if (state == 0) break;
+        }
+    } else {
+        int count = 1;   // parts, from their states, 32 at a time
+        for (int c = cta + 1;; c += 32) {
+            const int state = c + lane < ctas ? p.parts[2 * (c + lane)].x : 0;
+            const uint32_t stop = __ballot_sync(0xffffffffu, state != 1);
+            const int k = stop ? __ffs(stop) - 1 : 32;
+            count += k;
+            if (stop) {
+                if (__shfl_sync(0xffffffffu, state, k) == 2) ++count;
+                break;
+            }
+        }
+        for (int k = lane; k < count; k += 32) mx = fmaxf(mx, p.part_lse[part(k)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+        for (int k = warp % W; k < count; k += W) {
+            const float f = ex2_approx(p.part_lse[part(k)] - mu);
+            const float* src = p.part_o + part(k) * D + lane * kVec;
+            sum += f;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) y[i] = fmaf(src[i], f, y[i]);
+        }
+        if (lane == 0) ssum[warp] = sum;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sy[warp][lane * kVec + i] = y[i];
+        named_bar_sync(1 + warp / W, 32 * W);
+        if (warp % W > 0) return;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) y[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            sum += ssum[warp + w];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) y[i] += sy[warp + w][lane * kVec + i];
+        }
+    }
+    const int h = item.z * p.G + (row - in_token * p.G);
+    const bool empty = sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(
+        static_cast<T*>(p.out) + (p.cu ? (int64_t)(first + token) * p.os[1] : item.y * p.os[0] + token * p.os[1]) +
+        h * p.os[2] + lane * kVec);
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
+    if (p.lse && lane == 0)
+        p.lse[((p.cu ? (int64_t)first : (int64_t)item.y * p.T) + token) * p.Hq + h] =
+            empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <typename T, int W>
+cudaError_t launch_join_w(const ChunkParams& p, int D, cudaStream_t s) {
+    const dim3 grid((unsigned)(p.ctas - 1), (unsigned)(256 * W / 8));
+    const auto kernel = D == 64 ? chunk_join_kernel<T, 64, W>
+                                : D == 128 ? chunk_join_kernel<T, 128, W> : chunk_join_kernel<T, 256, W>;
+    return launch_maybe_pdl(kernel, grid, dim3(256), 0, s, true, p);
+}
+template <typename T>
+cudaError_t launch_join(const ChunkParams& p, int D, cudaStream_t s) {
+    if (p.ctas <= 1) return cudaSuccess;   // one CTA cuts nothing
+    return launch_join_w<T, 1>(p, D, s);
+}
+
 int rows_per_block(int64_t rows, int D) { return rows <= 16 || D > 128 ? 16 : 32; }
 // Blocks of rows of all requests: exactly (padded), or at most (packed).
 int64_t row_blocks(int R, int T, bool packed, int G, int block) {
@@ -463,10 +568,19 @@ cudaError_t launch_rows(const ChunkParams& p, int D, cudaStream_t s) {
 
 }  // namespace
 
-ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int num_sms) {
+ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int page, float scale, bool in_place,
+                     int num_sms) {
     ChunkPlan t;
-    // Clusters where the blocks are fewer than the CTAs that run at once (what the tiles in
-    // flight leave room for, or for D 64 the registers), at least 128 tokens a CTA.
+    // Pages have to be whole 8-row groups of a tile, a row tile whole tokens, the scale's
+    // reciprocal finite.  With head size 256 the two CTAs of an item both read all of its
+    // queries and each writes a half of its results, in no order: not where the results
+    // replace the queries.
+    t.mma = page % 8 == 0 && G <= 128 && scale > 1e-30f && num_sms > 1 && !(in_place && D == 256);
+    t.grid = num_sms;
+    t.stretches = t.mma ? D == 256 ? t.grid / 2 : t.grid : 0;
+    // The rows kernel (also for layouts without a tensor map): clusters where the blocks are
+    // fewer than the CTAs that run at once (what the tiles in flight leave room for, or for D
+    // 64 the registers), at least 128 tokens a CTA.
     const int at_once = num_sms * (D == 64 ? 4 : D == 128 ? 2 : 1);
     const int64_t blocks = row_blocks(R, T, packed, G, rows_per_block((int64_t)T * G, D)) * Hk;
     const int64_t tiles = (max_len + kTile - 1) / kTile;
@@ -479,6 +593,13 @@ ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t ma
 cudaError_t launch_chunk_attention(const ChunkParams& p, const ChunkPlan& plan, int D, bool f16, cudaStream_t s) {
     ChunkParams q = p;
     q.cluster = plan.cluster;
+    q.ctas = plan.stretches;
+    q.tile_tokens = 128 / q.G;
+    cudaError_t e = cudaSuccess;
+    if (plan.mma && launch_chunk_mma(q, D, f16, plan.grid, s, &e)) {
+        if (e != cudaSuccess) return e;
+        return f16 ? launch_join<__half>(q, D, s) : launch_join<__nv_bfloat16>(q, D, s);
+    }
     return f16 ? launch_rows<__half>(q, D, s) : launch_rows<__nv_bfloat16>(q, D, s);
 }
 

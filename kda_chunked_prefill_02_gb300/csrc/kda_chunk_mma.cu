@@ -1,0 +1,857 @@
+// kda_chunk_mma.cu -- kda_chunk_attention (include/kda_ops.h) on tcgen05 tensor cores:
+// tiles of 128 query rows (the new tokens times the query heads of a key head) and 128
+// keys, S and O in TMEM, queries and the pages of K and V by TMA.
+//
+// A tile of rows and keys costs 16 tcgen05.mma (S = Q K^T, then O += P V).  Persistent
+// CTAs, one an SM:
+//   warps 0-3, 4-7  two softmax streams: thread = row (TMEM lane), the whole row of S in
+//                   registers, so maximum and sum need no exchange; P goes back over S's
+//                   columns as 16-bit pairs, the A operand of the second product;
+//   warps 8-11      the rows' way out: O from TMEM, divided by the sum, to memory;
+//   warp 12         the loader: query tiles and a ring of K and V tiles;
+//   warp 13         issues the products;
+//   warp 14         deals out the work, item by item;
+//   warp 15         cleans the V tiles that need it.
+// An item is a pair of row tiles over the same keys, one a stream, each K and V tile read
+// for 256 rows; or a last single row tile, whose even and odd key tiles go to the two
+// streams and whose two halves are joined on the way out.  The streams alternate without
+// a break from item to item: while an item's last rows are on their way out, the next
+// one's first scores are formed and its softmax runs (its queries come into a buffer of
+// their own), so that short prompts, whose items are a few tiles long, keep the tensor
+// pipe as busy as long ones do.
+//
+// A row tile holds whole tokens (128 / G of them, G query heads a key head), so that its
+// queries are one box of the query tensor a block of 64 channels.
+//
+// The work of a call is one line, ordered by request, key head and pair of row tiles, an
+// item's length on it the keys that its last token sees and a constant for its way in and
+// out; every CTA takes an equal stretch, so that ragged batches and the causal triangle
+// leave no SM idle.  A stretch cuts at most two items; the parts of a cut item leave
+// normalised rows and their log-sum in the workspace (slot 0 of a CTA: a later part of an
+// item, slot 1: the first), joined in the CTAs' order by chunk_join_kernel (kda_chunk.cu).
+//
+// Head size 256: S of two row tiles and a whole O do not fit TMEM, so two neighbouring
+// CTAs take the same stretch, both with all of S and each with one half of V's columns.
+//
+// The running maximum moves only when a row's scores exceed it by a factor of 2^8 (2^4 in
+// fp16), so that O in TMEM is hardly ever rescaled; that is the softmax threads' work, in
+// the time between a score tile's arrival (which implies that the product before it is
+// done) and their P's.
+//
+// Keys behind a row's own: only an item's last tiles hold any; there every row compares
+// its 128 positions.  In those tiles a warp of its own clears V rows that no row of the
+// item sees and V elements that are not finite before the product sees them (0 * NaN is
+// NaN, also for a row whose P is zero), and remembers their positions; the rows that do
+// see such a position take its elements on their way out.
+//
+// Registers: 512 threads start with 128 each; the softmax warps take 192, the way out
+// keeps 72, the last four warps 56 (2 x 192 + 72 + 56 = 4 x 128).
+//
+// Every wait is bounded; one that runs out sets the abort flag, the roles fall through to
+// the end, and the status word reports KDA_ERR_TIMEOUT.  Whatever the others do, the loader
+// and the issuer end by waiting for their last copies and products (with the full
+// kWaitLimitNs), so that none is in flight when the CTA's memory goes to the next.
+#include "attn_mma.cuh"
+#include "kda_internal.h"
+#include "ops_internal.h"
+#include "sm103.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 256 + 128 s
+constexpr int kMaxSlots = 8, kMaxQ = 3;
+constexpr int kItems = 4;         // items dealt out ahead
+constexpr int kBadWords = 12;     // positions of an item's last tiles (three at most), a bit each
+// Length on the line of an item's way in and out, in keys.
+constexpr int kItemKeys = 256;
+// What a wait may take beside its bound, a key tile of the longest context (see kda_tree_mma.cu).
+constexpr uint64_t kTileWaitNs = 20000 * (kItems + 1);
+
+// One CTA's part of an item.
+struct Item {
+    int r, h, token0, tokens;   // request, key head, the pair's first token and its tokens
+    int t0, t1;                 // key tiles (t1 < 0: no more items)
+    int ctx, first;             // the request's context, and its first row of q (packed: in all)
+    int end;                    // keys that the last token sees (0: a request that does not fit the call)
+    uint8_t two, whole, flip;   // two row tiles; all of the key tiles; the stream of the first unit
+};
+
+// A CTA's memory behind the queries and the ring.
+struct Misc {
+    uint64_t kv_full[kMaxSlots], kv_free[kMaxSlots], kv_raw[kMaxSlots];
+    uint64_t q_full[kMaxQ], q_free[kMaxQ];
+    uint64_t s_full[2], p_half[2], p_ready[2], o_full[2], o_free[2], ml_full[2], ml_free[2];
+    uint64_t item_full[kItems], item_free[kItems], drained, never;   // never: the probe's, nothing arrives on it
+    float2 ml[2][128];          // the rows' maximum and sum, a stream each
+    uint32_t bad[kItems][kBadWords];   // positions with a V element that is not finite
+    Item item[kItems];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int D> struct Shape {
+    static constexpr int kV = D == 256 ? 128 : D;   // value columns a CTA
+    static constexpr int kHalves = D / kV;          // CTAs that share a stretch, each with its columns
+    static constexpr int kPer = kHalves + 1;        // ring slots a key tile: K by kV channels, V
+    static constexpr uint32_t kSlotBytes = (kV / 64) * kBlock, kQBytes = (D / 64) * kBlock;
+    static constexpr uint32_t kGroupBytes = (kV / 64) * 1024;   // 8 keys, 64 channels after the other
+    // query tiles: three where memory allows it, so that an item's first comes in while the
+    // two of the item before are still needed
+    static constexpr int kQ = D == 256 ? 2 : 3;
+    static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 4 : 3;
+    static constexpr uint32_t kMiscAt = kQ * kQBytes + kSlots * kSlotBytes;
+    static constexpr uint32_t kBytes = kMiscAt + sizeof(Misc);
+};
+static_assert(Shape<128>::kBytes <= 232448 && Shape<256>::kBytes <= 232448, "a CTA's shared memory");
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_mma_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+    using S = Shape<D>;
+    constexpr uint32_t kSlotBytes = S::kSlotBytes, kQBytes = S::kQBytes, kGroupBytes = S::kGroupBytes;
+    constexpr int kV = S::kV, kHalves = S::kHalves, kPer = S::kPer, kSlots = S::kSlots, kQ = S::kQ;
+    const int cta = (int)blockIdx.x / kHalves, half = (int)blockIdx.x % kHalves;
+    extern __shared__ __align__(1024) uint8_t sm[];   // at the window's begin: there is no static shared memory
+    uint8_t* const ring = sm + kQ * kQBytes;
+    Misc& m = *reinterpret_cast<Misc*>(sm + S::kMiscAt);
+
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    volatile int* abort = &m.abort;
+    const uint64_t limit = p.wait_ns;
+    const int tt = p.tile_tokens, G = p.G;      // tokens a row tile, query heads a key head
+    auto fail = [&]() {
+        *abort = 1;
+        if (p.status) atomicExch(p.status, 4);
+    };
+    if (smem_u32(sm) & 1023u) {   // the swizzled tiles' alignment (never seen: all threads leave)
+        if (p.status && tid == 0) atomicExch(p.status, 4);
+        return;
+    }
+
+    if (tid == 0) {
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(&m.kv_full[i], 1);
+            mbar_init(&m.kv_free[i], 1);
+            mbar_init(&m.kv_raw[i], 1);
+        }
+        for (int i = 0; i < kMaxQ; ++i) {
+            mbar_init(&m.q_full[i], 1);
+            mbar_init(&m.q_free[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&m.s_full[s], 1);
+            mbar_init(&m.p_half[s], 4);     // one arrival a warp
+            mbar_init(&m.p_ready[s], 4);
+            mbar_init(&m.o_full[s], 1);
+            mbar_init(&m.o_free[s], 4);
+            mbar_init(&m.ml_full[s], 4);
+            mbar_init(&m.ml_free[s], 4);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&m.item_full[i], 1);
+            mbar_init(&m.item_free[i], 15);   // 8 softmax warps, 4 of the way out, loader, issuer, cleaner
+        }
+        mbar_init(&m.drained, 1);
+        mbar_init(&m.never, 1);
+        m.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 13) {
+        tmem_alloc(&m.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = m.tmem;
+    // The k-th item of this CTA; false after the last (or on an abort).
+    auto take = [&](int k, Item& x, bool& ok) -> bool {
+        ok = ok && wait_for(&m.item_full[k % kItems], (k / kItems) & 1, abort, limit);
+        if (!ok) return false;
+        x = m.item[k % kItems];
+        return x.t1 >= 0;
+    };
+    auto release = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.item_free[k % kItems]);
+    };
+    // Keys from which on some row of an item does not see V: the tiles that are cleaned.
+    auto clean_from = [&](const Item& x) -> int { return min(x.end, x.ctx + x.token0 + 1) / kKeys; };
+
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 12) {
+            // ------------------------------------------------------------ loader
+            if (lane == 0) {
+                tma_prefetch_desc(&qmap);
+                tma_prefetch_desc(&kmap);
+                tma_prefetch_desc(&vmap);
+            }
+            const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
+            int issued = 0, queries = 0, item = 0;   // K and V tiles and query tiles asked for, items begun
+            uint32_t raw = 0, raw_phases = ~0u;   // slots whose last copy was a raw one, those copies' phases
+            bool ok = true;
+            Item x;
+            for (; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
+                release(item);
+                const int32_t* table = p.table + x.r * p.table_stride;
+                const int special = clean_from(x);
+                // this lane's page of a tile, -1: none (asked for a tile ahead, looked at
+                // later), and its first row there
+                int row_ahead = 0;
+                auto page_of = [&](int tile) -> int64_t {
+                    const int tok = tile * kKeys + lane * box;
+                    const int at = (int)page_div((uint32_t)tok, p.page, p.page_magic);
+                    row_ahead = tok - at * p.page;
+                    return tile < x.t1 && lane < per_tile && tok < x.end ? (int64_t)(uint32_t)table[at] : -1;
+                };
+                // row tile a of the item: a box of whole tokens a block of 64 channels (rows past
+                // the request's end, or the call's, are some other rows or zeros, and not stored)
+                auto load_queries = [&](int a) {
+                    const int b = queries % kQ, round = queries / kQ;
+                    if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.q_free[b], (round - 1) & 1, abort, limit));
+                    if (!ok) return;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&m.q_full[b], (uint32_t)(G * tt) * 128u * (D / 64));
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_5d(sm + b * kQBytes + c * kBlock, &qmap, 0, x.h * G, x.first + x.token0 + a * tt, c,
+                                        p.cu ? 0 : x.r, &m.q_full[b]);
+                    }
+                    __syncwarp();
+                    ++queries;
+                };
+                int64_t ahead = page_of(x.t0);
+                load_queries(0);
+                for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
+                    const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
+                    if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
+                    const int row = row_ahead;
+                    ahead = page_of(tile + 1);
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * kV * 2u;
+                    for (int part = 0; part < kPer && ok; ++part) {   // K by kV channels, then V
+                        const bool v = part == kHalves;
+                        if (v && tile == x.t0 && x.two) load_queries(1);
+                        const int slot = issued % kSlots, round = issued / kSlots;
+                        if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.kv_free[slot], (round - 1) & 1, abort, limit));
+                        if (!ok) break;
+                        uint8_t* dst = ring + slot * kSlotBytes;
+                        const bool to_clean = v && tile >= special;
+                        uint64_t* bar = to_clean ? &m.kv_raw[slot] : &m.kv_full[slot];   // raw: to warp 15 first
+                        raw = to_clean ? raw | 1u << slot : raw & ~(1u << slot);
+                        if (to_clean) raw_phases ^= 1u << slot;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (id >= 0)
+                            tma_load_5d(dst + lane * box * kV * 2, v ? &vmap : &kmap, 0, 0,
+                                        ((v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64)) + (v ? half : part) * (kV / 64),
+                                        row / 8, (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
+                        ++issued;
+                    }
+                }
+            }
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+            // the last copies into this CTA's memory
+            for (int i = max(0, queries - kQ); i < queries; ++i) wait_for(&m.q_full[i % kQ], (i / kQ) & 1, nullptr, kWaitLimitNs);
+            for (int i = max(0, issued - kSlots); i < issued; ++i)
+                if (!((raw >> (i % kSlots)) & 1)) wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, nullptr, kWaitLimitNs);
+                else wait_for(&m.kv_raw[i % kSlots], (raw_phases >> (i % kSlots)) & 1, nullptr, kWaitLimitNs);
+        } else if (warp == 13) {
+            // ------------------------------------------------------------ products
+            // Units (a row tile and a key tile) in their order over all items, unit g on stream
+            // g & 1; the scores run two units ahead of the second products.  The whole warp
+            // walks the loop and one elected lane issues, with every operand a warp-uniform
+            // value (see kda_tree_mma.cu).
+            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(kV);
+            const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
+            const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sm), 0), ring_at = q_at + kQ * kQBytes;
+            bool ok = true;
+            struct Cursor {
+                int item, u, units, base, queries;   // the unit of its item; ring and query tiles before the item
+                bool two, end;
+            };
+            auto enter = [&](Cursor& c) {   // the cursor's item
+                Item x;
+                c.end = !__all_sync(0xffffffffu, take(c.item, x, ok));
+                c.two = __shfl_sync(0xffffffffu, (int)x.two, 0) != 0;
+                c.units = (c.two ? 2 : 1) * __shfl_sync(0xffffffffu, x.t1 - x.t0, 0);
+                c.u = 0;
+            };
+            auto advance = [&](Cursor& c, bool done) {
+                if (++c.u < c.units) return;
+                if (done) release(c.item);
+                c.base += kPer * (c.two ? c.units / 2 : c.units);
+                c.queries += c.two ? 2 : 1;
+                ++c.item;
+                enter(c);
+            };
+            auto landed = [&](int i) { return wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, abort, limit); };
+            int g = 0;                         // score units issued
+            uint32_t done[2] = {0, 0}, items[2] = {0, 0};   // P tiles taken, items begun, a stream each
+            Cursor sc{0, 0, 0, 0, 0, false, false}, pv{0, 0, 0, 0, 0, false, false};
+            enter(sc);
+            enter(pv);
+            auto scores = [&]() {
+                const int s = g & 1, u = sc.u, i = sc.base + kPer * (sc.two ? u >> 1 : u);
+                const int q = sc.queries + (sc.two ? u & 1 : 0), b = q % kQ;
+                if (u < (sc.two ? 2 : 1)) ok = ok && wait_for(&m.q_full[b], (q / kQ) & 1, abort, limit);
+                if (!sc.two || !(u & 1)) {
+#pragma unroll
+                    for (int part = 0; part < kHalves; ++part) ok = ok && landed(i + part);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t ad = sdesc_kmajor_sw128(q_at + b * kQBytes);
+#pragma unroll
+                for (int part = 0; part < kHalves; ++part) {   // kV channels of K
+                    const int slot = (i + part) % kSlots;
+                    const uint64_t bd = sdesc_keys(ring_at + slot * kSlotBytes, kGroupBytes);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kV / 16; ++k)
+                            umma_bf16(tbu + kTmemS + 128 * s, ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
+                                      bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, part + k > 0 ? 1u : 0u);
+                        if (part == kHalves - 1) {
+                            umma_commit(&m.s_full[s]);
+                            if (u >= sc.units - (sc.two ? 2 : 1)) umma_commit(&m.q_free[b]);
+                        }
+                        if (!sc.two || (u & 1)) umma_commit(&m.kv_free[slot]);
+                    }
+                }
+                __syncwarp();
+                ++g;
+                advance(sc, false);
+            };
+            if (ok && !sc.end) scores();
+            if (ok && !sc.end) scores();
+            for (int n = 0; ok && !pv.end; ++n) {
+                const int s = n & 1, u = pv.u, i = pv.base + kPer * (pv.two ? u >> 1 : u) + kHalves;
+                // O still holds the rows of the stream's item before until they are out
+                if (u < 2) {
+                    if (items[s] > 0) ok = ok && wait_for(&m.o_free[s], (items[s] - 1) & 1, abort, limit);
+                    ++items[s];
+                }
+                if (!pv.two || !(u & 1)) ok = ok && landed(i);
+                const uint32_t phase = done[s] & 1;
+                ++done[s];
+                const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % kSlots) * kSlotBytes, 1024, kGroupBytes);
+                // the two halves of P as they come
+                auto product = [&](int k0, uint64_t* ready) {
+                    ok = __all_sync(0xffffffffu, ok && wait_for(ready, phase, abort, limit));
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kKeys / 32; ++k)
+                            umma_bf16_ta(tbu + kTmemO + 128 * s, tbu + kTmemS + 128 * s + 8 * (k0 + k),
+                                         bd + (k0 + k) * (kGroupBytes >> 3), id_pv, (u > 1 || k0 + k > 0) ? 1u : 0u);
+                        if (k0) {
+                            if (!pv.two || (u & 1)) umma_commit(&m.kv_free[i % kSlots]);
+                            if (u + 2 >= pv.units) umma_commit(&m.o_full[s]);
+                        }
+                    }
+                    __syncwarp();
+                };
+                product(0, &m.p_half[s]);
+                product(kKeys / 32, &m.p_ready[s]);
+                if (!ok) break;
+                if (!sc.end) scores();
+                advance(pv, true);
+            }
+            if (!ok && lane == 0) fail();
+            if (elect_one()) umma_commit(&m.drained);
+            __syncwarp();
+            wait_for(&m.drained, 0, nullptr, kWaitLimitNs);   // the last products
+            __syncwarp();
+        } else if (warp == 14) {
+            // ------------------------------------------------------------ work
+            // A request's length on the line: over its pairs of row tiles, the keys of each one's
+            // last token (a last single row tile four fifths of them, as measured) and kItemKeys,
+            // times the key heads.
+            struct Request {
+                int first, n, ctx, pairs;
+                bool ok, one;               // the last pair has one row tile
+                int64_t head;               // length of a key head's items
+            };
+            const int pt = 2 * tt;          // tokens a pair
+            auto last_length = [&](const Request& q) -> int64_t {
+                const int64_t keys = (int64_t)q.ctx + q.n;
+                return kItemKeys + (q.one ? keys * 4 / 5 + 1 : keys);
+            };
+            // where pair `rb` begins on a head's part of the line
+            auto pair_at = [&](const Request& q, int rb) -> int64_t {
+                return (int64_t)rb * (kItemKeys + q.ctx) + (int64_t)tt * rb * (rb + 1);
+            };
+            auto look = [&](int r, Request& q) {
+                q.n = q.pairs = 0;
+                q.head = 0;
+                if (r >= p.R) return;
+                int len;
+                q.ok = chunk_request(p, r, q.first, q.n, len);
+                q.ctx = len > 0 ? len - q.n : 0;
+                if (q.n == 0) return;
+                q.pairs = (q.n + pt - 1) / pt;
+                q.one = q.n - (q.pairs - 1) * pt <= tt;
+                q.head = pair_at(q, q.pairs - 1) + last_length(q);
+            };
+            int64_t total = 0;
+            for (int r0 = 0; r0 < p.R; r0 += 32) {
+                Request q;
+                look(r0 + lane, q);
+                if (r0 + lane < p.R && !q.ok && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
+                total += q.head * p.Hk;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            // at least two key tiles a CTA
+            const int64_t most = total / (2 * kKeys);
+            const int room = (int)gridDim.x / kHalves, ctas = most < 1 ? 1 : most < room ? (int)most : room;
+            int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+            int k = 0, flip = 0;
+            bool ok = true;
+            Item x{};
+            auto deal = [&]() {
+                if (k >= kItems) ok = __all_sync(0xffffffffu, wait_for(&m.item_free[k % kItems], (k / kItems - 1) & 1, abort, limit));
+                if (!ok) return;
+                if (lane == 0) {
+                    m.item[k % kItems] = x;
+                    mbar_arrive(&m.item_full[k % kItems]);
+                }
+                __syncwarp();
+                ++k;
+            };
+            if (cta < ctas && total > 0) {
+                const int64_t begin = quotient(total * cta, ctas), end = quotient(total * (cta + 1), ctas);
+                int64_t before = 0;         // length of the requests before r0
+                bool over = false;
+                for (int r0 = 0; r0 < p.R && !over && ok; r0 += 32) {
+                    Request mine;
+                    look(r0 + lane, mine);
+                    int64_t upto = mine.head * p.Hk;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += y;
+                    }
+                    const int64_t here = before;
+                    before += __shfl_sync(0xffffffffu, upto, 31);
+                    if (before <= begin) continue;
+                    // the requests of these that meet the stretch
+                    uint32_t meet = __ballot_sync(0xffffffffu, mine.n > 0 && here + upto > begin &&
+                                                                   here + upto - mine.head * p.Hk < end);
+                    while (meet && ok) {
+                        const int who = __ffs(meet) - 1;
+                        meet &= meet - 1;
+                        Request q;
+                        q.first = __shfl_sync(0xffffffffu, mine.first, who);
+                        q.n = __shfl_sync(0xffffffffu, mine.n, who);
+                        q.ctx = __shfl_sync(0xffffffffu, mine.ctx, who);
+                        q.pairs = __shfl_sync(0xffffffffu, mine.pairs, who);
+                        q.ok = __shfl_sync(0xffffffffu, (int)mine.ok, who) != 0;
+                        q.one = __shfl_sync(0xffffffffu, (int)mine.one, who) != 0;
+                        q.head = __shfl_sync(0xffffffffu, mine.head, who);
+                        const int64_t start = here + __shfl_sync(0xffffffffu, upto, who) - q.head * p.Hk;
+                        // the head and the pair that hold the stretch's begin
+                        int64_t off = begin > start ? begin - start : 0;
+                        x.h = (int)quotient(off, q.head);
+                        off -= x.h * q.head;
+                        int lo = 0, hi = q.pairs;
+                        while (hi - lo > 1) {
+                            const int mid = (lo + hi) >> 1;
+                            if (pair_at(q, mid) <= off) lo = mid; else hi = mid;
+                        }
+                        int rb = lo;
+                        for (; x.h < p.Hk && ok; ++x.h, rb = 0) {
+                            for (; rb < q.pairs && ok; ++rb) {
+                                const bool last = rb == q.pairs - 1;
+                                const int64_t at = start + x.h * q.head + pair_at(q, rb);
+                                if (at >= end) break;
+                                x.r = r0 + who;
+                                x.token0 = rb * pt;
+                                x.tokens = last ? q.n - x.token0 : pt;
+                                x.ctx = q.ctx;
+                                x.first = p.cu ? q.first : 0;
+                                x.two = !(last && q.one);
+                                x.end = q.ok ? q.ctx + x.token0 + x.tokens : 0;
+                                const int tiles = max(1, (x.end + kKeys - 1) / kKeys);
+                                const int64_t length = last ? last_length(q) : kItemKeys + (int64_t)q.ctx + x.token0 + pt;
+                                // key tiles before a place on the line: none in the first kItemKeys, then evenly
+                                auto tiles_before = [&](int64_t place) -> int {
+                                    const int64_t in = place - at - kItemKeys, of = length - kItemKeys;
+                                    return in <= 0 ? 0 : in >= of ? tiles : (int)quotient(in * tiles + of - 1, of);
+                                };
+                                x.t0 = tiles_before(begin);
+                                x.t1 = tiles_before(end);
+                                x.whole = x.t0 == 0 && x.t1 == tiles;
+                                if (x.t1 > x.t0) {
+                                    if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, rb);
+                                    x.flip = (uint8_t)flip;
+                                    if (!x.two) flip ^= (x.t1 - x.t0) & 1;
+                                    deal();
+                                }
+                            }
+                            if (start + (x.h + 1) * q.head >= end) break;
+                        }
+                    }
+                    over = before >= end;
+                }
+            }
+            x.t1 = -1;
+            if (ok) deal();
+            // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
+            if (half == 0 && lane == 0 && cta < room) {
+                p.parts[2 * cta] = slots[0];
+                p.parts[2 * cta + 1] = slots[1];
+            }
+            if (!ok && lane == 0) fail();
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ cleaning
+            // V tiles with positions that some row of the item does not see, between their copy
+            // and the products, so that the loader can go on.
+            int base_kv = 0, item = 0;      // ring tiles before this item, items begun
+            uint32_t phases = 0;            // of the slots' raw barriers
+            bool ok = true;
+            Item x;
+            for (; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
+                const int special = clean_from(x);
+                if (lane < kBadWords) m.bad[item % kItems][lane] = 0;   // the way out of four items before has read them
+                __syncwarp();
+                for (int tile = max(x.t0, special); tile < x.t1 && ok; ++tile) {
+                    const int i = base_kv + kPer * (tile - x.t0) + kHalves, slot = i % kSlots, base = tile * kKeys;
+                    uint8_t* const dst = ring + slot * kSlotBytes;
+                    ok = __all_sync(0xffffffffu, wait_for(&m.kv_raw[slot], (phases >> slot) & 1, abort, limit));
+                    if (!ok) break;
+                    phases ^= 1u << slot;
+                    constexpr uint32_t kExp = Elem<T>::kExpMask;
+                    constexpr int kPieces = kV / 8;
+                    auto piece = [&](int e) -> uint4* {   // 16-byte piece e of the tile, rows in order
+                        const int c = e % kPieces, krow = e / kPieces;
+                        return reinterpret_cast<uint4*>(dst + (krow >> 3) * kGroupBytes + (c >> 3) * 1024 +
+                                                        (krow & 7) * 128 + (c & 7) * 16);
+                    };
+                    // rows behind what any row sees, and those that every row sees
+                    const int past = max(0, min(x.end - base, kKeys)), seen = max(0, min(x.ctx + x.token0 + 1, x.end) - base);
+                    for (int e = past * kPieces + lane; e < kKeys * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+                    for (int e = seen * kPieces + lane; e < past * kPieces; e += 32) {
+                        const uint4 y = *piece(e);
+                        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                        bool bad = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((w[k] & kExp) == kExp) { bad = true; w[k] &= 0xffff0000u; }
+                            if (((w[k] >> 16) & kExp) == kExp) { bad = true; w[k] &= 0xffffu; }
+                        }
+                        if (bad) {
+                            const int j = base + e / kPieces - special * kKeys;
+                            atomicOr(&m.bad[item % kItems][j >> 5], 1u << (j & 31));
+                            *piece(e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m.kv_full[slot]);
+                }
+                base_kv += kPer * (x.t1 - x.t0);
+                release(item);
+            }
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- the rows' way out
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int row = tid & 127;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const int in_token = (int)page_div((uint32_t)row, G, p.group_magic), in_head = row - in_token * G;
+        const float c = p.scale_log2;
+        uint32_t outs[2] = {0, 0};    // items of each stream
+        bool ok = true;
+        Item x;
+        for (int item = 0; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
+            const int units = (x.two ? 2 : 1) * (x.t1 - x.t0);
+            const bool joined = !x.two && units > 1;
+            const int special = clean_from(x);
+            const bool cleaned = x.t1 > special;   // (otherwise the flags are not this item's)
+            // one row tile: one pass over both streams; two: a pass each
+            for (int a = 0; a < (x.two ? 2 : 1) && ok; ++a) {
+                const int s = x.flip ^ a, s2 = s ^ 1;
+                ok = wait_for(&m.ml_full[s], outs[s] & 1, abort, limit) && wait_for(&m.o_full[s], outs[s] & 1, abort, limit);
+                if (joined)
+                    ok = ok && wait_for(&m.ml_full[s2], outs[s2] & 1, abort, limit) &&
+                         wait_for(&m.o_full[s2], outs[s2] & 1, abort, limit);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                ++outs[s];
+                float2 ml = m.ml[s][row];
+                float f0 = 1.f, f1 = 0.f;
+                if (joined) {
+                    ++outs[s2];
+                    const float2 o = m.ml[s2][row];
+                    const float mj = fmaxf(ml.x, o.x), mu = mj == -INFINITY ? 0.f : mj;
+                    f0 = ex2_approx((ml.x - mu) * c);
+                    f1 = ex2_approx((o.x - mu) * c);
+                    ml = make_float2(mj, ml.y * f0 + o.y * f1);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&m.ml_free[s]);
+                    if (joined) mbar_arrive(&m.ml_free[s2]);
+                }
+                const int token = x.token0 + a * tt + in_token;   // of the request
+                const bool live = in_token < tt && token < x.token0 + x.tokens;
+                const bool empty = ml.y == 0.f, whole = x.whole;
+                const float inv = empty ? 0.f : 1.f / ml.y;
+                f0 *= inv;
+                f1 *= inv;
+                const int64_t part = (int64_t)(2 * cta + (x.t0 > 0 ? 0 : 1)) * 256 + a * 128 + row;
+                T* const dst = static_cast<T*>(p.out) + (p.cu ? (int64_t)(x.first + token) * p.os[1]
+                                                              : x.r * p.os[0] + token * p.os[1]) +
+                               (x.h * G + in_head) * p.os[2] + half * kV;
+                float* const pdst = p.part_o + part * D + half * kV;
+                uint32_t any_bad = 0;
+                if (cleaned) {
+#pragma unroll
+                    for (int w = 0; w < kBadWords; ++w) any_bad |= m.bad[item % kItems][w];
+                }
+                const uint32_t to = tb + lane_base + kTmemO + 128 * s, to2 = tb + lane_base + kTmemO + 128 * s2;
+#pragma unroll 1
+                for (int k = 0; k < kV / 16; ++k) {
+                    float o[16];
+                    if (joined) {
+                        uint32_t r0[16], r1[16];
+                        float y[16];
+                        tmem_ld16_issue(to + 16 * k, r0);
+                        tmem_ld16_issue(to2 + 16 * k, r1);
+                        tmem_wait_ld();
+                        tmem_take16(r0, o);
+                        tmem_take16(r1, y);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : fmaf(y[e], f1, o[e] * f0);
+                    } else {
+                        tmem_ld16(to + 16 * k, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : o[e] * f0;
+                    }
+                    if (k == kV / 16 - 1) {   // O is read: the next item's may come
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&m.o_free[s]);
+                            if (joined) mbar_arrive(&m.o_free[s2]);
+                        }
+                    }
+                    if (any_bad && live && !empty) {
+                        const int from = max(special, x.t0) * kKeys, to_key = min(x.ctx + token + 1, min(x.end, x.t1 * kKeys));
+                        for (int pos = from; pos < to_key; ++pos) {
+                            const int j = pos - special * kKeys;
+                            if (!((m.bad[item % kItems][j >> 5] >> (j & 31)) & 1u)) continue;
+                            const int id = p.table[x.r * p.table_stride + pos / p.page];
+                            if (id < 0 || id >= p.P) continue;
+                            const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (pos % p.page) * p.vs[1] +
+                                           x.h * p.vs[2] + half * kV + 16 * k;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float y = Elem<T>::one(src[e]);
+                                if (!isfinite(y)) o[e] += y;
+                            }
+                        }
+                    }
+                    if (live) {
+                        uint32_t w[8];
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = Elem<T>::pack(o[2 * e], o[2 * e + 1]);
+                            store32(dst + 16 * k, w, p.wide_out);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
+                            store32(pdst + 16 * k, w, true);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 + e]);
+                            store32(pdst + 16 * k + 8, w, true);
+                        }
+                    }
+                }
+                if (live && half == 0) {
+                    const float lse = empty ? -INFINITY : ml.x * c + log2f(ml.y);
+                    if (!whole) p.part_lse[part] = lse;
+                    else if (p.lse)
+                        p.lse[((p.cu ? (int64_t)x.first : (int64_t)x.r * p.T) + token) * p.Hq + x.h * G + in_head] =
+                            lse * 0.6931471805599453f;
+                }
+            }
+            if (ok) release(item);
+        }
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+    } else {
+        // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int stream = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tb + lane_base + kTmemS + 128 * stream, to = tb + lane_base + kTmemO + 128 * stream;
+        const float c = p.scale_log2, lazy = kLazy<T> / c;   // in units of the scores
+        const int in_token = (int)page_div((uint32_t)row, G, p.group_magic);
+        bool ok = true;
+        uint32_t seen_s = 0, items_s = 0;   // score tiles taken, items with work for this stream
+        for (int item = 0;; ++item) {
+            Item x;
+            if (!__all_sync(0xffffffffu, take(item, x, ok)) || !ok) break;
+            release(item);
+            const bool two = x.two;
+            const int units = (two ? 2 : 1) * (x.t1 - x.t0), u0 = stream ^ x.flip;
+            if (u0 >= units) continue;
+            // keys that this row sees, and the warp's first row
+            const int token = x.ctx + x.token0 + (two && u0 ? tt : 0) + in_token;
+            const int sees = min(token + 1, x.end), least = __shfl_sync(0xffffffffu, sees, 0);
+            const int tile0 = x.t0;
+            float mx = -INFINITY, l = 0.f;
+            if (p.timeout_probe && item == 0) ok = __all_sync(0xffffffffu, wait_for(&m.never, 0, abort, limit));
+            for (int u = u0; u < units && ok; u += 2) {
+                ok = __all_sync(0xffffffffu, wait_for(&m.s_full[stream], seen_s & 1, abort, limit));
+                if (!ok) break;
+                ++seen_s;
+                tc_fence_after();
+                uint32_t raw[8][16];
+                float v[128];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) tmem_ld16_issue(ts + 16 * k, raw[k]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) tmem_take16(raw[k], &v[16 * k]);
+                const int base = (tile0 + (two ? u >> 1 : u)) * kKeys;
+                if (base + kKeys > least) {
+                    const int n = sees - base;
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        if (e >= n) v[e] = -INFINITY;
+                }
+                float t8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t8[e] = v[e];
+#pragma unroll
+                for (int e = 8; e < 128; ++e) t8[e & 7] = fmaxf(t8[e & 7], v[e]);
+                const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])),
+                                        fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+                float alpha = 1.f;
+                if (top > mx + lazy || mx == -INFINITY) {
+                    const float mn = fmaxf(mx, kShift<T> == 0.f ? top : fmaf(lazy, -kShift<T> / kLazy<T>, top));
+                    if (mx != -INFINITY) alpha = ex2_approx((mx - mn) * c);
+                    mx = mn;
+                    l *= alpha;
+                }
+                if (u > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int k = 0; k < kV / 16; ++k) {
+                        float o[16];
+                        uint32_t w[16];
+                        tmem_ld16(to + 16 * k, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                        tmem_st16(to + 16 * k, w);
+                    }
+                }
+                const float mc = mx == -INFINITY ? 0.f : -mx * c;
+                const F2 c2 = f2(c, c), m2 = f2(mc, mc);
+                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = f2_parts(f2_fma(f2(v[32 * k + 2 * e], v[32 * k + 2 * e + 1]), c2, m2));
+                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                        sum[e & 1] = f2_add(sum[e & 1], f2(p0, p1));
+                        w[e] = Elem<T>::pack(p0, p1);
+                    }
+                    tmem_st16_issue(ts + 16 * k, w);
+                    if (k == 1) {   // half of P: its product may start
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&m.p_half[stream]);
+                    }
+                }
+                const float2 q = f2_parts(f2_add(sum[0], sum[1]));
+                l += q.x + q.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.p_ready[stream]);
+            }
+            // the rows' maximum and sum, once those of the stream's item before have been taken
+            if (items_s > 0) ok = ok && wait_for(&m.ml_free[stream], (items_s - 1) & 1, abort, limit);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++items_s;
+            m.ml[stream][row] = make_float2(mx, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.ml_full[stream]);
+        }
+        if (!ok && lane == 0) fail();
+    }
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tb, 512);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const ChunkParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
+                     cudaStream_t s) {
+    static std::atomic<uint64_t> smem_set;
+    cudaError_t e = set_smem_limit_once((const void*)chunk_mma_kernel<T, D>, (int)Shape<D>::kBytes, smem_set);
+    if (e != cudaSuccess) return e;
+    chunk_mma_kernel<T, D><<<grid - grid % Shape<D>::kHalves, kThreads, Shape<D>::kBytes, s>>>(p, qmap, kmap, vmap);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_d(const ChunkParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, int D,
+                     int grid, cudaStream_t s) {
+    return D == 64 ? launch_t<T, 64>(p, qmap, kmap, vmap, grid, s)
+                   : D == 128 ? launch_t<T, 128>(p, qmap, kmap, vmap, grid, s) : launch_t<T, 256>(p, qmap, kmap, vmap, grid, s);
+}
+
+// Tensor map of the queries as [64 channels, heads, tokens, blocks of 64 channels, requests],
+// a box the query heads of a key head of a row tile's tokens.
+bool query_map(CUtensorMap* map, const ChunkParams& p, int D, bool f16) {
+    const uint64_t dims[5] = {64, (uint64_t)p.Hq, (uint64_t)p.T, (uint64_t)D / 64, p.cu ? 1u : (uint64_t)p.R};
+    const uint64_t strides[4] = {(uint64_t)p.qs[2] * 2, (uint64_t)p.qs[1] * 2, 128, (uint64_t)(p.cu ? p.qs[1] : p.qs[0]) * 2};
+    const uint32_t box[5] = {64, (uint32_t)p.G, (uint32_t)p.tile_tokens, 1, 1};
+    return make_tensor_map(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, p.q, dims, strides,
+                           box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+bool launch_chunk_mma(const ChunkParams& q, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e) {
+    CUtensorMap qmap, kmap, vmap;
+    ChunkParams p = q;
+    p.tile_tokens = 128 / p.G;
+    p.wait_ns += (uint64_t)((p.max_len + kKeys - 1) / kKeys) * kTileWaitNs;
+    p.wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 && p.os[0] % 16 == 0 && p.os[1] % 16 == 0 && p.os[2] % 16 == 0;
+    if (!query_map(&qmap, p, D, f16) || !cache_map(&kmap, p.kc, p.ks, p.Hk, p.P, p.page, D, f16, &p.k_paged) ||
+        !cache_map(&vmap, p.vc, p.vs, p.Hk, p.P, p.page, D, f16, &p.v_paged))
+        return false;
+    if (f16) *e = launch_d<__half>(p, qmap, kmap, vmap, D, grid, s);
+    else *e = launch_d<__nv_bfloat16>(p, qmap, kmap, vmap, D, grid, s);
+    return true;
+}
+
+}  // namespace kda

@@ -110,7 +110,14 @@ int64_t chunk_max_len(const kda_chunk_attention_args* a) {
 
 ChunkPlan plan_of(const kda_chunk_attention_args* a, int64_t max_len, int num_sms) {
     return chunk_plan((int)a->num_requests, (int)a->seqlen, a->cu_seqlens != nullptr, (int)a->num_k_heads,
-                      (int)(a->num_q_heads / a->num_k_heads), (int)a->head_dim, max_len, num_sms);
+                      (int)(a->num_q_heads / a->num_k_heads), (int)a->head_dim, max_len, (int)a->page_size, a->scale,
+                      a->out == a->q, num_sms);
+}
+
+// The workspace: what the partial rows belong to, the rows, their log-sums (32-byte aligned each).
+size_t chunk_workspace(const kda_chunk_attention_args* a, const ChunkPlan& plan) {
+    const size_t parts = (size_t)2 * plan.stretches;
+    return parts * sizeof(int4) + parts * 256 * ((size_t)a->head_dim + 1) * sizeof(float);
 }
 
 uint32_t magic_of(int64_t d) { return d == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint64_t)d); }
@@ -297,16 +304,25 @@ kda_status kda_tree_attention_ex(const kda_tree_attention_args* a, const kda_ove
 }
 
 size_t kda_chunk_attention_workspace_size(const kda_chunk_attention_args* a) {
-    return 0;
+    if (check_chunk(a) != KDA_OK || a->num_requests == 0 || a->seqlen == 0) return 0;
+    const int64_t max_len = chunk_max_len(a);
+    return max_len < 0 ? 0 : chunk_workspace(a, plan_of(a, max_len, sm_count_or_default()));
 }
 
 kda_status kda_chunk_attention(const kda_chunk_attention_args* a, void* stream) {
+    return kda_chunk_attention_ex(a, nullptr, stream);
+}
+
+kda_status kda_chunk_attention_ex(const kda_chunk_attention_args* a, const kda_overrides* overrides, void* stream) {
     const kda_status st = check_chunk(a);
     if (st != KDA_OK || a->num_requests == 0 || a->seqlen == 0) return st;
     const int64_t max_len = chunk_max_len(a);
     if (max_len < 0) return KDA_ERR_UNSUPPORTED;
     if (device_sm_count() < 1) return KDA_ERR_CUDA;
     const ChunkPlan plan = plan_of(a, max_len, sm_count_or_default());
+    const size_t need = chunk_workspace(a, plan);
+    if (need && (!a->workspace || a->workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
+    if (need && (reinterpret_cast<uintptr_t>(a->workspace) & 255u)) return KDA_ERR_UNSUPPORTED;
     ChunkParams p;
     memset(&p, 0, sizeof(p));
     p.q = a->q; p.kc = a->k_cache; p.vc = a->v_cache; p.out = a->out; p.lse = a->lse;
@@ -322,7 +338,12 @@ kda_status kda_chunk_attention(const kda_chunk_attention_args* a, void* stream) 
     p.max_ctx = a->max_context >= 0 && a->max_context < INT32_MAX ? (int32_t)a->max_context : INT32_MAX;
     p.page_magic = magic_of(p.page);
     p.group_magic = magic_of(p.G);
+    p.parts = static_cast<int4*>(a->workspace);
+    p.part_o = reinterpret_cast<float*>(p.parts + 2 * plan.stretches);
+    p.part_lse = p.part_o + (size_t)2 * plan.stretches * 256 * a->head_dim;
     p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.wait_ns = overrides && overrides->wait_limit_ns > 0 ? (uint64_t)overrides->wait_limit_ns : kWaitLimitNs;
+    p.timeout_probe = overrides && overrides->timeout_probe ? 1 : 0;
     return status_of(launch_chunk_attention(p, plan, (int)a->head_dim, a->dtype == KDA_DTYPE_F16,
                                             static_cast<cudaStream_t>(stream)));
 }

@@ -463,7 +463,9 @@ PyObject* chunk_attention(PyObject* const* o) {
         a.workspace = ws.data_ptr();
         a.workspace_bytes = (size_t)ws.numel();
     }
-    done(kda_chunk_attention(&a, stream_of(q)));
+    const auto* overrides = o[12] == Py_None ? nullptr : static_cast<const kda_overrides*>(PyLong_AsVoidPtr(o[12]));
+    if (PyErr_Occurred()) throw Refused();
+    done(kda_chunk_attention_ex(&a, overrides, stream_of(q)));
     PyObject* ro = o[8] != Py_None ? Py_NewRef(o[8]) : THPVariable_Wrap(out);
     return want_lse ? both(ro, THPVariable_Wrap(lse)) : ro;
 }

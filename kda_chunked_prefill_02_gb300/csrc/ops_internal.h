@@ -116,14 +116,32 @@ struct ChunkParams {
     uint32_t page_magic, group_magic;
     int cluster;              // rows kernel: CTAs that share an item
     int stages;               // rows kernel: tiles in flight (set by the launcher)
+    // mma: partial rows [2 CTAs, 256, D] of items that are cut, their log-sums (base 2), and
+    // what they belong to, [2 CTAs]: state (0 nothing, 1 a part, 2 an item's last), request,
+    // key head, pair of row tiles
+    float* part_o;
+    float* part_lse;
+    int4* parts;
+    int ctas;                 // mma: stretches of the line of work
+    int tile_tokens;          // mma: tokens a row tile (set by the launcher, as what follows)
+    int k_paged, v_paged;     // the head is part of the map's page coordinate
+    int wide_out;             // rows of out are 32-byte aligned
     float scale_log2;         // scale * log2(e)
+    uint64_t wait_ns;         // mma: bound of the working waits (set by the entry; a wind-down's are kWaitLimitNs)
+    int timeout_probe;        // mma: the softmax warps' first wait runs out (tests)
 };
 // How a call is cut.
 struct ChunkPlan {
+    bool mma;                 // the tensor-core kernel
+    int grid;                 // and its CTAs
+    int stretches;            // its equal stretches of work (with head size 256 two CTAs share one)
     int cluster;              // rows kernel: CTAs that share an item
 };
-ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int num_sms);
+ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int page, float scale, bool in_place,
+                     int num_sms);
 cudaError_t launch_chunk_attention(const ChunkParams& p, const ChunkPlan& plan, int D, bool f16, cudaStream_t s);
+// The tensor-core kernel; false if the layouts have no tensor map.
+bool launch_chunk_mma(const ChunkParams& p, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e);
 
 // Request r of a call: its first row of q (packed: in all, padded: 0), its new tokens and
 // the keys it may see; false if they do not fit the call.  Tokens that lie inside the call
