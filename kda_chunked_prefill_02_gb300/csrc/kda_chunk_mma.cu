@@ -8,14 +8,16 @@
 //                   registers, so maximum and sum need no exchange; P goes back over S's
 //                   columns as 16-bit pairs, the A operand of the second product;
 //   warps 8-11      the rows' way out: O from TMEM, divided by the sum, to memory;
-//   warp 12         the loader: query tiles and a ring of K and V tiles;
-//   warp 13         issues the products;
-//   warp 14         deals out the work, item by item;
+//   warp 12         deals out the work, item by item, and loads it: query tiles and a ring
+//                   of K and V tiles;
+//   warps 13, 14    issue the products, a stream each (one warp for both was what bound the
+//                   kernel: some 2300 cycles a unit of waits, commits and 16 products that
+//                   take 1024);
 //   warp 15         cleans the V tiles that need it.
 // An item is a pair of row tiles over the same keys, one a stream, each K and V tile read
 // for 256 rows; or a last single row tile, whose even and odd key tiles go to the two
-// streams and whose two halves are joined on the way out.  The streams alternate without
-// a break from item to item: while an item's last rows are on their way out, the next
+// streams and whose two halves are joined on the way out.  The streams run without a break
+// from item to item: while an item's last rows are on their way out, the next
 // one's first scores are formed and its softmax runs (its queries come into a buffer of
 // their own), so that short prompts, whose items are a few tiles long, keep the tensor
 // pipe as busy as long ones do.
@@ -44,8 +46,8 @@
 // NaN, also for a row whose P is zero), and remembers their positions; the rows that do
 // see such a position take its elements on their way out.
 //
-// Registers: 512 threads start with 128 each; the softmax warps take 192, the way out
-// keeps 72, the last four warps 56 (2 x 192 + 72 + 56 = 4 x 128).
+// Registers: 512 threads start with 128 each; the softmax warps take 184, the way out
+// keeps 80, the last four warps 64 (2 x 184 + 80 + 64 = 4 x 128).
 //
 // Every wait is bounded; one that runs out sets the abort flag, the roles fall through to
 // the end, and the status word reports KDA_ERR_TIMEOUT.  Whatever the others do, the loader
@@ -75,15 +77,15 @@ struct Item {
     int t0, t1;                 // key tiles (t1 < 0: no more items)
     int ctx, first;             // the request's context, and its first row of q (packed: in all)
     int end;                    // keys that the last token sees (0: a request that does not fit the call)
-    uint8_t two, whole, flip;   // two row tiles; all of the key tiles; the stream of the first unit
+    uint8_t two, whole;         // two row tiles; all of the key tiles
 };
 
 // A CTA's memory behind the queries and the ring.
 struct Misc {
     uint64_t kv_full[kMaxSlots], kv_free[kMaxSlots], kv_raw[kMaxSlots];
-    uint64_t q_full[kMaxQ], q_free[kMaxQ];
+    uint64_t q_full[kItems][2], q_free[kMaxQ];   // full: an item's row tiles
     uint64_t s_full[2], p_half[2], p_ready[2], o_full[2], o_free[2], ml_full[2], ml_free[2];
-    uint64_t item_full[kItems], item_free[kItems], drained, never;   // never: the probe's, nothing arrives on it
+    uint64_t item_full[kItems], item_free[kItems], drained[2], never;   // never: the probe's, nothing arrives on it
     float2 ml[2][128];          // the rows' maximum and sum, a stream each
     uint32_t bad[kItems][kBadWords];   // positions with a V element that is not finite
     Item item[kItems];
@@ -145,13 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(&m.kv_full[i], 1);
-            mbar_init(&m.kv_free[i], 1);
+            mbar_init(&m.kv_free[i], 2);    // both streams' products
             mbar_init(&m.kv_raw[i], 1);
         }
-        for (int i = 0; i < kMaxQ; ++i) {
-            mbar_init(&m.q_full[i], 1);
-            mbar_init(&m.q_free[i], 1);
-        }
+        for (int i = 0; i < kMaxQ; ++i) mbar_init(&m.q_free[i], 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.s_full[s], 1);
             mbar_init(&m.p_half[s], 4);     // one arrival a warp
@@ -163,9 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&m.item_full[i], 1);
-            mbar_init(&m.item_free[i], 15);   // 8 softmax warps, 4 of the way out, loader, issuer, cleaner
+            mbar_init(&m.q_full[i][0], 1);
+            mbar_init(&m.q_full[i][1], 1);
+            mbar_init(&m.item_free[i], 15);   // 8 softmax warps, 4 of the way out, 2 issuers, the cleaner
         }
-        mbar_init(&m.drained, 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&m.drained[s], 1);
         mbar_init(&m.never, 1);
         m.abort = 0;
         fence_mbar_init();
@@ -193,192 +194,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto clean_from = [&](const Item& x) -> int { return min(x.end, x.ctx + x.token0 + 1) / kKeys; };
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 12) {
-            // ------------------------------------------------------------ loader
+            // ------------------------------------------------------------ work and loader
             if (lane == 0) {
                 tma_prefetch_desc(&qmap);
                 tma_prefetch_desc(&kmap);
                 tma_prefetch_desc(&vmap);
             }
-            const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
-            int issued = 0, queries = 0, item = 0;   // K and V tiles and query tiles asked for, items begun
-            uint32_t raw = 0, raw_phases = ~0u;   // slots whose last copy was a raw one, those copies' phases
-            bool ok = true;
-            Item x;
-            for (; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
-                release(item);
-                const int32_t* table = p.table + x.r * p.table_stride;
-                const int special = clean_from(x);
-                // this lane's page of a tile, -1: none (asked for a tile ahead, looked at
-                // later), and its first row there
-                int row_ahead = 0;
-                auto page_of = [&](int tile) -> int64_t {
-                    const int tok = tile * kKeys + lane * box;
-                    const int at = (int)page_div((uint32_t)tok, p.page, p.page_magic);
-                    row_ahead = tok - at * p.page;
-                    return tile < x.t1 && lane < per_tile && tok < x.end ? (int64_t)(uint32_t)table[at] : -1;
-                };
-                // row tile a of the item: a box of whole tokens a block of 64 channels (rows past
-                // the request's end, or the call's, are some other rows or zeros, and not stored)
-                auto load_queries = [&](int a) {
-                    const int b = queries % kQ, round = queries / kQ;
-                    if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.q_free[b], (round - 1) & 1, abort, limit));
-                    if (!ok) return;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&m.q_full[b], (uint32_t)(G * tt) * 128u * (D / 64));
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_5d(sm + b * kQBytes + c * kBlock, &qmap, 0, x.h * G, x.first + x.token0 + a * tt, c,
-                                        p.cu ? 0 : x.r, &m.q_full[b]);
-                    }
-                    __syncwarp();
-                    ++queries;
-                };
-                int64_t ahead = page_of(x.t0);
-                load_queries(0);
-                for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
-                    const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
-                    if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
-                    const int row = row_ahead;
-                    ahead = page_of(tile + 1);
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * kV * 2u;
-                    for (int part = 0; part < kPer && ok; ++part) {   // K by kV channels, then V
-                        const bool v = part == kHalves;
-                        if (v && tile == x.t0 && x.two) load_queries(1);
-                        const int slot = issued % kSlots, round = issued / kSlots;
-                        if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.kv_free[slot], (round - 1) & 1, abort, limit));
-                        if (!ok) break;
-                        uint8_t* dst = ring + slot * kSlotBytes;
-                        const bool to_clean = v && tile >= special;
-                        uint64_t* bar = to_clean ? &m.kv_raw[slot] : &m.kv_full[slot];   // raw: to warp 15 first
-                        raw = to_clean ? raw | 1u << slot : raw & ~(1u << slot);
-                        if (to_clean) raw_phases ^= 1u << slot;
-                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                        __syncwarp();
-                        if (id >= 0)
-                            tma_load_5d(dst + lane * box * kV * 2, v ? &vmap : &kmap, 0, 0,
-                                        ((v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64)) + (v ? half : part) * (kV / 64),
-                                        row / 8, (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
-                        ++issued;
-                    }
-                }
-            }
-            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
-            // the last copies into this CTA's memory
-            for (int i = max(0, queries - kQ); i < queries; ++i) wait_for(&m.q_full[i % kQ], (i / kQ) & 1, nullptr, kWaitLimitNs);
-            for (int i = max(0, issued - kSlots); i < issued; ++i)
-                if (!((raw >> (i % kSlots)) & 1)) wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, nullptr, kWaitLimitNs);
-                else wait_for(&m.kv_raw[i % kSlots], (raw_phases >> (i % kSlots)) & 1, nullptr, kWaitLimitNs);
-        } else if (warp == 13) {
-            // ------------------------------------------------------------ products
-            // Units (a row tile and a key tile) in their order over all items, unit g on stream
-            // g & 1; the scores run two units ahead of the second products.  The whole warp
-            // walks the loop and one elected lane issues, with every operand a warp-uniform
-            // value (see kda_tree_mma.cu).
-            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(kV);
-            const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
-            const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sm), 0), ring_at = q_at + kQ * kQBytes;
-            bool ok = true;
-            struct Cursor {
-                int item, u, units, base, queries;   // the unit of its item; ring and query tiles before the item
-                bool two, end;
-            };
-            auto enter = [&](Cursor& c) {   // the cursor's item
-                Item x;
-                c.end = !__all_sync(0xffffffffu, take(c.item, x, ok));
-                c.two = __shfl_sync(0xffffffffu, (int)x.two, 0) != 0;
-                c.units = (c.two ? 2 : 1) * __shfl_sync(0xffffffffu, x.t1 - x.t0, 0);
-                c.u = 0;
-            };
-            auto advance = [&](Cursor& c, bool done) {
-                if (++c.u < c.units) return;
-                if (done) release(c.item);
-                c.base += kPer * (c.two ? c.units / 2 : c.units);
-                c.queries += c.two ? 2 : 1;
-                ++c.item;
-                enter(c);
-            };
-            auto landed = [&](int i) { return wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, abort, limit); };
-            int g = 0;                         // score units issued
-            uint32_t done[2] = {0, 0}, items[2] = {0, 0};   // P tiles taken, items begun, a stream each
-            Cursor sc{0, 0, 0, 0, 0, false, false}, pv{0, 0, 0, 0, 0, false, false};
-            enter(sc);
-            enter(pv);
-            auto scores = [&]() {
-                const int s = g & 1, u = sc.u, i = sc.base + kPer * (sc.two ? u >> 1 : u);
-                const int q = sc.queries + (sc.two ? u & 1 : 0), b = q % kQ;
-                if (u < (sc.two ? 2 : 1)) ok = ok && wait_for(&m.q_full[b], (q / kQ) & 1, abort, limit);
-                if (!sc.two || !(u & 1)) {
-#pragma unroll
-                    for (int part = 0; part < kHalves; ++part) ok = ok && landed(i + part);
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t ad = sdesc_kmajor_sw128(q_at + b * kQBytes);
-#pragma unroll
-                for (int part = 0; part < kHalves; ++part) {   // kV channels of K
-                    const int slot = (i + part) % kSlots;
-                    const uint64_t bd = sdesc_keys(ring_at + slot * kSlotBytes, kGroupBytes);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kV / 16; ++k)
-                            umma_bf16(tbu + kTmemS + 128 * s, ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
-                                      bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, part + k > 0 ? 1u : 0u);
-                        if (part == kHalves - 1) {
-                            umma_commit(&m.s_full[s]);
-                            if (u >= sc.units - (sc.two ? 2 : 1)) umma_commit(&m.q_free[b]);
-                        }
-                        if (!sc.two || (u & 1)) umma_commit(&m.kv_free[slot]);
-                    }
-                }
-                __syncwarp();
-                ++g;
-                advance(sc, false);
-            };
-            if (ok && !sc.end) scores();
-            if (ok && !sc.end) scores();
-            for (int n = 0; ok && !pv.end; ++n) {
-                const int s = n & 1, u = pv.u, i = pv.base + kPer * (pv.two ? u >> 1 : u) + kHalves;
-                // O still holds the rows of the stream's item before until they are out
-                if (u < 2) {
-                    if (items[s] > 0) ok = ok && wait_for(&m.o_free[s], (items[s] - 1) & 1, abort, limit);
-                    ++items[s];
-                }
-                if (!pv.two || !(u & 1)) ok = ok && landed(i);
-                const uint32_t phase = done[s] & 1;
-                ++done[s];
-                const uint64_t bd = sdesc_mnmajor_sw128(ring_at + (i % kSlots) * kSlotBytes, 1024, kGroupBytes);
-                // the two halves of P as they come
-                auto product = [&](int k0, uint64_t* ready) {
-                    ok = __all_sync(0xffffffffu, ok && wait_for(ready, phase, abort, limit));
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kKeys / 32; ++k)
-                            umma_bf16_ta(tbu + kTmemO + 128 * s, tbu + kTmemS + 128 * s + 8 * (k0 + k),
-                                         bd + (k0 + k) * (kGroupBytes >> 3), id_pv, (u > 1 || k0 + k > 0) ? 1u : 0u);
-                        if (k0) {
-                            if (!pv.two || (u & 1)) umma_commit(&m.kv_free[i % kSlots]);
-                            if (u + 2 >= pv.units) umma_commit(&m.o_full[s]);
-                        }
-                    }
-                    __syncwarp();
-                };
-                product(0, &m.p_half[s]);
-                product(kKeys / 32, &m.p_ready[s]);
-                if (!ok) break;
-                if (!sc.end) scores();
-                advance(pv, true);
-            }
-            if (!ok && lane == 0) fail();
-            if (elect_one()) umma_commit(&m.drained);
-            __syncwarp();
-            wait_for(&m.drained, 0, nullptr, kWaitLimitNs);   // the last products
-            __syncwarp();
-        } else if (warp == 14) {
-            // ------------------------------------------------------------ work
             // A request's length on the line: over its pairs of row tiles, the keys of each one's
             // last token (a last single row tile four fifths of them, as measured) and kItemKeys,
             // times the key heads.
@@ -421,18 +244,89 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t most = total / (2 * kKeys);
             const int room = (int)gridDim.x / kHalves, ctas = most < 1 ? 1 : most < room ? (int)most : room;
             int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
-            int k = 0, flip = 0;
+            const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
+            int item = 0, issued = 0, queries = 0;   // items dealt, K and V tiles and query tiles asked for
+            uint32_t raw = 0, raw_phases = ~0u;      // slots whose last copy was a raw one, those copies' phases
+            int q_asked = 0, q_phase = 0;            // q_full barriers with a copy, those copies' phases
             bool ok = true;
             Item x{};
+            // The item to the other warps.
             auto deal = [&]() {
-                if (k >= kItems) ok = __all_sync(0xffffffffu, wait_for(&m.item_free[k % kItems], (k / kItems - 1) & 1, abort, limit));
+                const int at = item % kItems;
+                if (item >= kItems) ok = __all_sync(0xffffffffu, wait_for(&m.item_free[at], (item / kItems - 1) & 1, abort, limit));
                 if (!ok) return;
                 if (lane == 0) {
-                    m.item[k % kItems] = x;
-                    mbar_arrive(&m.item_full[k % kItems]);
+                    m.item[at] = x;
+                    mbar_arrive(&m.item_full[at]);
                 }
                 __syncwarp();
-                ++k;
+                ++item;
+            };
+            // Its queries and its tiles.
+            auto load = [&]() {
+                if (!ok) return;
+                const int32_t* table = p.table + x.r * p.table_stride;
+                const int special = clean_from(x);
+                // this lane's page of a tile, -1: none (asked for a tile ahead, looked at
+                // later), and its first row there
+                int row_ahead = 0;
+                auto page_of = [&](int tile) -> int64_t {
+                    const int tok = tile * kKeys + lane * box;
+                    const int at = (int)page_div((uint32_t)tok, p.page, p.page_magic);
+                    row_ahead = tok - at * p.page;
+                    return tile < x.t1 && lane < per_tile && tok < x.end ? (int64_t)(uint32_t)table[at] : -1;
+                };
+                // row tile a of the item: a box of whole tokens a block of 64 channels (rows past
+                // the request's end, or the call's, are some other rows or zeros, and not stored)
+                auto load_queries = [&](int a) {
+                    const int b = queries % kQ, round = queries / kQ;
+                    if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.q_free[b], (round - 1) & 1, abort, limit));
+                    if (!ok) return;
+                    const int at = (item - 1) % kItems, bit = 1 << (2 * at + a);   // the item is dealt already
+                    uint64_t* bar = &m.q_full[at][a];
+                    q_asked |= bit;
+                    q_phase = ((item - 1) / kItems) & 1 ? q_phase | bit : q_phase & ~bit;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, (uint32_t)(G * tt) * 128u * (D / 64));
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_5d(sm + b * kQBytes + c * kBlock, &qmap, 0, x.h * G, x.first + x.token0 + a * tt, c,
+                                        p.cu ? 0 : x.r, bar);
+                    }
+                    __syncwarp();
+                    ++queries;
+                };
+                int64_t ahead = page_of(x.t0);
+                if (!x.two) {   // no second row tile: its phase all the same (a copy four items before is over)
+                    q_asked &= ~(2 << (2 * ((item - 1) % kItems)));
+                    if (lane == 0) mbar_arrive(&m.q_full[(item - 1) % kItems][1]);
+                }
+                load_queries(0);
+                for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
+                    const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
+                    if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
+                    const int row = row_ahead;
+                    ahead = page_of(tile + 1);
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * kV * 2u;
+                    for (int part = 0; part < kPer && ok; ++part) {   // K by kV channels, then V
+                        const bool v = part == kHalves;
+                        if (v && tile == x.t0 && x.two) load_queries(1);
+                        const int slot = issued % kSlots, round = issued / kSlots;
+                        if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.kv_free[slot], (round - 1) & 1, abort, limit));
+                        if (!ok) break;
+                        uint8_t* dst = ring + slot * kSlotBytes;
+                        const bool to_clean = v && tile >= special;
+                        uint64_t* bar = to_clean ? &m.kv_raw[slot] : &m.kv_full[slot];   // raw: to warp 15 first
+                        raw = to_clean ? raw | 1u << slot : raw & ~(1u << slot);
+                        if (to_clean) raw_phases ^= 1u << slot;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (id >= 0)
+                            tma_load_5d(dst + lane * box * kV * 2, v ? &vmap : &kmap, 0, 0,
+                                        ((v ? p.v_paged : p.k_paged) ? 0 : x.h * (D / 64)) + (v ? half : part) * (kV / 64),
+                                        row / 8, (v ? p.v_paged : p.k_paged) ? id * p.Hk + x.h : id, bar);
+                        ++issued;
+                    }
+                }
             };
             if (cta < ctas && total > 0) {
                 const int64_t begin = quotient(total * cta, ctas), end = quotient(total * (cta + 1), ctas);
@@ -499,9 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 x.whole = x.t0 == 0 && x.t1 == tiles;
                                 if (x.t1 > x.t0) {
                                     if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, rb);
-                                    x.flip = (uint8_t)flip;
-                                    if (!x.two) flip ^= (x.t1 - x.t0) & 1;
                                     deal();
+                                    load();
                                 }
                             }
                             if (start + (x.h + 1) * q.head >= end) break;
@@ -517,7 +410,155 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.parts[2 * cta] = slots[0];
                 p.parts[2 * cta + 1] = slots[1];
             }
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+            // the last copies into this CTA's memory
+            for (int i = 0; i < 2 * kItems; ++i)
+                if ((q_asked >> i) & 1) wait_for(&m.q_full[i >> 1][i & 1], (q_phase >> i) & 1, nullptr, kWaitLimitNs);
+            for (int i = max(0, issued - kSlots); i < issued; ++i)
+                if (!((raw >> (i % kSlots)) & 1)) wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, nullptr, kWaitLimitNs);
+                else wait_for(&m.kv_raw[i % kSlots], (raw_phases >> (i % kSlots)) & 1, nullptr, kWaitLimitNs);
+        } else if (warp < 15) {
+            // ------------------------------------------------------------ products
+            // A warp a stream: a tile's second product, as soon as its P is there, and the next
+            // tile's scores behind it, also those of the next item.  The whole warp walks the
+            // loop and one elected lane issues, with every operand a warp-uniform value (see
+            // kda_tree_mma.cu).
+            constexpr uint32_t id_qk = MmaTypes<T>::qk(kKeys), id_pv = MmaTypes<T>::pv(kV);
+            const int s = warp - 13;
+            const uint32_t tbu = __shfl_sync(0xffffffffu, tb, 0);
+            const uint32_t tsu = tbu + kTmemS + 128 * s, tou = tbu + kTmemO + 128 * s;
+            const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sm), 0), ring_at = q_at + kQ * kQBytes;
+            bool ok = true, two = false;
+            int item = 0, base = 0, queries = 0;   // ring and query tiles before the item
+            int tiles = 0, step = 1, j = 0;        // the item's key tiles; this stream's are j, j + step ..
+            uint32_t p_phase = 0, outs = 0;        // items whose O this stream has formed
+            auto landed = [&](int i) { return wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, abort, limit); };
+            auto keys_landed = [&](int t) {
+                bool all = true;
+#pragma unroll
+                for (int part = 0; part < kHalves; ++part) all = all && landed(base + kPer * t + part);
+                return all;
+            };
+            // A tile of the other stream's (one row tile): seen and given back all the same, so that
+            // neither stream is ever a phase ahead of, or behind, a place of the ring.
+            auto pass = [&](int t) {
+                ok = ok && keys_landed(t) && landed(base + kPer * t + kHalves);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && lane <= kHalves) mbar_arrive(&m.kv_free[(base + kPer * t + lane) % kSlots]);
+                __syncwarp();
+            };
+            // The next item with tiles for this stream, and the tile before its first there;
+            // false after the last.
+            auto enter = [&]() -> bool {
+                for (;; ++item) {
+                    ok = __all_sync(0xffffffffu, ok && wait_for(&m.item_full[item % kItems], (item / kItems) & 1, abort, limit));
+                    if (!ok) return false;
+                    const Item& x = m.item[item % kItems];
+                    const int t1 = __shfl_sync(0xffffffffu, x.t1, 0);
+                    if (t1 < 0) return false;
+                    tiles = t1 - __shfl_sync(0xffffffffu, x.t0, 0);
+                    two = __shfl_sync(0xffffffffu, (int)x.two, 0) != 0;
+                    release(item);
+                    j = two ? 0 : s;
+                    step = two ? 1 : 2;
+                    if (j > 0) pass(0);
+                    if (!ok) return false;
+                    if (j < tiles) return true;
+                    base += kPer * tiles;
+                    queries += 1;
+                }
+            };
+            // Scores of tile t (one elected lane).
+            auto scores = [&](int t) {
+                const int b = (queries + (two ? s : 0)) % kQ;
+                const uint64_t ad = sdesc_kmajor_sw128(q_at + b * kQBytes);
+#pragma unroll
+                for (int part = 0; part < kHalves; ++part) {   // kV channels of K
+                    const uint64_t bd = sdesc_keys(ring_at + (base + kPer * t + part) % kSlots * kSlotBytes, kGroupBytes);
+#pragma unroll
+                    for (int k = 0; k < kV / 16; ++k)
+                        umma_bf16(tsu, ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
+                                  bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, part + k > 0 ? 1u : 0u);
+                }
+                umma_commit(&m.s_full[s]);
+#pragma unroll
+                for (int part = 0; part < kHalves; ++part) umma_commit(&m.kv_free[(base + kPer * t + part) % kSlots]);
+                if (t + step >= tiles) {   // two arrivals free a row tile's queries: a stream's each, or one's both
+                    umma_commit(&m.q_free[b]);
+                    if (two || tiles == 1) umma_commit(&m.q_free[b]);
+                }
+            };
+            auto first_scores = [&]() {
+                ok = __all_sync(0xffffffffu, ok && wait_for(&m.q_full[item % kItems][two ? s : 0], (item / kItems) & 1, abort, limit) &&
+                                                 keys_landed(j));
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) scores(j);
+                __syncwarp();
+            };
+            bool more = enter(), begun = false;
+            if (more) first_scores();
+            while (more && ok) {
+                const int slot = (base + kPer * j + kHalves) % kSlots;
+                const bool last = j + step >= tiles;
+                // O still holds the rows of the item before until they are out
+                if (!begun && outs > 0) ok = wait_for(&m.o_free[s], (outs - 1) & 1, abort, limit);
+                // with two row tiles the next scores' keys before P is there; with one, memory is the
+                // bound, and waiting for a K would hold up the V before it
+                const bool early = two && !last;
+                ok = ok && landed(base + kPer * j + kHalves);
+                if (early) ok = ok && keys_landed(j + step);
+                const uint64_t bd = sdesc_mnmajor_sw128(ring_at + slot * kSlotBytes, 1024, kGroupBytes);
+                const uint32_t add = begun ? 1u : 0u;
+                // the two halves of P as they come
+                ok = __all_sync(0xffffffffu, ok && wait_for(&m.p_half[s], p_phase, abort, limit));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 32; ++k)
+                        umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, k > 0 ? 1u : add);
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, wait_for(&m.p_ready[s], p_phase, abort, limit));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = kKeys / 32; k < kKeys / 16; ++k)
+                        umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, 1u);
+                    if (early) scores(j + step);   // commits behind the scores: V is free a product later
+                    umma_commit(&m.kv_free[slot]);
+                    if (last) umma_commit(&m.o_full[s]);
+                }
+                __syncwarp();
+                p_phase ^= 1;
+                begun = true;
+                if (!two && j + 1 < tiles) pass(j + 1);
+                if (!ok) break;
+                if (!last) {
+                    j += step;
+                    if (!early) {
+                        ok = __all_sync(0xffffffffu, keys_landed(j));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) scores(j);
+                        __syncwarp();
+                    }
+                } else {
+                    ++outs;
+                    begun = false;
+                    base += kPer * tiles;
+                    queries += two ? 2 : 1;
+                    ++item;
+                    more = enter();
+                    if (more) first_scores();
+                }
+            }
             if (!ok && lane == 0) fail();
+            if (elect_one()) umma_commit(&m.drained[s]);
+            __syncwarp();
+            wait_for(&m.drained[s], 0, nullptr, kWaitLimitNs);   // the last products
             __syncwarp();
         } else {
             // ------------------------------------------------------------ cleaning
@@ -574,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- the rows' way out
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int in_token = (int)page_div((uint32_t)row, G, p.group_magic), in_head = row - in_token * G;
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool cleaned = x.t1 > special;   // (otherwise the flags are not this item's)
             // one row tile: one pass over both streams; two: a pass each
             for (int a = 0; a < (x.two ? 2 : 1) && ok; ++a) {
-                const int s = x.flip ^ a, s2 = s ^ 1;
+                const int s = a, s2 = a ^ 1;
                 ok = wait_for(&m.ml_full[s], outs[s] & 1, abort, limit) && wait_for(&m.o_full[s], outs[s] & 1, abort, limit);
                 if (joined)
                     ok = ok && wait_for(&m.ml_full[s2], outs[s2] & 1, abort, limit) &&
@@ -701,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
     } else {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int stream = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tb + lane_base + kTmemS + 128 * stream, to = tb + lane_base + kTmemO + 128 * stream;
@@ -714,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, take(item, x, ok)) || !ok) break;
             release(item);
             const bool two = x.two;
-            const int units = (two ? 2 : 1) * (x.t1 - x.t0), u0 = stream ^ x.flip;
+            const int units = (two ? 2 : 1) * (x.t1 - x.t0), u0 = stream;
             if (u0 >= units) continue;
             // keys that this row sees, and the warp's first row
             const int token = x.ctx + x.token0 + (two && u0 ? tt : 0) + in_token;
