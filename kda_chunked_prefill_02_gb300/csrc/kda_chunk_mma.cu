@@ -46,8 +46,8 @@
 // NaN, also for a row whose P is zero), and remembers their positions; the rows that do
 // see such a position take its elements on their way out.
 //
-// Registers: 512 threads start with 128 each; the softmax warps take 184, the way out
-// keeps 80, the last four warps 64 (2 x 184 + 80 + 64 = 4 x 128).
+// Registers: 512 threads start with 128 each; the softmax warps take 168, the way out
+// keeps 72, the last four warps 104 (2 x 168 + 72 + 104 = 4 x 128).
 //
 // Every wait is bounded; one that runs out sets the abort flag, the roles fall through to
 // the end, and the status word reports KDA_ERR_TIMEOUT.  Whatever the others do, the loader
@@ -117,6 +117,25 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
         reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
         reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
+}
+
+// Whether N pieces of 8 elements are finite: the sum of their products with 0 is 0 or NaN.
+template <typename T, int N>
+__device__ __forceinline__ bool all_finite(const uint4 (&y)[N]) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    uint32_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t zero = 0;
+            const T2 r = __hfma2(*reinterpret_cast<const T2*>(&w[i]), *reinterpret_cast<const T2*>(&zero),
+                                 *reinterpret_cast<const T2*>(&sum));
+            sum = *reinterpret_cast<const uint32_t*>(&r);
+        }
+    }
+    return (sum & 0x7fff7fffu) == 0;
 }
 
 template <typename T, int D>
@@ -190,11 +209,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.item_free[k % kItems]);
     };
+    // Keys that the last row of stream s sees, and how many of the item's key tiles are its
+    // units (one at least, so that rows without keys are written too).
+    auto stream_end = [&](const Item& x, int s) -> int { return x.two && s == 0 ? min(x.end, x.ctx + x.token0 + tt) : x.end; };
+    auto stream_units = [&](const Item& x, int s) -> int {
+        if (!x.two) return (x.t1 - x.t0 + 1 - s) / 2;   // every other tile
+        return max(1, min(x.t1, (stream_end(x, s) + kKeys - 1) / kKeys) - x.t0);
+    };
     // Keys from which on some row of an item does not see V: the tiles that are cleaned.
     auto clean_from = [&](const Item& x) -> int { return min(x.end, x.ctx + x.token0 + 1) / kKeys; };
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 12) {
             // ------------------------------------------------------------ work and loader
             if (lane == 0) {
@@ -431,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true, two = false;
             int item = 0, base = 0, queries = 0;   // ring and query tiles before the item
             int tiles = 0, step = 1, j = 0;        // the item's key tiles; this stream's are j, j + step ..
+            int units = 0, left = 0;               // how many of them are still to come; keys from the item's first tile on
             uint32_t p_phase = 0, outs = 0;        // items whose O this stream has formed
             auto landed = [&](int i) { return wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, abort, limit); };
             auto keys_landed = [&](int t) {
@@ -458,19 +485,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t1 < 0) return false;
                     tiles = t1 - __shfl_sync(0xffffffffu, x.t0, 0);
                     two = __shfl_sync(0xffffffffu, (int)x.two, 0) != 0;
+                    units = __shfl_sync(0xffffffffu, stream_units(x, s), 0);
+                    left = __shfl_sync(0xffffffffu, stream_end(x, s) - x.t0 * kKeys, 0);
                     release(item);
                     j = two ? 0 : s;
                     step = two ? 1 : 2;
                     if (j > 0) pass(0);
                     if (!ok) return false;
-                    if (j < tiles) return true;
+                    if (units > 0) return true;
                     base += kPer * tiles;
                     queries += 1;
                 }
             };
-            // Scores of tile t (one elected lane).
-            auto scores = [&](int t) {
+            // Keys of tile t that the stream's rows see, in steps of 16 (one at least): products
+            // behind them are left out.
+            auto steps_of = [&](int t) { return max(1, min(kKeys / 16, (left - t * kKeys + 15) >> 4)); };
+            // Scores of tile t (one elected lane).  With two row tiles the softmax warps give K, V
+            // and the queries back, once they have seen the scores: a commit takes the issuer and
+            // the tensor pipe some 100 cycles.
+            auto scores = [&](int t, bool last_unit) {
                 const int b = (queries + (two ? s : 0)) % kQ;
+                const uint32_t id = id_qk - ((uint32_t)(kKeys - 16 * steps_of(t)) >> 3 << 17);   // N keys
                 const uint64_t ad = sdesc_kmajor_sw128(q_at + b * kQBytes);
 #pragma unroll
                 for (int part = 0; part < kHalves; ++part) {   // kV channels of K
@@ -478,14 +513,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kV / 16; ++k)
                         umma_bf16(tsu, ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
-                                  bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id_qk, part + k > 0 ? 1u : 0u);
+                                  bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id, part + k > 0 ? 1u : 0u);
                 }
                 umma_commit(&m.s_full[s]);
+                if (!two) {
 #pragma unroll
-                for (int part = 0; part < kHalves; ++part) umma_commit(&m.kv_free[(base + kPer * t + part) % kSlots]);
-                if (t + step >= tiles) {   // two arrivals free a row tile's queries: a stream's each, or one's both
-                    umma_commit(&m.q_free[b]);
-                    if (two || tiles == 1) umma_commit(&m.q_free[b]);
+                    for (int part = 0; part < kHalves; ++part) umma_commit(&m.kv_free[(base + kPer * t + part) % kSlots]);
+                    if (last_unit) {   // two arrivals free a row tile's queries: a stream's each, or one's both
+                        umma_commit(&m.q_free[b]);
+                        if (tiles == 1) umma_commit(&m.q_free[b]);
+                    }
                 }
             };
             auto first_scores = [&]() {
@@ -493,14 +530,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  keys_landed(j));
                 if (!ok) return;
                 tc_fence_after();
-                if (elect_one()) scores(j);
+                if (elect_one()) scores(j, units == 1);
                 __syncwarp();
             };
             bool more = enter(), begun = false;
             if (more) first_scores();
             while (more && ok) {
                 const int slot = (base + kPer * j + kHalves) % kSlots;
-                const bool last = j + step >= tiles;
+                const bool last = units == 1;
+                const int steps = steps_of(j);
                 // O still holds the rows of the item before until they are out
                 if (!begun && outs > 0) ok = wait_for(&m.o_free[s], (outs - 1) & 1, abort, limit);
                 // with two row tiles the next scores' keys before P is there; with one, memory is the
@@ -517,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 32; ++k)
-                        umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, k > 0 ? 1u : add);
+                        if (k < steps) umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, k > 0 ? 1u : add);
                 }
                 __syncwarp();
                 ok = __all_sync(0xffffffffu, wait_for(&m.p_ready[s], p_phase, abort, limit));
@@ -526,23 +564,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int k = kKeys / 32; k < kKeys / 16; ++k)
-                        umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, 1u);
-                    if (early) scores(j + step);   // commits behind the scores: V is free a product later
-                    umma_commit(&m.kv_free[slot]);
+                        if (k < steps) umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, 1u);
+                    if (early) scores(j + step, units == 2);
+                    if (!two || last) umma_commit(&m.kv_free[slot]);
                     if (last) umma_commit(&m.o_full[s]);
                 }
                 __syncwarp();
                 p_phase ^= 1;
                 begun = true;
                 if (!two && j + 1 < tiles) pass(j + 1);
+                if (two && last)
+                    for (int t = j + 1; t < tiles && ok; ++t) pass(t);   // tiles that this stream's rows do not see
                 if (!ok) break;
+                --units;
                 if (!last) {
                     j += step;
                     if (!early) {
                         ok = __all_sync(0xffffffffu, keys_landed(j));
                         if (!ok) break;
                         tc_fence_after();
-                        if (elect_one()) scores(j);
+                        if (elect_one()) scores(j, units == 1);
                         __syncwarp();
                     }
                 } else {
@@ -585,23 +626,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return reinterpret_cast<uint4*>(dst + (krow >> 3) * kGroupBytes + (c >> 3) * 1024 +
                                                         (krow & 7) * 128 + (c & 7) * 16);
                     };
-                    // rows behind what any row sees, and those that every row sees
+                    // rows behind what any row sees (in the last step of 16 keys alone: the products
+                    // leave the others out), and those that every row sees
                     const int past = max(0, min(x.end - base, kKeys)), seen = max(0, min(x.ctx + x.token0 + 1, x.end) - base);
-                    for (int e = past * kPieces + lane; e < kKeys * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-                    for (int e = seen * kPieces + lane; e < past * kPieces; e += 32) {
-                        const uint4 y = *piece(e);
-                        uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                        bool bad = false;
+                    const int upto = max(16, (past + 15) & ~15);
+                    for (int e = past * kPieces + lane; e < upto * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
+                    // is anything between not finite?  0 times such a value is NaN, and so is a sum with it
+                    bool bad = false;
+                    int e = seen * kPieces + lane;
+                    for (; e + 7 * 32 < past * kPieces; e += 8 * 32) {
+                        uint4 y[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((w[k] & kExp) == kExp) { bad = true; w[k] &= 0xffff0000u; }
-                            if (((w[k] >> 16) & kExp) == kExp) { bad = true; w[k] &= 0xffffu; }
-                        }
-                        if (bad) {
-                            const int j = base + e / kPieces - special * kKeys;
-                            atomicOr(&m.bad[item % kItems][j >> 5], 1u << (j & 31));
-                            *piece(e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int k = 0; k < 8; ++k) y[k] = *piece(e + 32 * k);
+                        bad |= !all_finite<T, 8>(y);
+                    }
+                    for (; e < past * kPieces; e += 32) {
+                        const uint4 y[1] = {*piece(e)};
+                        bad |= !all_finite<T, 1>(y);
+                    }
+                    if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                        for (e = seen * kPieces + lane; e < past * kPieces; e += 32) {
+                            const uint4 y = *piece(e);
+                            uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                            bad = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((w[k] & kExp) == kExp) { bad = true; w[k] &= 0xffff0000u; }
+                                if (((w[k] >> 16) & kExp) == kExp) { bad = true; w[k] &= 0xffffu; }
+                            }
+                            if (bad) {
+                                const int j = base + e / kPieces - special * kKeys;
+                                atomicOr(&m.bad[item % kItems][j >> 5], 1u << (j & 31));
+                                *piece(e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
                         }
                     }
                     fence_proxy_async_smem();
@@ -615,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- the rows' way out
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int in_token = (int)page_div((uint32_t)row, G, p.group_magic), in_head = row - in_token * G;
@@ -624,8 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         Item x;
         for (int item = 0; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
-            const int units = (x.two ? 2 : 1) * (x.t1 - x.t0);
-            const bool joined = !x.two && units > 1;
+            const bool joined = !x.two && x.t1 - x.t0 > 1;
             const int special = clean_from(x);
             const bool cleaned = x.t1 > special;   // (otherwise the flags are not this item's)
             // one row tile: one pass over both streams; two: a pass each
@@ -672,30 +729,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t to = tb + lane_base + kTmemO + 128 * s, to2 = tb + lane_base + kTmemO + 128 * s2;
 #pragma unroll 1
-                for (int k = 0; k < kV / 16; ++k) {
-                    float o[16];
+                for (int k = 0; k < kV / 32; ++k) {
+                    float o[32];
                     if (joined) {
-                        uint32_t r0[16], r1[16];
-                        float y[16];
-                        tmem_ld16_issue(to + 16 * k, r0);
-                        tmem_ld16_issue(to2 + 16 * k, r1);
-                        tmem_wait_ld();
-                        tmem_take16(r0, o);
-                        tmem_take16(r1, y);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : fmaf(y[e], f1, o[e] * f0);
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t r0[16], r1[16];
+                            float y[16];
+                            tmem_ld16_issue(to + 32 * k + 16 * i, r0);
+                            tmem_ld16_issue(to2 + 32 * k + 16 * i, r1);
+                            tmem_wait_ld();
+                            tmem_take16(r0, o + 16 * i);
+                            tmem_take16(r1, y);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[16 * i + e] = fmaf(y[e], f1, o[16 * i + e] * f0);
+                        }
                     } else {
-                        tmem_ld16(to + 16 * k, o);
+                        tmem_ld32(to + 32 * k, o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : o[e] * f0;
+                        for (int e = 0; e < 32; ++e) o[e] *= f0;
                     }
-                    if (k == kV / 16 - 1) {   // O is read: the next item's may come
+                    if (k == kV / 32 - 1) {   // O is read: the next item's may come
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&m.o_free[s]);
                             if (joined) mbar_arrive(&m.o_free[s2]);
                         }
+                    }
+                    if (empty) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
                     }
                     if (any_bad && live && !empty) {
                         const int from = max(special, x.t0) * kKeys, to_key = min(x.ctx + token + 1, min(x.end, x.t1 * kKeys));
@@ -705,27 +769,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int id = p.table[x.r * p.table_stride + pos / p.page];
                             if (id < 0 || id >= p.P) continue;
                             const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (pos % p.page) * p.vs[1] +
-                                           x.h * p.vs[2] + half * kV + 16 * k;
+                                           x.h * p.vs[2] + half * kV + 32 * k;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 32; ++e) {
                                 const float y = Elem<T>::one(src[e]);
                                 if (!isfinite(y)) o[e] += y;
                             }
                         }
                     }
                     if (live) {
-                        uint32_t w[8];
-                        if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = Elem<T>::pack(o[2 * e], o[2 * e + 1]);
-                            store32(dst + 16 * k, w, p.wide_out);
-                        } else {
+                        for (int i = 0; i < 32; i += 16) {
+                            uint32_t w[8];
+                            if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
-                            store32(pdst + 16 * k, w, true);
+                                for (int e = 0; e < 8; ++e) w[e] = Elem<T>::pack(o[i + 2 * e], o[i + 2 * e + 1]);
+                                store32(dst + 32 * k + i, w, p.wide_out);
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 + e]);
-                            store32(pdst + 16 * k + 8, w, true);
+                                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[i + e]);
+                                store32(pdst + 32 * k + i, w, true);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[i + 8 + e]);
+                                store32(pdst + 32 * k + i + 8, w, true);
+                            }
                         }
                     }
                 }
@@ -742,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
     } else {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         const int stream = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tb + lane_base + kTmemS + 128 * stream, to = tb + lane_base + kTmemO + 128 * stream;
@@ -750,24 +817,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int in_token = (int)page_div((uint32_t)row, G, p.group_magic);
         bool ok = true;
         uint32_t seen_s = 0, items_s = 0;   // score tiles taken, items with work for this stream
+        int ring = 0, queries = 0;          // ring and query tiles before the item
         for (int item = 0;; ++item) {
             Item x;
             if (!__all_sync(0xffffffffu, take(item, x, ok)) || !ok) break;
             release(item);
             const bool two = x.two;
-            const int units = (two ? 2 : 1) * (x.t1 - x.t0), u0 = stream;
-            if (u0 >= units) continue;
+            const int units = stream_units(x, stream), step = two ? 1 : 2;
+            const int ring_base = ring, b = (queries + stream) % kQ;   // (of two row tiles)
+            ring += kPer * (x.t1 - x.t0);
+            queries += two ? 2 : 1;
+            if (units == 0) continue;
             // keys that this row sees, and the warp's first row
-            const int token = x.ctx + x.token0 + (two && u0 ? tt : 0) + in_token;
+            const int token = x.ctx + x.token0 + (two && stream ? tt : 0) + in_token;
             const int sees = min(token + 1, x.end), least = __shfl_sync(0xffffffffu, sees, 0);
-            const int tile0 = x.t0;
+            const int tile0 = x.t0 + (two ? 0 : stream);
             float mx = -INFINITY, l = 0.f;
             if (p.timeout_probe && item == 0) ok = __all_sync(0xffffffffu, wait_for(&m.never, 0, abort, limit));
-            for (int u = u0; u < units && ok; u += 2) {
+            for (int u = 0; u < units && ok; ++u) {
                 ok = __all_sync(0xffffffffu, wait_for(&m.s_full[stream], seen_s & 1, abort, limit));
                 if (!ok) break;
                 ++seen_s;
                 tc_fence_after();
+                if (two && (warp & 3) == 0 && lane == 0) {
+                    // these scores are formed, and the stream's second product before them: this K and
+                    // that V are free, and with the last scores the row tile's queries
+                    const int at = ring_base + kPer * u;
+#pragma unroll
+                    for (int part = 0; part < kHalves; ++part) mbar_arrive(&m.kv_free[(at + part) % kSlots]);
+                    if (u > 0) mbar_arrive(&m.kv_free[(at - 1) % kSlots]);
+                    if (u == units - 1) {
+                        mbar_arrive(&m.q_free[b]);   // for both streams
+                        mbar_arrive(&m.q_free[b]);
+                    }
+                }
                 uint32_t raw[8][16];
                 float v[128];
 #pragma unroll
@@ -775,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) tmem_take16(raw[k], &v[16 * k]);
-                const int base = (tile0 + (two ? u >> 1 : u)) * kKeys;
+                const int base = (tile0 + u * step) * kKeys;
                 if (base + kKeys > least) {
                     const int n = sees - base;
 #pragma unroll
@@ -796,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mx = mn;
                     l *= alpha;
                 }
-                if (u > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
                     for (int k = 0; k < kV / 16; ++k) {
                         float o[16];
