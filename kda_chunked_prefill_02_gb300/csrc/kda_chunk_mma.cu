@@ -47,7 +47,7 @@
 // see such a position take its elements on their way out.
 //
 // Registers: 512 threads start with 128 each; the softmax warps take 168, the way out
-// keeps 72, the last four warps 104 (2 x 168 + 72 + 104 = 4 x 128).
+// keeps 80, the last four warps 96 (2 x 168 + 80 + 96 = 4 x 128).
 //
 // Every wait is bounded; one that runs out sets the abort flag, the roles fall through to
 // the end, and the status word reports KDA_ERR_TIMEOUT.  Whatever the others do, the loader
@@ -84,7 +84,7 @@ struct Item {
 struct Misc {
     uint64_t kv_full[kMaxSlots], kv_free[kMaxSlots], kv_raw[kMaxSlots];
     uint64_t q_full[kItems][2], q_free[kMaxQ];   // full: an item's row tiles
-    uint64_t s_full[2], p_half[2], p_ready[2], o_full[2], o_free[2], ml_full[2], ml_free[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], ml_full[2], ml_free[2];
     uint64_t item_full[kItems], item_free[kItems], drained[2], never;   // never: the probe's, nothing arrives on it
     float2 ml[2][128];          // the rows' maximum and sum, a stream each
     uint32_t bad[kItems][kBadWords];   // positions with a V element that is not finite
@@ -119,6 +119,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // Whether N pieces of 8 elements are finite: the sum of their products with 0 is 0 or NaN.
 template <typename T, int N>
 __device__ __forceinline__ bool all_finite(const uint4 (&y)[N]) {
@@ -172,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kMaxQ; ++i) mbar_init(&m.q_free[i], 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.s_full[s], 1);
-            mbar_init(&m.p_half[s], 4);     // one arrival a warp
-            mbar_init(&m.p_ready[s], 4);
+            mbar_init(&m.p_full[s][0], 4);     // the halves of P: one arrival a warp
+            mbar_init(&m.p_full[s][1], 4);
             mbar_init(&m.o_full[s], 1);
             mbar_init(&m.o_free[s], 4);
             mbar_init(&m.ml_full[s], 4);
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto clean_from = [&](const Item& x) -> int { return min(x.end, x.ctx + x.token0 + 1) / kKeys; };
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 12) {
             // ------------------------------------------------------------ work and loader
             if (lane == 0) {
@@ -231,44 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A request's length on the line: over its pairs of row tiles, the keys of each one's
             // last token (a last single row tile four fifths of them, as measured) and kItemKeys,
             // times the key heads.
-            struct Request {
-                int first, n, ctx, pairs;
-                bool ok, one;               // the last pair has one row tile
-                int64_t head;               // length of a key head's items
-            };
             const int pt = 2 * tt;          // tokens a pair
-            auto last_length = [&](const Request& q) -> int64_t {
-                const int64_t keys = (int64_t)q.ctx + q.n;
-                return kItemKeys + (q.one ? keys * 4 / 5 + 1 : keys);
-            };
             // where pair `rb` begins on a head's part of the line
-            auto pair_at = [&](const Request& q, int rb) -> int64_t {
-                return (int64_t)rb * (kItemKeys + q.ctx) + (int64_t)tt * rb * (rb + 1);
+            auto pair_at = [&](int ctx, int rb) -> int64_t {
+                return (int64_t)rb * (kItemKeys + ctx) + (int64_t)tt * rb * (rb + 1);
             };
-            auto look = [&](int r, Request& q) {
-                q.n = q.pairs = 0;
-                q.head = 0;
-                if (r >= p.R) return;
-                int len;
-                q.ok = chunk_request(p, r, q.first, q.n, len);
-                q.ctx = len > 0 ? len - q.n : 0;
-                if (q.n == 0) return;
-                q.pairs = (q.n + pt - 1) / pt;
-                q.one = q.n - (q.pairs - 1) * pt <= tt;
-                q.head = pair_at(q, q.pairs - 1) + last_length(q);
-            };
-            int64_t total = 0;
-            for (int r0 = 0; r0 < p.R; r0 += 32) {
-                Request q;
-                look(r0 + lane, q);
-                if (r0 + lane < p.R && !q.ok && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
-                total += q.head * p.Hk;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            // at least two key tiles a CTA
-            const int64_t most = total / (2 * kKeys);
-            const int room = (int)gridDim.x / kHalves, ctas = most < 1 ? 1 : most < room ? (int)most : room;
+            const int room = (int)gridDim.x / kHalves;
             int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
             const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
             int item = 0, issued = 0, queries = 0;   // items dealt, K and V tiles and query tiles asked for
@@ -312,13 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t* bar = &m.q_full[at][a];
                     q_asked |= bit;
                     q_phase = ((item - 1) / kItems) & 1 ? q_phase | bit : q_phase & ~bit;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar, (uint32_t)(G * tt) * 128u * (D / 64));
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_5d(sm + b * kQBytes + c * kBlock, &qmap, 0, x.h * G, x.first + x.token0 + a * tt, c,
-                                        p.cu ? 0 : x.r, bar);
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(G * tt) * 128u * (D / 64));
                     __syncwarp();
+                    if (lane < D / 64)
+                        tma_load_5d(sm + b * kQBytes + lane * kBlock, &qmap, 0, x.h * G, (p.cu ? x.first : 0) + x.token0 + a * tt, lane,
+                                    p.cu ? 0 : x.r, bar);
                     ++queries;
                 };
                 int64_t ahead = page_of(x.t0);
@@ -326,16 +297,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q_asked &= ~(2 << (2 * ((item - 1) % kItems)));
                     if (lane == 0) mbar_arrive(&m.q_full[(item - 1) % kItems][1]);
                 }
-                load_queries(0);
+#pragma unroll 1
                 for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
                     const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
                     if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
                     const int row = row_ahead;
                     ahead = page_of(tile + 1);
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * kV * 2u;
-                    for (int part = 0; part < kPer && ok; ++part) {   // K by kV channels, then V
+#pragma unroll 1
+                    for (int part = 0; part < kPer; ++part) {   // K by kV channels, then V
                         const bool v = part == kHalves;
-                        if (v && tile == x.t0 && x.two) load_queries(1);
+                        if (tile == x.t0 && (part == 0 || (v && x.two))) load_queries(v);   // a row tile's queries before each
                         const int slot = issued % kSlots, round = issued / kSlots;
                         if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.kv_free[slot], (round - 1) & 1, abort, limit));
                         if (!ok) break;
@@ -354,14 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            if (cta < ctas && total > 0) {
-                const int64_t begin = quotient(total * cta, ctas), end = quotient(total * (cta + 1), ctas);
+            // The requests, 32 at a time: once for the line's length, once for this CTA's stretch of it.
+            int64_t total = 0, begin = 0, end = 0;
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
                 int64_t before = 0;         // length of the requests before r0
-                bool over = false;
-                for (int r0 = 0; r0 < p.R && !over && ok; r0 += 32) {
-                    Request mine;
-                    look(r0 + lane, mine);
-                    int64_t upto = mine.head * p.Hk;
+#pragma unroll 1
+                for (int r0 = 0; r0 < p.R && ok; r0 += 32) {
+                    int first = 0, n = 0, ctx = 0, pairs = 0;
+                    bool fits = true;
+                    int64_t head = 0;       // length of a key head's items
+                    if (r0 + lane < p.R) {
+                        int len;
+                        fits = chunk_request(p, r0 + lane, first, n, len);
+                        ctx = fits ? len - n : 0;
+                        if (n > 0) {
+                            pairs = (n - 1) / pt + 1;
+                            const int64_t keys = (int64_t)ctx + n;
+                            head = pair_at(ctx, pairs - 1) + kItemKeys + (n - (pairs - 1) * pt <= tt ? keys * 4 / 5 + 1 : keys);
+                        }
+                    }
+                    int64_t upto = head * p.Hk;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -369,64 +354,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int64_t here = before;
                     before += __shfl_sync(0xffffffffu, upto, 31);
-                    if (before <= begin) continue;
+                    if (pass == 0) {
+                        if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
+                        total = before;
+                        continue;
+                    }
+                    if (here >= end) break;
                     // the requests of these that meet the stretch
-                    uint32_t meet = __ballot_sync(0xffffffffu, mine.n > 0 && here + upto > begin &&
-                                                                   here + upto - mine.head * p.Hk < end);
+                    uint32_t meet = __ballot_sync(0xffffffffu, n > 0 && here + upto > begin && here + upto - head * p.Hk < end);
+#pragma unroll 1
                     while (meet && ok) {
                         const int who = __ffs(meet) - 1;
                         meet &= meet - 1;
-                        Request q;
-                        q.first = __shfl_sync(0xffffffffu, mine.first, who);
-                        q.n = __shfl_sync(0xffffffffu, mine.n, who);
-                        q.ctx = __shfl_sync(0xffffffffu, mine.ctx, who);
-                        q.pairs = __shfl_sync(0xffffffffu, mine.pairs, who);
-                        q.ok = __shfl_sync(0xffffffffu, (int)mine.ok, who) != 0;
-                        q.one = __shfl_sync(0xffffffffu, (int)mine.one, who) != 0;
-                        q.head = __shfl_sync(0xffffffffu, mine.head, who);
-                        const int64_t start = here + __shfl_sync(0xffffffffu, upto, who) - q.head * p.Hk;
-                        // the head and the pair that hold the stretch's begin
+                        const int q_n = __shfl_sync(0xffffffffu, n, who), q_ctx = __shfl_sync(0xffffffffu, ctx, who),
+                                  q_pairs = __shfl_sync(0xffffffffu, pairs, who);
+                        const bool q_fits = __shfl_sync(0xffffffffu, (int)fits, who) != 0;
+                        const int64_t q_head = __shfl_sync(0xffffffffu, head, who);
+                        const int64_t start = here + __shfl_sync(0xffffffffu, upto, who) - q_head * p.Hk;
+                        x.r = r0 + who;
+                        x.first = __shfl_sync(0xffffffffu, first, who);
+                        x.ctx = q_ctx;
+                        // the head, and the pair, that hold the stretch's begin
                         int64_t off = begin > start ? begin - start : 0;
-                        x.h = (int)quotient(off, q.head);
-                        off -= x.h * q.head;
-                        int lo = 0, hi = q.pairs;
+                        int lo = 0, hi = p.Hk;
+#pragma unroll 1
                         while (hi - lo > 1) {
                             const int mid = (lo + hi) >> 1;
-                            if (pair_at(q, mid) <= off) lo = mid; else hi = mid;
+                            if (mid * q_head <= off) lo = mid; else hi = mid;
+                        }
+                        x.h = lo;
+                        off -= x.h * q_head;
+                        lo = 0;
+                        hi = q_pairs;
+#pragma unroll 1
+                        while (hi - lo > 1) {
+                            const int mid = (lo + hi) >> 1;
+                            if (pair_at(q_ctx, mid) <= off) lo = mid; else hi = mid;
                         }
                         int rb = lo;
-                        for (; x.h < p.Hk && ok; ++x.h, rb = 0) {
-                            for (; rb < q.pairs && ok; ++rb) {
-                                const bool last = rb == q.pairs - 1;
-                                const int64_t at = start + x.h * q.head + pair_at(q, rb);
-                                if (at >= end) break;
-                                x.r = r0 + who;
-                                x.token0 = rb * pt;
-                                x.tokens = last ? q.n - x.token0 : pt;
-                                x.ctx = q.ctx;
-                                x.first = p.cu ? q.first : 0;
-                                x.two = !(last && q.one);
-                                x.end = q.ok ? q.ctx + x.token0 + x.tokens : 0;
-                                const int tiles = max(1, (x.end + kKeys - 1) / kKeys);
-                                const int64_t length = last ? last_length(q) : kItemKeys + (int64_t)q.ctx + x.token0 + pt;
-                                // key tiles before a place on the line: none in the first kItemKeys, then evenly
-                                auto tiles_before = [&](int64_t place) -> int {
-                                    const int64_t in = place - at - kItemKeys, of = length - kItemKeys;
-                                    return in <= 0 ? 0 : in >= of ? tiles : (int)quotient(in * tiles + of - 1, of);
-                                };
-                                x.t0 = tiles_before(begin);
-                                x.t1 = tiles_before(end);
-                                x.whole = x.t0 == 0 && x.t1 == tiles;
-                                if (x.t1 > x.t0) {
-                                    if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, rb);
-                                    deal();
-                                    load();
-                                }
+#pragma unroll 1
+                        while (ok) {
+                            const int64_t at = start + x.h * q_head + pair_at(q_ctx, rb) + kItemKeys;   // where its keys begin
+                            if (at - kItemKeys >= end) break;
+                            x.token0 = rb * pt;
+                            x.tokens = min(q_n - x.token0, pt);
+                            x.two = x.tokens > tt;
+                            x.end = q_fits ? q_ctx + x.token0 + x.tokens : 0;
+                            const int tiles = max(1, (x.end + kKeys - 1) / kKeys);
+                            // key tiles before a place on the line: one in 128 (102.4) of the keys' part
+                            auto tiles_before = [&](int64_t place) -> int {
+                                const int64_t in = max((int64_t)0, place - at);
+                                return (int)min((int64_t)tiles, x.two ? (in + 127) >> 7 : (5 * in + 511) >> 9);
+                            };
+                            x.t0 = tiles_before(begin);
+                            const int64_t next = start + (rb + 1 < q_pairs ? x.h * q_head + pair_at(q_ctx, rb + 1) : (x.h + 1) * q_head);
+                            x.t1 = next <= end ? tiles : tiles_before(end);
+                            if (at - kItemKeys < begin && next <= begin) x.t0 = tiles;   // (an item before the stretch)
+                            x.whole = x.t0 == 0 && x.t1 == tiles;
+                            if (x.t1 > x.t0) {
+                                if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, rb);
+                                deal();
+                                load();
                             }
-                            if (start + (x.h + 1) * q.head >= end) break;
+                            if (++rb == q_pairs) {
+                                rb = 0;
+                                if (++x.h == p.Hk) break;
+                            }
                         }
                     }
-                    over = before >= end;
+                }
+                if (pass == 0) {
+                    // equal stretches, of at least two key tiles
+                    const int64_t most = total / (2 * kKeys);
+                    const int ctas = most < 1 ? 1 : most < room ? (int)most : room;
+                    if (cta >= ctas) break;
+                    int64_t each = 0, rest = total;   // a division in few instructions: it runs once
+#pragma unroll 1
+                    for (int bit = 46; bit >= 0; --bit)
+                        if (rest >> bit >= ctas) {
+                            rest -= (int64_t)ctas << bit;
+                            each += (int64_t)1 << bit;
+                        }
+                    begin = each * cta + min((int64_t)cta, rest);
+                    end = begin + each + (cta < rest ? 1 : 0);
                 }
             }
             x.t1 = -1;
@@ -438,8 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
             // the last copies into this CTA's memory
+#pragma unroll 1
             for (int i = 0; i < 2 * kItems; ++i)
                 if ((q_asked >> i) & 1) wait_for(&m.q_full[i >> 1][i & 1], (q_phase >> i) & 1, nullptr, kWaitLimitNs);
+#pragma unroll 1
             for (int i = max(0, issued - kSlots); i < issued; ++i)
                 if (!((raw >> (i % kSlots)) & 1)) wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, nullptr, kWaitLimitNs);
                 else wait_for(&m.kv_raw[i % kSlots], (raw_phases >> (i % kSlots)) & 1, nullptr, kWaitLimitNs);
@@ -500,101 +512,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Keys of tile t that the stream's rows see, in steps of 16 (one at least): products
             // behind them are left out.
             auto steps_of = [&](int t) { return max(1, min(kKeys / 16, (left - t * kKeys + 15) >> 4)); };
-            // Scores of tile t (one elected lane).  With two row tiles the softmax warps give K, V
-            // and the queries back, once they have seen the scores: a commit takes the issuer and
-            // the tensor pipe some 100 cycles.
-            auto scores = [&](int t, bool last_unit) {
+            auto scores = [&](int j, int units) {   // one elected lane
                 const int b = (queries + (two ? s : 0)) % kQ;
-                const uint32_t id = id_qk - ((uint32_t)(kKeys - 16 * steps_of(t)) >> 3 << 17);   // N keys
-                const uint64_t ad = sdesc_kmajor_sw128(q_at + b * kQBytes);
+                    const uint32_t id = id_qk - ((uint32_t)(kKeys - 16 * steps_of(j)) >> 3 << 17);   // N keys
+                    const uint64_t ad = sdesc_kmajor_sw128(q_at + b * kQBytes);
 #pragma unroll
-                for (int part = 0; part < kHalves; ++part) {   // kV channels of K
-                    const uint64_t bd = sdesc_keys(ring_at + (base + kPer * t + part) % kSlots * kSlotBytes, kGroupBytes);
+                    for (int part = 0; part < kHalves; ++part) {   // kV channels of K
+                        const uint64_t bd = sdesc_keys(ring_at + (base + kPer * j + part) % kSlots * kSlotBytes, kGroupBytes);
 #pragma unroll
-                    for (int k = 0; k < kV / 16; ++k)
-                        umma_bf16(tsu, ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
-                                  bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id, part + k > 0 ? 1u : 0u);
-                }
-                umma_commit(&m.s_full[s]);
-                if (!two) {
-#pragma unroll
-                    for (int part = 0; part < kHalves; ++part) umma_commit(&m.kv_free[(base + kPer * t + part) % kSlots]);
-                    if (last_unit) {   // two arrivals free a row tile's queries: a stream's each, or one's both
-                        umma_commit(&m.q_free[b]);
-                        if (tiles == 1) umma_commit(&m.q_free[b]);
+                        for (int k = 0; k < kV / 16; ++k)
+                            umma_bf16(tsu, ad + ((part * kV / 16 + k) >> 2) * (kBlock >> 4) + (k & 3) * 2,
+                                      bd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, id, part + k > 0 ? 1u : 0u);
                     }
-                }
+                    umma_commit(&m.s_full[s]);
+                    if (!two) {
+#pragma unroll 1
+                        for (int part = 0; part < kHalves; ++part) umma_commit(&m.kv_free[(base + kPer * j + part) % kSlots]);
+                        if (units == 1) {   // two arrivals free a row tile's queries: a stream's each, or one's both
+                            umma_commit(&m.q_free[b]);
+                            if (tiles == 1) umma_commit(&m.q_free[b]);
+                        }
+                    }
             };
-            auto first_scores = [&]() {
-                ok = __all_sync(0xffffffffu, ok && wait_for(&m.q_full[item % kItems][two ? s : 0], (item / kItems) & 1, abort, limit) &&
-                                                 keys_landed(j));
-                if (!ok) return;
-                tc_fence_after();
-                if (elect_one()) scores(j, units == 1);
-                __syncwarp();
-            };
-            bool more = enter(), begun = false;
-            if (more) first_scores();
+            // Every product's place in the code is one: what an item's change costs is fetching it.
+            bool more = enter(), begun = false, pending = false;
+#pragma unroll 1
             while (more && ok) {
-                const int slot = (base + kPer * j + kHalves) % kSlots;
-                const bool last = units == 1;
-                const int steps = steps_of(j);
-                // O still holds the rows of the item before until they are out
-                if (!begun && outs > 0) ok = wait_for(&m.o_free[s], (outs - 1) & 1, abort, limit);
-                // with two row tiles the next scores' keys before P is there; with one, memory is the
-                // bound, and waiting for a K would hold up the V before it
-                const bool early = two && !last;
-                ok = ok && landed(base + kPer * j + kHalves);
-                if (early) ok = ok && keys_landed(j + step);
-                const uint64_t bd = sdesc_mnmajor_sw128(ring_at + slot * kSlotBytes, 1024, kGroupBytes);
-                const uint32_t add = begun ? 1u : 0u;
-                // the two halves of P as they come
-                ok = __all_sync(0xffffffffu, ok && wait_for(&m.p_half[s], p_phase, abort, limit));
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
+                bool waited = false;   // for the next scores' keys
+                if (pending) {
+                    // the second product of tile j
+                    const int slot = (base + kPer * j + kHalves) % kSlots, steps = steps_of(j);
+                    const bool last = units == 1;
+                    // O still holds the rows of the item before until they are out
+                    if (!begun && outs > 0) ok = wait_for(&m.o_free[s], (outs - 1) & 1, abort, limit);
+                    ok = ok && landed(base + kPer * j + kHalves);
+                    // with two row tiles the next scores' keys before P is there; with one, memory is the
+                    // bound, and waiting for a K would hold up the V before it
+                    if (two && !last) {
+                        ok = ok && keys_landed(j + step);
+                        waited = true;
+                    }
+                    const uint64_t bd = sdesc_mnmajor_sw128(ring_at + slot * kSlotBytes, 1024, kGroupBytes);
 #pragma unroll
-                    for (int k = 0; k < kKeys / 32; ++k)
-                        if (k < steps) umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, k > 0 ? 1u : add);
-                }
-                __syncwarp();
-                ok = __all_sync(0xffffffffu, wait_for(&m.p_ready[s], p_phase, abort, limit));
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = kKeys / 32; k < kKeys / 16; ++k)
-                        if (k < steps) umma_bf16_ta(tou, tsu + 8 * k, bd + k * (kGroupBytes >> 3), id_pv, 1u);
-                    if (early) scores(j + step, units == 2);
-                    if (!two || last) umma_commit(&m.kv_free[slot]);
-                    if (last) umma_commit(&m.o_full[s]);
-                }
-                __syncwarp();
-                p_phase ^= 1;
-                begun = true;
-                if (!two && j + 1 < tiles) pass(j + 1);
-                if (two && last)
-                    for (int t = j + 1; t < tiles && ok; ++t) pass(t);   // tiles that this stream's rows do not see
-                if (!ok) break;
-                --units;
-                if (!last) {
-                    j += step;
-                    if (!early) {
-                        ok = __all_sync(0xffffffffu, keys_landed(j));
+                    for (int h = 0; h < 2; ++h) {   // the two halves of P as they come
+                        ok = __all_sync(0xffffffffu, ok && wait_for(&m.p_full[s][h], p_phase, abort, limit));
                         if (!ok) break;
                         tc_fence_after();
-                        if (elect_one()) scores(j, units == 1);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < kKeys / 32; ++k)
+                                if (4 * h + k < steps)
+                                    umma_bf16_ta(tou, tsu + 32 * h + 8 * k, bd + (4 * h + k) * (kGroupBytes >> 3), id_pv,
+                                                 begun || h + k > 0 ? 1u : 0u);
+                            if (h && waited) scores(j + step, units - 1);
+                            if (h && (!two || last)) umma_commit(&m.kv_free[slot]);
+                            if (h && last) umma_commit(&m.o_full[s]);
+                        }
                         __syncwarp();
                     }
-                } else {
-                    ++outs;
-                    begun = false;
-                    base += kPer * tiles;
-                    queries += two ? 2 : 1;
-                    ++item;
-                    more = enter();
-                    if (more) first_scores();
+                    if (!ok) break;
+                    p_phase ^= 1;
+                    begun = true;
+                    // tiles of the other stream, or that this stream's rows do not see
+                    if (!two || last) {
+#pragma unroll 1
+                        for (int t = j + 1; t < (two ? tiles : min(tiles, j + 2)) && ok; ++t) pass(t);
+                        if (!ok) break;
+                    }
+                    --units;
+                    j += step;
+                    if (last) {
+                        ++outs;
+                        begun = false;
+                        base += kPer * tiles;
+                        queries += two ? 2 : 1;
+                        ++item;
+                        more = enter();
+                        if (!more) break;
+                    }
                 }
+                // Scores of tile j: as many keys as its rows see.  With two row tiles the softmax warps
+                // give K, V and the queries back, once they have seen the scores: a commit takes the
+                // issuer and the tensor pipe some 100 cycles.
+                if (!waited) {
+                    if (!begun) ok = ok && wait_for(&m.q_full[item % kItems][two ? s : 0], (item / kItems) & 1, abort, limit);
+                    ok = __all_sync(0xffffffffu, ok && keys_landed(j));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (!waited) {
+                    if (elect_one()) scores(j, units);
+                    __syncwarp();
+                }
+                pending = true;
             }
             if (!ok && lane == 0) fail();
             if (elect_one()) umma_commit(&m.drained[s]);
@@ -630,19 +640,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // leave the others out), and those that every row sees
                     const int past = max(0, min(x.end - base, kKeys)), seen = max(0, min(x.ctx + x.token0 + 1, x.end) - base);
                     const int upto = max(16, (past + 15) & ~15);
+#pragma unroll 1
                     for (int e = past * kPieces + lane; e < upto * kPieces; e += 32) *piece(e) = make_uint4(0, 0, 0, 0);
                     // is anything between not finite?  0 times such a value is NaN, and so is a sum with it
                     bool bad = false;
                     int e = seen * kPieces + lane;
-                    for (; e + 7 * 32 < past * kPieces; e += 8 * 32) {
+#pragma unroll 1
+                    for (; e < past * kPieces; e += 8 * 32) {
                         uint4 y[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = *piece(e + 32 * k);
+                        for (int k = 0; k < 8; ++k) y[k] = e + 32 * k < past * kPieces ? *piece(e + 32 * k) : make_uint4(0, 0, 0, 0);
                         bad |= !all_finite<T, 8>(y);
-                    }
-                    for (; e < past * kPieces; e += 32) {
-                        const uint4 y[1] = {*piece(e)};
-                        bad |= !all_finite<T, 1>(y);
                     }
                     if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll 1
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- the rows' way out
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int in_token = (int)page_div((uint32_t)row, G, p.group_magic), in_head = row - in_token * G;
@@ -728,71 +736,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int w = 0; w < kBadWords; ++w) any_bad |= m.bad[item % kItems][w];
                 }
                 const uint32_t to = tb + lane_base + kTmemO + 128 * s, to2 = tb + lane_base + kTmemO + 128 * s2;
-#pragma unroll 1
-                for (int k = 0; k < kV / 32; ++k) {
-                    float o[32];
-                    if (joined) {
+                auto out16 = [&](int k, const float* o) {   // columns 16 k ..
+                    uint32_t w[8];
+                    if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t r0[16], r1[16];
-                            float y[16];
-                            tmem_ld16_issue(to + 32 * k + 16 * i, r0);
-                            tmem_ld16_issue(to2 + 32 * k + 16 * i, r1);
-                            tmem_wait_ld();
-                            tmem_take16(r0, o + 16 * i);
-                            tmem_take16(r1, y);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[16 * i + e] = fmaf(y[e], f1, o[16 * i + e] * f0);
-                        }
+                        for (int e = 0; e < 8; ++e) w[e] = Elem<T>::pack(o[2 * e], o[2 * e + 1]);
+                        store32(dst + 16 * k, w, p.wide_out);
                     } else {
-                        tmem_ld32(to + 32 * k, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f0;
+                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
+                        store32(pdst + 16 * k, w, true);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 + e]);
+                        store32(pdst + 16 * k + 8, w, true);
                     }
-                    if (k == kV / 32 - 1) {   // O is read: the next item's may come
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&m.o_free[s]);
-                            if (joined) mbar_arrive(&m.o_free[s2]);
-                        }
+                };
+                auto o_read = [&]() {   // the next item's O may come
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&m.o_free[s]);
+                        if (joined) mbar_arrive(&m.o_free[s2]);
                     }
-                    if (empty) {
+                };
+                if (!joined) {
+#pragma unroll 1
+                    for (int k = 0; k < kV / 16; k += 2) {   // 32 columns on one wait
+                        uint32_t r[2][16];
+                        float o[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        for (int i = 0; i < 2; ++i) tmem_ld16_issue(to + 16 * (k + i), r[i]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) tmem_take16(r[i], o + 16 * i);
+                        if (k == kV / 16 - 2) o_read();
+                        if (!live) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = empty ? 0.f : o[e] * f0;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) out16(k + i, o + 16 * i);
                     }
-                    if (any_bad && live && !empty) {
-                        const int from = max(special, x.t0) * kKeys, to_key = min(x.ctx + token + 1, min(x.end, x.t1 * kKeys));
-                        for (int pos = from; pos < to_key; ++pos) {
-                            const int j = pos - special * kKeys;
-                            if (!((m.bad[item % kItems][j >> 5] >> (j & 31)) & 1u)) continue;
-                            const int id = p.table[x.r * p.table_stride + pos / p.page];
-                            if (id < 0 || id >= p.P) continue;
-                            const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (pos % p.page) * p.vs[1] +
-                                           x.h * p.vs[2] + half * kV + 32 * k;
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < kV / 16; ++k) {
+                        uint32_t r0[16], r1[16];
+                        float o[16], y[16];
+                        tmem_ld16_issue(to + 16 * k, r0);
+                        tmem_ld16_issue(to2 + 16 * k, r1);
+                        tmem_wait_ld();
+                        tmem_take16(r0, o);
+                        tmem_take16(r1, y);
+                        if (k == kV / 16 - 1) o_read();
+                        if (!live) continue;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float y = Elem<T>::one(src[e]);
-                                if (!isfinite(y)) o[e] += y;
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : fmaf(y[e], f1, o[e] * f0);
+                        out16(k, o);
                     }
-                    if (live) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 16) {
-                            uint32_t w[8];
-                            if (whole) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) w[e] = Elem<T>::pack(o[i + 2 * e], o[i + 2 * e + 1]);
-                                store32(dst + 32 * k + i, w, p.wide_out);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[i + e]);
-                                store32(pdst + 32 * k + i, w, true);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[i + 8 + e]);
-                                store32(pdst + 32 * k + i + 8, w, true);
-                            }
+                }
+                if (any_bad && live && !empty) {   // elements of V that are not finite, to the rows that see them
+                    const int to_key = min(x.ctx + token + 1, min(x.end, x.t1 * kKeys));
+#pragma unroll 1
+                    for (int pos = max(special, x.t0) * kKeys; pos < to_key; ++pos) {
+                        const int j = pos - special * kKeys;
+                        if (!((m.bad[item % kItems][j >> 5] >> (j & 31)) & 1u)) continue;
+                        const int id = p.table[x.r * p.table_stride + pos / p.page];
+                        if (id < 0 || id >= p.P) continue;
+                        const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (pos % p.page) * p.vs[1] + x.h * p.vs[2] + half * kV;
+#pragma unroll 1
+                        for (int e = 0; e < kV; ++e) {
+                            const float y = Elem<T>::one(src[e]);
+                            if (isfinite(y)) continue;
+                            if (whole) dst[e] = static_cast<T>(Elem<T>::one(dst[e]) + y);
+                            else pdst[e] += y;
                         }
                     }
                 }
@@ -828,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ring += kPer * (x.t1 - x.t0);
             queries += two ? 2 : 1;
             if (units == 0) continue;
-            // keys that this row sees, and the warp's first row
+            // keys that this row sees, and the warp's first
             const int token = x.ctx + x.token0 + (two && stream ? tt : 0) + in_token;
             const int sees = min(token + 1, x.end), least = __shfl_sync(0xffffffffu, sees, 0);
             const int tile0 = x.t0 + (two ? 0 : stream);
@@ -860,18 +875,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 8; ++k) tmem_take16(raw[k], &v[16 * k]);
                 const int base = (tile0 + u * step) * kKeys;
                 if (base + kKeys > least) {
-                    const int n = sees - base;
+                    const int n = sees - base, n_all = least - base;   // what this row sees, and all of the warp's
 #pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e >= n) v[e] = -INFINITY;
+                    for (int g = 0; g < 4; ++g) {
+                        if (32 * g + 32 <= n_all) continue;
+#pragma unroll
+                        for (int e = 32 * g; e < 32 * g + 32; ++e)
+                            if (e >= n) v[e] = -INFINITY;
+                    }
                 }
                 float t8[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t8[e] = v[e];
+                for (int e = 0; e < 8; ++e) t8[e] = max3(v[e], v[8 + e], v[16 + e]);
 #pragma unroll
-                for (int e = 8; e < 128; ++e) t8[e & 7] = fmaxf(t8[e & 7], v[e]);
-                const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])),
-                                        fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+                for (int e = 24; e < 120; e += 16)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t8[i] = max3(t8[i], v[e + i], v[e + 8 + i]);
+                const float top = fmaxf(max3(max3(t8[0], t8[1], v[120]), max3(t8[2], t8[3], v[121]), max3(t8[4], t8[5], v[122])),
+                                        max3(max3(t8[6], t8[7], v[123]), max3(v[124], v[125], v[126]), v[127]));
                 float alpha = 1.f;
                 if (top > mx + lazy || mx == -INFINITY) {
                     const float mn = fmaxf(mx, kShift<T> == 0.f ? top : fmaf(lazy, -kShift<T> / kLazy<T>, top));
@@ -908,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&m.p_half[stream]);
+                        if (lane == 0) mbar_arrive(&m.p_full[stream][0]);
                     }
                 }
                 const float2 q = f2_parts(f2_add(sum[0], sum[1]));
@@ -916,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&m.p_ready[stream]);
+                if (lane == 0) mbar_arrive(&m.p_full[stream][1]);
             }
             // the rows' maximum and sum, once those of the stream's item before have been taken
             if (items_s > 0) ok = ok && wait_for(&m.ml_free[stream], (items_s - 1) & 1, abort, limit);
