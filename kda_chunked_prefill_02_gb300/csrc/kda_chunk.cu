@@ -417,98 +417,92 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
 // Joins the parts of an item that kda_chunk_mma.cu has cut: out = sum_c 2^(lse_c - M) o_c /
 // sum_c 2^(lse_c - M) over the CTAs c that hold one, in their order: slot 1 of CTA
 // blockIdx.x, then slot 0 of those behind it up to the item's last part.  A row is the work
-// of one warp that takes part after part, or of W > 1 warps, of every W-th part each (the
-// order of the sums is fixed all the same).
+// of one warp that takes part after part, or of the block's 8 warps, of every 8th part each
+// (the order of the sums is fixed all the same).  A block takes rows blockIdx.y (times 8, with
+// a warp a row), and so on: with a block for every 8 rows of a pair the kernel took 6 us where
+// nothing was cut.
 template <typename T, int D, int W>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p) {
     constexpr int kVec = D / 32;
     __shared__ float sy[W > 1 ? 8 : 1][W > 1 ? D : 1], ssum[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = blockIdx.y * (8 / W) + warp / W;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cta = blockIdx.x, ctas = p.ctas;
     const int4 item = p.parts[2 * cta + 1];   // state, request, key head, pair of row tiles
-    if (item.x == 0 || in >= 256) return;     // all of a row's warps
+    if (item.x == 0) return;
     int first, n, len;
     chunk_request(p, item.y, first, n, len);
-    const int tile = in >> 7, row = in & 127, in_token = (int)page_div((uint32_t)row, p.G, p.group_magic);
-    const int token = (2 * item.w + tile) * p.tile_tokens + in_token;
-    if (in_token >= p.tile_tokens || token >= n) return;
-    const auto part = [&](int k) { return (int64_t)(k ? 2 * (cta + k) : 2 * cta + 1) * 256 + in; };
-    float mx = -INFINITY, sum = 0.f, y[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) y[i] = 0.f;
-    if (W == 1) {
-        for (int k = 0, state = item.x;;) {
-            const float lse = p.part_lse[part(k)];
-            const float* src = p.part_o + part(k) * D + lane * kVec;
-            float o[kVec];
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) o[i] = src[i];
-            const float mn = fmaxf(mx, lse), mu = mn == -INFINITY ? 0.f : mn;
-            const float fo = ex2_approx(mx - mu), fn = ex2_approx(lse - mu);
-            sum = sum * fo + fn;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) y[i] = y[i] * fo + o[i] * fn;
-            mx = mn;
-            if (state == 2 || cta + ++k >= ctas) break;
-            state = p.parts[2 * (cta + k)].x;
-            if (state == 0) break;
+    int count = 1;   // parts, from their states, 32 at a time
+    for (int c = cta + 1;; c += 32) {
+        const int state = c + lane < ctas ? p.parts[2 * (c + lane)].x : 0;
+        const uint32_t stop = __ballot_sync(0xffffffffu, state != 1);
+        const int k = stop ? __ffs(stop) - 1 : 32;
+        count += k;
+        if (stop) {
+            if (__shfl_sync(0xffffffffu, state, k) == 2) ++count;
+            break;
         }
-    } else {
-        int count = 1;   // parts, from their states, 32 at a time
-        for (int c = cta + 1;; c += 32) {
-            const int state = c + lane < ctas ? p.parts[2 * (c + lane)].x : 0;
-            const uint32_t stop = __ballot_sync(0xffffffffu, state != 1);
-            const int k = stop ? __ffs(stop) - 1 : 32;
-            count += k;
-            if (stop) {
-                if (__shfl_sync(0xffffffffu, state, k) == 2) ++count;
-                break;
-            }
-        }
+    }
+    for (int in = (int)blockIdx.y * (8 / W) + warp / W; in < 256; in += (int)gridDim.y * (8 / W)) {
+        const int row = in & 127, in_token = (int)page_div((uint32_t)row, p.G, p.group_magic);
+        const int token = (2 * item.w + (in >> 7)) * p.tile_tokens + in_token;
+        if (in_token >= p.tile_tokens || token >= n) continue;   // all of a row's warps
+        const auto part = [&](int k) { return (int64_t)(k ? 2 * (cta + k) : 2 * cta + 1) * 256 + in; };
+        float mx = -INFINITY, sum = 0.f, y[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) y[i] = 0.f;
         for (int k = lane; k < count; k += 32) mx = fmaxf(mx, p.part_lse[part(k)]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const float mu = mx == -INFINITY ? 0.f : mx;
 #pragma unroll 4
-        for (int k = warp % W; k < count; k += W) {
+        for (int k = W > 1 ? warp : 0; k < count; k += W) {
             const float f = ex2_approx(p.part_lse[part(k)] - mu);
             const float* src = p.part_o + part(k) * D + lane * kVec;
             sum += f;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) y[i] = fmaf(src[i], f, y[i]);
         }
-        if (lane == 0) ssum[warp] = sum;
+        if (W > 1) {
+            __syncthreads();   // the row before has been read
+            if (lane == 0) ssum[warp] = sum;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sy[warp][lane * kVec + i] = y[i];
-        named_bar_sync(1 + warp / W, 32 * W);
-        if (warp % W > 0) return;
-        sum = 0.f;
+            for (int i = 0; i < kVec; ++i) sy[warp][lane * kVec + i] = y[i];
+            __syncthreads();
+            if (warp > 0) continue;
+            sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) y[i] = 0.f;
+            for (int i = 0; i < kVec; ++i) y[i] = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            sum += ssum[warp + w];
+            for (int w = 0; w < W; ++w) {
+                sum += ssum[w];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) y[i] += sy[warp + w][lane * kVec + i];
+                for (int i = 0; i < kVec; ++i) y[i] += sy[w][lane * kVec + i];
+            }
         }
-    }
-    const int h = item.z * p.G + (row - in_token * p.G);
-    const bool empty = sum == 0.f;
-    const float inv = empty ? 0.f : 1.f / sum;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(
-        static_cast<T*>(p.out) + (p.cu ? (int64_t)(first + token) * p.os[1] : item.y * p.os[0] + token * p.os[1]) +
-        h * p.os[2] + lane * kVec);
+        const int h = item.z * p.G + (row - in_token * p.G);
+        const bool empty = sum == 0.f;
+        const float inv = empty ? 0.f : 1.f / sum;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+            static_cast<T*>(p.out) + (p.cu ? (int64_t)(first + token) * p.os[1] : item.y * p.os[0] + token * p.os[1]) +
+            h * p.os[2] + lane * kVec);
 #pragma unroll
-    for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[((p.cu ? (int64_t)first : (int64_t)item.y * p.T) + token) * p.Hq + h] =
-            empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+        for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[((p.cu ? (int64_t)first : (int64_t)item.y * p.T) + token) * p.Hq + h] =
+                empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+    }
+}
+
+// Pairs of row tiles of all requests, at most.
+int64_t row_pairs(int R, int T, bool packed, int G) {
+    const int tt = 128 / G, pt = 2 * tt;
+    return packed ? (int64_t)T / pt + R : (int64_t)R * ((T + pt - 1) / pt);
 }
 
 template <typename T, int W>
 cudaError_t launch_join_w(const ChunkParams& p, int D, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.ctas - 1), (unsigned)(256 * W / 8));
+    const dim3 grid((unsigned)(p.ctas - 1), 16);
     const auto kernel = D == 64 ? chunk_join_kernel<T, 64, W>
                                 : D == 128 ? chunk_join_kernel<T, 128, W> : chunk_join_kernel<T, 256, W>;
     return launch_maybe_pdl(kernel, grid, dim3(256), 0, s, true, p);
@@ -516,7 +510,9 @@ cudaError_t launch_join_w(const ChunkParams& p, int D, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_join(const ChunkParams& p, int D, cudaStream_t s) {
     if (p.ctas <= 1) return cudaSuccess;   // one CTA cuts nothing
-    return launch_join_w<T, 1>(p, D, s);
+    // Eight warps a row where the rows are few and are cut into many parts.
+    const bool wide = (int64_t)p.T * p.G <= 64 && p.ctas >= 8 * row_pairs(p.R, p.T, p.cu != nullptr, p.G) * p.Hk;
+    return wide ? launch_join_w<T, 8>(p, D, s) : launch_join_w<T, 1>(p, D, s);
 }
 
 int rows_per_block(int64_t rows, int D) { return rows <= 16 || D > 128 ? 16 : 32; }
@@ -587,6 +583,21 @@ ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t ma
     int64_t parts = blocks > 0 ? at_once / blocks : 1;
     if (parts > (tiles + 1) / 2) parts = (tiles + 1) / 2;
     t.cluster = parts >= 8 ? 8 : parts >= 4 ? 4 : parts >= 2 ? 2 : 1;
+    if (t.mma) {
+        // The kernel for few rows where its estimated time (us) is the shorter one by a margin, since
+        // ragged contexts are the other's strength: a 64-key tile a CTA and wave against the
+        // tensor-core kernel's 17 us of set-up and join and its stretch of the line of work, in
+        // 128-key tiles.  Head size 128: 1 request, 2 key heads, 1 token over 250 keys 6.9 us
+        // against 13.8, over 4000 13.4 and 17.3, over 16000 35.7 and 20.8; 256 tokens, 8 key heads
+        // over 250 19 and 25, over 1000 37 and 29; 16 requests x 1 token, 8 key heads over up to
+        // 1000 18 and 23, over 4000 53 and 41.
+        const double waves = (double)((blocks * t.cluster + at_once - 1) / at_once);
+        const double rows_us = 4.0 + waves * ((tiles + t.cluster - 1) / t.cluster) * (D == 64 ? 0.9 : D == 128 ? 1.15 : 2.2);
+        const double keys = (double)row_pairs(R, T, packed, G) * Hk * (0.8 * max_len + 256.0) / t.stretches;
+        const double mma_us = 17.0 + keys / 128 * (D == 64 ? 1.15 : D == 128 ? 1.4 : 2.1);
+        t.mma = mma_us < 1.25 * rows_us;
+        if (!t.mma) t.stretches = 0;
+    }
     return t;
 }
 

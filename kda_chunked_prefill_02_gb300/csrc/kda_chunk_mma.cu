@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // chunk_join_kernel waits for this grid's end itself
     const uint32_t tb = m.tmem;
     // The k-th item of this CTA; false after the last (or on an abort).
     auto take = [&](int k, Item& x, bool& ok) -> bool {

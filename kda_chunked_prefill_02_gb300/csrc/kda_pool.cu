@@ -52,17 +52,21 @@ __global__ void __launch_bounds__(kPoolThreads) pool_copy_kernel(const __grid_co
 
 constexpr int kPathMax = 256;
 
-// A CTA takes a request's path in one cache (or a split of the rows' pieces).  The path
-// ascends, so path[j] >= j: in the order of j no row is written before it has been read,
-// and a batch of pieces in that order can be read as a whole before it is written.
+// A CTA takes a request's path in `group` caches (or a split of the rows' pieces).  The path
+// ascends, so path[j] >= j: in the order of j no row is written before it has been read, and a
+// batch of pieces in that order can be read as a whole before it is written.  The pieces of
+// all of the CTA's caches, which have rows of the same size then, are one sequence: finding the
+// rows' places is a chain of four loads, which a CTA a cache paid each time (256 requests, 32
+// caches, rows of 2 KB: XXX us, 49 with a CTA a cache).
 __global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
     __shared__ int2 s_from[kPathMax], s_to[kPathMax];   // page (< 0: none) and row of a moved node and of its new place
     __shared__ int s_first;
-    const PoolDesc& d = p.pool[blockIdx.z];
+    const int k0 = blockIdx.z * p.group, caches = min(p.group, p.pools - k0);
+    const PoolDesc& d0 = p.pool[k0];
     const int r = blockIdx.y, tid = threadIdx.x;
     const int ctx = p.ctx[r], n = p.accepted[r];
     const int32_t* path = p.path + (int64_t)r * p.max_path;
-    const bool report = p.status && blockIdx.x == 0 && blockIdx.z == 0;
+    const bool report = p.status && blockIdx.x == 0;
     if (ctx < 0 || n < 0 || n > p.max_path) {
         if (report && tid == 0) atomicExch(p.status, 1);
         return;
@@ -76,10 +80,7 @@ __global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid
         if (ok && node != tid) {
             const auto place = [&](int at) {
                 const int pg = (int)page_div((uint32_t)at, p.page, p.page_magic);
-                const int id = p.table[r * p.table_stride + pg];
-                const bool in = id >= 0 && id < d.entries;
-                if (!in && report) atomicExch(p.status, 1);
-                return make_int2(in ? id : -1, at - pg * p.page);
+                return make_int2(p.table[r * p.table_stride + pg], at - pg * p.page);
             };
             s_from[tid] = place(ctx + node);
             s_to[tid] = place(ctx + tid);
@@ -91,10 +92,11 @@ __global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid
         return;
     }
     // path[j] = j up to s_first, and never again behind it
-    const uint32_t row_pieces = (uint32_t)(d.cols * d.pieces);
+    const int first = s_first;
+    const uint32_t row_pieces = (uint32_t)(d0.cols * d0.pieces);
     const uint32_t c0 = (uint32_t)((uint64_t)row_pieces * blockIdx.x / gridDim.x),
                    width = (uint32_t)((uint64_t)row_pieces * (blockIdx.x + 1) / gridDim.x) - c0;
-    const uint32_t total = (uint32_t)(n - s_first) * width;
+    const uint32_t each = (uint32_t)(n - first) * width, total = each * (uint32_t)caches;
     for (uint32_t base = tid; base - tid < total; base += kSlicePieces) {
         uint4 v[kBatch];
         char* to[kBatch];
@@ -103,13 +105,16 @@ __global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid
             const uint32_t e = base + k * kPoolThreads;
             to[k] = nullptr;
             if (e < total) {
-                const uint32_t j = e / width, c = c0 + (e - j * width);
-                const int2 a = s_from[s_first + j], b = s_to[s_first + j];
-                const uint32_t col = page_div(c, (uint32_t)d.pieces, d.piece_magic), piece = c - col * (uint32_t)d.pieces;
+                const uint32_t cache = e / each, in = e - cache * each, j = in / width, c = c0 + (in - j * width);
+                const PoolDesc& d = p.pool[k0 + cache];
+                const int2 a = s_from[first + j], b = s_to[first + j];
+                const uint32_t col = page_div(c, (uint32_t)d0.pieces, d0.piece_magic), piece = c - col * (uint32_t)d0.pieces;
                 const int64_t in_row = col * d.st[2] + (int64_t)piece * 16;
-                if (a.x >= 0 && b.x >= 0) {
+                if (a.x >= 0 && a.x < d.entries && b.x >= 0 && b.x < d.entries) {
                     v[k] = *reinterpret_cast<const uint4*>(d.data + a.x * d.st[0] + a.y * d.st[1] + in_row);
                     to[k] = d.data + b.x * d.st[0] + b.y * d.st[1] + in_row;
+                } else if (p.status) {
+                    atomicExch(p.status, 1);
                 }
             }
         }
@@ -136,18 +141,24 @@ cudaError_t launch_pool_copy(const PoolCopyParams& q, int num_sms, cudaStream_t 
 }
 
 cudaError_t launch_cache_commit(const CacheCommitParams& q, int num_sms, cudaStream_t s) {
-    // Rows are cut where the (request, cache) pairs are fewer than two CTAs an SM, at least 8
-    // pieces (128 bytes) a CTA.
-    int least = 1 << 30;
-    for (int k = 0; k < q.pools; ++k) {
-        const int n = q.pool[k].cols * q.pool[k].pieces;
-        least = n < least ? n : least;
+    CacheCommitParams p = q;
+    const auto row = [&](int k) { return p.pool[k].cols * p.pool[k].pieces; };
+    int least = row(0);
+    bool same = true;   // rows of one size in every cache (a layout of their own each)
+    for (int k = 1; k < p.pools; ++k) {
+        same = same && p.pool[k].cols == p.pool[0].cols && p.pool[k].pieces == p.pool[0].pieces;
+        least = row(k) < least ? row(k) : least;
     }
-    int64_t splits = 2 * num_sms / ((int64_t)q.R * q.pools);
+    // Some 8 CTAs an SM: so many caches a CTA, or where the (request, cache) pairs are fewer than
+    // two CTAs an SM the rows are cut, at least 8 pieces (128 bytes) a CTA.
+    const int64_t pairs = (int64_t)p.R * p.pools;
+    p.group = same ? (int)((pairs + 8 * num_sms - 1) / (8 * num_sms)) : 1;
+    if (p.group > p.pools) p.group = p.pools;
+    int64_t splits = 2 * num_sms / pairs;
     if (splits > least / 8) splits = least / 8;
     if (splits < 1) splits = 1;
-    const dim3 grid((unsigned)splits, (unsigned)q.R, (unsigned)q.pools);
-    cache_commit_kernel<<<grid, kPoolThreads, 0, s>>>(q);
+    const dim3 grid((unsigned)splits, (unsigned)p.R, (unsigned)((p.pools + p.group - 1) / p.group));
+    cache_commit_kernel<<<grid, kPoolThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -196,7 +196,8 @@ struct CacheCommitParams {
     const int32_t *table, *ctx, *path, *accepted;
     int32_t* status;
     int64_t table_stride, room;      // room: tokens a page row holds
-    int R, max_path, page, pools, splits;
+    int R, max_path, page, pools;
+    int group;                       // caches a CTA takes (set by the launcher)
     uint32_t page_magic;
 };
 cudaError_t launch_cache_commit(const CacheCommitParams& p, int num_sms, cudaStream_t s);
