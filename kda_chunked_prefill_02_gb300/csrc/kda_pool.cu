@@ -51,16 +51,18 @@ __global__ void __launch_bounds__(kPoolThreads) pool_copy_kernel(const __grid_co
 }
 
 constexpr int kPathMax = 256;
+constexpr int kCommitBatch = 4;   // as kBatch: with 8, and the registers for them, 32 us in the case below
 
 // A CTA takes a request's path in `group` caches (or a split of the rows' pieces).  The path
 // ascends, so path[j] >= j: in the order of j no row is written before it has been read, and a
 // batch of pieces in that order can be read as a whole before it is written.  The pieces of
 // all of the CTA's caches, which have rows of the same size then, are one sequence: finding the
 // rows' places is a chain of four loads, which a CTA a cache paid each time (256 requests, 32
-// caches, rows of 2 KB: XXX us, 49 with a CTA a cache).
-__global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
+// caches, rows of 2 KB: 27 us, 49 with a CTA a cache).
+__global__ void __launch_bounds__(kPoolThreads, 6) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
     __shared__ int2 s_from[kPathMax], s_to[kPathMax];   // page (< 0: none) and row of a moved node and of its new place
     __shared__ int s_first;
+    __shared__ uint32_t s_magic[2];   // of the two divisions of a piece's number
     const int k0 = blockIdx.z * p.group, caches = min(p.group, p.pools - k0);
     const PoolDesc& d0 = p.pool[k0];
     const int r = blockIdx.y, tid = threadIdx.x;
@@ -93,19 +95,27 @@ __global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid
     }
     // path[j] = j up to s_first, and never again behind it
     const int first = s_first;
+    if (first == n) return;   // nothing moves
     const uint32_t row_pieces = (uint32_t)(d0.cols * d0.pieces);
     const uint32_t c0 = (uint32_t)((uint64_t)row_pieces * blockIdx.x / gridDim.x),
                    width = (uint32_t)((uint64_t)row_pieces * (blockIdx.x + 1) / gridDim.x) - c0;
     const uint32_t each = (uint32_t)(n - first) * width, total = each * (uint32_t)caches;
-    for (uint32_t base = tid; base - tid < total; base += kSlicePieces) {
-        uint4 v[kBatch];
-        char* to[kBatch];
+    if (tid < 2) {
+        const uint32_t d = tid ? width : each;
+        s_magic[tid] = d == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / d);
+    }
+    __syncthreads();
+    const uint32_t each_magic = s_magic[0], width_magic = s_magic[1];
+    for (uint32_t base = tid; base - tid < total; base += kCommitBatch * kPoolThreads) {
+        uint4 v[kCommitBatch];
+        char* to[kCommitBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kCommitBatch; ++k) {
             const uint32_t e = base + k * kPoolThreads;
             to[k] = nullptr;
             if (e < total) {
-                const uint32_t cache = e / each, in = e - cache * each, j = in / width, c = c0 + (in - j * width);
+                const uint32_t cache = page_div(e, each, each_magic), in = e - cache * each;
+                const uint32_t j = page_div(in, width, width_magic), c = c0 + (in - j * width);
                 const PoolDesc& d = p.pool[k0 + cache];
                 const int2 a = s_from[first + j], b = s_to[first + j];
                 const uint32_t col = page_div(c, (uint32_t)d0.pieces, d0.piece_magic), piece = c - col * (uint32_t)d0.pieces;
@@ -120,7 +130,7 @@ __global__ void __launch_bounds__(kPoolThreads) cache_commit_kernel(const __grid
         }
         __syncthreads();   // the batch is read
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
+        for (int k = 0; k < kCommitBatch; ++k)
             if (to[k]) *reinterpret_cast<uint4*>(to[k]) = v[k];
     }
 }
@@ -149,10 +159,10 @@ cudaError_t launch_cache_commit(const CacheCommitParams& q, int num_sms, cudaStr
         same = same && p.pool[k].cols == p.pool[0].cols && p.pool[k].pieces == p.pool[0].pieces;
         least = row(k) < least ? row(k) : least;
     }
-    // Some 8 CTAs an SM: so many caches a CTA, or where the (request, cache) pairs are fewer than
+    // Some 12 CTAs an SM, two waves: so many caches a CTA, or where the (request, cache) pairs are fewer than
     // two CTAs an SM the rows are cut, at least 8 pieces (128 bytes) a CTA.
     const int64_t pairs = (int64_t)p.R * p.pools;
-    p.group = same ? (int)((pairs + 8 * num_sms - 1) / (8 * num_sms)) : 1;
+    p.group = same ? (int)((pairs + 12 * num_sms - 1) / (12 * num_sms)) : 1;
     if (p.group > p.pools) p.group = p.pools;
     int64_t splits = 2 * num_sms / pairs;
     if (splits > least / 8) splits = least / 8;
