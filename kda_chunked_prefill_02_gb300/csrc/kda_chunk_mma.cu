@@ -119,6 +119,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
     }
 }
 
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -141,6 +146,18 @@ __device__ __forceinline__ bool all_finite(const uint4 (&y)[N]) {
         }
     }
     return (sum & 0x7fff7fffu) == 0;
+}
+
+// The other roles' wait: no clock of its own, which every use of it would add to the code (the
+// roles' code does not fit the instruction cache together, and an item's change takes as long as
+// fetching it).  What holds a role up holds up the rows' way out too, whose waits run out by the
+// clock and set the abort flag; the number of tries ends this one in any case.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (i % 64 == 0 && (*abort || i >> 27)) return false;
+    }
 }
 
 template <typename T, int D>
@@ -206,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tb = m.tmem;
     // The k-th item of this CTA; false after the last (or on an abort).
     auto take = [&](int k, Item& x, bool& ok) -> bool {
-        ok = ok && wait_for(&m.item_full[k % kItems], (k / kItems) & 1, abort, limit);
+        ok = ok && wait_on(&m.item_full[k % kItems], (k / kItems) & 1, abort);
         if (!ok) return false;
         x = m.item[k % kItems];
         return x.t1 >= 0;
@@ -253,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The item to the other warps.
             auto deal = [&]() {
                 const int at = item % kItems;
-                if (item >= kItems) ok = __all_sync(0xffffffffu, wait_for(&m.item_free[at], (item / kItems - 1) & 1, abort, limit));
+                if (item >= kItems) ok = __all_sync(0xffffffffu, wait_on(&m.item_free[at], (item / kItems - 1) & 1, abort));
                 if (!ok) return;
                 if (lane == 0) {
                     m.item[at] = x;
@@ -280,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the request's end, or the call's, are some other rows or zeros, and not stored)
                 auto load_queries = [&](int a) {
                     const int b = queries % kQ, round = queries / kQ;
-                    if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.q_free[b], (round - 1) & 1, abort, limit));
+                    if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_on(&m.q_free[b], (round - 1) & 1, abort));
                     if (!ok) return;
                     const int at = (item - 1) % kItems, bit = 1 << (2 * at + a);   // the item is dealt already
                     uint64_t* bar = &m.q_full[at][a];
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool v = part == kHalves;
                         if (tile == x.t0 && (part == 0 || (v && x.two))) load_queries(v);   // a row tile's queries before each
                         const int slot = issued % kSlots, round = issued / kSlots;
-                        if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_for(&m.kv_free[slot], (round - 1) & 1, abort, limit));
+                        if (round > 0) ok = __all_sync(0xffffffffu, ok && wait_on(&m.kv_free[slot], (round - 1) & 1, abort));
                         if (!ok) break;
                         uint8_t* dst = ring + slot * kSlotBytes;
                         const bool to_clean = v && tile >= special;
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int tiles = 0, step = 1, j = 0;        // the item's key tiles; this stream's are j, j + step ..
             int units = 0, left = 0;               // how many of them are still to come; keys from the item's first tile on
             uint32_t p_phase = 0, outs = 0;        // items whose O this stream has formed
-            auto landed = [&](int i) { return wait_for(&m.kv_full[i % kSlots], (i / kSlots) & 1, abort, limit); };
+            auto landed = [&](int i) { return wait_on(&m.kv_full[i % kSlots], (i / kSlots) & 1, abort); };
             auto keys_landed = [&](int t) {
                 bool all = true;
 #pragma unroll
@@ -491,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // false after the last.
             auto enter = [&]() -> bool {
                 for (;; ++item) {
-                    ok = __all_sync(0xffffffffu, ok && wait_for(&m.item_full[item % kItems], (item / kItems) & 1, abort, limit));
+                    ok = __all_sync(0xffffffffu, ok && wait_on(&m.item_full[item % kItems], (item / kItems) & 1, abort));
                     if (!ok) return false;
                     const Item& x = m.item[item % kItems];
                     const int t1 = __shfl_sync(0xffffffffu, x.t1, 0);
@@ -545,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int slot = (base + kPer * j + kHalves) % kSlots, steps = steps_of(j);
                     const bool last = units == 1;
                     // O still holds the rows of the item before until they are out
-                    if (!begun && outs > 0) ok = wait_for(&m.o_free[s], (outs - 1) & 1, abort, limit);
+                    if (!begun && outs > 0) ok = wait_on(&m.o_free[s], (outs - 1) & 1, abort);
                     ok = ok && landed(base + kPer * j + kHalves);
                     // with two row tiles the next scores' keys before P is there; with one, memory is the
                     // bound, and waiting for a K would hold up the V before it
@@ -556,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t bd = sdesc_mnmajor_sw128(ring_at + slot * kSlotBytes, 1024, kGroupBytes);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // the two halves of P as they come
-                        ok = __all_sync(0xffffffffu, ok && wait_for(&m.p_full[s][h], p_phase, abort, limit));
+                        ok = __all_sync(0xffffffffu, ok && wait_on(&m.p_full[s][h], p_phase, abort));
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -596,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // give K, V and the queries back, once they have seen the scores: a commit takes the
                 // issuer and the tensor pipe some 100 cycles.
                 if (!waited) {
-                    if (!begun) ok = ok && wait_for(&m.q_full[item % kItems][two ? s : 0], (item / kItems) & 1, abort, limit);
+                    if (!begun) ok = ok && wait_on(&m.q_full[item % kItems][two ? s : 0], (item / kItems) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok && keys_landed(j));
                     if (!ok) break;
                     tc_fence_after();
@@ -627,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int tile = max(x.t0, special); tile < x.t1 && ok; ++tile) {
                     const int i = base_kv + kPer * (tile - x.t0) + kHalves, slot = i % kSlots, base = tile * kKeys;
                     uint8_t* const dst = ring + slot * kSlotBytes;
-                    ok = __all_sync(0xffffffffu, wait_for(&m.kv_raw[slot], (phases >> slot) & 1, abort, limit));
+                    ok = __all_sync(0xffffffffu, wait_on(&m.kv_raw[slot], (phases >> slot) & 1, abort));
                     if (!ok) break;
                     phases ^= 1u << slot;
                     constexpr uint32_t kExp = Elem<T>::kExpMask;
@@ -690,7 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t outs[2] = {0, 0};    // items of each stream
         bool ok = true;
         Item x;
-        for (int item = 0; __all_sync(0xffffffffu, take(item, x, ok)) && ok; ++item) {
+        for (int item = 0;; ++item) {
+            ok = ok && wait_for(&m.item_full[item % kItems], (item / kItems) & 1, abort, limit);
+            if (!__all_sync(0xffffffffu, take(item, x, ok)) || !ok) break;
             const bool joined = !x.two && x.t1 - x.t0 > 1;
             const int special = clean_from(x);
             const bool cleaned = x.t1 > special;   // (otherwise the flags are not this item's)
@@ -737,7 +756,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int w = 0; w < kBadWords; ++w) any_bad |= m.bad[item % kItems][w];
                 }
                 const uint32_t to = tb + lane_base + kTmemO + 128 * s, to2 = tb + lane_base + kTmemO + 128 * s2;
-                auto out16 = [&](int k, const float* o) {   // columns 16 k ..
+#pragma unroll 1
+                for (int k = 0; k < kV / 16; ++k) {
+                    uint32_t r0[16], r1[16];
+                    float o[16];
+                    tmem_ld16_issue(to + 16 * k, r0);
+                    if (joined) tmem_ld16_issue(to2 + 16 * k, r1);
+                    tmem_wait_ld();
+                    tmem_take16(r0, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] *= f0;   // (0 where no key is seen: then O is 0 too)
+                    if (joined) {
+                        float y[16];
+                        tmem_take16(r1, y);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = fmaf(y[e], f1, o[e]);
+                    }
+                    if (k == kV / 16 - 1) {   // O is read: the next item's may come
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&m.o_free[s]);
+                            if (joined) mbar_arrive(&m.o_free[s2]);
+                        }
+                    }
+                    if (!live) continue;
                     uint32_t w[8];
                     if (whole) {
 #pragma unroll
@@ -745,53 +788,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         store32(dst + 16 * k, w, p.wide_out);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[e]);
-                        store32(pdst + 16 * k, w, true);
+                        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 + e]);
-                        store32(pdst + 16 * k + 8, w, true);
-                    }
-                };
-                auto o_read = [&]() {   // the next item's O may come
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&m.o_free[s]);
-                        if (joined) mbar_arrive(&m.o_free[s2]);
-                    }
-                };
-                if (!joined) {
-#pragma unroll 1
-                    for (int k = 0; k < kV / 16; k += 2) {   // 32 columns on one wait
-                        uint32_t r[2][16];
-                        float o[32];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) tmem_ld16_issue(to + 16 * (k + i), r[i]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) tmem_take16(r[i], o + 16 * i);
-                        if (k == kV / 16 - 2) o_read();
-                        if (!live) continue;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = empty ? 0.f : o[e] * f0;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) out16(k + i, o + 16 * i);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int k = 0; k < kV / 16; ++k) {
-                        uint32_t r0[16], r1[16];
-                        float o[16], y[16];
-                        tmem_ld16_issue(to + 16 * k, r0);
-                        tmem_ld16_issue(to2 + 16 * k, r1);
-                        tmem_wait_ld();
-                        tmem_take16(r0, o);
-                        tmem_take16(r1, y);
-                        if (k == kV / 16 - 1) o_read();
-                        if (!live) continue;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : fmaf(y[e], f1, o[e] * f0);
-                        out16(k, o);
+                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 * i + e]);
+                            store32(pdst + 16 * k + 8 * i, w, true);
+                        }
                     }
                 }
                 if (any_bad && live && !empty) {   // elements of V that are not finite, to the rows that see them
@@ -800,9 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int pos = max(special, x.t0) * kKeys; pos < to_key; ++pos) {
                         const int j = pos - special * kKeys;
                         if (!((m.bad[item % kItems][j >> 5] >> (j & 31)) & 1u)) continue;
-                        const int id = p.table[x.r * p.table_stride + pos / p.page];
+                        const int pg = (int)page_div((uint32_t)pos, p.page, p.page_magic), id = p.table[x.r * p.table_stride + pg];
                         if (id < 0 || id >= p.P) continue;
-                        const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (pos % p.page) * p.vs[1] + x.h * p.vs[2] + half * kV;
+                        const T* src = static_cast<const T*>(p.vc) + id * p.vs[0] + (pos - pg * p.page) * p.vs[1] + x.h * p.vs[2] + half * kV;
 #pragma unroll 1
                         for (int e = 0; e < kV; ++e) {
                             const float y = Elem<T>::one(src[e]);
@@ -812,10 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (live && half == 0) {
-                    const float lse = empty ? -INFINITY : ml.x * c + log2f(ml.y);
+                if (live && half == 0 && (!whole || p.lse)) {
+                    const float lse = empty ? -INFINITY : ml.x * c + lg2_approx(ml.y);
                     if (!whole) p.part_lse[part] = lse;
-                    else if (p.lse)
+                    else
                         p.lse[((p.cu ? (int64_t)x.first : (int64_t)x.r * p.T) + token) * p.Hq + x.h * G + in_head] =
                             lse * 0.6931471805599453f;
                 }
@@ -849,9 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sees = min(token + 1, x.end), least = __shfl_sync(0xffffffffu, sees, 0);
             const int tile0 = x.t0 + (two ? 0 : stream);
             float mx = -INFINITY, l = 0.f;
-            if (p.timeout_probe && item == 0) ok = __all_sync(0xffffffffu, wait_for(&m.never, 0, abort, limit));
+            if (p.timeout_probe && item == 0) ok = __all_sync(0xffffffffu, wait_on(&m.never, 0, abort));
             for (int u = 0; u < units && ok; ++u) {
-                ok = __all_sync(0xffffffffu, wait_for(&m.s_full[stream], seen_s & 1, abort, limit));
+                ok = __all_sync(0xffffffffu, wait_on(&m.s_full[stream], seen_s & 1, abort));
                 if (!ok) break;
                 ++seen_s;
                 tc_fence_after();
@@ -941,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&m.p_full[stream][1]);
             }
             // the rows' maximum and sum, once those of the stream's item before have been taken
-            if (items_s > 0) ok = ok && wait_for(&m.ml_free[stream], (items_s - 1) & 1, abort, limit);
+            if (items_s > 0) ok = ok && wait_on(&m.ml_free[stream], (items_s - 1) & 1, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ++items_s;
