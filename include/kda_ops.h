@@ -324,8 +324,21 @@ typedef struct kda_chunk_attention_args {
 } kda_chunk_attention_args;
 size_t kda_chunk_attention_workspace_size(const kda_chunk_attention_args* args);
 kda_status kda_chunk_attention(const kda_chunk_attention_args* args, void* stream);
-/* The same with overrides for tests, as kda_tree_attention_ex. */
+/* The same with overrides for tests, as kda_tree_attention_ex (for the tensor-core kernel). */
 kda_status kda_chunk_attention_ex(const kda_chunk_attention_args* args, const kda_overrides* overrides, void* stream);
+/*
+ * How kda_chunk_attention cuts these arguments on a GPU with num_sms SMs (host only, as
+ * kda_tree_attention_schedule).  kernel: KDA_CHUNK_ROWS, the kernel for few rows, `ctas`
+ * CTAs sharing a block of them; KDA_CHUNK_TENSOR, the tensor-core kernel, `ctas` equal
+ * stretches of the call's work (queries or caches without a tensor map take the kernel
+ * for few rows all the same).
+ */
+#define KDA_CHUNK_ROWS 0
+#define KDA_CHUNK_TENSOR 1
+typedef struct kda_chunk_schedule {
+    int32_t kernel, ctas;
+} kda_chunk_schedule;
+kda_status kda_chunk_attention_schedule(const kda_chunk_attention_args* args, int num_sms, kda_chunk_schedule* schedule);
 
 /*
  * The residual stream between two blocks: a block's output y added to the stream x,

@@ -11,6 +11,6 @@ from .kda import (CHUNK, HEAD_DIM, KdaError, host_staging_size, kda_prefill,  # 
                   overrides, prefill_schedule,
                   kda_prefill_host, kda_verify, lib, status_string, workspace_layout,
                   workspace_size)
-from .ops import (kda_cache_commit, kda_chunk_attention, kda_pool_copy,  # noqa: F401
+from .ops import (chunk_attention_schedule, kda_cache_commit, kda_chunk_attention, kda_pool_copy,  # noqa: F401
                   kda_qk_norm_rope, kda_residual_norm, kda_short_conv, kda_tree_attention,
                   rope_frequencies, tree_attention_schedule, tree_mask)

@@ -309,6 +309,19 @@ size_t kda_chunk_attention_workspace_size(const kda_chunk_attention_args* a) {
     return max_len < 0 ? 0 : chunk_workspace(a, plan_of(a, max_len, sm_count_or_default()));
 }
 
+kda_status kda_chunk_attention_schedule(const kda_chunk_attention_args* a, int num_sms, kda_chunk_schedule* schedule) {
+    if (!schedule || num_sms < 1) return KDA_ERR_INVALID_ARG;
+    memset(schedule, 0, sizeof(*schedule));
+    const kda_status st = check_chunk(a);
+    if (st != KDA_OK || a->num_requests == 0 || a->seqlen == 0) return st;
+    const int64_t max_len = chunk_max_len(a);
+    if (max_len < 0) return KDA_ERR_UNSUPPORTED;
+    const ChunkPlan plan = plan_of(a, max_len, num_sms);
+    schedule->kernel = plan.mma ? KDA_CHUNK_TENSOR : KDA_CHUNK_ROWS;
+    schedule->ctas = plan.mma ? plan.stretches : plan.cluster;
+    return KDA_OK;
+}
+
 kda_status kda_chunk_attention(const kda_chunk_attention_args* a, void* stream) {
     return kda_chunk_attention_ex(a, nullptr, stream);
 }

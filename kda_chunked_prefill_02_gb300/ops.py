@@ -75,6 +75,10 @@ class ChunkAttentionArgs(ctypes.Structure):
         f32: scale""")
 
 
+class ChunkSchedule(ctypes.Structure):
+    _fields_ = _fields("i32: kernel ctas")
+
+
 class ResidualNormArgs(ctypes.Structure):
     _fields_ = _fields("""
         p: x y gate out x_out weight post_weight
@@ -122,6 +126,8 @@ def _fn():
         L.kda_tree_attention_workspace_size.argtypes = [_p]
         L.kda_chunk_attention_workspace_size.restype = ctypes.c_size_t
         L.kda_chunk_attention_workspace_size.argtypes = [_p]
+        L.kda_chunk_attention_schedule.restype = ctypes.c_int
+        L.kda_chunk_attention_schedule.argtypes = [_p, ctypes.c_int, _p]
         L.kda_tree_attention_schedule.restype = ctypes.c_int
         L.kda_tree_attention_schedule.argtypes = [_p, ctypes.c_int, _p]
         _funcs = L
@@ -315,6 +321,27 @@ def kda_chunk_attention(q, k_cache, v_cache, page_table, context_lens, *, cu_seq
     return _run((_binding or _native()).chunk_attention, stream,
                 (q, k_cache, v_cache, page_table, context_lens, cu_seqlens, scale, max_context, out, return_lse,
                  workspace, device_status, None if given is None else ctypes.addressof(given)))
+
+
+def chunk_attention_schedule(q, k_cache, page_table, *, packed=True, scale=None, max_context=None, num_sms=None):
+    """How kda_chunk_attention cuts a call (kda_chunk_attention_schedule): dict(kernel, ctas),
+    kernel "rows" or "tensor".  Host only; of the tensors only types and shapes are read;
+    packed: q is [T_total, Hq, D] (with cu_seqlens).  num_sms as in tree_attention_schedule."""
+    a = ChunkAttentionArgs()
+    a.q = a.k_cache = a.v_cache = a.page_table = a.context_lens = 16   # not followed
+    a.out = 32
+    a.cu_seqlens = 16 if packed else None
+    a.dtype = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_F16}.get(q.dtype, KDA_DTYPE_F32)
+    a.num_requests, a.pages_per_request = page_table.shape
+    a.seqlen, a.num_q_heads, a.head_dim = q.shape[-3:]
+    a.num_pages, a.page_size, a.num_k_heads, _ = k_cache.shape
+    a.max_context = -1 if max_context is None else max_context
+    a.scale = q.shape[-1] ** -0.5 if scale is None else scale
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    s = ChunkSchedule()
+    _check(_fn().kda_chunk_attention_schedule(ctypes.byref(a), int(num_sms), ctypes.byref(s)))
+    return dict(kernel=("rows", "tensor")[s.kernel], ctas=s.ctas)
 
 
 def kda_residual_norm(x, y=None, *, weight=None, post_norm=False, post_weight=None, gate=None, gate_sigmoid=False,

@@ -56,9 +56,19 @@ def _check(q, kc, vc, table, ctx, cu, got, lse, **kw):
         within(torch.where(seen, lse, 0), torch.where(seen, want, 0), torch.where(seen, lb, 0))
 
 
-def _chunk_case(seed, ctx, new, Hq, Hk, D, page, dtype, *, scale=None, room=0, max_context=None):
+# tokens a page table has room for: enough for the tensor-core kernel, whatever the lengths
+ROOM = 300000
+
+
+def _kernel(q, kc, table, **kw):
+    return K.chunk_attention_schedule(q, kc, table, packed=q.dim() == 3, **kw)["kernel"]
+
+
+def _chunk_case(seed, ctx, new, Hq, Hk, D, page, dtype, *, scale=None, room=0, max_context=None, kernel=None):
     q, kc, vc, table, lens, cu = _chunk_inputs(seed, ctx, new, Hq, Hk, D, page, dtype, room)
     status = _status()
+    if kernel:
+        assert _kernel(q, kc, table, scale=scale, max_context=max_context) == kernel
     got, lse = K.kda_chunk_attention(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), cu_seqlens=cu.cuda(),
                                      scale=scale, max_context=max_context, return_lse=True, device_status=status)
     assert status.item() == 0
@@ -70,21 +80,35 @@ RAGGED = ([0, 700, 1, 64, 63, 127, 200, 5], [1, 0, 5, 33, 130, 64, 1, 128])
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("Hq,Hk,page", [(2, 2, 16), (8, 2, 64), (16, 1, 128), (10, 2, 24), (3, 1, 5), (6, 2, 100)])
-def test_chunk_ragged(dtype, D, Hq, Hk, page):
-    _chunk_case(1, *RAGGED, Hq, Hk, D, page, dtype)
+def test_chunk_ragged(dtype, D, Hq, Hk, page, room):
+    _chunk_case(1, *RAGGED, Hq, Hk, D, page, dtype, room=room, kernel="tensor" if room and page % 8 == 0 else None)
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("Hq,Hk", [(7, 1), (12, 1), (20, 1), (48, 1), (100, 1), (128, 1), (200, 1), (256, 1), (300, 1)])
-def test_chunk_query_heads_of_a_key_head(Hq, Hk):
-    _chunk_case(2, [130, 0, 9], [3, 40, 17], Hq, Hk, 64, 16, BF16)
+def test_chunk_query_heads_of_a_key_head(Hq, Hk, room):
+    """Row tiles that are not full, and more query heads than a row tile has rows."""
+    _chunk_case(2, [130, 0, 9], [3, 40, 17], Hq, Hk, 64, 16, BF16, room=room,
+                kernel="tensor" if room and Hq <= 128 else None)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("tokens", [1, 2, 63, 64, 65, 127, 128, 129, 300])
-def test_chunk_of_one_request(dtype, tokens):
-    for ctx in (0, 1, 127, 128, 1000):
-        _chunk_case(3, [ctx], [tokens], 8, 2, 128, 64, dtype)
+@pytest.mark.parametrize("room", [0, ROOM])
+@pytest.mark.parametrize("tokens", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300])
+def test_chunk_of_one_request(dtype, tokens, room):
+    """Last row tiles of every kind, key tiles that end inside and at the tokens' own."""
+    for ctx in (0, 1, 95, 96, 97, 127, 128, 1000):
+        _chunk_case(3, [ctx], [tokens], 8, 2, 128, 64, dtype, room=room, kernel="tensor" if room else None)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [128, 129, 255, 256, 257, 600])
+def test_chunk_row_tiles_that_see_different_key_tiles(D, tokens):
+    """One query head a key head: the first of two row tiles ends before the last key tile."""
+    for ctx in (0, 1, 64, 127):
+        _chunk_case(21, [ctx, 5], [tokens, 140], 2, 2, D, 16, BF16, room=ROOM, kernel="tensor")
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -98,31 +122,37 @@ def test_chunk_many_requests():
     """More requests than a warp looks at in one go, single tokens between longer pieces."""
     ctx = [(i * 37) % 300 if i % 50 else 900 + i for i in range(400)]
     new = [1 if i % 7 else (i * 13) % 90 for i in range(400)]
-    _chunk_case(5, ctx, new, 4, 2, 64, 16, BF16)
+    _chunk_case(5, ctx, new, 4, 2, 64, 16, BF16, kernel="rows")
+    _chunk_case(5, ctx, new, 8, 2, 128, 16, BF16, room=ROOM, kernel="tensor")
     _chunk_case(6, ctx[:70], new[:70], 8, 2, 128, 16, F16, max_context=max(ctx))
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("T", [1, 3, 40, 140])
-def test_chunk_padded(T):
+def test_chunk_padded(T, room):
     """[R, T, Hq, D]: as the packed form of equal lengths."""
     ctx = [0, 77, 300]
-    q, kc, vc, table, lens, cu = _chunk_inputs(7, ctx, [T] * 3, 8, 2, 128, 16, BF16)
+    q, kc, vc, table, lens, cu = _chunk_inputs(7, ctx, [T] * 3, 8, 2, 128, 16, BF16, room)
     got, lse = K.kda_chunk_attention(q.view(3, T, 8, 128).cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(),
                                      return_lse=True)
     assert got.shape == (3, T, 8, 128) and lse.shape == (3, T, 8)
     _check(q, kc, vc, table, lens, cu, got.flatten(0, 1), lse.flatten(0, 1))
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("scale", [1.0, 0.01, 0.0, -0.3, 1e-38])
-def test_chunk_scales(scale):
-    _chunk_case(8, [100, 0], [30, 200], 4, 1, 64, 16, BF16, scale=scale)
+def test_chunk_scales(scale, room):
+    """Scales that are not above zero, or whose reciprocal is no fp32 number, take the kernel for few rows."""
+    _chunk_case(8, [100, 0], [30, 200], 4, 1, 64, 16, BF16, scale=scale, room=room,
+                kernel=("tensor" if scale > 1e-30 else "rows") if room else None)
 
 
-def test_chunk_strides():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_chunk_strides(room):
     """q as heads of a fused projection, results into a wider buffer, caches with the heads
     before the rows, with keys and values in one tensor, and with rows that belong to no map."""
     ctx, new = [50, 0, 260], [70, 5, 129]
-    q, kc, vc, table, lens, cu = _chunk_inputs(9, ctx, new, 8, 2, 128, 16, BF16)
+    q, kc, vc, table, lens, cu = _chunk_inputs(9, ctx, new, 8, 2, 128, 16, BF16, room)
     T = sum(new)
     wide = torch.zeros(T, 14, 128, dtype=BF16, device="cuda")
     wide[:, 3:11] = q.cuda()
@@ -137,22 +167,28 @@ def test_chunk_strides():
         got = K.kda_chunk_attention(wide[:, 3:11], k, v, tab, ln, out=res[:, 1:9], **dev)
         _check(q, kc, vc, table, lens, cu, got, None)
         assert bool((res[:, 0] == 7).all()) and bool((res[:, 9] == 7).all())
+        # results that start on 16 bytes, not on 32
+        odd = torch.full((T * 1032 + 8,), 7.0, dtype=BF16, device="cuda")[8:].view(T, 1032)[:, :1024].view(T, 8, 128)
+        got = K.kda_chunk_attention(wide[:, 3:11], k, v, tab, ln, out=odd, **dev)
+        _check(q, kc, vc, table, lens, cu, got, None)
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("ctx,new", [([300], [4]), ([0, 90, 4000], [300, 1, 37])])
-def test_chunk_results_over_the_queries(D, ctx, new):
-    q, kc, vc, table, lens, cu = _chunk_inputs(10, ctx, new, 8, 2, D, 16, BF16)
+def test_chunk_results_over_the_queries(D, ctx, new, room):
+    q, kc, vc, table, lens, cu = _chunk_inputs(10, ctx, new, 8, 2, D, 16, BF16, room)
     qd = q.cuda()
     got = K.kda_chunk_attention(qd, kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), cu_seqlens=cu.cuda(), out=qd)
     assert got is qd
     _check(q, kc, vc, table, lens, cu, got, None)
 
 
-def test_chunk_rows_behind_the_last_request_are_left():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_chunk_rows_behind_the_last_request_are_left(room):
     """A batch padded to a fixed number of rows, whatever the padding holds."""
     ctx, new = [20, 3], [33, 70]
-    q, kc, vc, table, lens, cu = _chunk_inputs(11, ctx, new, 8, 2, 128, 16, BF16)
+    q, kc, vc, table, lens, cu = _chunk_inputs(11, ctx, new, 8, 2, 128, 16, BF16, room)
     T = sum(new)
     qd = torch.full((T + 100, 8, 128), math.nan, dtype=BF16, device="cuda")
     qd[:T] = q.cuda()
@@ -165,13 +201,15 @@ def test_chunk_rows_behind_the_last_request_are_left():
     assert bool((res[T:] == 7).all())
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("D,Hq,Hk,page", [(128, 8, 2, 16), (64, 2, 2, 64), (256, 4, 1, 24), (128, 4, 2, 10)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
-def test_chunk_what_a_row_does_not_see(D, Hq, Hk, page, what):
+def test_chunk_what_a_row_does_not_see(D, Hq, Hk, page, what, dtype, room):
     """Unused pages, rows behind a request's end, and the keys of its last tokens: only the
     rows that see a token feel it.  Values that are not finite reach those."""
     ctx, new = [70, 0, 129], [90, 40, 3]
-    q, kc, vc, table, lens, cu = _chunk_inputs(12, ctx, new, Hq, Hk, D, page, BF16)
+    q, kc, vc, table, lens, cu = _chunk_inputs(12, ctx, new, Hq, Hk, D, page, dtype, room)
     clean_k, clean_v = kc.clone(), vc.clone()
     used = torch.zeros(kc.shape[0], page, dtype=torch.bool)
     for r in range(3):
@@ -198,10 +236,11 @@ def test_chunk_what_a_row_does_not_see(D, Hq, Hk, page, what):
     within(torch.where(hit, 0, got), torch.where(hit, 0, out), torch.where(hit, 1.0, ob))
 
 
-def test_chunk_keys_that_are_not_finite():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_chunk_keys_that_are_not_finite(room):
     """A key that is NaN makes NaN of the rows that see it, and of no other."""
     ctx, new = [10], [200]
-    q, kc, vc, table, lens, cu = _chunk_inputs(13, ctx, new, 4, 1, 128, 16, BF16)
+    q, kc, vc, table, lens, cu = _chunk_inputs(13, ctx, new, 4, 1, 128, 16, BF16, room)
     out, ob, _, _ = chunk_reference(q, kc, vc, table, lens, new)
     p = 10 + 150
     kc[int(table[0, p // 16]), p % 16, 0, 7] = math.nan
@@ -210,9 +249,10 @@ def test_chunk_keys_that_are_not_finite():
     within(got[:150], out[:150], ob[:150])
 
 
-def test_chunk_reports_what_only_the_device_sees():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_chunk_reports_what_only_the_device_sees(room):
     ctx, new = [20, 30, 40, 50], [9, 70, 1, 30]
-    q, kc, vc, table, lens, cu = _chunk_inputs(14, ctx, new, 8, 2, 128, 16, BF16)
+    q, kc, vc, table, lens, cu = _chunk_inputs(14, ctx, new, 8, 2, 128, 16, BF16, room)
     out, ob, lse_ref, _ = chunk_reference(q, kc, vc, table, lens, new)
     dev = [t.cuda() for t in (q, kc, vc, table)]
 
@@ -279,14 +319,15 @@ def test_chunk_weight_in_many_keys_far_below_the_largest(dtype, gap, n, R):
         within(glse[r], lse, lb)
 
 
-def test_chunk_offsets_past_32_bits():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_chunk_offsets_past_32_bits(room):
     """A cache of more than 2^32 bytes: the pages at its end."""
     pages, page, Hk, D = 70000, 64, 4, 128
     kc = torch.zeros(pages, page, Hk, D, dtype=BF16, device="cuda")
     vc = torch.zeros_like(kc)
     assert kc.numel() > 1 << 31
     ctx, new = [150, 10], [40, 3]
-    q, ks, vs, table, lens, cu = _chunk_inputs(17, ctx, new, 8, Hk, D, page, BF16)
+    q, ks, vs, table, lens, cu = _chunk_inputs(17, ctx, new, 8, Hk, D, page, BF16, room)
     far = pages - ks.shape[0]
     kc[far:], vc[far:] = ks.cuda(), vs.cuda()
     got = K.kda_chunk_attention(q.cuda(), kc, vc, (table + far).cuda(), lens.cuda(), cu_seqlens=cu.cuda())
@@ -311,11 +352,12 @@ def test_chunk_in_pieces_and_as_drafts():
     within(drafts[0], out[300:], ob[300:])
 
 
-def test_chunk_repeats_and_graphs():
+@pytest.mark.parametrize("room", [8192, ROOM])
+def test_chunk_repeats_and_graphs(room):
     """The same bits each time, on other streams, and from a captured call whose lengths are
     those of the replay."""
     ctx, new = [500, 0, 3000, 77], [30, 250, 1, 129]
-    q, kc, vc, table, lens, cu = _chunk_inputs(19, ctx, new, 8, 2, 128, 16, BF16, room=8192)
+    q, kc, vc, table, lens, cu = _chunk_inputs(19, ctx, new, 8, 2, 128, 16, BF16, room=room)
     dev = [t.cuda() for t in (q, kc, vc, table, lens)]
     cud = cu.cuda()
     first = K.kda_chunk_attention(*dev, cu_seqlens=cud)
@@ -341,6 +383,77 @@ def test_chunk_repeats_and_graphs():
     c2.copy_(other)
     graph.replay()
     assert torch.equal(out, K.kda_chunk_attention(*dev[:4], _i32([10, 2000, 0, 300]).cuda(), cu_seqlens=other))
+
+
+KDA_ERR_TIMEOUT = 4
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ctx,new", [([3000, 0, 900, 17], [24, 1, 7, 30]), ([20000, 5, 300, 700] * 8, [300, 64, 1, 500] * 8)])
+def test_chunk_wait_that_runs_out_is_reported_and_the_context_survives(D, ctx, new):
+    """The first wait of the softmax warps is for a barrier that nothing arrives on, so that it
+    runs out with copies and products in flight.  The call returns and says so, and the next
+    one on the same stream and workspace gives the usual bits."""
+    pages = 4000   # the requests share them
+    kc = torch.randn(pages, 16, 2, D, device="cuda").to(BF16)
+    vc = torch.randn_like(kc)
+    g = _gen(23)
+    table = torch.randint(0, pages, (len(ctx), ROOM // 16), generator=g).to(torch.int32).cuda()
+    q, lens = _rand(g, (sum(new), 8, D), BF16).cuda(), _i32(ctx).cuda()
+    cu = _i32([0] + new).cumsum(0).to(torch.int32).cuda()
+    assert _kernel(q, kc, table) == "tensor"
+    status = _status()
+    usual = K.kda_chunk_attention(q, kc, vc, table, lens, cu_seqlens=cu, device_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for limit in (2000, 200000):
+        with K.overrides(wait_limit_ns=limit, timeout_probe=True):
+            K.kda_chunk_attention(q, kc, vc, table, lens, cu_seqlens=cu, device_status=status)
+        torch.cuda.synchronize()            # returns: no hang, no fault
+        assert status.item() == KDA_ERR_TIMEOUT
+        status.zero_()
+        again = K.kda_chunk_attention(q, kc, vc, table, lens, cu_seqlens=cu, device_status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0 and torch.equal(again, usual)
+
+
+def test_chunk_waits_that_last_as_long_as_an_item_do_not_run_out():
+    """Items of 8192 key tiles take a CTA some 14 ms; the bound of a wait here is 1 ms beside
+    what the contexts themselves may take."""
+    g = _gen(24)
+    R, pages = 38, 600   # the requests share their pages
+    kc, vc = (torch.randn(pages, 64, 4, 128, device="cuda").to(BF16) for _ in range(2))
+    table = torch.randint(0, pages, (R, (1 << 14) + 1), generator=g).to(torch.int32).cuda()
+    q, lens = _rand(g, (R, 32, 32, 128), BF16).cuda(), torch.full((R,), 1 << 20, dtype=torch.int32).cuda()
+    status = _status()
+    usual = K.kda_chunk_attention(q, kc, vc, table, lens)
+    with K.overrides(wait_limit_ns=1000000):
+        got = K.kda_chunk_attention(q, kc, vc, table, lens, device_status=status)
+    assert status.item() == 0 and torch.equal(got, usual)
+
+
+def test_one_token_as_a_transposed_column():
+    """The row of a transposed column has strides (1, 1): what a matrix times a column leaves
+    behind.  Every operator takes it as the contiguous row that it is."""
+    g = _gen(25)
+
+    def row(n):
+        r = _rand(g, (n, 1), BF16).cuda().t()
+        assert r.stride() == (1, 1) and r.is_contiguous()
+        return r
+
+    for room in (0, ROOM):
+        q, kc, vc, table, lens, cu = _chunk_inputs(26, [200], [1], 4, 2, 128, 16, BF16, room)
+        dev = [t.cuda() for t in (kc, vc, table, lens)]
+        qd = row(512).as_strided((1, 4, 128), (1, 128, 1))
+        want = K.kda_chunk_attention(qd.contiguous().clone(), *dev, cu_seqlens=cu.cuda())
+        assert torch.equal(K.kda_chunk_attention(qd, *dev, cu_seqlens=cu.cuda()), want)
+    x, y = row(384), row(384)
+    a, b = K.kda_residual_norm(x, y), K.kda_residual_norm(x.clone().view(1, 384), y.clone().view(1, 384))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    pool = torch.arange(2 * 64, dtype=F32, device="cuda").view(2, 1, 64).as_strided((2, 1, 64), (64, 1, 1))
+    K.kda_pool_copy(pool, _i32([0]).cuda(), _i32([1]).cuda())
+    assert torch.equal(pool[1], pool[0])
 
 
 # ---------------------------------------------------------------- the residual stream's norm

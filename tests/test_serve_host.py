@@ -67,6 +67,45 @@ def test_chunk_workspace_of_what_is_refused(ops):
     assert size(out=PTR, out_stride0=4096) == 0
 
 
+def _schedule(ops, R, T, Hq, Hk, D, tokens, page=16, num_sms=152, dtype=BF16, packed=True, **kw):
+    empty = lambda *shape: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    q = empty(T, Hq, D) if packed else empty(R, T, Hq, D)
+    return ops.chunk_attention_schedule(q, empty(10, page, Hk, D), empty(R, tokens // page), packed=packed,
+                                        num_sms=num_sms, **kw)
+
+
+def test_chunk_schedule(ops):
+    """One clear case of either kernel, and what takes the kernel for few rows whatever its size."""
+    assert _schedule(ops, 1, 1, 8, 2, 128, 1008) == dict(kernel="rows", ctas=8)
+    assert _schedule(ops, 1, 8192, 32, 8, 128, 8192) == dict(kernel="tensor", ctas=152)
+    assert _schedule(ops, 4, 2048, 16, 2, 256, 8192, packed=False) == dict(kernel="tensor", ctas=76)
+    # the bound of the contexts counts, not the table's width
+    assert _schedule(ops, 1, 1, 8, 2, 128, 131072)["kernel"] == "tensor"
+    assert _schedule(ops, 1, 1, 8, 2, 128, 131072, max_context=1000)["kernel"] == "rows"
+    assert _schedule(ops, 1, 1, 8, 2, 128, 131072, max_context=0)["kernel"] == "rows"
+    for kw in (dict(page=10, tokens=8190), dict(scale=0.0), dict(scale=-1.0), dict(Hq=129, Hk=1)):
+        assert _schedule(ops, **{**dict(R=1, T=8192, Hq=32, Hk=8, D=128, tokens=8192), **kw})["kernel"] == "rows"
+
+
+def test_chunk_schedule_refusals(ops):
+    from kda_chunked_prefill_02_gb300 import KdaError
+    for kw in (dict(D=96), dict(dtype=torch.float32), dict(num_sms=0), dict(Hq=7)):
+        with pytest.raises(KdaError):
+            _schedule(ops, **{**dict(R=2, T=4, Hq=8, Hk=2, D=128, tokens=800), **kw})
+    assert _schedule(ops, 0, 0, 8, 2, 128, 800)["ctas"] == 0
+
+
+def test_chunk_workspace(ops):
+    """The tensor-core kernel's parts: two items a stretch, 256 rows of their values and log-sums."""
+    size = lambda **kw: ops._fn().kda_chunk_attention_workspace_size(ctypes.byref(_chunk_args(ops, **kw)))  # noqa: E731
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 152
+    long = dict(pages_per_request=20000, page_table_stride=20000)
+    assert size(**long) == 2 * sms * (16 + 256 * 129 * 4)
+    assert size(**long, max_context=100) == 0
+    for bound in ((1 << 63) - 1, 1 << 62, 1 << 31):   # no bound
+        assert size(**long, max_context=bound) == size(**long)
+
+
 # ---------------------------------------------------------------- the residual stream's norm
 def _norm(ops, **kw):
     a = ops.ResidualNormArgs()
