@@ -1,6 +1,6 @@
 """One serving step of a small decoder that mixes KDA layers with softmax-attention
-layers: a ragged batch of prompts, then the verification of a tree of drafted tokens
-for every request.
+layers: a ragged batch of prompts, the verification of a tree of drafted tokens for
+every request, the next token behind the accepted ones, and a request that is forked.
 
     python examples/hybrid_step.py
 
@@ -9,9 +9,13 @@ and plain torch matrix products between the operators.  KDA layers run
 kda_short_conv -> kda_prefill on the prompts and kda_short_conv -> kda_verify on the
 drafts, where every root-to-leaf path of a tree is a request of kda_verify (a state
 belongs to a path); attention layers run kda_qk_norm_rope, which puts keys and values
-into the paged cache, -> kda_tree_attention, one call for all trees.  The accepted
-paths are then committed to the KDA layers' states.  The step is checked against
-running the accepted paths token by token.
+into the paged cache, -> kda_chunk_attention, one call for all prompts, or
+kda_tree_attention, one call for all trees.  Between them kda_residual_norm adds a
+layer's output to the residual stream and norms it for the next.  The accepted paths
+are then committed: to the KDA layers' states, and by kda_cache_commit to the caches,
+where they move together behind their context.  A fork is a kda_pool_copy of the
+request's pages and states.  The step is checked against running the accepted paths
+token by token.
 """
 import os
 import sys
@@ -46,10 +50,6 @@ def gates(x, w):
     return -5.0 * torch.sigmoid((x @ w["gate"]).float()).unflatten(-1, (H, D)), (x @ w["beta"]).float()
 
 
-def norm(x):
-    return torch.nn.functional.rms_norm(x.float(), (E,)).to(BF16)
-
-
 class Decoder:
     def __init__(self, requests, room, seed=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -68,8 +68,8 @@ class Decoder:
         return (self.table[request, position // PAGE].long() * PAGE + position % PAGE)
 
     def attention_in(self, w, i, x, positions, slots):
-        """Queries of tokens x [T, E]; their keys and values go into the cache."""
-        qkv = (norm(x) @ w["aqkv"]).view(-1, HQ + 2 * HK, D)
+        """Queries of normed tokens x [T, E]; their keys and values go into the cache."""
+        qkv = (x @ w["aqkv"]).view(-1, HQ + 2 * HK, D)
         q, _ = K.kda_qk_norm_rope(qkv[:, :HQ], qkv[:, HQ:HQ + HK], positions.to(torch.int32), self.freq,
                                   q_weight=w["qw"], k_weight=w["kw"], rope_scale=self.scale, v=qkv[:, HQ + HK:],
                                   k_cache=self.kc[i], v_cache=self.vc[i], slots=slots)
@@ -79,22 +79,19 @@ class Decoder:
         """A packed batch of prompts x [T, E], request n's tokens cu[n] .. cu[n+1]-1."""
         lens = cu[1:] - cu[:-1]
         request = torch.repeat_interleave(torch.arange(self.R, device="cuda"), lens)
-        position = torch.arange(x.shape[0], device="cuda") - cu[:-1].long()[request]
+        position = torch.arange(x.shape[0], device="cuda") + (self.lens - cu[:-1]).long()[request]
+        h, _ = K.kda_residual_norm(x)
         for i, w in enumerate(self.w):
-            h = norm(x)
             y = K.kda_short_conv(h @ w["qkv"], w["conv"], conv_state=self.conv[i], cu_seqlens=cu,
                                  norm_channels=2 * E).unflatten(-1, (3 * H, D))
             g, beta = gates(h, w)
             o, fin = K.kda_prefill(y[:, :H], y[:, H:2 * H], y[:, 2 * H:], g, beta, initial_state=self.state[i],
                                    cu_seqlens=cu)
             self.state[i].copy_(fin)
-            x = x + o.flatten(1) @ w["out"]
-            q = self.attention_in(w, i, x, position, self.slots(request, position))
-            # (a server has a prompt attention of its own; here every token is a tree of one node)
-            rows = [K.kda_tree_attention(q[t:t + 1, None].contiguous(), self.kc[i], self.vc[i],
-                                         self.table[request[t]:request[t] + 1], position[t:t + 1].to(torch.int32))
-                    for t in range(x.shape[0])]
-            x = x + torch.cat(rows).flatten(1) @ w["aout"]
+            h, x = K.kda_residual_norm(x, o.flatten(1) @ w["out"])
+            q = self.attention_in(w, i, h, position, self.slots(request, position))
+            a = K.kda_chunk_attention(q, self.kc[i], self.vc[i], self.table, self.lens, cu_seqlens=cu)
+            h, x = K.kda_residual_norm(x, a.flatten(1) @ w["aout"])
         self.lens += lens
         return x
 
@@ -123,8 +120,8 @@ class Decoder:
         row = self.lens[:, None].long() + torch.arange(N, device="cuda")        # a node's place in the cache
         slots = self.slots(torch.arange(self.R, device="cuda")[:, None], row).flatten().contiguous()
         zero = torch.zeros(len(paths), dtype=torch.int32, device="cuda")
+        h, _ = K.kda_residual_norm(x)
         for i, w in enumerate(self.w):
-            h = norm(x)
             # the KDA layer runs every path from a copy of its request's states
             proj = (h @ w["qkv"])[of[:, None], idx]
             conv, state = self.conv[i][of].contiguous(), self.state[i][of].contiguous()
@@ -144,12 +141,23 @@ class Decoder:
                              acc, replay_only=True)
             out = torch.empty((self.R, N, E), dtype=BF16, device="cuda")
             out[of[:, None], idx] = o.flatten(2)      # nodes that paths share: the same values
-            x = x + out @ w["out"]
-            q = self.attention_in(w, i, x.flatten(0, 1), position.flatten().contiguous(), slots)
+            h, x = K.kda_residual_norm(x, out @ w["out"])
+            q = self.attention_in(w, i, h.flatten(0, 1), position.flatten().contiguous(), slots)
             a = K.kda_tree_attention(q.view(self.R, N, HQ, D), self.kc[i], self.vc[i], self.table, self.lens,
                                      tree_mask=mask)
-            x = x + a.flatten(2) @ w["aout"]
+            h, x = K.kda_residual_norm(x, a.flatten(2) @ w["aout"])
+        if accepted is not None:
+            path = torch.tensor([a + [0] * (N - len(a)) for a in accepted], dtype=torch.int32, device="cuda")
+            count = torch.tensor([len(a) for a in accepted], dtype=torch.int32, device="cuda")
+            K.kda_cache_commit(self.kc + self.vc, self.table, self.lens, path, count)
         return x
+
+    def fork(self, parent, child):
+        """Request `child` goes on from where `parent` is."""
+        src, dst = torch.tensor([[parent], [child]], dtype=torch.int32, device="cuda")
+        K.kda_pool_copy(self.state + self.conv, src, dst)
+        K.kda_pool_copy(self.kc + self.vc, self.table[parent], self.table[child])   # (a server copies the last page)
+        self.lens[child] = self.lens[parent]
 
 
 def main():
@@ -181,9 +189,16 @@ def main():
             if live[r]:
                 worst = max(worst, float((z[r, 0].float() - y[r, node[r]].float()).abs().max()))
         step.lens += torch.tensor(live, dtype=torch.int32, device="cuda")
+    # the next token behind what was accepted, and behind a fork of the first request
+    tree.lens += torch.tensor([len(a) for a in accepted], dtype=torch.int32, device="cuda")
     state = max(float((a - b).norm() / a.norm()) for a, b in zip(tree.state, step.state))
     conv = all(torch.equal(a, b) for a, b in zip(tree.conv[:1], step.conv[:1]))
     size = float(y.float().abs().max())
+    x, root = torch.randn((R, 1, E), generator=gen, device="cuda").to(BF16), torch.full((R, 1), -1)
+    worst = max(worst, float((tree.verify(x, root).float() - step.verify(x, root).float()).abs().max()))
+    tree.fork(0, 2)
+    z = tree.verify(x[:1].expand(R, 1, E).contiguous(), root)
+    worst = max(worst, float((z[0].float() - z[2].float()).abs().max()))
     print("tree step against token by token: outputs within %.3f (largest %.1f), KDA states within %.1e, first layer's "
           "conv states %s" % (worst, size, state, "equal" if conv else "differ"))
     return worst, size, state, conv
