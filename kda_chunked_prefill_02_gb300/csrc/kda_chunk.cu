@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
 }
 
 // Joins the parts of an item that kda_chunk_mma.cu has cut: out = sum_c 2^(lse_c - M) o_c /
-// sum_c 2^(lse_c - M) over the CTAs c that hold one, in their order: slot 1 of CTA
-// blockIdx.x, then slot 0 of those behind it up to the item's last part.  A row is the work
+// sum_c 2^(lse_c - M) over the stretches c that hold one, in their order: slot 1 of a
+// stretch, then slot 0 of those behind it up to the item's last part.  A row is the work
 // of one warp that takes part after part, or of the block's 8 warps, of every 8th part each
 // (the order of the sums is fixed all the same).  A block takes rows blockIdx.y (times 8, with
 // a warp a row), and so on: with a block for every 8 rows of a pair the kernel took 6 us where
@@ -427,70 +427,76 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p) {
     __shared__ float sy[W > 1 ? 8 : 1][W > 1 ? D : 1], ssum[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int cta = blockIdx.x, ctas = p.ctas;
-    const int4 item = p.parts[2 * cta + 1];   // state, request, key head, pair of row tiles
-    if (item.x == 0) return;
-    int first, n, len;
-    chunk_request(p, item.y, first, n, len);
-    int count = 1;   // parts, from their states, 32 at a time
-    for (int c = cta + 1;; c += 32) {
-        const int state = c + lane < ctas ? p.parts[2 * (c + lane)].x : 0;
-        const uint32_t stop = __ballot_sync(0xffffffffu, state != 1);
-        const int k = stop ? __ffs(stop) - 1 : 32;
-        count += k;
-        if (stop) {
-            if (__shfl_sync(0xffffffffu, state, k) == 2) ++count;
-            break;
-        }
-    }
-    for (int in = (int)blockIdx.y * (8 / W) + warp / W; in < 256; in += (int)gridDim.y * (8 / W)) {
-        const int row = in & 127, in_token = (int)page_div((uint32_t)row, p.G, p.group_magic);
-        const int token = (2 * item.w + (in >> 7)) * p.tile_tokens + in_token;
-        if (in_token >= p.tile_tokens || token >= n) continue;   // all of a row's warps
-        const auto part = [&](int k) { return (int64_t)(k ? 2 * (cta + k) : 2 * cta + 1) * 256 + in; };
-        float mx = -INFINITY, sum = 0.f, y[kVec];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) y[i] = 0.f;
-        for (int k = lane; k < count; k += 32) mx = fmaxf(mx, p.part_lse[part(k)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mu = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-        for (int k = W > 1 ? warp : 0; k < count; k += W) {
-            const float f = ex2_approx(p.part_lse[part(k)] - mu);
-            const float* src = p.part_o + part(k) * D + lane * kVec;
-            sum += f;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) y[i] = fmaf(src[i], f, y[i]);
-        }
-        if (W > 1) {
-            __syncthreads();   // the row before has been read
-            if (lane == 0) ssum[warp] = sum;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) sy[warp][lane * kVec + i] = y[i];
-            __syncthreads();
-            if (warp > 0) continue;
-            sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) y[i] = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                sum += ssum[w];
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) y[i] += sy[w][lane * kVec + i];
+    // this block's stretches, one of each wave (at most 32), are looked at together
+    const int ctas = p.ctas, mine = (int)blockIdx.x + lane * (int)gridDim.x;
+    const int4 items = mine < ctas ? p.parts[2 * mine + 1] : make_int4(0, 0, 0, 0);
+    for (uint32_t cut = __ballot_sync(0xffffffffu, items.x != 0); cut; cut &= cut - 1) {
+        const int wave = __ffs(cut) - 1, cta = (int)blockIdx.x + wave * (int)gridDim.x;
+        // its item: request, key head, pair of row tiles
+        const int4 item = make_int4(1, __shfl_sync(0xffffffffu, items.y, wave), __shfl_sync(0xffffffffu, items.z, wave),
+                                    __shfl_sync(0xffffffffu, items.w, wave));
+        int first, n, len;
+        chunk_request(p, item.y, first, n, len);
+        int count = 1;   // parts, from their states, 32 at a time
+        for (int c = cta + 1;; c += 32) {
+            const int state = c + lane < ctas ? p.parts[2 * (c + lane)].x : 0;
+            const uint32_t stop = __ballot_sync(0xffffffffu, state != 1);
+            const int k = stop ? __ffs(stop) - 1 : 32;
+            count += k;
+            if (stop) {
+                if (__shfl_sync(0xffffffffu, state, k) == 2) ++count;
+                break;
             }
         }
-        const int h = item.z * p.G + (row - in_token * p.G);
-        const bool empty = sum == 0.f;
-        const float inv = empty ? 0.f : 1.f / sum;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(
-            static_cast<T*>(p.out) + (p.cu ? (int64_t)(first + token) * p.os[1] : item.y * p.os[0] + token * p.os[1]) +
-            h * p.os[2] + lane * kVec);
+        for (int in = (int)blockIdx.y * (8 / W) + warp / W; in < 256; in += (int)gridDim.y * (8 / W)) {
+            const int row = in & 127, in_token = (int)page_div((uint32_t)row, p.G, p.group_magic);
+            const int token = (2 * item.w + (in >> 7)) * p.tile_tokens + in_token;
+            if (in_token >= p.tile_tokens || token >= n) continue;   // all of a row's warps
+            const auto part = [&](int k) { return (int64_t)(k ? 2 * (cta + k) : 2 * cta + 1) * 256 + in; };
+            float mx = -INFINITY, sum = 0.f, y[kVec];
 #pragma unroll
-        for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
-        if (p.lse && lane == 0)
-            p.lse[((p.cu ? (int64_t)first : (int64_t)item.y * p.T) + token) * p.Hq + h] =
-                empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+            for (int i = 0; i < kVec; ++i) y[i] = 0.f;
+            for (int k = lane; k < count; k += 32) mx = fmaxf(mx, p.part_lse[part(k)]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+            for (int k = W > 1 ? warp : 0; k < count; k += W) {
+                const float f = ex2_approx(p.part_lse[part(k)] - mu);
+                const float* src = p.part_o + part(k) * D + lane * kVec;
+                sum += f;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) y[i] = fmaf(src[i], f, y[i]);
+            }
+            if (W > 1) {
+                __syncthreads();   // the row before has been read
+                if (lane == 0) ssum[warp] = sum;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) sy[warp][lane * kVec + i] = y[i];
+                __syncthreads();
+                if (warp > 0) continue;
+                sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) y[i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    sum += ssum[w];
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) y[i] += sy[w][lane * kVec + i];
+                }
+            }
+            const int h = item.z * p.G + (row - in_token * p.G);
+            const bool empty = sum == 0.f;
+            const float inv = empty ? 0.f : 1.f / sum;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                static_cast<T*>(p.out) + (p.cu ? (int64_t)(first + token) * p.os[1] : item.y * p.os[0] + token * p.os[1]) +
+                h * p.os[2] + lane * kVec);
+#pragma unroll
+            for (int k = 0; k < kVec; k += 2) dst[k / 2] = Elem<T>::pack(y[k] * inv, y[k + 1] * inv);
+            if (p.lse && lane == 0)
+                p.lse[((p.cu ? (int64_t)first : (int64_t)item.y * p.T) + token) * p.Hq + h] =
+                    empty ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+        }
     }
 }
 
@@ -502,7 +508,7 @@ int64_t row_pairs(int R, int T, bool packed, int G) {
 
 template <typename T, int W>
 cudaError_t launch_join_w(const ChunkParams& p, int D, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.ctas - 1), 16);
+    const dim3 grid((unsigned)(p.ctas / p.waves), 16);
     const auto kernel = D == 64 ? chunk_join_kernel<T, 64, W>
                                 : D == 128 ? chunk_join_kernel<T, 128, W> : chunk_join_kernel<T, 256, W>;
     return launch_maybe_pdl(kernel, grid, dim3(256), 0, s, true, p);
@@ -574,6 +580,7 @@ ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t ma
     t.mma = page % 8 == 0 && G <= 128 && scale > 1e-30f && num_sms > 1 && !(in_place && D == 256);
     t.grid = num_sms;
     t.stretches = t.mma ? D == 256 ? t.grid / 2 : t.grid : 0;
+    t.waves = 1;
     // The rows kernel (also for layouts without a tensor map): clusters where the blocks are
     // fewer than the CTAs that run at once (what the tiles in flight leave room for, or for D
     // 64 the registers), at least 128 tokens a CTA.
@@ -597,6 +604,10 @@ ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t ma
         const double mma_us = 17.0 + keys / 128 * (D == 64 ? 1.15 : D == 128 ? 1.4 : 2.1);
         t.mma = mma_us < 1.25 * rows_us;
         if (!t.mma) t.stretches = 0;
+        // Waves where several pairs of row tiles may share more keys than L2 keeps (the kernel
+        // looks at the lengths themselves).
+        else if ((int64_t)T * G > 1024 && (double)R * Hk * max_len * 4 * D > (64 << 20)) t.waves = 8;
+        t.stretches *= t.waves;
     }
     return t;
 }
@@ -605,6 +616,7 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, const ChunkPlan& plan, 
     ChunkParams q = p;
     q.cluster = plan.cluster;
     q.ctas = plan.stretches;
+    q.waves = plan.waves;
     q.tile_tokens = 128 / q.G;
     cudaError_t e = cudaSuccess;
     if (plan.mma && launch_chunk_mma(q, D, f16, plan.grid, s, &e)) {

@@ -68,6 +68,8 @@ constexpr int kItems = 4;         // items dealt out ahead
 constexpr int kBadWords = 12;     // positions of an item's last tiles (three at most), a bit each
 // Length on the line of an item's way in and out, in keys.
 constexpr int kItemKeys = 256;
+// K and V of a wave over the line of work (L2 has 129 MB).
+constexpr int64_t kWaveBytes = 64 << 20;
 // What a wait may take beside its bound, a key tile of the longest context (see kda_tree_mma.cu).
 constexpr uint64_t kTileWaitNs = 20000 * (kItems + 1);
 
@@ -77,6 +79,7 @@ struct Item {
     int t0, t1;                 // key tiles (t1 < 0: no more items)
     int ctx, first;             // the request's context, and its first row of q (packed: in all)
     int end;                    // keys that the last token sees (0: a request that does not fit the call)
+    int part;                   // where its partial rows go (not whole)
     uint8_t two, whole;         // two row tiles; all of the key tiles
 };
 
@@ -260,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return (int64_t)rb * (kItemKeys + ctx) + (int64_t)tt * rb * (rb + 1);
             };
             const int room = (int)gridDim.x / kHalves;
-            int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
             const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
             int item = 0, issued = 0, queries = 0;   // items dealt, K and V tiles and query tiles asked for
             uint32_t raw = 0, raw_phases = ~0u;      // slots whose last copy was a raw one, those copies' phases
@@ -345,9 +347,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             // The requests, 32 at a time: once for the line's length, once for this CTA's stretch of it.
-            int64_t total = 0, begin = 0, end = 0;
+            int64_t total = 0, keys = 0, begin = 0, end = 0, each = 0, rest = 0;
+            int ctas = 1, waves = 1;
 #pragma unroll 1
-            for (int pass = 0; pass < 2; ++pass) {
+            for (int pass = 0; pass <= waves; ++pass) {
+                int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+                const int stretch = (pass - 1) * ctas + cta;
+                if (pass > 0) {
+                    begin = each * stretch + min((int64_t)stretch, rest);
+                    end = begin + each + (stretch < rest ? 1 : 0);
+                }
                 int64_t before = 0;         // length of the requests before r0
 #pragma unroll 1
                 for (int r0 = 0; r0 < p.R && ok; r0 += 32) {
@@ -360,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ctx = fits ? len - n : 0;
                         if (n > 0) {
                             pairs = (n - 1) / pt + 1;
-                            const int64_t keys = (int64_t)ctx + n;
-                            head = pair_at(ctx, pairs - 1) + kItemKeys + (n - (pairs - 1) * pt <= tt ? keys * 4 / 5 + 1 : keys);
+                            const int64_t all = (int64_t)ctx + n;
+                            head = pair_at(ctx, pairs - 1) + kItemKeys + (n - (pairs - 1) * pt <= tt ? all * 4 / 5 + 1 : all);
+                            if (pass == 0) keys += all;
                         }
                     }
                     int64_t upto = head * p.Hk;
@@ -430,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (at - kItemKeys < begin && next <= begin) x.t0 = tiles;   // (an item before the stretch)
                             x.whole = x.t0 == 0 && x.t1 == tiles;
                             if (x.t1 > x.t0) {
+                                x.part = 2 * stretch + (x.t0 > 0 ? 0 : 1);
                                 if (!x.whole) slots[x.t0 > 0 ? 0 : 1] = make_int4(x.t1 == tiles ? 2 : 1, x.r, x.h, rb);
                                 deal();
                                 load();
@@ -441,29 +452,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (pass == 0) {
-                    // equal stretches, of at least two key tiles
-                    const int64_t most = total / (2 * kKeys);
-                    const int ctas = most < 1 ? 1 : most < room ? (int)most : room;
-                    if (cta >= ctas) break;
-                    int64_t each = 0, rest = total;   // a division in few instructions: it runs once
-#pragma unroll 1
-                    for (int bit = 46; bit >= 0; --bit)
-                        if (rest >> bit >= ctas) {
-                            rest -= (int64_t)ctas << bit;
-                            each += (int64_t)1 << bit;
-                        }
-                    begin = each * cta + min((int64_t)cta, rest);
-                    end = begin + each + (cta < rest ? 1 : 0);
+                if (pass > 0) {
+                    // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
+                    if (half == 0 && lane == 0) {
+                        p.parts[2 * stretch] = slots[0];
+                        p.parts[2 * stretch + 1] = slots[1];
+                    }
+                    continue;
                 }
+                // Equal stretches, of at least two key tiles.  Where the row tiles of a key head share
+                // keys that do not stay in L2 (kWaveBytes of K and V), the line is walked in waves: all
+                // CTAs on one part of it, then on the next, of at least 64 key tiles a CTA.
+                const int64_t most = total / (2 * kKeys);
+                ctas = most < 1 ? 1 : most < room ? (int)most : room;
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+                keys *= p.Hk;
+#pragma unroll 1
+                while (waves < p.waves && total > 4 * keys && keys * (4 * D) > waves * kWaveBytes &&
+                       total >= (waves + 1) * ctas * (int64_t)(64 * kKeys))
+                    ++waves;
+                rest = total;   // a division in few instructions: it runs once
+#pragma unroll 1
+                for (int bit = 46; bit >= 0; --bit)
+                    if (rest >> bit >= ctas * waves) {
+                        rest -= (int64_t)(ctas * waves) << bit;
+                        each += (int64_t)1 << bit;
+                    }
+                if (half == 0 && lane < 2)   // the stretches that are not there
+                    for (int k = ctas * waves + cta; k < room * p.waves; k += room) p.parts[2 * k + lane] = make_int4(0, 0, 0, 0);
+                if (cta >= ctas) break;
             }
             x.t1 = -1;
             if (ok) deal();
-            // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
-            if (half == 0 && lane == 0 && cta < room) {
-                p.parts[2 * cta] = slots[0];
-                p.parts[2 * cta + 1] = slots[1];
-            }
             if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
             // the last copies into this CTA's memory
 #pragma unroll 1
@@ -745,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = empty ? 0.f : 1.f / ml.y;
                 f0 *= inv;
                 f1 *= inv;
-                const int64_t part = (int64_t)(2 * cta + (x.t0 > 0 ? 0 : 1)) * 256 + a * 128 + row;
+                const int64_t part = (int64_t)x.part * 256 + a * 128 + row;
                 T* const dst = static_cast<T*>(p.out) + (p.cu ? (int64_t)(x.first + token) * p.os[1]
                                                               : x.r * p.os[0] + token * p.os[1]) +
                                (x.h * G + in_head) * p.os[2] + half * kV;

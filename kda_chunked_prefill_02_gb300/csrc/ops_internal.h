@@ -122,7 +122,8 @@ struct ChunkParams {
     float* part_o;
     float* part_lse;
     int4* parts;
-    int ctas;                 // mma: stretches of the line of work
+    int ctas;                 // mma: stretches of the line of work, at most
+    int waves;                // mma: waves over it that the workspace has room for
     int tile_tokens;          // mma: tokens a row tile (set by the launcher, as what follows)
     int k_paged, v_paged;     // the head is part of the map's page coordinate
     int wide_out;             // rows of out are 32-byte aligned
@@ -134,7 +135,8 @@ struct ChunkParams {
 struct ChunkPlan {
     bool mma;                 // the tensor-core kernel
     int grid;                 // and its CTAs
-    int stretches;            // its equal stretches of work (with head size 256 two CTAs share one)
+    int stretches;            // its equal stretches of work at most (with head size 256 two CTAs share one)
+    int waves;                // and the waves that they belong to
     int cluster;              // rows kernel: CTAs that share an item
 };
 ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int page, float scale, bool in_place,
