@@ -285,9 +285,10 @@ kda_status kda_tree_attention_schedule(const kda_tree_attention_args* args, int 
  * table can address); it sets how the work is cut, not the result's definition.  Give it
  * where the table is much wider than the contexts.
  * A request whose context length is below zero, above max_context, or with its new tokens
- * past what a row of the page table addresses gives zero rows (lse -inf), one whose
- * cu_seqlens decreases or passes seqlen has none; a page outside 0 .. num_pages - 1 reads
- * as zeros; all are reported in device_status.
+ * past what a row of the page table addresses gives zero rows (lse -inf); a page outside
+ * 0 .. num_pages - 1 reads as zeros; both are reported in device_status.  cu_seqlens that
+ * does not start at 0, decreases or passes seqlen is reported too, and which of the call's
+ * requests are computed is then not defined (rows of q and out of the call alone are used).
  * workspace: kda_chunk_attention_workspace_size(args) bytes, 256-byte aligned, used
  * during the call's kernels only.
  * Size limits: R <= 65535, Hk <= 65535, Hq / Hk <= 65536, tokens (of a request where padded)
@@ -431,8 +432,9 @@ kda_status kda_pool_copy(const kda_pool_copy_args* args, void* stream);
  * A path that does not ascend or leaves the page table's row, an accepted[r] outside 0 ..
  * max_path or a context below zero leaves the request out, a page outside the pool the
  * row; both are reported in device_status.  No other request may use the pages that rows
- * are moved to.  All caches have the same rows (the page size).
- * Size limits: max_path <= 256, R and num_caches <= 65535, a request's tokens <= 2^30.
+ * are moved to.  All caches have the same rows (the page size), and do not overlap.
+ * Size limits: max_path <= 256, R and num_caches <= 65535, a request's tokens <= 2^30, a row
+ * of a page up to 16 MB.
  */
 typedef struct kda_cache_commit_args {
     const kda_pool* caches;     /* host array [num_caches] */

@@ -14,8 +14,9 @@
 // Where the blocks are few, a cluster of up to 8 CTAs shares one, an equal stretch of
 // its tiles each, and joins the rows through distributed shared memory.
 //
-// Which request a block belongs to is found on the device: a call's grid has room for
-// floor(tokens * G / rows) + requests blocks, as many as ragged requests can need.
+// Which request a block belongs to is found on the device, by a search in cu_seqlens: a
+// call's grid has floor(tokens * G / rows) + requests blocks, as many as ragged requests can
+// need.
 //
 // Keys behind a row's own are taken out of the scores by a select; V rows past the
 // request's end are zero-filled, and a tile in which some row does not see a key whose V
@@ -51,50 +52,42 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int cluster = kCluster ? p.cluster : 1, rank = kCluster ? blockIdx.x % cluster : 0;
     const int kvh = blockIdx.y;
-    // this CTA's block of rows: the requests' blocks one after the other
-    if (warp == 0) {
-        const int64_t at = blockIdx.x / cluster;
-        int64_t before = 0;
-        int request = -1, block = 0;
-        if (!p.cu) {
-            const int each = (int)(((int64_t)p.T * p.G + kRows - 1) / kRows);
-            request = (int)(at / each);
-            block = (int)(at - (int64_t)request * each);
-        } else {
-            for (int r0 = 0; r0 < p.R; r0 += 32) {
-                int first, n = 0, len, blocks = 0;
-                if (r0 + lane < p.R) {
-                    const bool ok = chunk_request(p, r0 + lane, first, n, len);
-                    if (!ok && p.status && at == 0 && rank == 0 && kvh == 0) atomicExch(p.status, 1);
-                    blocks = (int)(((int64_t)n * p.G + kRows - 1) / kRows);
-                }
-                int upto = blocks;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                const int64_t off = at - before - (upto - blocks);
-                const uint32_t here = __ballot_sync(0xffffffffu, off >= 0 && off < blocks);
-                if (here && request < 0) {
-                    const int who = __ffs(here) - 1;
-                    request = r0 + who;
-                    block = __shfl_sync(0xffffffffu, (int)off, who);
-                    if (at > 0) break;   // the first block looks at every request
-                }
-                before += __shfl_sync(0xffffffffu, upto, 31);
+    const int64_t at = blockIdx.x / cluster;
+    if (p.cu) {
+        // Request r has the blocks from floor(cu[r] G / kRows) + r up to the next one's: never fewer
+        // than it needs.  A warp looks at 32 requests at a time, evenly spread over those left.
+        if (warp == 0) {
+            const auto begin = [&](int i) { return (int64_t)p.cu[i] * p.G / kRows + i; };
+            int lo = 0, hi = p.R;   // begin(lo) <= at < begin(hi)
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32, i = lo + step * lane;
+                const uint32_t before = __ballot_sync(0xffffffffu, i < hi && begin(i) <= at) | 1u;
+                const int last = 31 - __clz(before);
+                hi = min(hi, lo + step * (last + 1));
+                lo += step * last;
+            }
+            if (lane == 0) {
+                s_request = lo;
+                s_block = (int)max((int64_t)0, min(at - begin(lo), (int64_t)INT32_MAX / kRows));
             }
         }
-        if (lane == 0) {
-            s_request = request;
-            s_block = block;
+        // every request's lengths are looked at by one thread (there are R blocks at least)
+        const int64_t mine = at * kChunkThreads + tid;
+        if (kvh == 0 && rank == 0 && p.status && mine < p.R) {
+            int first, n, len;
+            if (!chunk_request(p, (int)mine, first, n, len)) atomicExch(p.status, 1);
         }
+        __syncthreads();
+    } else {
+        const int64_t each = ((int64_t)p.T * p.G + kRows - 1) / kRows;
+        s_request = (int)(at / each);   // (all threads write the same)
+        s_block = (int)(at - at / each * each);
+        __syncthreads();
     }
-    __syncthreads();
     const int r = s_request, row0 = s_block * kRows;
-    if (r < 0) return;   // no such block (all CTAs of a cluster)
     int first, n, len;
     if (!chunk_request(p, r, first, n, len) && !p.cu && p.status && tid == 0) atomicExch(p.status, 1);
+    if (row0 >= n * p.G) return;   // no such block (all CTAs of a cluster)
     const int rows = n * p.G, ctx = len - n;   // without keys (len 0) no row sees any
     const int token0 = (int)page_div((uint32_t)row0, p.G, p.group_magic);
     const int token1 = min((int)page_div((uint32_t)(row0 + kRows - 1), p.G, p.group_magic), n - 1);

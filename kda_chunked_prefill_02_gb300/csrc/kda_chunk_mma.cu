@@ -66,7 +66,9 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 2
 constexpr int kMaxSlots = 8, kMaxQ = 3;
 constexpr int kItems = 4;         // items dealt out ahead
 constexpr int kBadWords = 12;     // positions of an item's last tiles (three at most), a bit each
-// Length on the line of an item's way in and out, in keys.
+// Length on the line of an item's way in and out, in keys: with 128, 256, 384, 640 an 8192-token
+// prompt (32 / 8 heads) takes 360, 337, 344, 347 us, four of 2048 132, 126, 128, 138, 24 ragged
+// prompts of head size 64 82, 77, 79, 75.
 constexpr int kItemKeys = 256;
 // K and V of a wave over the line of work (L2 has 129 MB).
 constexpr int64_t kWaveBytes = 64 << 20;
@@ -159,7 +161,7 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const vo
 #pragma unroll 1
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (i % 64 == 0 && (*abort || i >> 27)) return false;
+        if (i % 64 == 0 && (*abort || i >> 31)) return false;
     }
 }
 
@@ -255,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&vmap);
             }
             // A request's length on the line: over its pairs of row tiles, the keys of each one's
-            // last token (a last single row tile four fifths of them, as measured) and kItemKeys,
-            // times the key heads.
+            // last token (a last single row tile four fifths of them: 60 single tokens over 4096 and
+            // four pieces 225 us, 252 with all of them) and kItemKeys, times the key heads.
             const int pt = 2 * tt;          // tokens a pair
             // where pair `rb` begins on a head's part of the line
             auto pair_at = [&](int ctx, int rb) -> int64_t {
@@ -374,6 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (pass == 0) keys += all;
                         }
                     }
+                    if (pass == 0) {
+                        if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
+                        total += head * p.Hk;   // this lane's
+                        continue;
+                    }
                     int64_t upto = head * p.Hk;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -382,11 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int64_t here = before;
                     before += __shfl_sync(0xffffffffu, upto, 31);
-                    if (pass == 0) {
-                        if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
-                        total = before;
-                        continue;
-                    }
                     if (here >= end) break;
                     // the requests of these that meet the stretch
                     uint32_t meet = __ballot_sync(0xffffffffu, n > 0 && here + upto > begin && here + upto - head * p.Hk < end);
@@ -463,10 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Equal stretches, of at least two key tiles.  Where the row tiles of a key head share
                 // keys that do not stay in L2 (kWaveBytes of K and V), the line is walked in waves: all
                 // CTAs on one part of it, then on the next, of at least 64 key tiles a CTA.
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) {
+                    keys += __shfl_xor_sync(0xffffffffu, keys, o);
+                    total += __shfl_xor_sync(0xffffffffu, total, o);
+                }
                 const int64_t most = total / (2 * kKeys);
                 ctas = most < 1 ? 1 : most < room ? (int)most : room;
-#pragma unroll 1
-                for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
                 keys *= p.Hk;
 #pragma unroll 1
                 while (waves < p.waves && total > 4 * keys && keys * (4 * D) > waves * kWaveBytes &&

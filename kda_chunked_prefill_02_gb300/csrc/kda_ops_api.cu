@@ -87,8 +87,7 @@ kda_status check_chunk(const kda_chunk_attention_args* a) {
         a->page_size > (1 << 30) || a->pages_per_request > INT32_MAX || a->page_table_stride < 0 ||
         a->seqlen > INT32_MAX / group)
         return KDA_ERR_UNSUPPORTED;
-    if (a->num_requests == 0) return a->cu_seqlens && a->seqlen > 0 ? KDA_ERR_INVALID_ARG : KDA_OK;
-    if (a->seqlen == 0) return KDA_OK;
+    if (a->num_requests == 0 || a->seqlen == 0) return KDA_OK;
     if (!a->q || !a->k_cache || !a->v_cache || !a->out || !a->page_table || !a->context_lens || a->num_pages < 1)
         return KDA_ERR_INVALID_ARG;
     if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->out) ||
@@ -440,6 +439,7 @@ kda_status kda_cache_commit(const kda_cache_commit_args* a, void* stream) {
         if (a->caches[k].rows < 1 || a->caches[k].rows != a->caches[0].rows || a->caches[k].cols < 1 ||
             a->caches[k].bytes < 16)
             return KDA_ERR_INVALID_ARG;
+        if (a->caches[k].cols * a->caches[k].bytes > (16 << 20)) return KDA_ERR_UNSUPPORTED;
     }
     if (a->num_caches == 0 || a->num_requests == 0 || a->max_path == 0) return KDA_OK;
     if (!a->page_table || !a->context_lens || !a->path || !a->accepted) return KDA_ERR_INVALID_ARG;

@@ -164,6 +164,8 @@ cudaError_t launch_cache_commit(const CacheCommitParams& q, int num_sms, cudaStr
     const int64_t pairs = (int64_t)p.R * p.pools;
     p.group = same ? (int)((pairs + 12 * num_sms - 1) / (12 * num_sms)) : 1;
     if (p.group > p.pools) p.group = p.pools;
+    // a CTA's pieces are counted in 32 bits
+    while (p.group > 1 && (int64_t)p.max_path * row(0) * p.group > (1 << 30)) p.group /= 2;
     int64_t splits = 2 * num_sms / pairs;
     if (splits > least / 8) splits = least / 8;
     if (splits < 1) splits = 1;

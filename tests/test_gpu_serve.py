@@ -127,6 +127,29 @@ def test_chunk_many_requests():
     _chunk_case(6, ctx[:70], new[:70], 8, 2, 128, 16, F16, max_context=max(ctx))
 
 
+@pytest.mark.parametrize("kernel", ["rows", "tensor"])
+def test_chunk_thousands_of_requests(kernel):
+    """Runs of requests without tokens among single tokens and short pieces; a decrease of
+    cu_seqlens is reported wherever it is."""
+    R = 5000
+    new = [0 if i % 9 < 6 else 1 + (i % 5) * (i % 70 == 7) for i in range(R)]
+    ctx = [(i * 7) % 30 for i in range(R)]
+    D = 64 if kernel == "rows" else 128
+    q, kc, vc, table, lens, cu = _chunk_inputs(27, ctx, new, 2, 1, D, 16, BF16, 0 if kernel == "rows" else 20000)
+    dev = [t.cuda() for t in (q, kc, vc, table, lens)]
+    assert _kernel(q, kc, table) == kernel
+    status = _status()
+    got = K.kda_chunk_attention(*dev, cu_seqlens=cu.cuda(), device_status=status)
+    assert status.item() == 0
+    _check(q, kc, vc, table, lens, cu, got, None)
+    for at in (1, 31, 32, 33, 2500, 4999):
+        bad = cu.clone()
+        bad[at] = -1 if at % 2 else int(cu[-1]) + 1
+        status.zero_()
+        K.kda_chunk_attention(*dev, cu_seqlens=bad.cuda(), device_status=status)
+        assert status.item() == 1
+
+
 @pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("T", [1, 3, 40, 140])
 def test_chunk_padded(T, room):
@@ -274,11 +297,12 @@ def test_chunk_reports_what_only_the_device_sees(room):
         assert bool((got[a:b] == 0).all()) and bool((lse[a:b] == -math.inf).all())
         within(got[:a], out[:a], ob[:a])
         within(got[b:b + 1], out[b:b + 1], ob[b:b + 1])
-    # a request that decreases or passes the rows has none; the others are computed where
-    # their own bounds stand
+    # bounds that do not start at 0, decrease, or pass the rows
     for bad in ([0, 9, 200, 80, 110], [0, 9, 5, 80, 110], [0, 9, -4, 80, 110], [3, 9, 79, 80, 110]):
         got, _, st = run(lens, _i32(bad))
         assert st == 1
+    for good in ([0, 9, 9, 9, 9], [0, 0, 0, 0, 0], [0, 9, 79, 80, 100]):
+        assert run(lens, _i32(good))[2] == 0
     # pages outside the pool read as zeros
     t2 = table.clone()
     t2[1, 2], t2[1, 3] = kc.shape[0], -5

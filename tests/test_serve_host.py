@@ -49,7 +49,7 @@ def test_chunk_refusals(ops):
     for kw in (dict(q=None), dict(k_cache=None), dict(v_cache=None), dict(out=None), dict(page_table=None),
                dict(context_lens=None), dict(seqlen=-1), dict(num_requests=-1), dict(num_q_heads=7),
                dict(num_k_heads=0), dict(num_pages=0), dict(page_size=0), dict(pages_per_request=-1),
-               dict(scale=math.nan), dict(scale=math.inf), dict(num_requests=0, cu_seqlens=PTR),
+               dict(scale=math.nan), dict(scale=math.inf),
                dict(out=PTR, out_stride0=4096), dict(out=PTR, out_stride1=2048), dict(out=PTR, out_stride2=256),
                dict(out=PTR, out_stride2=256, cu_seqlens=PTR)):
         assert run(**kw) == BAD, kw
@@ -57,7 +57,8 @@ def test_chunk_refusals(ops):
                dict(k_cache=PTR + 8), dict(q_stride1=1020), dict(v_cache_stride0=-8), dict(num_requests=70000),
                dict(pages_per_request=1 << 30), dict(seqlen=1 << 30), dict(page_table_stride=-1)):
         assert run(**kw) == NO, kw
-    assert run(num_requests=0) == 0 and run(seqlen=0) == 0 and run(seqlen=0, cu_seqlens=PTR) == 0
+    for kw in (dict(num_requests=0), dict(seqlen=0)):
+        assert run(**kw) == 0 and run(cu_seqlens=PTR, **kw) == 0, kw
 
 
 def test_chunk_workspace_of_what_is_refused(ops):
@@ -180,7 +181,8 @@ def test_commit_refusals(ops):
                dict(pool=dict(rows=8, stride0=8192)), dict(pool=dict(cols=0)), dict(second=dict(bytes=0))):
         assert run(**kw) == BAD, kw
     for kw in (dict(num_caches=70000), dict(num_requests=70000), dict(max_path=257), dict(pages_per_request=1 << 31),
-               dict(page_table_stride=-1), dict(pages_per_request=1 << 27)):
+               dict(page_table_stride=-1), dict(pages_per_request=1 << 27),
+               dict(pool=dict(cols=1 << 10, bytes=1 << 15))):
         assert run(**kw) == NO, kw
     for kw in POOL_BAD:
         assert run(pool=kw) == BAD and run(second=kw) == BAD, kw
