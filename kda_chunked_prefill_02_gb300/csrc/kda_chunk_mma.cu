@@ -66,9 +66,9 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 2
 constexpr int kMaxSlots = 8, kMaxQ = 3;
 constexpr int kItems = 4;         // items dealt out ahead
 constexpr int kBadWords = 12;     // positions of an item's last tiles (three at most), a bit each
-// Length on the line of an item's way in and out, in keys: with 128, 256, 384, 640 an 8192-token
-// prompt (32 / 8 heads) takes 360, 337, 344, 347 us, four of 2048 132, 126, 128, 138, 24 ragged
-// prompts of head size 64 82, 77, 79, 75.
+// Length on the line of an item's way in and out, in keys: with 128, 192, 256, 384 an 8192-token
+// prompt (32 / 8 heads) takes 364, 351, 345, 351 us, four of 2048 130, 125, 125, 126, 24 ragged
+// prompts of head size 64 74, 65, 65, 65.
 constexpr int kItemKeys = 256;
 // K and V of a wave over the line of work (L2 has 129 MB).
 constexpr int64_t kWaveBytes = 64 << 20;
@@ -92,7 +92,7 @@ struct Misc {
     uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], ml_full[2], ml_free[2];
     uint64_t item_full[kItems], item_free[kItems], drained[2], never;   // never: the probe's, nothing arrives on it
     float2 ml[2][128];          // the rows' maximum and sum, a stream each
-    uint32_t bad[kItems][kBadWords];   // positions with a V element that is not finite
+    alignas(16) uint32_t bad[kItems][kBadWords];   // positions with a V element that is not finite
     Item item[kItems];
     uint32_t tmem;
     int abort;
@@ -153,15 +153,38 @@ __device__ __forceinline__ bool all_finite(const uint4 (&y)[N]) {
     return (sum & 0x7fff7fffu) == 0;
 }
 
-// The other roles' wait: no clock of its own, which every use of it would add to the code (the
-// roles' code does not fit the instruction cache together, and an item's change takes as long as
-// fetching it).  What holds a role up holds up the rows' way out too, whose waits run out by the
-// clock and set the abort flag; the number of tries ends this one in any case.
+// The waits are loops of few instructions: the roles' code does not fit the instruction cache
+// together, and an item's change takes as long as fetching it (unrolled by the compiler, the
+// same waits cost 32 prompts of 512 tokens 133 us instead of 119).
+//
+// The rows' way out waits by the clock, up to 20 us a try: its polls take issue slots from the
+// softmax (head size 64: 8192 tokens 302 us without that, 286 with it).
+__device__ __forceinline__ bool wait_out(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (*abort) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > limit_ns) return false;
+    }
+}
+// The other roles' wait has no clock.  What holds a role up holds up the rows' way out too,
+// whose waits run out and set the abort flag; the number of tries ends this one in any case.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const volatile int* abort) {
 #pragma unroll 1
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (i % 64 == 0 && (*abort || i >> 31)) return false;
+        if (*abort || i >> 31) return false;
     }
 }
 
@@ -400,46 +423,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   q_pairs = __shfl_sync(0xffffffffu, pairs, who);
                         const bool q_fits = __shfl_sync(0xffffffffu, (int)fits, who) != 0;
                         const int64_t q_head = __shfl_sync(0xffffffffu, head, who);
-                        const int64_t start = here + __shfl_sync(0xffffffffu, upto, who) - q_head * p.Hk;
+                        int64_t place = __shfl_sync(0xffffffffu, here + upto - head * p.Hk, who);   // of the item on the line
                         x.r = r0 + who;
                         x.first = __shfl_sync(0xffffffffu, first, who);
                         x.ctx = q_ctx;
-                        // the head, and the pair, that hold the stretch's begin
-                        int64_t off = begin > start ? begin - start : 0;
-                        int lo = 0, hi = p.Hk;
+                        x.h = 0;
+                        int rb = 0;
+                        if (place < begin) {   // the head, and the pair, that hold the stretch's begin
+                            int hi = p.Hk;
 #pragma unroll 1
-                        while (hi - lo > 1) {
-                            const int mid = (lo + hi) >> 1;
-                            if (mid * q_head <= off) lo = mid; else hi = mid;
+                            while (hi - x.h > 1) {
+                                const int mid = (x.h + hi) >> 1;
+                                if (place + mid * q_head <= begin) x.h = mid; else hi = mid;
+                            }
+                            place += x.h * q_head;
+                            hi = q_pairs;
+#pragma unroll 1
+                            while (hi - rb > 1) {
+                                const int mid = (rb + hi) >> 1;
+                                if (place + pair_at(q_ctx, mid) <= begin) rb = mid; else hi = mid;
+                            }
+                            place += pair_at(q_ctx, rb);
                         }
-                        x.h = lo;
-                        off -= x.h * q_head;
-                        lo = 0;
-                        hi = q_pairs;
 #pragma unroll 1
-                        while (hi - lo > 1) {
-                            const int mid = (lo + hi) >> 1;
-                            if (pair_at(q_ctx, mid) <= off) lo = mid; else hi = mid;
-                        }
-                        int rb = lo;
-#pragma unroll 1
-                        while (ok) {
-                            const int64_t at = start + x.h * q_head + pair_at(q_ctx, rb) + kItemKeys;   // where its keys begin
-                            if (at - kItemKeys >= end) break;
+                        while (ok && place < end) {
                             x.token0 = rb * pt;
                             x.tokens = min(q_n - x.token0, pt);
                             x.two = x.tokens > tt;
-                            x.end = q_fits ? q_ctx + x.token0 + x.tokens : 0;
+                            const int keys_all = q_ctx + x.token0 + x.tokens;
+                            x.end = q_fits ? keys_all : 0;
                             const int tiles = max(1, (x.end + kKeys - 1) / kKeys);
                             // key tiles before a place on the line: one in 128 (102.4) of the keys' part
-                            auto tiles_before = [&](int64_t place) -> int {
-                                const int64_t in = max((int64_t)0, place - at);
+                            const int64_t next = place + kItemKeys + (x.two ? keys_all : keys_all * (int64_t)4 / 5 + 1);
+                            auto tiles_before = [&](int64_t to) -> int {
+                                const int64_t in = max((int64_t)0, to - place - kItemKeys);
                                 return (int)min((int64_t)tiles, x.two ? (in + 127) >> 7 : (5 * in + 511) >> 9);
                             };
-                            x.t0 = tiles_before(begin);
-                            const int64_t next = start + (rb + 1 < q_pairs ? x.h * q_head + pair_at(q_ctx, rb + 1) : (x.h + 1) * q_head);
+                            x.t0 = next <= begin ? tiles : tiles_before(begin);   // (an item before the stretch)
                             x.t1 = next <= end ? tiles : tiles_before(end);
-                            if (at - kItemKeys < begin && next <= begin) x.t0 = tiles;   // (an item before the stretch)
+                            place = next;
                             x.whole = x.t0 == 0 && x.t1 == tiles;
                             if (x.t1 > x.t0) {
                                 x.part = 2 * stretch + (x.t0 > 0 ? 0 : 1);
@@ -578,10 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
             };
-            // Every product's place in the code is one: what an item's change costs is fetching it.
-            bool more = enter(), begun = false, pending = false;
+            // One place in the code for an item's change and for what both ends of the line share:
+            // what an item's change costs is fetching it.
+            bool fresh = true, begun = false, pending = false;
 #pragma unroll 1
-            while (more && ok) {
+            while (ok) {
                 bool waited = false;   // for the next scores' keys
                 if (pending) {
                     // the second product of tile j
@@ -631,10 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         base += kPer * tiles;
                         queries += two ? 2 : 1;
                         ++item;
-                        more = enter();
-                        if (!more) break;
+                        fresh = true;
                     }
                 }
+                if (fresh && !enter()) break;
+                fresh = false;
                 // Scores of tile j: as many keys as its rows see.  With two row tiles the softmax warps
                 // give K, V and the queries back, once they have seen the scores: a commit takes the
                 // issuer and the tensor pipe some 100 cycles.
@@ -730,11 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int in_token = (int)page_div((uint32_t)row, G, p.group_magic), in_head = row - in_token * G;
         const float c = p.scale_log2;
-        uint32_t outs[2] = {0, 0};    // items of each stream
+        uint32_t outs = 0;            // items of each stream, odd or even
         bool ok = true;
         Item x;
         for (int item = 0;; ++item) {
-            ok = ok && wait_for(&m.item_full[item % kItems], (item / kItems) & 1, abort, limit);
+            ok = ok && wait_out(&m.item_full[item % kItems], (item / kItems) & 1, abort, limit);
             if (!__all_sync(0xffffffffu, take(item, x, ok)) || !ok) break;
             const bool joined = !x.two && x.t1 - x.t0 > 1;
             const int special = clean_from(x);
@@ -742,18 +766,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // one row tile: one pass over both streams; two: a pass each
             for (int a = 0; a < (x.two ? 2 : 1) && ok; ++a) {
                 const int s = a, s2 = a ^ 1;
-                ok = wait_for(&m.ml_full[s], outs[s] & 1, abort, limit) && wait_for(&m.o_full[s], outs[s] & 1, abort, limit);
-                if (joined)
-                    ok = ok && wait_for(&m.ml_full[s2], outs[s2] & 1, abort, limit) &&
-                         wait_for(&m.o_full[s2], outs[s2] & 1, abort, limit);
+#pragma unroll 1
+                for (int w = 0; w < (joined ? 4 : 2); ++w) {   // the rows' statistics and O, of s and then of s2
+                    const int t = w < 2 ? s : s2;
+                    ok = ok && wait_out(w & 1 ? &m.o_full[t] : &m.ml_full[t], (outs >> t) & 1, abort, limit);
+                }
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                ++outs[s];
+                outs ^= joined ? 3 : 1 << s;
                 float2 ml = m.ml[s][row];
                 float f0 = 1.f, f1 = 0.f;
                 if (joined) {
-                    ++outs[s2];
                     const float2 o = m.ml[s2][row];
                     const float mj = fmaxf(ml.x, o.x), mu = mj == -INFINITY ? 0.f : mj;
                     f0 = ex2_approx((ml.x - mu) * c);
@@ -779,7 +803,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t any_bad = 0;
                 if (cleaned) {
 #pragma unroll
-                    for (int w = 0; w < kBadWords; ++w) any_bad |= m.bad[item % kItems][w];
+                    for (int w = 0; w < kBadWords; w += 4) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(&m.bad[item % kItems][w]);
+                        any_bad |= y.x | y.y | y.z | y.w;
+                    }
                 }
                 const uint32_t to = tb + lane_base + kTmemO + 128 * s, to2 = tb + lane_base + kTmemO + 128 * s2;
 #pragma unroll 1
@@ -907,9 +934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         if (32 * g + 32 <= n_all) continue;
+                        const uint32_t hidden = n >= 32 * g + 32 ? 0u : n <= 32 * g ? ~0u : ~0u << (n - 32 * g);
 #pragma unroll
-                        for (int e = 32 * g; e < 32 * g + 32; ++e)
-                            if (e >= n) v[e] = -INFINITY;
+                        for (int e = 0; e < 32; ++e)
+                            if ((hidden >> e) & 1u) v[32 * g + e] = -INFINITY;
                     }
                 }
                 float t8[8];
