@@ -4,8 +4,9 @@ The compute lives in libkda.so (C ABI, include/kda.h); ``kda`` is its ctypes
 binding, and ``ops`` that of the operators around KDA (include/kda_ops.h): the
 short causal convolution, the query / key norm with rotation, the attention of
 prompts and of drafted tokens over a paged cache, the residual stream's norm, and the
-moves in caches and pools that verified trees and forked requests need.  Importing this package loads nothing; the library is loaded on the
-first call and its absence is an error, never a fallback.
+moves in caches and pools that verified trees and forked requests need.  Importing
+this package loads nothing; the library is loaded on the first call and its absence
+is an error, never a fallback.
 """
 from .kda import (CHUNK, HEAD_DIM, KdaError, host_staging_size, kda_prefill,  # noqa: F401
                   overrides, prefill_schedule,

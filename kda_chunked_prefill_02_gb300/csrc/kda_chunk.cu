@@ -18,6 +18,9 @@
 // call's grid has floor(tokens * G / rows) + requests blocks, as many as ragged requests can
 // need.
 //
+// Few rows are bound by a chain of latencies (lengths, page table, K and V, products, join): one
+// token over 1000 keys, 8 / 2 heads 7.6 us, 16 tokens 10.4.
+//
 // Keys behind a row's own are taken out of the scores by a select; V rows past the
 // request's end are zero-filled, and a tile in which some row does not see a key whose V
 // is not finite takes a scalar product that leaves out what a row does not see

