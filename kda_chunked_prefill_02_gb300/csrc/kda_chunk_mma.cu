@@ -295,8 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pt = 2 * tt;          // tokens a pair
             // where pair `rb` begins on a head's part of the line
             auto pair_at = [&](int ctx, int rb) -> int64_t {
-                return (int64_t)rb * (kItemKeys + ctx) + (int64_t)tt * rb * (rb + 1);
+                return (int64_t)rb * (uint32_t)(kItemKeys + ctx + tt * (rb + 1));   // (32 bits: contexts and tokens have 30)
             };
+            // four fifths of a single row tile's keys
+            auto single = [](int keys) -> int { return keys - (int)(((uint32_t)keys + 4u) / 5u) + 1; };
             const int room = (int)gridDim.x / kHalves;
             const int box = box_of(p.page), per_tile = kKeys / box;   // this lane's box: tokens lane * box ..
             int item = 0, issued = 0, queries = 0;   // items dealt, K and V tiles and query tiles asked for
@@ -381,39 +383,93 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            // The requests, 32 at a time: once for the line's length, once for this CTA's stretch of it.
-            int64_t total = 0, keys = 0, begin = 0, end = 0, each = 0, rest = 0;
-            int ctas = 1, waves = 1;
-#pragma unroll 1
-            for (int pass = 0; pass <= waves; ++pass) {
-                int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
-                const int stretch = (pass - 1) * ctas + cta;
-                if (pass > 0) {
-                    begin = each * stretch + min((int64_t)stretch, rest);
-                    end = begin + each + (stretch < rest ? 1 : 0);
+            // Of a request (its lengths at q): true if they fit the call; its first token, new tokens,
+            // context, pairs of row tiles and length on a key head's line.
+            auto request = [&](int r, const ChunkLengths& q, int& first, int& n, int& ctx, int& pairs, int64_t& head) -> bool {
+                int len;
+                const bool fits = chunk_request(p, r, q, first, n, len);
+                ctx = fits ? len - n : 0;
+                pairs = 0;
+                head = 0;
+                if (n > 0) {
+                    pairs = (n - 1) / pt + 1;
+                    const int all = ctx + n;
+                    head = pair_at(ctx, pairs - 1) + kItemKeys + (n - (pairs - 1) * pt <= tt ? single(all) : all);
                 }
-                int64_t before = 0;         // length of the requests before r0
+                return fits;
+            };
+            // The line's length.  Until the first tile is loaded the ring keeps the length of every 32
+            // requests, so that this CTA begins with its own.
+            // (asked for four rounds ahead: a round is a few instructions.)
+            int64_t* const groups = reinterpret_cast<int64_t*>(ring);
+            int64_t total = 0, keys = 0, each = 0, rest = 0;
+            const auto lengths = [&](int r) { return chunk_lengths(p, min(r, p.R - 1)); };
+            ChunkLengths q0 = lengths(lane), q1 = lengths(lane + 32), q2 = lengths(lane + 64), q3 = lengths(lane + 96);
 #pragma unroll 1
-                for (int r0 = 0; r0 < p.R && ok; r0 += 32) {
+            for (int r0 = 0; r0 < p.R; r0 += 32) {
+                const ChunkLengths q = q0;
+                q0 = q1;
+                q1 = q2;
+                q2 = q3;
+                q3 = lengths(r0 + 128 + lane);
+                int first, n = 0, ctx, pairs;
+                int64_t head = 0;
+                if (r0 + lane < p.R) {
+                    const bool fits = request(r0 + lane, q, first, n, ctx, pairs, head);
+                    if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
+                    if (n > 0) keys += ctx + n;
+                }
+                head *= p.Hk;
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) head += __shfl_xor_sync(0xffffffffu, head, o);
+                total += head;
+                if (lane == 0) groups[r0 / 32] = head;
+            }
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+            __syncwarp();
+            // Equal stretches, of at least two key tiles.  Where the row tiles of a key head share
+            // keys that do not stay in L2 (kWaveBytes of K and V), the line is walked in waves: all
+            // CTAs on one part of it, then on the next, of at least 64 key tiles a CTA.
+            const int64_t most = total / (2 * kKeys);
+            const int ctas = most < 1 ? 1 : most < room ? (int)most : room;
+            int waves = 1;
+            keys *= p.Hk;
+#pragma unroll 1
+            while (waves < p.waves && total > 4 * keys && keys * (4 * D) > waves * kWaveBytes &&
+                   total >= (waves + 1) * ctas * (int64_t)(64 * kKeys))
+                ++waves;
+            rest = total;   // a division in few instructions: it runs once
+#pragma unroll 1
+            for (int bit = 46; bit >= 0; --bit)
+                if (rest >> bit >= ctas * waves) {
+                    rest -= (int64_t)(ctas * waves) << bit;
+                    each += (int64_t)1 << bit;
+                }
+            if (half == 0 && lane < 2)   // the stretches that are not there
+                for (int k = ctas * waves + cta; k < room * p.waves; k += room) p.parts[2 * k + lane] = make_int4(0, 0, 0, 0);
+            // This CTA's stretches of the line, the requests 32 at a time.
+            const int mine = cta < ctas ? waves : 0;
+#pragma unroll 1
+            for (int wave = 0; wave < mine; ++wave) {
+                int4 slots[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+                const int stretch = wave * ctas + cta;
+                const int64_t begin = each * stretch + min((int64_t)stretch, rest);
+                const int64_t end = begin + each + (stretch < rest ? 1 : 0);
+                int64_t before = 0;         // length of the requests before r0
+                int r0 = 0;
+                if (wave == 0) {
+#pragma unroll 1
+                    for (; r0 + 32 < p.R && before + groups[r0 / 32] <= begin; r0 += 32) before += groups[r0 / 32];
+                    fence_proxy_async_smem();   // the ring is the copies' from here on
+                    __syncwarp();
+                }
+#pragma unroll 1
+                for (; r0 < p.R && ok; r0 += 32) {
                     int first = 0, n = 0, ctx = 0, pairs = 0;
                     bool fits = true;
-                    int64_t head = 0;       // length of a key head's items
-                    if (r0 + lane < p.R) {
-                        int len;
-                        fits = chunk_request(p, r0 + lane, first, n, len);
-                        ctx = fits ? len - n : 0;
-                        if (n > 0) {
-                            pairs = (n - 1) / pt + 1;
-                            const int64_t all = (int64_t)ctx + n;
-                            head = pair_at(ctx, pairs - 1) + kItemKeys + (n - (pairs - 1) * pt <= tt ? all * 4 / 5 + 1 : all);
-                            if (pass == 0) keys += all;
-                        }
-                    }
-                    if (pass == 0) {
-                        if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
-                        total += head * p.Hk;   // this lane's
-                        continue;
-                    }
+                    int64_t head = 0;
+                    if (r0 + lane < p.R) fits = request(r0 + lane, lengths(r0 + lane), first, n, ctx, pairs, head);
                     int64_t upto = head * p.Hk;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -464,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x.end = q_fits ? keys_all : 0;
                             const int tiles = max(1, (x.end + kKeys - 1) / kKeys);
                             // key tiles before a place on the line: one in 128 (102.4) of the keys' part
-                            const int64_t next = place + kItemKeys + (x.two ? keys_all : keys_all * (int64_t)4 / 5 + 1);
+                            const int64_t next = place + kItemKeys + (x.two ? keys_all : single(keys_all));
                             auto tiles_before = [&](int64_t to) -> int {
                                 const int64_t in = max((int64_t)0, to - place - kItemKeys);
                                 return (int)min((int64_t)tiles, x.two ? (in + 127) >> 7 : (5 * in + 511) >> 9);
@@ -486,39 +542,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (pass > 0) {
-                    // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
-                    if (half == 0 && lane == 0) {
-                        p.parts[2 * stretch] = slots[0];
-                        p.parts[2 * stretch + 1] = slots[1];
-                    }
-                    continue;
+                // what the two slots hold: 0 nothing, 1 a part of item (r, h, rb), 2 its last
+                if (half == 0 && lane == 0) {
+                    p.parts[2 * stretch] = slots[0];
+                    p.parts[2 * stretch + 1] = slots[1];
                 }
-                // Equal stretches, of at least two key tiles.  Where the row tiles of a key head share
-                // keys that do not stay in L2 (kWaveBytes of K and V), the line is walked in waves: all
-                // CTAs on one part of it, then on the next, of at least 64 key tiles a CTA.
-#pragma unroll 1
-                for (int o = 16; o > 0; o >>= 1) {
-                    keys += __shfl_xor_sync(0xffffffffu, keys, o);
-                    total += __shfl_xor_sync(0xffffffffu, total, o);
-                }
-                const int64_t most = total / (2 * kKeys);
-                ctas = most < 1 ? 1 : most < room ? (int)most : room;
-                keys *= p.Hk;
-#pragma unroll 1
-                while (waves < p.waves && total > 4 * keys && keys * (4 * D) > waves * kWaveBytes &&
-                       total >= (waves + 1) * ctas * (int64_t)(64 * kKeys))
-                    ++waves;
-                rest = total;   // a division in few instructions: it runs once
-#pragma unroll 1
-                for (int bit = 46; bit >= 0; --bit)
-                    if (rest >> bit >= ctas * waves) {
-                        rest -= (int64_t)(ctas * waves) << bit;
-                        each += (int64_t)1 << bit;
-                    }
-                if (half == 0 && lane < 2)   // the stretches that are not there
-                    for (int k = ctas * waves + cta; k < room * p.waves; k += room) p.parts[2 * k + lane] = make_int4(0, 0, 0, 0);
-                if (cta >= ctas) break;
             }
             x.t1 = -1;
             if (ok) deal();

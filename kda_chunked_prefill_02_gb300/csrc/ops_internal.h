@@ -148,21 +148,31 @@ bool launch_chunk_mma(const ChunkParams& p, int D, bool f16, int grid, cudaStrea
 // Request r of a call: its first row of q (packed: in all, padded: 0), its new tokens and
 // the keys it may see; false if they do not fit the call.  Tokens that lie inside the call
 // keep their rows (their results are zero then), others are none.
-__device__ __forceinline__ bool chunk_request(const ChunkParams& p, int r, int& first, int& n, int& len) {
+struct ChunkLengths {
+    int a, b, ctx;   // cu_seqlens of the request and the next one, its context
+};
+__device__ __forceinline__ ChunkLengths chunk_lengths(const ChunkParams& p, int r) {
+    return {p.cu ? p.cu[r] : 0, p.cu ? p.cu[r + 1] : 0, p.ctx[r]};
+}
+__device__ __forceinline__ bool chunk_request(const ChunkParams& p, int r, const ChunkLengths& q, int& first, int& n,
+                                              int& len) {
     bool ok = true;
     first = 0;
     n = p.T;
     if (p.cu) {
-        const int a = p.cu[r], b = p.cu[r + 1];
+        const int a = q.a, b = q.b;
         ok = (r > 0 || a == 0) && a >= 0 && a <= b && b <= p.T;
         first = ok ? a : 0;
         n = ok ? b - a : 0;
     }
-    const int ctx = p.ctx[r];
+    const int ctx = q.ctx;
     len = 0;
     if (ctx < 0 || ctx > p.max_ctx || (int64_t)ctx + n > p.max_len) ok = false;
     else len = ctx + n;
     return ok;
+}
+__device__ __forceinline__ bool chunk_request(const ChunkParams& p, int r, int& first, int& n, int& len) {
+    return chunk_request(p, r, chunk_lengths(p, r), first, n, len);
 }
 
 // The residual stream's norm (kda_residual.cu).
