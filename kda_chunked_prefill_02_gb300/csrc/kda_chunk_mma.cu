@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // requests, so that this CTA begins with its own.
             // (asked for four rounds ahead: a round is a few instructions.)
             int64_t* const groups = reinterpret_cast<int64_t*>(ring);
-            int64_t total = 0, keys = 0, each = 0, rest = 0;
+            int64_t total = 0, keys = 0, walked = 0, each = 0, rest = 0;   // keys: of the requests, and of all row tiles
             const auto lengths = [&](int r) { return chunk_lengths(p, min(r, p.R - 1)); };
             ChunkLengths q0 = lengths(lane), q1 = lengths(lane + 32), q2 = lengths(lane + 64), q3 = lengths(lane + 96);
 #pragma unroll 1
@@ -417,7 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (r0 + lane < p.R) {
                     const bool fits = request(r0 + lane, q, first, n, ctx, pairs, head);
                     if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
-                    if (n > 0) keys += ctx + n;
+                    if (n > 0) {
+                        keys += ctx + n;
+                        walked += head - (int64_t)pairs * kItemKeys;
+                    }
                 }
                 head *= p.Hk;
 #pragma unroll 1
@@ -426,7 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) groups[r0 / 32] = head;
             }
 #pragma unroll 1
-            for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+            for (int o = 16; o > 0; o >>= 1) {
+                keys += __shfl_xor_sync(0xffffffffu, keys, o);
+                walked += __shfl_xor_sync(0xffffffffu, walked, o);
+            }
             __syncwarp();
             // Equal stretches, of at least two key tiles.  Where the row tiles of a key head share
             // keys that do not stay in L2 (kWaveBytes of K and V), the line is walked in waves: all
@@ -434,9 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t most = total / (2 * kKeys);
             const int ctas = most < 1 ? 1 : most < room ? (int)most : room;
             int waves = 1;
-            keys *= p.Hk;
 #pragma unroll 1
-            while (waves < p.waves && total > 4 * keys && keys * (4 * D) > waves * kWaveBytes &&
+            while (waves < p.waves && walked > 4 * keys && keys * p.Hk * (4 * D) > waves * kWaveBytes &&
                    total >= (waves + 1) * ctas * (int64_t)(64 * kKeys))
                 ++waves;
             rest = total;   // a division in few instructions: it runs once
