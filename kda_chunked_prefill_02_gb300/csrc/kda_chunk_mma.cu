@@ -399,10 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return fits;
             };
             // The line's length.  Until the first tile is loaded the ring keeps the length of every 32
-            // requests, so that this CTA begins with its own.
-            // (asked for four rounds ahead: a round is a few instructions.)
+            // requests, so that this CTA begins with its own.  Lengths are asked for four rounds ahead.
             int64_t* const groups = reinterpret_cast<int64_t*>(ring);
-            int64_t total = 0, keys = 0, walked = 0, each = 0, rest = 0;   // keys: of the requests, and of all row tiles
+            int64_t total = 0, each = 0, rest = 0, tokens = 0, keys = 0, walked = 0;   // walked: the keys of all row tiles
             const auto lengths = [&](int r) { return chunk_lengths(p, min(r, p.R - 1)); };
             ChunkLengths q0 = lengths(lane), q1 = lengths(lane + 32), q2 = lengths(lane + 64), q3 = lengths(lane + 96);
 #pragma unroll 1
@@ -418,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool fits = request(r0 + lane, q, first, n, ctx, pairs, head);
                     if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
                     if (n > 0) {
+                        tokens += n;
                         keys += ctx + n;
                         walked += head - (int64_t)pairs * kItemKeys;
                     }
@@ -432,8 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = 16; o > 0; o >>= 1) {
                 keys += __shfl_xor_sync(0xffffffffu, keys, o);
                 walked += __shfl_xor_sync(0xffffffffu, walked, o);
+                tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
             }
             __syncwarp();
+            if (p.cu && tokens > p.T) total = 0;   // a cu_seqlens that goes back again and again: any amount of work
             // Equal stretches, of at least two key tiles.  Where the row tiles of a key head share
             // keys that do not stay in L2 (kWaveBytes of K and V), the line is walked in waves: all
             // CTAs on one part of it, then on the next, of at least 64 key tiles a CTA.

@@ -301,6 +301,9 @@ def test_chunk_reports_what_only_the_device_sees(room):
     for bad in ([0, 9, 200, 80, 110], [0, 9, 5, 80, 110], [0, 9, -4, 80, 110], [3, 9, 79, 80, 110]):
         got, _, st = run(lens, _i32(bad))
         assert st == 1
+    # the same rows over and over: no more work than the call's rows
+    again = _i32([0, int(cu[-1])] * 2 + [0])
+    assert run(lens, again)[2] == 1
     for good in ([0, 9, 9, 9, 9], [0, 0, 0, 0, 0], [0, 9, 79, 80, 100]):
         assert run(lens, _i32(good))[2] == 0
     # pages outside the pool read as zeros
