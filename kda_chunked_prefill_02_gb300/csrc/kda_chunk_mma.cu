@@ -19,8 +19,7 @@
 // streams and whose two halves are joined on the way out.  The streams run without a break
 // from item to item: while an item's last rows are on their way out, the next
 // one's first scores are formed and its softmax runs (its queries come into a buffer of
-// their own), so that short prompts, whose items are a few tiles long, keep the tensor
-// pipe as busy as long ones do.
+// their own); what is left of an item's change is some 4 us.
 //
 // A row tile holds whole tokens (128 / G of them, G query heads a key head), so that its
 // queries are one box of the query tensor a block of 64 channels.
@@ -49,11 +48,11 @@
 // see such a position take its elements on their way out.
 //
 // Measured (us of GPU time, 32 / 8 heads of 128, bf16; rates of the products that rows see):
-// a prompt of 8192 tokens 345 (1.59 PFLOP/s, the tensor pipe 75 % busy), of 32768 5000 (1.75),
-// 2048 tokens over 126976 2600 (1.65), 32 prompts of 512 119 (0.58), 64 single tokens over 4096
-// 173 (6.2 TB/s of K and V).  What bounds it: with many tiles an item the products and the
+// a prompt of 8192 tokens 341 (1.61 PFLOP/s, the tensor pipe 75 % busy), of 32768 5000 (1.75),
+// 2048 tokens over 126976 2600 (1.65), 32 prompts of 512 118 (0.58), 64 single tokens over 4096
+// 175 (6.1 TB/s of K and V).  What bounds it: with many tiles an item the products and the
 // exponentials together, with few an item's change, most of which is fetching the roles' code
-// (74 KB) into the instruction cache.
+// (77 KB) into the instruction cache.
 //
 // Registers: 512 threads start with 128 each; the softmax warps take 168, the way out
 // keeps 80, the last four warps 96 (2 x 168 + 80 + 96 = 4 x 128).
