@@ -14,6 +14,10 @@
  * non-NULL) while the kernels skip the offending work, 16-byte aligned base
  * pointers and strides that are multiples of 8 elements (KDA_ERR_UNSUPPORTED
  * otherwise).  No call allocates memory.
+ * A status word keeps the largest value reported, whatever the order: 1
+ * (KDA_ERR_INVALID_ARG: what was out of range gave zeros or was left out, as each
+ * operator says), 4 (KDA_ERR_TIMEOUT: a call's results are not all there), also
+ * where several calls of these operators share it.
  */
 #ifndef KDA_OPS_H
 #define KDA_OPS_H

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
         const int64_t mine = at * kChunkThreads + tid;
         if (kvh == 0 && rank == 0 && p.status && mine < p.R) {
             int first, n, len;
-            if (!chunk_request(p, (int)mine, first, n, len)) atomicExch(p.status, 1);
+            if (!chunk_request(p, (int)mine, first, n, len)) atomicMax(p.status, 1);
         }
         __syncthreads();
     } else {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
     }
     const int r = s_request, row0 = s_block * kRows;
     int first, n, len;
-    if (!chunk_request(p, r, first, n, len) && !p.cu && p.status && tid == 0) atomicExch(p.status, 1);
+    if (!chunk_request(p, r, first, n, len) && !p.cu && p.status && tid == 0) atomicMax(p.status, 1);
     if (row0 >= n * p.G) return;   // no such block (all CTAs of a cluster)
     const int rows = n * p.G, ctx = len - n;   // without keys (len 0) no row sees any
     const int token0 = (int)page_div((uint32_t)row0, p.G, p.group_magic);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
             int id = p.table[r * p.table_stride + page0 + e];
             if (id < 0 || id >= p.P) {
                 id = -1;
-                if (p.status) atomicExch(p.status, 1);
+                if (p.status) atomicMax(p.status, 1);
             }
             spage[e] = id;
         }

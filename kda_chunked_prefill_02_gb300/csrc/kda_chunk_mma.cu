@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
                     const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
-                    if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
+                    if (ahead >= p.P && p.status) atomicMax(p.status, 1);   // reads zeros: past the map's pages
                     const int row = row_ahead;
                     ahead = page_of(tile + 1);
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * kV * 2u;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int64_t head = 0;
                 if (r0 + lane < p.R) {
                     const bool fits = request(r0 + lane, q, first, n, ctx, pairs, head);
-                    if (!fits && p.status && blockIdx.x == 0) atomicExch(p.status, 1);
+                    if (!fits && p.status && blockIdx.x == 0) atomicMax(p.status, 1);
                     if (n > 0) {
                         tokens += n;
                         keys += ctx + n;

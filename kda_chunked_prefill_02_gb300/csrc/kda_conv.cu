@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvPara
         for (int64_t n = (int64_t)tile * kConvThreads + tid; n < p.N; n += step) {
             const int s = p.cu[n], e = p.cu[n + 1];
             if (s < 0 || e < s || e > total || (n == 0 && s != 0) || (n == p.N - 1 && e != total))
-                atomicExch(p.status, 1);
+                atomicMax(p.status, 1);
         }
     }
     if (c0 - (tid & 31) * kConvVec >= p.C) return;  // the whole warp is past the channels
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvPara
     const bool last = t1 == total;
     auto start = [&](int n) -> int { return p.cu ? p.cu[n] : n * p.T; };
     auto report = [&]() {
-        if (p.status && tid == 0) atomicExch(p.status, 1);
+        if (p.status && tid == 0) atomicMax(p.status, 1);
     };
 
     // first sequence that starts at or after t0, or the one that runs into it
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_token_kernel(const Co
         const int slot = p.slot ? p.slot[n] : n;
         if (p.accepted) a[u] = p.accepted[n];
         if (a[u] < 0 || a[u] > 1 || (p.pool && (slot < 0 || slot >= p.P))) {
-            if (p.status && tid == 0) atomicExch(p.status, 1);
+            if (p.status && tid == 0) atomicMax(p.status, 1);
             ok[u] = false;
             continue;
         }

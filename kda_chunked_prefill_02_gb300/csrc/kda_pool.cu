@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kPoolThreads) pool_copy_kernel(const __grid_co
     const int src = p.src[i], dst = p.dst[i], given = p.rows ? p.rows[i] : d.rows;
     if (src < 0 || dst < 0 || src == dst) return;
     if (src >= d.entries || dst >= d.entries || given < 0 || given > d.rows) {
-        if (p.status && threadIdx.x == 0 && blockIdx.x == 0) atomicExch(p.status, 1);
+        if (p.status && threadIdx.x == 0 && blockIdx.x == 0) atomicMax(p.status, 1);
         return;
     }
     const uint32_t total = (uint32_t)given * (uint32_t)d.cols * (uint32_t)d.pieces;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPoolThreads, 6) cache_commit_kernel(const __g
     const int32_t* path = p.path + (int64_t)r * p.max_path;
     const bool report = p.status && blockIdx.x == 0;
     if (ctx < 0 || n < 0 || n > p.max_path) {
-        if (report && tid == 0) atomicExch(p.status, 1);
+        if (report && tid == 0) atomicMax(p.status, 1);
         return;
     }
     if (tid == 0) s_first = n;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kPoolThreads, 6) cache_commit_kernel(const __g
         }
     }
     if (!__syncthreads_and(ok)) {
-        if (report && tid == 0) atomicExch(p.status, 1);
+        if (report && tid == 0) atomicMax(p.status, 1);
         return;
     }
     // path[j] = j up to s_first, and never again behind it
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kPoolThreads, 6) cache_commit_kernel(const __g
                     v[k] = *reinterpret_cast<const uint4*>(d.data + a.x * d.st[0] + a.y * d.st[1] + in_row);
                     to[k] = d.data + b.x * d.st[0] + b.y * d.st[1] + in_row;
                 } else if (p.status) {
-                    atomicExch(p.status, 1);
+                    atomicMax(p.status, 1);
                 }
             }
         }

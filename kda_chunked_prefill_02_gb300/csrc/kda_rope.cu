@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
         // where the token's cache row is
         int64_t kc_off = -1, vc_off = -1;
         if (cur.slot >= p.cache_rows) {
-            if (p.slots && cur.end > qp && p.status && lane == 0) atomicExch(p.status, 1);
+            if (p.slots && cur.end > qp && p.status && lane == 0) atomicMax(p.status, 1);
         } else if (cur.slot >= 0) {
             const int64_t page = cur.slot / p.page, row = cur.slot - page * p.page;
             kc_off = page * p.kcs[0] + row * p.kcs[1];

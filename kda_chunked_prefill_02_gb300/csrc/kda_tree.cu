@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
     for (;;) {   // once, or an item of the line after the other
         if (kLine && item + kItem >= end) break;   // none of its tiles
         int ctx, n;
-        if (!tree_lengths(p, r, ctx, n) && p.status && tid == 0) atomicExch(p.status, 1);
+        if (!tree_lengths(p, r, ctx, n) && p.status && tid == 0) atomicMax(p.status, 1);
         const int len = ctx + n;
         if (kLine) {
             kvh = hb / p.row_blocks;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_rows_kernel(const TreeParam
                 int id = p.table[r * p.table_stride + page0 + e];
                 if (id < 0 || id >= p.P) {
                     id = -1;
-                    if (p.status) atomicExch(p.status, 1);
+                    if (p.status) atomicMax(p.status, 1);
                 }
                 spage[e] = id;
             }

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 int64_t ahead = page_of(x.t0);
                 for (int tile = x.t0; tile < x.t1 && ok; ++tile) {
                     const int id = ahead < 0 ? -1 : (int)min(ahead, (int64_t)p.P);
-                    if (ahead >= p.P && p.status) atomicExch(p.status, 1);   // reads zeros: past the map's pages
+                    if (ahead >= p.P && p.status) atomicMax(p.status, 1);   // reads zeros: past the map's pages
                     const int row = row_ahead;
                     ahead = page_of(tile + 1);
                     const int base = tile * kKeys;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 const int r = r0 + lane;
                 int ctx, n, t = 0;
                 if (r < p.count) {
-                    if (!tree_lengths(p, p.r0 + r, ctx, n) && p.status) atomicExch(p.status, 1);
+                    if (!tree_lengths(p, p.r0 + r, ctx, n) && p.status) atomicMax(p.status, 1);
                     t = max(1, (ctx + n + kKeys - 1) / kKeys);
                 }
                 int sum = t;

@@ -1,0 +1,100 @@
+"""Chunk attention, pool copies and the operators' status word on the GPU at the edges: the
+walk over the line of work in several waves, scores that are all minus infinity, empty
+pools, errors after a timeout."""
+import math
+
+import pytest
+import torch
+
+import kda_chunked_prefill_02_gb300 as K
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+KDA_ERR_TIMEOUT = 4
+# tokens a page table has room for: enough for the tensor-core kernel, whatever the lengths
+ROOM = 300000
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _rand(gen, shape, dtype, scale=1.0):
+    return (torch.randn(shape, generator=gen) * scale).to(dtype)
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def _word(value=0):
+    return torch.full((1,), value, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------- the status word
+def _reports():
+    """Calls that report a length, an entry or a page, by name: functions of the status word."""
+    g = _gen(1)
+    calls = {}
+    x, w = _rand(g, (4, 6, 128), BF16).cuda(), _rand(g, (128, 4), F32).cuda()
+    state = _rand(g, (4, 3, 128), BF16).cuda()
+    calls["conv slot"] = lambda s: K.kda_short_conv(x, w, conv_state=state.clone(), slot=_i32([0, 4, 2, 3]).cuda(), device_status=s)
+    calls["conv lengths"] = lambda s: K.kda_short_conv(x.view(24, 128), w, cu_seqlens=_i32([0, 6, 4, 24]).cuda(), device_status=s)
+    freq, _ = K.rope_frequencies(64, device="cuda")
+    qr, kr = _rand(g, (5, 2, 64), BF16).cuda(), _rand(g, (5, 1, 64), BF16).cuda()
+    cache = torch.zeros(2, 16, 1, 64, dtype=BF16, device="cuda")
+    calls["rope slot"] = lambda s: K.kda_qk_norm_rope(qr, kr, torch.arange(5, dtype=torch.int32, device="cuda"), freq,
+                                                      k_cache=cache.clone(), slots=torch.tensor([0, 1, 32, 3, 4]).cuda(),
+                                                      device_status=s)
+    kc, vc = _rand(g, (12, 16, 1, 64), BF16).cuda(), _rand(g, (12, 16, 1, 64), BF16).cuda()
+    lens = _i32([30, 20]).cuda()
+    for room in (64, ROOM):
+        table = torch.zeros(2, room // 16, dtype=torch.int32)
+        table[:, :4] = torch.arange(8, dtype=torch.int32).view(2, 4)
+        page = table.clone()
+        page[1, 0] = 12
+        q = _rand(g, (2, 8, 24, 64), BF16).cuda()
+        kind = "rows" if room == 64 else "tensor"
+        assert K.chunk_attention_schedule(q, kc, table, packed=False)["kernel"] == kind
+        for name, tab, ln in (("page", page.cuda(), lens), ("length", table.cuda(), _i32([30, -1]).cuda())):
+            calls["chunk %s %s" % (kind, name)] = lambda s, t=tab, n=ln, q=q: K.kda_chunk_attention(q, kc, vc, t, n, device_status=s)
+            calls["tree %s %s" % (kind, name)] = lambda s, t=tab, n=ln, q=q: K.kda_tree_attention(q, kc, vc, t, n, device_status=s)
+    pool = torch.zeros(4, 16, 1, 64, dtype=BF16, device="cuda")
+    calls["copy"] = lambda s: K.kda_pool_copy(pool, _i32([0]).cuda(), _i32([4]).cuda(), device_status=s)
+    tab = _i32([[0, 1]]).cuda()
+    for name, path, t in (("path", [[1, 1]], tab), ("page", [[1, 2]], _i32([[4, 1]]).cuda()), ("count", [[1, 2]], tab)):
+        calls["commit " + name] = lambda s, p=path, t=t, n=3 if name == "count" else 2: K.kda_cache_commit(
+            pool, t, _i32([3]).cuda(), _i32(p).cuda(), _i32([n]).cuda(), device_status=s)
+    return calls
+
+
+def test_a_timeout_is_kept():
+    """A status word shared by a step's calls: what a later one reports (1) does not replace the
+    timeout of one before (4), whose results are not all there."""
+    for name, call in _reports().items():
+        for before, after in ((0, 1), (KDA_ERR_TIMEOUT, KDA_ERR_TIMEOUT)):
+            status = _word(before)
+            call(status)
+            assert status.item() == after, name
+
+
+@pytest.mark.parametrize("op", ["chunk", "tree"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_timeout_and_bad_pages_in_one_call(op, D):
+    """Waits that run out in some CTAs, pages outside the pool in others, in any order."""
+    R, N = 60, 40
+    kc = torch.randn(500, 16, 2, D, device="cuda").to(BF16)
+    vc = torch.randn_like(kc)
+    g = _gen(2)
+    table = torch.randint(0, 520, (R, ROOM // 16), generator=g).to(torch.int32).cuda()   # one in 26 is none
+    q, lens = _rand(g, (R, N, 8, D), BF16).cuda(), _i32([100 + 331 * (i % 13) for i in range(R)]).cuda()
+    call = K.kda_chunk_attention if op == "chunk" else K.kda_tree_attention
+    for limit in (2000, 20000, 200000):
+        status = _word()
+        with K.overrides(wait_limit_ns=limit, timeout_probe=True):
+            call(q, kc, vc, table, lens, device_status=status)
+        torch.cuda.synchronize()
+        assert status.item() == KDA_ERR_TIMEOUT
+    status = _word()
+    call(q, kc, vc, table, lens, device_status=status)
+    assert status.item() == 1
