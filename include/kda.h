@@ -36,7 +36,8 @@
  *    ending at the token count, accepted or slot out of range, a bounded wait
  *    that ran out) are written as a kda_status value to *device_status when it
  *    is non-NULL (a caller-owned device int32 that the caller zeroes); the
- *    kernels then skip the offending work instead of faulting.
+ *    kernels then skip the offending work instead of faulting.  Of a wait that
+ *    ran out and anything else that a call reports, the former stays.
  *  - Per-device set-up (the kernels' shared-memory limits, the no-alloc
  *    scratch address) is done on a device's first call and remembered for the
  *    process; after cudaDeviceReset the library must not be called again in

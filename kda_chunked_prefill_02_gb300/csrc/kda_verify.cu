@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
                 }
             }
         } else if (tid == 0 && p.status) {
-            atomicExch(p.status, 1);
+            atomicMax(p.status, 1);
         }
         stall_point<kStall>(p.stall_seed, 2, k);
         __syncthreads();  // the state block is in registers: its buffer takes the next item

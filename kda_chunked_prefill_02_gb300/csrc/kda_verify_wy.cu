@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kWyThreads, 1) verify_wy_kernel(const VerifyPa
         cp_async_wait0_wy();   // this item's drafts have landed
         __syncthreads();
         if (!cur.valid) {
-            if (tid == 0 && p.status) atomicExch(p.status, 1);
+            if (tid == 0 && p.status) atomicMax(p.status, 1);
         } else {
             // ---- gate prefix Gam (in place of g) and beta
             if (tid < kHeadDim) {

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import kda_chunked_prefill_02_gb300 as K
+from kda_chunked_prefill_02_gb300 import inputs
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -98,3 +99,24 @@ def test_a_timeout_and_bad_pages_in_one_call(op, D):
     status = _word()
     call(q, kc, vc, table, lens, device_status=status)
     assert status.item() == 1
+
+
+@pytest.mark.parametrize("kernel", ["sequential", "tensor"])
+def test_a_timeout_is_kept_by_the_verification_of_drafts(kernel):
+    """kda_verify with counts that no draft has: in a word that holds a timeout, and beside waits
+    that run out in other CTAs."""
+    d = inputs.verify_inputs(1206, R=400, D=6, H=4).to("cuda")
+    accepted = d.accepted.clone()
+    accepted[::2] = 7
+
+    def run(status):
+        K.kda_verify(d.q, d.k, d.v, d.g, d.beta, d.state_pool.clone(), accepted, device_status=status)
+        torch.cuda.synchronize()
+        return status.item()
+
+    with K.overrides(verify_kernel=kernel):
+        assert run(_word()) == 1 and run(_word(KDA_ERR_TIMEOUT)) == KDA_ERR_TIMEOUT
+    if kernel == "tensor":
+        for limit in (2000, 20000):
+            with K.overrides(verify_kernel=kernel, wait_limit_ns=limit, timeout_probe=True):
+                assert run(_word()) == KDA_ERR_TIMEOUT
