@@ -139,9 +139,9 @@ kda_status pool_desc(const kda_pool& q, PoolDesc& d) {
     const bool one = q.cols == 1 || q.stride[2] == q.bytes;
     d.cols = one ? 1 : (int32_t)q.cols;
     d.pieces = (int32_t)(one ? q.cols * pieces : pieces);
-    if (d.pieces == 0 || d.cols == 0) d.rows = 0, d.cols = d.pieces = 1;   // nothing to copy
+    if (d.pieces == 0 || d.cols == 0) d.cols = 0, d.pieces = 1;   // rows of nothing: no piece is looked for
     d.piece_magic = magic_of(d.pieces);
-    d.col_magic = magic_of(d.cols);
+    d.col_magic = magic_of(d.cols ? d.cols : 1);
     return KDA_OK;
 }
 

@@ -120,3 +120,22 @@ def test_a_timeout_is_kept_by_the_verification_of_drafts(kernel):
         for limit in (2000, 20000):
             with K.overrides(verify_kernel=kernel, wait_limit_ns=limit, timeout_probe=True):
                 assert run(_word()) == KDA_ERR_TIMEOUT
+
+
+# ---------------------------------------------------------------- pools
+@pytest.mark.parametrize("shape", [(5, 4, 0, 64), (5, 4, 3, 0, 64)])
+def test_copy_of_rows_that_hold_nothing(shape):
+    """A pool of empty rows beside others has the rows it has: its first ones are nothing to copy,
+    and nothing to report; a row count past them is, as for any pool."""
+    empty = torch.empty(shape, dtype=F32, device="cuda")
+    pool = torch.arange(5 * 4 * 8, dtype=torch.int32, device="cuda").view(5, 4, 8)
+    want = pool.clone()
+    want[3, :2] = want[0, :2]
+    want[4] = want[1]
+    src, dst, status = _i32([0, 1]).cuda(), _i32([3, 4]).cuda(), _word()
+    K.kda_pool_copy([empty, pool], src, dst, rows=_i32([2, 4]).cuda(), device_status=status)
+    assert status.item() == 0 and torch.equal(pool, want)
+    K.kda_pool_copy([empty, pool], src, dst, device_status=status)
+    assert status.item() == 0
+    K.kda_pool_copy(empty, src, dst, rows=_i32([5, 4]).cuda(), device_status=status)
+    assert status.item() == 1
