@@ -175,7 +175,8 @@ kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* args, void* stream);
  *     out_i = sum_{p in S_i} e^{scale q_i.k_p - m} v_p / sum_{p in S_i} e^{scale q_i.k_p - m},
  *     lse_i = ln sum_{p in S_i} e^{scale q_i.k_p}
  *
- * An empty S_i (and every row past num_nodes[r]) gives out = 0 and lse = -inf.
+ * An empty S_i (and every row past num_nodes[r], and a node whose scores are all
+ * minus infinity) gives out = 0 and lse = -inf.
  * Keys and values that a node does not see have no influence on it, whatever
  * they hold (NaN and infinities too).  Products and sums are fp32; the weights
  * e^{..} enter the product with v in the element type (fp16: scaled, so that those
@@ -271,7 +272,8 @@ kda_status kda_tree_attention_schedule(const kda_tree_attention_args* args, int 
  *     lse_i = ln sum_p e^{scale q_i.k_p}
  *
  * Keys and values behind a token's own position have no influence on it, whatever they
- * hold (NaN and infinities too).  Products and sums are fp32; the weights e^{..} enter
+ * hold (NaN and infinities too).  A token whose scores are all minus infinity gives NaN
+ * (lse -inf), as the formula does.  Products and sums are fp32; the weights e^{..} enter
  * the product with v in the element type (fp16: scaled, so that those down to 2^-35 of
  * the largest are kept).
  *

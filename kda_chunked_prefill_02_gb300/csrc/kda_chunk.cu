@@ -399,9 +399,9 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows_kernel(const ChunkPa
         }
         const int i = (int)page_div((uint32_t)q, p.G, p.group_magic), h = kvh * p.G + (q - i * p.G);
         const bool empty = sum == 0.f;
-        const float inv = empty ? 0.f : 1.f / sum;
+        const float inv = 1.f / sum;   // (every score -inf: 0 / 0)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = empty ? 0.f : y[k] * inv;
+        for (int k = 0; k < 8; ++k) y[k] = len == 0 ? 0.f : y[k] * inv;
         *reinterpret_cast<uint4*>(obase + i * p.os[1] + h * p.os[2] + c * 8) = pack8<T>(y);
         if (p.lse && c == 0)
             p.lse[((p.cu ? (int64_t)first : (int64_t)r * p.T) + i) * p.Hq + h] =
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p) {
             }
             const int h = item.z * p.G + (row - in_token * p.G);
             const bool empty = sum == 0.f;
-            const float inv = empty ? 0.f : 1.f / sum;
+            const float inv = 1.f / sum;   // (every score -inf: 0 / 0; a request without keys is not cut)
             uint32_t* dst = reinterpret_cast<uint32_t*>(
                 static_cast<T*>(p.out) + (p.cu ? (int64_t)(first + token) * p.os[1] : item.y * p.os[0] + token * p.os[1]) +
                 h * p.os[2] + lane * kVec);

@@ -836,7 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int token = x.token0 + a * tt + in_token;   // of the request
                 const bool live = in_token < tt && token < x.token0 + x.tokens;
                 const bool empty = ml.y == 0.f, whole = x.whole;
-                const float inv = empty ? 0.f : 1.f / ml.y;
+                // no weight: zeros for a part without keys or a request that does not fit the call; a whole
+                // row whose scores are all -inf is 0 / 0
+                const float inv = empty && (!whole || x.end == 0) ? 0.f : 1.f / ml.y;
                 f0 *= inv;
                 f1 *= inv;
                 const int64_t part = (int64_t)x.part * 256 + a * 128 + row;

@@ -8,6 +8,8 @@ import torch
 
 import kda_chunked_prefill_02_gb300 as K
 from kda_chunked_prefill_02_gb300 import inputs
+from ops_test_util import within
+from serve_test_util import chunk_reference
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -139,3 +141,39 @@ def test_copy_of_rows_that_hold_nothing(shape):
     assert status.item() == 0
     K.kda_pool_copy(empty, src, dst, rows=_i32([5, 4]).cuda(), device_status=status)
     assert status.item() == 1
+
+
+# ---------------------------------------------------------------- scores that are minus infinity
+def _one_request(seed, ctx, new, Hq, Hk, D, page, dtype, room):
+    """q, caches, a page table and lengths of one request, on the host."""
+    g = _gen(seed)
+    pages = (ctx + new + page - 1) // page
+    table = torch.zeros(1, max(pages, room // page), dtype=torch.int32)
+    table[0, :pages] = torch.randperm(pages, generator=g).to(torch.int32)
+    return (_rand(g, (new, Hq, D), dtype, 1.5), _rand(g, (pages, page, Hk, D), dtype), _rand(g, (pages, page, Hk, D), dtype),
+            table, _i32([ctx]))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("room", [0, ROOM])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ctx,new,hidden", [(0, 200, 48), (0, 3, 16), (100, 1, 96), (100, 30, 144), (6000, 1, 6000), (6000, 300, 5008),
+                                            (40000, 1, 40000), (40000, 20, 48000)])
+def test_chunk_scores_that_are_minus_infinity(dtype, room, D, ctx, new, hidden):
+    """The first `hidden` keys have a component of minus infinity that every query meets with 1: a
+    token that sees others beside them sees those alone, one that sees no others is 0 / 0."""
+    page, n = 16, min(hidden, ctx + new)
+    q, kc, vc, table, lens = _one_request(4, ctx, new, 4, 1, D, page, dtype, room)
+    q[..., 5] = 1
+    kind = K.chunk_attention_schedule(q, kc, table)["kernel"]
+    assert kind == "tensor" or room == 0
+    kc[table[0, :(n + page - 1) // page].long(), :, :, 5] = -math.inf
+    got, lse = K.kda_chunk_attention(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(),
+                                     cu_seqlens=_i32([0, new]).cuda(), return_lse=True)
+    got, lse = got.cpu(), lse.cpu()
+    gone = max(0, min(new, hidden - ctx))      # tokens that see nothing else
+    assert bool(torch.isnan(got[:gone]).all()) and bool((lse[:gone] == -math.inf).all())
+    if gone < new:   # the others as over a context without those keys
+        out, ob, want, lb = chunk_reference(q[gone:], kc, vc, table[:, hidden // page:], [ctx + gone - hidden], [new - gone])
+        within(got[gone:], out, ob)
+        within(lse[gone:], want, lb)
