@@ -8,7 +8,8 @@ import torch
 
 import kda_chunked_prefill_02_gb300 as K
 from kda_chunked_prefill_02_gb300 import inputs
-from ops_test_util import within
+from ops_test_util import F64, U32, UNIT, rounding, within
+from serve_edges_util import waves_of
 from serve_test_util import chunk_reference
 
 pytestmark = pytest.mark.gpu
@@ -177,3 +178,87 @@ def test_chunk_scores_that_are_minus_infinity(dtype, room, D, ctx, new, hidden):
         out, ob, want, lb = chunk_reference(q[gone:], kc, vc, table[:, hidden // page:], [ctx + gone - hidden], [new - gone])
         within(got[gone:], out, ob)
         within(lse[gone:], want, lb)
+
+
+# ---------------------------------------------------------------- the line of work in waves
+def _reference(q, kc, vc, table, ctx, new, start):
+    """chunk_reference (serve_test_util.py) of one request on the GPU, a key head and 256 rows at a
+    time, for values that are all finite: out, its bound [new, Hq, D], log-sums, theirs."""
+    Hq, D = q.shape[1:]
+    page, Hk = kc.shape[1], kc.shape[2]
+    G, L, unit = Hq // Hk, ctx + new, UNIT[q.dtype]
+    at = torch.arange(L, device="cuda")
+    pages = table.long()[at // page]
+    out, bound = (torch.empty(new, Hq, D, dtype=F64, device="cuda") for _ in range(2))
+    lse, lse_bound = (torch.empty(new, Hq, dtype=F64, device="cuda") for _ in range(2))
+    summed = (L + 16) * U32
+    for h in range(Hk):
+        k, v = (c[pages, at % page, h].to(F64) for c in (kc, vc))
+        for i in range(0, new, 256 // min(G, 256)):
+            x = q[start + i:start + min(i + 256 // min(G, 256), new), h * G:(h + 1) * G].to(F64)   # [n, G, D]
+            n = x.shape[0]
+            sees = (at[None] <= ctx + i + torch.arange(n, device="cuda")[:, None])[:, None]        # [n, 1, L]
+            s = torch.where(sees, x @ k.t() * D ** -0.5, -math.inf)
+            p = torch.softmax(s, -1)
+            y, near = p @ v, p @ v.abs()
+            mag = torch.where(sees, x.abs() @ k.abs().t(), 0).amax(-1)
+            top = torch.where(sees, s, 0).abs().amax(-1)
+            ds = (D + 8) * U32 * D ** -0.5 * mag + top * 2.0 ** -21 + 2.0 ** -20
+            b = near * (unit + 2 * ds + 2 * summed)[..., None] * (1 + unit) + rounding(y, q.dtype) * (1 + unit)
+            z, heads = torch.logsumexp(s, -1), slice(h * G, (h + 1) * G)
+            out[i:i + n, heads], bound[i:i + n, heads], lse[i:i + n, heads] = y, b, z
+            lse_bound[i:i + n, heads] = ds + summed + z.abs() * 2.0 ** -21 + 2.0 ** -20
+    return out.cpu(), bound.cpu(), lse.cpu(), lse_bound.cpu()
+
+
+@pytest.mark.parametrize("dtype,Hq,Hk,D,page,ctx,new,waves,form", [
+    (BF16, 32, 8, 128, 64, [30000], [1024], 2, "packed"),
+    (BF16, 32, 8, 128, 16, [126976], [700], 8, "packed"),
+    (F16, 16, 16, 64, 16, [60000], [1500], 4, "packed"),
+    (BF16, 16, 4, 256, 64, [50000], [900], 4, "packed"),
+    (F16, 32, 4, 128, 128, [70011], [333], 2, "in place"),
+    (BF16, 32, 8, 128, 64, [0, 20000, 3, 9000, 100, 40, 2500, 0], [900, 700, 0, 600, 1, 1, 33, 1], 2, "packed"),
+    (BF16, 32, 8, 128, 64, [25000, 24000], [800, 800], 4, "padded")])
+def test_chunk_in_waves(dtype, Hq, Hk, D, page, ctx, new, waves, form):
+    """Every row of calls whose line of work is walked in several waves against 64 bits: items cut
+    between two CTAs and between two waves, the requests walked again in each.  A part of an
+    item's keys that is lost or counted twice shows in the log-sums, a part of its values in
+    channels whose mean is 1 or -1 by a bit of the position."""
+    g = torch.Generator("cuda").manual_seed(3)
+
+    def rand(*shape, scale=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert sms != 152 or waves_of(ctx, new, Hk, Hq // Hk, D, sms) == waves
+    need = [(c + n + page - 1) // page for c, n in zip(ctx, new)]
+    kc, vc = rand(sum(need), page, Hk, D), rand(sum(need), page, Hk, D)
+    table = torch.zeros(len(ctx), max(need), dtype=torch.int32, device="cuda")
+    order, at = torch.randperm(sum(need), generator=g, device="cuda").to(torch.int32), 0
+    for r, n in enumerate(need):
+        table[r, :n] = order[at:at + n]
+        at += n
+        pos = torch.arange(n * page, device="cuda")
+        mean = 2 * ((pos[:, None] >> (torch.arange(D, device="cuda") % 9 + 7)) & 1) - 1
+        vc[table[r, :n].long()] += mean.view(n, page, 1, D).to(dtype)
+    q, lens, cu = rand(sum(new), Hq, D, scale=1.5), _i32(ctx).cuda(), _i32([0] + new).cumsum(0).to(torch.int32)
+    shaped = q.view(len(ctx), -1, Hq, D) if form == "padded" else q
+    cut = K.chunk_attention_schedule(shaped, kc, table, packed=form != "padded")
+    assert cut["kernel"] == "tensor"
+    # the workspace begins with what each stretch of a wave left in its two slots: a state (0: nothing) and an item
+    ws = torch.zeros(cut["ctas"] * 2 * (16 + 256 * (D + 1) * 4), dtype=torch.uint8, device="cuda")
+    status = _word()
+    x = shaped.clone()
+    got, lse = K.kda_chunk_attention(x, kc, vc, table, lens, cu_seqlens=None if form == "padded" else cu.cuda(), workspace=ws,
+                                     out=x if form == "in place" else None, return_lse=True, device_status=status)
+    assert status.item() == 0
+    states = ws[:cut["ctas"] * 32].view(torch.int32).view(-1, 2, 4)[:, :, 0]
+    used = int(states.any(1).nonzero().max()) // (sms // 2 if D == 256 else sms) + 1
+    assert used == waves_of(ctx, new, Hk, Hq // Hk, D, sms)
+    got, lse = got.view(-1, Hq, D), lse.view(-1, Hq)
+    for r, (c, n) in enumerate(zip(ctx, new)):
+        if n > 0:
+            a = int(cu[r])
+            want, bound, lse_want, lse_bound = _reference(q, kc, vc, table[r], c, n, a)
+            within(got[a:a + n], want, bound)
+            within(lse[a:a + n], lse_want, lse_bound)
