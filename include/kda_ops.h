@@ -296,7 +296,9 @@ kda_status kda_tree_attention_schedule(const kda_tree_attention_args* args, int 
  * does not start at 0, decreases or passes seqlen is reported too, and which of the call's
  * requests are computed is then not defined (rows of q and out of the call alone are used).
  * workspace: kda_chunk_attention_workspace_size(args) bytes, 256-byte aligned, used
- * during the call's kernels only.
+ * during the call's kernels only.  None for the kernel for few rows; for the other 40 MB
+ * (head size 64: 20), and up to eight times that where several hundred new tokens may
+ * share a long context, of which the lengths on the device use a part (152 SMs).
  * Size limits: R <= 65535, Hk <= 65535, Hq / Hk <= 65536, tokens (of a request where padded)
  * times Hq / Hk below 2^31, contexts with their new tokens up to 2^30.
  */
@@ -336,9 +338,10 @@ kda_status kda_chunk_attention_ex(const kda_chunk_attention_args* args, const kd
 /*
  * How kda_chunk_attention cuts these arguments on a GPU with num_sms SMs (host only, as
  * kda_tree_attention_schedule).  kernel: KDA_CHUNK_ROWS, the kernel for few rows, `ctas`
- * CTAs sharing a block of them; KDA_CHUNK_TENSOR, the tensor-core kernel, `ctas` equal
- * stretches of the call's work (queries or caches without a tensor map take the kernel
- * for few rows all the same).
+ * CTAs sharing a block of them; KDA_CHUNK_TENSOR, the tensor-core kernel, at most `ctas`
+ * equal stretches of the call's work, what the workspace has room for: the lengths on the
+ * device decide (queries or caches without a tensor map take the kernel for few rows all
+ * the same).
  */
 #define KDA_CHUNK_ROWS 0
 #define KDA_CHUNK_TENSOR 1

@@ -25,6 +25,8 @@
 // request's end are zero-filled, and a tile in which some row does not see a key whose V
 // is not finite takes a scalar product that leaves out what a row does not see
 // (0 * NaN is NaN).
+#include <math.h>
+
 #include "kda_internal.h"
 #include "ops_internal.h"
 #include "sm103.cuh"
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p) {
     __shared__ float sy[W > 1 ? 8 : 1][W > 1 ? D : 1], ssum[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // this block's stretches, one of each wave (at most 32), are looked at together
+    // this block's stretches, one of each wave (kMaxWaves at most), are looked at together
     const int ctas = p.ctas, mine = (int)blockIdx.x + lane * (int)gridDim.x;
     const int4 items = mine < ctas ? p.parts[2 * mine + 1] : make_int4(0, 0, 0, 0);
     for (uint32_t cut = __ballot_sync(0xffffffffu, items.x != 0); cut; cut &= cut - 1) {
@@ -500,6 +502,25 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p) {
 int64_t row_pairs(int R, int T, bool packed, int G) {
     const int tt = 128 / G, pt = 2 * tt;
     return packed ? (int64_t)T / pt + R : (int64_t)R * ((T + pt - 1) / pt);
+}
+
+// Waves that chunk_mma_kernel may walk, at most: its own conditions (there on the lengths
+// themselves), with what they can come to for requests that fit the call.  Pairs beside a
+// request's first are together `more` at most, so the row tiles of a head walk no more than
+// keys + len * more keys, which has to be above 4 * keys (some request's five pairs or more);
+// a wave has kWaveBytes of K and V, and 64 key tiles a stretch.  What a call may need of the
+// workspace follows it: 60 single tokens and four pieces of 512 over 4096 (32 / 8 heads of 128)
+// 40 MB, where room for eight waves is 321.
+int most_waves(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int stretches) {
+    const int pt = 2 * (128 / G), beside = (T - 1) / pt;
+    if (beside < 4) return 1;
+    const double more = packed ? (double)beside : (double)R * beside;
+    const double len = (double)max_len, requests = packed && T < R ? T : R;
+    const double keys = requests * len < len * more / 3 ? requests * len : len * more / 3;
+    const double by_keys = ceil(keys * Hk * 4 * D / kWaveBytes);
+    const double by_line = floor(Hk * (keys + len * more + kItemKeys * (more + requests)) / (64.0 * 128 * stretches));
+    const double waves = by_keys < by_line ? by_keys : by_line;
+    return waves < 1 ? 1 : waves > kMaxWaves ? kMaxWaves : (int)waves;
 }
 
 template <typename T, int W>
@@ -600,9 +621,7 @@ ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t ma
         const double mma_us = 17.0 + keys / 128 * (D == 64 ? 1.15 : D == 128 ? 1.4 : 2.1);
         t.mma = mma_us < 1.25 * rows_us;
         if (!t.mma) t.stretches = 0;
-        // Waves where several pairs of row tiles may share more keys than L2 keeps (the kernel
-        // looks at the lengths themselves).
-        else if ((int64_t)T * G > 1024 && (double)R * Hk * max_len * 4 * D > (64 << 20)) t.waves = 8;
+        else t.waves = most_waves(R, T, packed, Hk, G, D, max_len, t.stretches);
         t.stretches *= t.waves;
     }
     return t;

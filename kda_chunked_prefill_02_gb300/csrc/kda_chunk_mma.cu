@@ -74,13 +74,6 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;   // S of stream s at 128 s, O at 2
 constexpr int kMaxSlots = 8, kMaxQ = 3;
 constexpr int kItems = 4;         // items dealt out ahead
 constexpr int kBadWords = 12;     // positions of an item's last tiles (three at most), a bit each
-// Length on the line of an item's way in and out, in keys: with 128, 192, 256, 384 an 8192-token
-// prompt (32 / 8 heads) takes 364, 351, 345, 351 us, four of 2048 130, 125, 125, 126, 24 ragged
-// prompts of head size 64 74, 65, 65, 65.
-constexpr int kItemKeys = 256;
-// K and V of a wave over the line of work (L2 has 129 MB): 2048 tokens over 126976 with 32, 64,
-// 100 MB 2570, 2580, 2770 us.
-constexpr int64_t kWaveBytes = 64 << 20;
 // What a wait may take beside its bound, a key tile of the longest context (see kda_tree_mma.cu).
 constexpr uint64_t kTileWaitNs = 20000 * (kItems + 1);
 

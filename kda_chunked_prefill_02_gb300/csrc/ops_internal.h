@@ -99,6 +99,14 @@ cudaError_t launch_tree_join(const TreeParams& p, int D, bool f16, cudaStream_t 
 bool launch_tree_mma(const TreeParams& p, int D, bool f16, int grid, cudaStream_t s, cudaError_t* e);
 
 // Attention of chunks of new tokens (kda_chunk.cu, kda_chunk_mma.cu).
+// Length on the line of an item's way in and out, in keys: with 128, 192, 256, 384 an 8192-token
+// prompt (32 / 8 heads) takes 364, 351, 345, 351 us, four of 2048 130, 125, 125, 126, 24 ragged
+// prompts of head size 64 74, 65, 65, 65.
+constexpr int kItemKeys = 256;
+// K and V of a wave over the line of work (L2 has 129 MB): 2048 tokens over 126976 with 32, 64,
+// 100 MB 2570, 2580, 2770 us.
+constexpr int64_t kWaveBytes = 64 << 20;
+constexpr int kMaxWaves = 8;   // (kda_chunk_mma.cu has what more and fewer measured)
 struct ChunkParams {
     const void *q, *kc, *vc;
     void* out;
@@ -136,7 +144,7 @@ struct ChunkPlan {
     bool mma;                 // the tensor-core kernel
     int grid;                 // and its CTAs
     int stretches;            // its equal stretches of work at most (with head size 256 two CTAs share one)
-    int waves;                // and the waves that they belong to
+    int waves;                // and the waves that they belong to, at most
     int cluster;              // rows kernel: CTAs that share an item
 };
 ChunkPlan chunk_plan(int R, int T, bool packed, int Hk, int G, int D, int64_t max_len, int page, float scale, bool in_place,
