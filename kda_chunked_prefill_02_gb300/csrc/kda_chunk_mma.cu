@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (smem_u32(sm) & 1023u) {   // the swizzled tiles' alignment (never seen: all threads leave)
         if (p.status && tid == 0) atomicExch(p.status, 4);
+        if (half == 0 && tid < 2 * p.waves)   // no parts for the join
+            p.parts[2 * (cta + (tid >> 1) * ((int)gridDim.x / kHalves)) + (tid & 1)] = make_int4(0, 0, 0, 0);
         return;
     }
 
