@@ -394,9 +394,8 @@ kda_status kda_residual_norm(const kda_residual_norm_args* a, void* stream) {
     p.tokens = a->tokens; p.E = (int)a->channels; p.post = a->post_norm ? 1 : 0; p.sigmoid = a->gate_sigmoid ? 1 : 0;
     p.w_f32 = a->weight_dtype == KDA_DTYPE_F32 ? 1 : 0;
     p.alpha = a->alpha; p.eps = a->norm_eps;
-    const int sms = device_sm_count();
-    if (sms < 1) return KDA_ERR_CUDA;
-    return status_of(launch_residual_norm(p, a->dtype == KDA_DTYPE_F16, a->x_dtype == KDA_DTYPE_F32, sms,
+    if (device_sm_count() < 1) return KDA_ERR_CUDA;
+    return status_of(launch_residual_norm(p, a->dtype == KDA_DTYPE_F16, a->x_dtype == KDA_DTYPE_F32,
                                           static_cast<cudaStream_t>(stream)));
 }
 
@@ -411,14 +410,13 @@ kda_status kda_pool_copy(const kda_pool_copy_args* a, void* stream) {
     }
     if (a->num_pools == 0 || a->count == 0) return KDA_OK;
     if (!a->src || !a->dst) return KDA_ERR_INVALID_ARG;
-    const int sms = device_sm_count();
-    if (sms < 1) return KDA_ERR_CUDA;
+    if (device_sm_count() < 1) return KDA_ERR_CUDA;
     p.src = a->src; p.dst = a->dst; p.rows = a->rows; p.status = a->device_status;
     p.count = (int)a->count;
     for (int64_t k = 0; k < a->num_pools; k += kPoolSlice) {
         p.pools = (int)(a->num_pools - k < kPoolSlice ? a->num_pools - k : kPoolSlice);
         for (int i = 0; i < p.pools; ++i) pool_desc(a->pools[k + i], p.pool[i]);
-        const cudaError_t e = launch_pool_copy(p, sms, static_cast<cudaStream_t>(stream));
+        const cudaError_t e = launch_pool_copy(p, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return KDA_OK;

@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(kPoolThreads, 6) cache_commit_kernel(const __g
 
 }  // namespace
 
-cudaError_t launch_pool_copy(const PoolCopyParams& q, int num_sms, cudaStream_t s) {
-    (void)num_sms;
+cudaError_t launch_pool_copy(const PoolCopyParams& q, cudaStream_t s) {
     int64_t most = 1;
     for (int k = 0; k < q.pools; ++k) {
         const int64_t n = (int64_t)q.pool[k].rows * q.pool[k].cols * q.pool[k].pieces;

@@ -188,8 +188,7 @@ cudaError_t launch_t(const ResidualParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_residual_norm(const ResidualParams& p, bool f16, bool x_f32, int num_sms, cudaStream_t s) {
-    (void)num_sms;
+cudaError_t launch_residual_norm(const ResidualParams& p, bool f16, bool x_f32, cudaStream_t s) {
     if (f16) return x_f32 ? launch_t<__half, float>(p, s) : launch_t<__half, __half>(p, s);
     return x_f32 ? launch_t<__nv_bfloat16, float>(p, s) : launch_t<__nv_bfloat16, __nv_bfloat16>(p, s);
 }

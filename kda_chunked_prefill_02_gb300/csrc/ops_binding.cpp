@@ -606,7 +606,8 @@ Pools pools_of(const char* name, PyObject* o, bool page_rows) {
 
 // pools, src, dst, rows, device_status
 PyObject* pool_copy(PyObject* const* o) {
-    const at::Tensor &src = *tensor("src", o[1]), &dst = *tensor("dst", o[2]);
+    const at::Tensor& src = *tensor("src", o[1]);
+    tensor("dst", o[2]);   // (no None)
     const Pools pools = pools_of("pools", o[0], false);
     const Call c{pools.first ? pools.first->device() : src.device()};
     need_cuda(c, "src", src, at::kInt);
@@ -619,7 +620,6 @@ PyObject* pool_copy(PyObject* const* o) {
     a.dst = flat<int32_t>(c, "dst", o[2], at::kInt, {a.count});
     a.rows = flat<int32_t>(c, "rows", o[3], at::kInt, {a.count});
     a.device_status = status_word(c, o[4]);
-    (void)dst;
     const c10::cuda::CUDAGuard guard(c.device);
     done(kda_pool_copy(&a, stream_of(src)));
     return none();

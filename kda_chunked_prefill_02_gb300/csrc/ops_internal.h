@@ -193,7 +193,7 @@ struct ResidualParams {
     int E, post, sigmoid, w_f32;
     float alpha, eps;
 };
-cudaError_t launch_residual_norm(const ResidualParams& p, bool f16, bool x_f32, int num_sms, cudaStream_t s);
+cudaError_t launch_residual_norm(const ResidualParams& p, bool f16, bool x_f32, cudaStream_t s);
 
 // Copies between entries of pools (kda_pool.cu).  A pool's entry is rows x cols runs of
 // `pieces` 16-byte pieces, byte strides st (entry, row, col).
@@ -208,9 +208,9 @@ struct PoolCopyParams {
     PoolDesc pool[kPoolSlice];
     const int32_t *src, *dst, *rows;
     int32_t* status;
-    int count, pools, slices;        // copies; pools of this launch; slices of an entry (set by the launcher)
+    int count, pools;                // copies; pools of this launch
 };
-cudaError_t launch_pool_copy(const PoolCopyParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_pool_copy(const PoolCopyParams& p, cudaStream_t s);
 struct CacheCommitParams {
     PoolDesc pool[kPoolSlice];
     const int32_t *table, *ctx, *path, *accepted;
