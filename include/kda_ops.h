@@ -235,10 +235,11 @@ size_t kda_tree_attention_workspace_size(const kda_tree_attention_args* args);
 kda_status kda_tree_attention(const kda_tree_attention_args* args, void* stream);
 /*
  * The same with overrides for tests (NULL: none): wait_limit_ns and timeout_probe
- * apply to the kernel for many rows, whose waits are the only ones of these
- * operators: bounded by wait_limit_ns (200 ms by default) and 0.1 ms for every 128
- * tokens of the longest context, since some last as long as a context's work.  A
- * wait that runs out reports KDA_ERR_TIMEOUT in device_status.
+ * apply to the kernel for many rows, whose waits, with those of kda_chunk_attention's
+ * tensor-core kernel, are the only ones of these operators: bounded by wait_limit_ns
+ * (200 ms by default) and 0.1 ms for every 128 tokens of the longest context, since some
+ * last as long as a context's work.  A wait that runs out reports KDA_ERR_TIMEOUT in
+ * device_status.
  */
 kda_status kda_tree_attention_ex(const kda_tree_attention_args* args, const kda_overrides* overrides, void* stream);
 /*
@@ -290,6 +291,14 @@ kda_status kda_tree_attention_schedule(const kda_tree_attention_args* args, int 
  * max_context: an upper bound of context_lens that the host knows (< 0: what the page
  * table can address); it sets how the work is cut, not the result's definition.  Give it
  * where the table is much wider than the contexts.
+ * Prompts run on tensor cores (8192 tokens, 32 / 8 heads of 128: 341 us, by the kernel for
+ * few rows 2851).  That kernel needs a page_size that is a multiple of 8, at most 128
+ * query heads a key head, a scale above 1e-30, caches whose heads follow one another within
+ * a row (stride [2] = head_dim) or a page (stride [0] = Hk * stride [2]; one key head: any)
+ * and, with head size 256, results that are not over the queries; any other call takes the
+ * one for few rows, whatever its size.  Thousands of single tokens without longer pieces
+ * among them are a call for kda_tree_attention (4096 over about 80 keys, one over 20000, 32 / 8
+ * heads of 128: 0.55 ms, 0.80 here).
  * A request whose context length is below zero, above max_context, or with its new tokens
  * past what a row of the page table addresses gives zero rows (lse -inf); a page outside
  * 0 .. num_pages - 1 reads as zeros; both are reported in device_status.  cu_seqlens that
@@ -340,8 +349,8 @@ kda_status kda_chunk_attention_ex(const kda_chunk_attention_args* args, const kd
  * kda_tree_attention_schedule).  kernel: KDA_CHUNK_ROWS, the kernel for few rows, `ctas`
  * CTAs sharing a block of them; KDA_CHUNK_TENSOR, the tensor-core kernel, at most `ctas`
  * equal stretches of the call's work, what the workspace has room for: the lengths on the
- * device decide (queries or caches without a tensor map take the kernel for few rows all
- * the same).
+ * device decide (strides are not looked at: queries or caches without a tensor map take the
+ * kernel for few rows all the same).
  */
 #define KDA_CHUNK_ROWS 0
 #define KDA_CHUNK_TENSOR 1

@@ -28,10 +28,11 @@
 // item's length on it the keys that its last token sees and a constant for its way in and
 // out; every CTA takes an equal stretch, so that ragged batches and the causal triangle
 // leave no SM idle.  Where row tiles share more keys than L2 keeps, the CTAs walk the line in
-// waves, all on one part of it and then on the next (2048 tokens over 126976: 3010 us without,
-// 2660 with four waves, 2580 with eight, 2620 with sixteen).  A stretch cuts at most two items; the parts of a cut item leave
-// normalised rows and their log-sum in the workspace (slot 0 of a CTA: a later part of an
-// item, slot 1: the first), joined in the CTAs' order by chunk_join_kernel (kda_chunk.cu).
+// waves, all on one part of it and then on the next (2048 tokens over 126976: 2970 us without,
+// 2610 with four waves, 2570 with eight).  A stretch cuts at most two items; the parts of a
+// cut item leave normalised rows and their log-sum in the workspace (slot 0 of a CTA: a later
+// part of an item, slot 1: the first), joined in the CTAs' order by chunk_join_kernel
+// (kda_chunk.cu).
 //
 // Head size 256: S of two row tiles and a whole O do not fit TMEM, so two neighbouring
 // CTAs take the same stretch, both with all of S and each with one half of V's columns.
@@ -51,8 +52,9 @@
 // a prompt of 8192 tokens 341 (1.61 PFLOP/s, the tensor pipe 75 % busy), of 32768 5000 (1.75),
 // 2048 tokens over 126976 2600 (1.65), 32 prompts of 512 118 (0.58), 64 single tokens over 4096
 // 175 (6.1 TB/s of K and V).  What bounds it: with many tiles an item the products and the
-// exponentials together, with few an item's change, most of which is fetching the roles' code
-// (77 KB) into the instruction cache.
+// exponentials together (head size 64: neither, 8192 tokens 279 with the tensor pipe 44 % and the
+// exponentials' 45 % busy, but a stream's chain of one score tile after the other), with few an
+// item's change, most of which is fetching the roles' code (77 KB) into the instruction cache.
 //
 // Registers: 512 threads start with 128 each; the softmax warps take 168, the way out
 // keeps 80, the last four warps 96 (2 x 168 + 80 + 96 = 4 x 128).

@@ -7,8 +7,9 @@
 // loads are on their way before the first store.  All pools of a call (48 a launch) go in
 // one grid, since a layer's share alone would not fill the GPU.  Measured (GPU time): 16
 // states in 12 pools (805 MB read and written) 117 us, 6.9 TB/s; 24 pages in 32 caches 18.8 us
-// (5.6); the accepted rows of 256 requests in 32 caches 28 us for 108 MB, bound by the chains of
-// path, page table and rows of a CTA's few hundred KB, one request 3 us.
+// (5.6); the accepted rows of 256 requests in 32 caches 28 us for 108 MB, two waves of CTAs of some
+// 60 KB, bound by the chain of path, page table and rows and the barriers between their reads and
+// writes, one request 3 us.
 #include "kda_internal.h"
 #include "ops_internal.h"
 
@@ -54,14 +55,16 @@ __global__ void __launch_bounds__(kPoolThreads) pool_copy_kernel(const __grid_co
 }
 
 constexpr int kPathMax = 256;
-constexpr int kCommitBatch = 4;   // as kBatch: with 8, and the registers for them, 32 us in the case below
+// As kBatch.  With 8 the case below takes 47 us instead of 30 where six CTAs share an SM
+// (registers spill), and 29, hardly less, where four do.
+constexpr int kCommitBatch = 4;
 
 // A CTA takes a request's path in `group` caches (or a split of the rows' pieces).  The path
 // ascends, so path[j] >= j: in the order of j no row is written before it has been read, and a
 // batch of pieces in that order can be read as a whole before it is written.  The pieces of
 // all of the CTA's caches, which have rows of the same size then, are one sequence: finding the
 // rows' places is a chain of four loads, which a CTA a cache paid each time (256 requests, 32
-// caches, rows of 2 KB: 27 us, 49 with a CTA a cache).
+// caches, rows of 2 KB, calls one after the other: 30 us, 37 with a CTA a cache).
 __global__ void __launch_bounds__(kPoolThreads, 6) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
     __shared__ int2 s_from[kPathMax], s_to[kPathMax];   // page (< 0: none) and row of a moved node and of its new place
     __shared__ int s_first;

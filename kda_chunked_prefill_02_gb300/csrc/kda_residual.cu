@@ -12,7 +12,8 @@
 // and both norms stay in fp32, and x' and h are rounded once, h from the unrounded x'.
 // Measured (GPU time): 32768 tokens of 4096 with both norms and a gate 207 us (6.5 TB/s), 8191
 // of 1288 in fp16 over an fp32 stream 23.7 us (6.2), one token of 2048 2.4 us (a launch and one
-// chain of loads).
+// chain of loads).  Rows of fewer than 256 channels leave lanes of their warp idle: the sum and the
+// norm of 2^27 elements move 7.1 TB/s in rows of 512, 6.0 in rows of 256, 3.6 of 128, 1.9 of 64.
 #include "kda_internal.h"
 #include "ops_internal.h"
 

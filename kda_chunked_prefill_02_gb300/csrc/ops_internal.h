@@ -103,10 +103,10 @@ bool launch_tree_mma(const TreeParams& p, int D, bool f16, int grid, cudaStream_
 // prompt (32 / 8 heads) takes 364, 351, 345, 351 us, four of 2048 130, 125, 125, 126, 24 ragged
 // prompts of head size 64 74, 65, 65, 65.
 constexpr int kItemKeys = 256;
-// K and V of a wave over the line of work (L2 has 129 MB): 2048 tokens over 126976 with 32, 64,
-// 100 MB 2570, 2580, 2770 us.
+// K and V of a wave over the line of work (L2 has 129 MB): 2048 tokens over 126976 with 32 MB
+// (sixteen waves), 64 (eight), 100 (six) 2690, 2590, 2750 us.
 constexpr int64_t kWaveBytes = 64 << 20;
-constexpr int kMaxWaves = 8;   // (kda_chunk_mma.cu has what more and fewer measured)
+constexpr int kMaxWaves = 8;   // (kda_chunk_mma.cu has what fewer measured)
 struct ChunkParams {
     const void *q, *kc, *vc;
     void* out;

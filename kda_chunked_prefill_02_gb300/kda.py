@@ -56,8 +56,8 @@ def _make_overrides(state_kernel=None, segment_chunks=None, prep_ctas=None, no_p
 
 @contextlib.contextmanager
 def overrides(**kw):
-    """Within the block, calls of this module (and kda_tree_attention, for
-    wait_limit_ns and timeout_probe) pass these kda_overrides to the
+    """Within the block, calls of this module (and kda_tree_attention and
+    kda_chunk_attention, for wait_limit_ns and timeout_probe) pass these kda_overrides to the
     library (tests and measurements): state_kernel ("slab" | "head"),
     segment_chunks (0: never segment, n: segments of n chunks), prep_ctas,
     no_pdl, stall_seed, wait_limit_ns, scan_segments (1: never run the

@@ -313,6 +313,7 @@ def kda_chunk_attention(q, k_cache, v_cache, page_table, context_lens, *, cu_seq
     The keys and values of the new tokens follow their request's context in the cache
     (kda_qk_norm_rope puts them there); token i sees the context and the new tokens up
     to itself.  Rows of q behind cu_seqlens[R] belong to no request and are left out.
+    Calls of single tokens alone are faster as kda_tree_attention's where they are thousands.
     scale defaults to D^-0.5; max_context: a host upper bound of context_lens (None:
     what the page table can address); out may be q itself.  Returns out, or (out, lse)
     with lse fp32 [T_total, Hq] ([R, T, Hq]).
@@ -325,7 +326,7 @@ def kda_chunk_attention(q, k_cache, v_cache, page_table, context_lens, *, cu_seq
 
 def chunk_attention_schedule(q, k_cache, page_table, *, packed=True, scale=None, max_context=None, num_sms=None):
     """How kda_chunk_attention cuts a call (kda_chunk_attention_schedule): dict(kernel, ctas),
-    kernel "rows" or "tensor".  Host only; of the tensors only types and shapes are read;
+    kernel "rows" or "tensor" (ctas: stretches of the work, at most).  Host only; of the tensors only types and shapes are read;
     packed: q is [T_total, Hq, D] (with cu_seqlens).  num_sms as in tree_attention_schedule."""
     a = ChunkAttentionArgs()
     a.q = a.k_cache = a.v_cache = a.page_table = a.context_lens = 16   # not followed
